@@ -231,7 +231,7 @@ def prepare(case, seed):
             s["k_order"], s["v_order"] = _tile_order(dim)
         if own:
             import block_paged_kv_gb300 as pkv
-            s["rope"] = pkv.make_rope(_inv_freq(rd), DEV, axis_of_pair=_axis_of_pair(rd, axes),
+            s["rope"] = pkv.make_rope(_inv_freq(rd), axis_of_pair=_axis_of_pair(rd, axes),
                                       interleaved=case["interleaved"])
         return s
     B, W, S = case["batch"], case["window"], case["sinks"]
