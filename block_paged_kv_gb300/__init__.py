@@ -27,6 +27,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_WORKSPACE, PKV_ERR_OUT_OF_BLOCKS = range(6)
+PKV_ERR_HOST_MEMORY = 6
 PKV_F32, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_BAD_PREFIX, DEV_TIMEOUT = 1, 2, 4, 8, 16
 DEV_Q_RANGE = 32
@@ -55,6 +56,15 @@ class _Group(ctypes.Structure):
                 ("block_tables", ctypes.c_void_p), ("max_blocks_per_seq", ctypes.c_int32),
                 ("seq_lens", ctypes.c_void_p), ("max_seq_len", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+ROPE_MAX_AXES, ROPE_MAX_PAIRS = 4, 128
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("freq", ctypes.c_uint64 * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS)]
 
 
 MAX_DECODE_GROUPS = 4
@@ -107,9 +117,27 @@ _lib.paged_decode_attention_no_alloc.argtypes = [_vp, _i32, _PP, _vp, _i32, _vp,
 _lib.paged_decode_attention_no_alloc.restype = ctypes.c_int
 NO_ALLOC_SCRATCH_BYTES = 16 << 20
 _u64p = ctypes.POINTER(ctypes.c_uint64)
+_i64, _RP = ctypes.c_int64, ctypes.POINTER(_Rope)
+_lib.pkv_rope_init.argtypes = [_RP, _i32, _vp, _i32, _vp, _i32, ctypes.c_float]
+_lib.pkv_rope_init.restype = ctypes.c_int
+_lib.paged_kv_append_rope.argtypes = [_PP, _vp, _i32, _vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64,
+                                      _RP, _vp, _i64, _vp, _vp]
+_lib.paged_kv_append_rope.restype = ctypes.c_int
+_lib.paged_copy_blocks.argtypes = [_PP, _PP, _i32, _vp, _vp, _i32, _vp, _vp]
+_lib.paged_copy_blocks.restype = ctypes.c_int
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _lib.pkv_slot_mapping_check_host.argtypes = [_vp, _i32, _i32, _i32, _i32p]
 _lib.pkv_slot_mapping_check_host.restype = ctypes.c_int
+_lib.pkv_block_copies_check_host.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _i32p]
+_lib.pkv_block_copies_check_host.restype = ctypes.c_int
+_lib.pkv_allocator_expire_window.argtypes = [_vp, _i32, _i32, _i32]
+_lib.pkv_allocator_expire_window.restype = ctypes.c_int
+_lib.pkv_allocator_fork.argtypes = [_vp, _i32, _i32, _i32p, _i32p, _i32p]
+_lib.pkv_allocator_fork.restype = ctypes.c_int
+_lib.pkv_allocator_truncate.argtypes = [_vp, _i32, _i32, _i32p, _i32p]
+_lib.pkv_allocator_truncate.restype = ctypes.c_int
+_lib.pkv_allocator_compact.argtypes = [_vp, _i32, _vp, _vp, _i32, _i32p]
+_lib.pkv_allocator_compact.restype = ctypes.c_int
 _lib.pkv_allocator_create.argtypes = [_i32, _i32, _i32]
 _lib.pkv_allocator_create.restype = _vp
 _lib.pkv_allocator_destroy.argtypes = [_vp]
@@ -133,7 +161,7 @@ _lib.pkv_allocator_refcount.restype = _i32
 _lib.pkv_allocator_stats.argtypes = [_vp, _i32p, _i32p, _i32p, _i32p]
 _lib.pkv_allocator_stats.restype = ctypes.c_int
 
-KERNEL_APPEND, KERNEL_DECODE_PREFIX, KERNEL_DECODE_SPLIT, KERNEL_DECODE_COMBINE, KERNEL_PREFILL = range(5)
+KERNEL_APPEND, KERNEL_DECODE_PREFIX, KERNEL_DECODE_SPLIT, KERNEL_DECODE_COMBINE, KERNEL_PREFILL, KERNEL_COPY = range(6)
 
 EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_attention",
             "paged_prefill_workspace_size", "paged_prefill_chunk_attention", "pkv_status_string",
@@ -145,7 +173,10 @@ EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_atte
             "pkv_allocator_destroy", "pkv_allocator_begin", "pkv_allocator_find_cached_prefix",
             "pkv_allocator_reserve", "pkv_allocator_publish", "pkv_allocator_expire",
             "pkv_allocator_release",
-            "pkv_allocator_table", "pkv_allocator_refcount", "pkv_allocator_stats"]
+            "pkv_allocator_table", "pkv_allocator_refcount", "pkv_allocator_stats",
+            "pkv_rope_init", "paged_kv_append_rope", "paged_copy_blocks", "pkv_block_copies_check_host",
+            "pkv_allocator_expire_window", "pkv_allocator_fork", "pkv_allocator_truncate",
+            "pkv_allocator_compact"]
 
 
 class PkvError(RuntimeError):
@@ -190,7 +221,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _on(device: torch.device):
@@ -345,6 +376,167 @@ def paged_kv_append(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mapping: to
         _check("paged_kv_append", _lib.paged_kv_append(
             ctypes.byref(pool), slot_mapping.data_ptr(), k_new.shape[0], k_new.data_ptr(),
             v_new.data_ptr(), _ptr(status), _stream(dev)))
+
+
+class RopeDesc:
+    """Rotary descriptor (host memory, passed by value into every launch)."""
+
+    def __init__(self, c: _Rope):
+        self._c = c
+
+    @property
+    def rotary_dim(self) -> int:
+        return int(self._c.rotary_dim)
+
+    @property
+    def num_axes(self) -> int:
+        return int(self._c.num_axes)
+
+
+def make_rope(inv_freq, axis_of_pair=None, num_axes: Optional[int] = None, interleaved: bool = False,
+              factor: float = 1.0) -> RopeDesc:
+    """Rotary descriptor of ``rotary_dim = 2 * len(inv_freq)`` dims: pair i turns
+    by ``positions[axis_of_pair[i]] * inv_freq[i]`` radians (float64).
+    ``axis_of_pair`` defaults to one axis, ``num_axes`` to its largest entry + 1;
+    ``interleaved`` pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2);
+    ``factor`` multiplies the rotated dims."""
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64)).reshape(-1)
+    a = None
+    if axis_of_pair is not None:
+        a = np.ascontiguousarray(np.asarray(axis_of_pair, dtype=np.int32)).reshape(-1)
+        _require(a.shape == f.shape, "one axis per pair")
+    if num_axes is None:
+        num_axes = int(a.max()) + 1 if a is not None and a.size else 1
+    c = _Rope()
+    _check("pkv_rope_init", _lib.pkv_rope_init(
+        ctypes.byref(c), 2 * f.size, f.ctypes.data if f.size else None, num_axes,
+        a.ctypes.data if a is not None else None, int(interleaved), float(factor)))
+    return RopeDesc(c)
+
+
+def _token_stride(t: torch.Tensor, rows: int, dim: int, name: str) -> int:
+    """Elements between a [T, rows, dim] operand's tokens; each token's rows are contiguous."""
+    s = t.stride()
+    if not ((s[2] == 1 or dim == 1) and (s[1] == dim or rows == 1)):
+        raise ValueError(f"{name}: each token's [heads, head_dim] rows are contiguous")
+    return s[0] if t.shape[0] > 1 else rows * dim
+
+
+def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mapping: torch.Tensor,
+                         q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                         positions: torch.Tensor, rope: RopeDesc,
+                         q_out: Optional[torch.Tensor] = None,
+                         status: Optional[torch.Tensor] = None, k_scale: Optional[float] = None,
+                         v_scale: Optional[float] = None) -> Optional[torch.Tensor]:
+    """Rotate ``q`` [T, Hq, D] and ``k_new`` [T, Hkv, D] by ``positions`` ([T], or
+    [num_axes, T]; int32) and append the rotated k and ``v_new`` into the pools at
+    ``slot_mapping`` [T]; returns the rotated q (``q_out``, which may be ``q``).
+    Token rows may be cut from a wider projection output.  ``q`` None: k alone."""
+    pool = _pool(k_pool, v_pool, k_scale, v_scale)
+    dev = k_pool.device
+    hkv, D = pool.num_kv_heads, pool.head_dim
+    act = _act_dtype(k_pool.dtype)
+    _i32_dev(slot_mapping, "slot_mapping", dev)
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    _require(k_new.shape == (T, hkv, D) and v_new.shape == (T, hkv, D),
+             "k_new/v_new are [T, num_kv_heads, head_dim], one slot per token")
+    _require(k_new.dtype == act and v_new.dtype == act, "new rows match the pool dtype (bf16 for FP8)")
+    _on_device(k_new, "k_new", dev)
+    _on_device(v_new, "v_new", dev)
+    _require(positions.dtype == torch.int32 and positions.device == dev and
+             (positions.shape == (rope.num_axes, T) or (rope.num_axes == 1 and positions.shape == (T,))) and
+             (positions.stride(-1) == 1 or T <= 1),
+             "positions are int32 [num_axes, T] (or [T]) on the pools' GPU, each axis contiguous")
+    # one axis has no stride to speak of
+    pos_stride = positions.stride(0) if rope.num_axes > 1 else T
+    _status_ok(status, dev)
+    hq = qs = os_ = 0
+    if q is not None:
+        _require(q.dim() == 3 and q.shape[0] == T and q.shape[2] == D and q.dtype == act,
+                 "q is [T, num_q_heads, head_dim], pool dtype (bf16 for FP8)")
+        _on_device(q, "q", dev)
+        hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=act, device=dev)
+        else:
+            _require(q_out.shape == q.shape and q_out.dtype == act, "q_out matches q")
+            _on_device(q_out, "q_out", dev)
+        if hq:
+            qs, os_ = _token_stride(q, hq, D, "q"), _token_stride(q_out, hq, D, "q_out")
+    else:
+        _require(q_out is None, "q_out without q")
+    with _on(dev):
+        _check("paged_kv_append_rope", _lib.paged_kv_append_rope(
+            ctypes.byref(pool), slot_mapping.data_ptr(), T, _ptr(q), qs, hq,
+            k_new.data_ptr(), _token_stride(k_new, hkv, D, "k_new"), v_new.data_ptr(),
+            _token_stride(v_new, hkv, D, "v_new"), positions.data_ptr(), pos_stride,
+            ctypes.byref(rope._c), _ptr(q_out), os_, _ptr(status), _stream(dev)))
+    return q_out
+
+
+class PoolSet:
+    """The (K, V) pools of several layers that share block ids, checked once: what
+    ``paged_copy_blocks`` copies in.  Holds the tensors."""
+
+    def __init__(self, pools):
+        self.pools = [(k, v) for k, v in pools]
+        _require(len(self.pools) > 0, "at least one pool")
+        self.device = self.pools[0][0].device
+        # page copies move bytes: FP8 scales play no part
+        self._c = (_Pool * len(self.pools))(*[_pool(k, v, 1.0, 1.0) for k, v in self.pools])
+        f = self._c[0]
+        for (k, v), c in zip(self.pools, self._c):
+            _require(k.device == self.device and v.device == self.device, "every pool on one GPU")
+            _require((c.dtype, c.block_size, c.num_kv_heads, c.head_dim) ==
+                     (f.dtype, f.block_size, f.num_kv_heads, f.head_dim),
+                     "the pools share dtype, block size, kv heads and head_dim")
+
+    def __len__(self) -> int:
+        return len(self.pools)
+
+
+def paged_copy_blocks(pools: PoolSet, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
+                      dst_pools: Optional[PoolSet] = None,
+                      status: Optional[torch.Tensor] = None) -> None:
+    """Copy pages ``src_blocks[i]`` of every pool to pages ``dst_blocks[i]`` (int32
+    [n]) of the same pool, or of ``dst_pools``'; negative ids are skipped.  Within
+    a call no page may be written twice, nor written and read
+    (``check_block_copies``)."""
+    dev = pools.device
+    _i32_dev(src_blocks, "src_blocks", dev)
+    _i32_dev(dst_blocks, "dst_blocks", dev)
+    _require(src_blocks.dim() == 1 and src_blocks.shape == dst_blocks.shape,
+             "one destination page per source page")
+    if dst_pools is not None:
+        _require(dst_pools.device == dev and len(dst_pools) == len(pools),
+                 "as many destination pools as source pools, on one GPU")
+    _status_ok(status, dev)
+    with _on(dev):
+        _check("paged_copy_blocks", _lib.paged_copy_blocks(
+            pools._c, dst_pools._c if dst_pools is not None else None, len(pools),
+            src_blocks.data_ptr(), dst_blocks.data_ptr(), src_blocks.shape[0], _ptr(status),
+            _stream(dev)))
+
+
+def check_block_copies(src_blocks, dst_blocks, num_blocks: int,
+                       dst_num_blocks: Optional[int] = None) -> None:
+    """Debug check of a page copy list (library helper, host arrays): ids inside
+    the pools, no page written twice or both written and read.  Raises ValueError
+    naming the first pair at fault.  ``dst_num_blocks``: the destination is
+    another pool, of that size."""
+    s = np.ascontiguousarray(np.asarray(src_blocks, dtype=np.int32)).reshape(-1)
+    d = np.ascontiguousarray(np.asarray(dst_blocks, dtype=np.int32)).reshape(-1)
+    _require(s.shape == d.shape, "one destination page per source page")
+    bad = ctypes.c_int32(-1)
+    same = dst_num_blocks is None
+    code = _lib.pkv_block_copies_check_host(s.ctypes.data, d.ctypes.data, s.size, num_blocks,
+                                            num_blocks if same else dst_num_blocks, int(same),
+                                            ctypes.byref(bad))
+    if code != PKV_OK:
+        if bad.value < 0:
+            raise ValueError("check_block_copies: invalid arguments")
+        raise ValueError(f"check_block_copies: pair {bad.value} ({int(s[bad.value])} -> "
+                         f"{int(d[bad.value])}) lies past a pool or meets an earlier pair's page")
 
 
 def decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -698,6 +890,37 @@ class BlockAllocator:
         """Drop the blocks wholly before ``first_live_token`` (a sliding
         window's start); their table entries become -1."""
         _check("pkv_allocator_expire", _lib.pkv_allocator_expire(self._a, req, int(first_live_token)))
+
+    def expire_window(self, req: int, first_live_token: int, sinks: int) -> None:
+        """``expire``, keeping the blocks that hold any of the first ``sinks`` tokens."""
+        _check("pkv_allocator_expire_window", _lib.pkv_allocator_expire_window(
+            self._a, req, int(first_live_token), int(sinks)))
+
+    def fork(self, req: int, n_tokens: int):
+        """A new request that shares ``req``'s first ``n_tokens`` tokens: its id and
+        the page copy to make, ``(src, dst)``, or None when none is needed."""
+        v = [ctypes.c_int32(-1) for _ in range(3)]
+        _check("pkv_allocator_fork", _lib.pkv_allocator_fork(
+            self._a, req, int(n_tokens), *[ctypes.byref(x) for x in v]))
+        return int(v[0].value), (None if v[1].value < 0 else (int(v[1].value), int(v[2].value)))
+
+    def truncate(self, req: int, n_tokens: int):
+        """Roll ``req`` back to its first ``n_tokens`` tokens; the page copy to make,
+        ``(src, dst)``, or None."""
+        v = [ctypes.c_int32(-1) for _ in range(2)]
+        _check("pkv_allocator_truncate", _lib.pkv_allocator_truncate(
+            self._a, req, int(n_tokens), *[ctypes.byref(x) for x in v]))
+        return None if v[0].value < 0 else (int(v[0].value), int(v[1].value))
+
+    def compact(self, num_blocks: int):
+        """Shrink the pool to ``num_blocks`` blocks: the page copies to make, int32
+        arrays ``(src, dst)``."""
+        cap = self.stats()[0]
+        src, dst = np.empty(max(cap, 1), np.int32), np.empty(max(cap, 1), np.int32)
+        n = ctypes.c_int32(0)
+        _check("pkv_allocator_compact", _lib.pkv_allocator_compact(
+            self._a, int(num_blocks), src.ctypes.data, dst.ctypes.data, cap, ctypes.byref(n)))
+        return src[:n.value].copy(), dst[:n.value].copy()
 
     def release(self, req: int) -> None:
         _check("pkv_allocator_release", _lib.pkv_allocator_release(self._a, req))

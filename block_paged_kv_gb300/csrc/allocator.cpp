@@ -12,6 +12,7 @@
 #include <list>
 #include <set>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pkv.h"
@@ -249,6 +250,137 @@ pkv_status pkv_allocator_expire(pkv_allocator *a, int32_t req, int32_t first_liv
         t[i] = -1;
     }
     return PKV_OK;
+}
+
+pkv_status pkv_allocator_expire_window(pkv_allocator *a, int32_t req, int32_t first_live_token, int32_t sinks)
+{
+    if (a == nullptr || first_live_token < 0 || sinks < 0) return PKV_ERR_INVALID_ARG;
+    auto it = a->reqs.find(req);
+    if (it == a->reqs.end()) return PKV_ERR_INVALID_ARG;
+    std::vector<int32_t> &t = it->second.table;
+    const int64_t n = std::min<int64_t>(first_live_token / a->bs, static_cast<int64_t>(t.size()));
+    for (int64_t i = (static_cast<int64_t>(sinks) + a->bs - 1) / a->bs; i < n; ++i) {
+        if (t[i] < 0) continue;
+        a->drop_ref(t[i]);
+        t[i] = -1;
+    }
+    return PKV_OK;
+}
+
+pkv_status pkv_allocator_fork(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *new_req,
+                              int32_t *src, int32_t *dst)
+try {
+    if (a == nullptr || new_req == nullptr || src == nullptr || dst == nullptr || n_tokens < 0)
+        return PKV_ERR_INVALID_ARG;
+    auto it = a->reqs.find(req);
+    if (it == a->reqs.end()) return PKV_ERR_INVALID_ARG;
+    const Request &r = it->second;
+    if (n_tokens > static_cast<int64_t>(r.table.size()) * a->bs) return PKV_ERR_INVALID_ARG;
+    const size_t full = static_cast<size_t>(n_tokens / a->bs);
+    const bool part = n_tokens % a->bs != 0;
+    Request c;
+    c.fresh = false;
+    c.table.assign(r.table.begin(), r.table.begin() + static_cast<ptrdiff_t>(full));
+    c.hashes.assign(r.hashes.begin(), r.hashes.begin() + static_cast<ptrdiff_t>(std::min(full, r.hashes.size())));
+    c.published = static_cast<int32_t>(std::min<size_t>(full, static_cast<size_t>(r.published)));
+    int32_t from = -1, to = -1;
+    if (part) {
+        std::vector<int32_t> got;
+        if (r.table[full] >= 0) {
+            if (!a->take(1, got)) return PKV_ERR_OUT_OF_BLOCKS;
+            from = r.table[full];
+            to = got[0];
+        }
+        c.table.push_back(to);
+    }
+    for (size_t i = 0; i < full; ++i)
+        if (c.table[i] >= 0) ++a->blocks[c.table[i]].refcount;
+    const int32_t id = a->next_req++;
+    a->reqs.emplace(id, std::move(c));
+    *new_req = id;
+    *src = from;
+    *dst = to;
+    return PKV_OK;
+} catch (...) {
+    return PKV_ERR_HOST_MEMORY;
+}
+
+pkv_status pkv_allocator_truncate(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *src, int32_t *dst)
+try {
+    if (a == nullptr || src == nullptr || dst == nullptr || n_tokens < 0) return PKV_ERR_INVALID_ARG;
+    auto it = a->reqs.find(req);
+    if (it == a->reqs.end()) return PKV_ERR_INVALID_ARG;
+    Request &r = it->second;
+    if (n_tokens > static_cast<int64_t>(r.table.size()) * a->bs) return PKV_ERR_INVALID_ARG;
+    const size_t full = static_cast<size_t>(n_tokens / a->bs);
+    const bool part = n_tokens % a->bs != 0;
+    int32_t from = -1, to = -1;
+    if (part && r.table[full] >= 0) {
+        const Block &tail = a->blocks[r.table[full]];
+        if (tail.refcount > 1 || tail.published) {
+            std::vector<int32_t> got;
+            if (!a->take(1, got)) return PKV_ERR_OUT_OF_BLOCKS;
+            from = r.table[full];
+            to = got[0];
+            a->drop_ref(from);
+            r.table[full] = to;
+        }
+    }
+    const size_t keep = full + (part ? 1 : 0);
+    for (size_t i = keep; i < r.table.size(); ++i)
+        if (r.table[i] >= 0) a->drop_ref(r.table[i]);
+    r.table.resize(keep);
+    if (r.hashes.size() > full) r.hashes.resize(full);
+    r.published = static_cast<int32_t>(std::min<size_t>(full, static_cast<size_t>(r.published)));
+    r.fresh = false;
+    *src = from;
+    *dst = to;
+    return PKV_OK;
+} catch (...) {
+    return PKV_ERR_HOST_MEMORY;
+}
+
+pkv_status pkv_allocator_compact(pkv_allocator *a, int32_t num_blocks, int32_t *src, int32_t *dst, int32_t cap,
+                                 int32_t *n_moves)
+try {
+    if (a == nullptr || n_moves == nullptr || num_blocks < 0 || num_blocks > a->num_blocks() || cap < 0 ||
+        (cap > 0 && (src == nullptr || dst == nullptr)))
+        return PKV_ERR_INVALID_ARG;
+    const int32_t held = a->num_blocks() - static_cast<int32_t>(a->free_set.size());  // in use or cached
+    const int32_t evict = std::max(0, held - num_blocks);
+    if (evict > static_cast<int32_t>(a->lru.size())) return PKV_ERR_OUT_OF_BLOCKS;
+    // the plan, nothing changed yet: what moves, and where to
+    std::set<int32_t> gone;
+    for (auto it = a->lru.begin(); static_cast<int32_t>(gone.size()) < evict; ++it) gone.insert(*it);
+    std::vector<int32_t> from, to;
+    for (int32_t b = num_blocks; b < a->num_blocks(); ++b)
+        if (a->free_set.count(b) == 0 && gone.count(b) == 0) from.push_back(b);
+    for (int32_t b = 0; b < num_blocks && to.size() < from.size(); ++b)
+        if (a->free_set.count(b) != 0 || gone.count(b) != 0) to.push_back(b);
+    *n_moves = static_cast<int32_t>(from.size());
+    if (*n_moves > cap) return PKV_ERR_INVALID_ARG;
+    std::unordered_map<int32_t, int32_t> moved;
+    for (size_t i = 0; i < from.size(); ++i) moved.emplace(from[i], to[i]);
+    for (int32_t i = 0; i < evict; ++i) a->evict_one();
+    for (size_t i = 0; i < from.size(); ++i) {
+        Block &blk = a->blocks[from[i]];
+        if (blk.published) a->table[blk.hash] = to[i];
+        if (blk.cached) *blk.lru_it = to[i];
+        a->blocks[to[i]] = blk;
+        a->free_set.erase(to[i]);
+        src[i] = from[i];
+        dst[i] = to[i];
+    }
+    for (auto &kv : a->reqs)
+        for (int32_t &b : kv.second.table) {
+            auto m = b >= 0 ? moved.find(b) : moved.end();
+            if (m != moved.end()) b = m->second;
+        }
+    a->blocks.resize(static_cast<size_t>(num_blocks));
+    a->free_set.erase(a->free_set.lower_bound(num_blocks), a->free_set.end());
+    return PKV_OK;
+} catch (...) {
+    return PKV_ERR_HOST_MEMORY;
 }
 
 pkv_status pkv_allocator_release(pkv_allocator *a, int32_t req)

@@ -459,6 +459,7 @@ const char *pkv_status_string(pkv_status s)
     case PKV_ERR_CUDA: return "CUDA error";
     case PKV_ERR_WORKSPACE: return "workspace too small or misaligned";
     case PKV_ERR_OUT_OF_BLOCKS: return "block pool exhausted at its maximum size";
+    case PKV_ERR_HOST_MEMORY: return "out of host memory";
     }
     return "unknown status";
 }
@@ -870,6 +871,158 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
         err = launch_prefill_f32(p, st);
     }
     return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// A row operand of the rotary append: aligned, tokens at least a token's rows
+// apart, strides in whole 16-byte vectors.
+bool rope_rows_ok(const void *ptr, int64_t stride, int64_t row_elems, int eb)
+{
+    return ptr != nullptr && aligned16(ptr) && stride >= row_elems && stride <= (INT64_MAX >> 8) &&
+           (stride * eb) % 16 == 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_rope_init(pkv_rope *rope, int32_t rotary_dim, const double *inv_freq, int32_t num_axes,
+                         const int32_t *axis_of_pair, int32_t interleaved, float factor)
+{
+    if (rope == nullptr || inv_freq == nullptr || rotary_dim < 2 || rotary_dim % 2 != 0 ||
+        rotary_dim > 2 * PKV_ROPE_MAX_PAIRS || num_axes < 1 || num_axes > PKV_ROPE_MAX_AXES ||
+        !std::isfinite(factor))
+        return PKV_ERR_INVALID_ARG;
+    pkv_rope r{};
+    for (int32_t i = 0; i < rotary_dim / 2; ++i) {
+        const int32_t a = axis_of_pair != nullptr ? axis_of_pair[i] : 0;
+        if (!std::isfinite(inv_freq[i]) || a < 0 || a >= num_axes) return PKV_ERR_INVALID_ARG;
+        r.axis[i] = static_cast<uint8_t>(a);
+        // |f| / 2 pi as a double t and its error e (1 / 2 pi carried as two
+        // doubles), whole turns dropped, then rounded to fractions of 2^64
+        constexpr double kInv2PiHi = 0.15915494309189535, kInv2PiLo = -9.839338337591243e-18;
+        const double f = std::fabs(inv_freq[i]), t = f * kInv2PiHi;
+        const double e = std::fma(f, kInv2PiHi, -t) + f * kInv2PiLo;
+        const double f64 = std::ldexp(t - std::floor(t), 64), whole = std::floor(f64);  // exact, < 2^64
+        const double e64 = std::nearbyint(std::ldexp(e - std::nearbyint(e), 64) + (f64 - whole));  // |.| <= 2^63
+        constexpr double kHalf = 9223372036854775808.0;  // 2^63: half a turn, either way
+        uint64_t bits = static_cast<uint64_t>(whole);
+        bits += std::fabs(e64) >= kHalf ? (1ull << 63) : static_cast<uint64_t>(static_cast<int64_t>(e64));
+        r.freq[i] = inv_freq[i] < 0 ? 0 - bits : bits;
+    }
+    r.rotary_dim = rotary_dim;
+    r.num_axes = num_axes;
+    r.interleaved = interleaved != 0 ? 1 : 0;
+    r.factor = factor;
+    *rope = r;
+    return PKV_OK;
+}
+
+pkv_status paged_kv_append_rope(const pkv_pool *pool, const int32_t *slot_mapping, int32_t num_tokens,
+                                const void *q, int64_t q_stride, int32_t num_q_heads, const void *k_new,
+                                int64_t k_stride, const void *v_new, int64_t v_stride,
+                                const int32_t *positions, int64_t pos_stride, const pkv_rope *rope,
+                                void *q_out, int64_t q_out_stride, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (!valid_pool(pool) || num_tokens < 0 || num_q_heads < 0 || rope == nullptr) return PKV_ERR_INVALID_ARG;
+    const int32_t rd = rope->rotary_dim;
+    if (rd < 2 || rd % 2 != 0 || rd > pool->head_dim || rd > 2 * PKV_ROPE_MAX_PAIRS || rope->num_axes < 1 ||
+        rope->num_axes > PKV_ROPE_MAX_AXES || !std::isfinite(rope->factor))
+        return PKV_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < rd / 2; ++i)
+        if (rope->axis[i] >= rope->num_axes) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    const int eb = elem_bytes(out_dtype(pool->dtype));
+    const int64_t q_row = static_cast<int64_t>(num_q_heads) * pool->head_dim;
+    const int64_t kv_row = static_cast<int64_t>(pool->num_kv_heads) * pool->head_dim;
+    if (slot_mapping == nullptr || positions == nullptr || (rope->num_axes > 1 && pos_stride < num_tokens) ||
+        !rope_rows_ok(k_new, k_stride, kv_row, eb) || !rope_rows_ok(v_new, v_stride, kv_row, eb))
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads > 0 &&
+        (!rope_rows_ok(q, q_stride, q_row, eb) || !rope_rows_ok(q_out, q_out_stride, q_row, eb)))
+        return PKV_ERR_INVALID_ARG;
+    if ((static_cast<int64_t>(pool->head_dim) * eb) % 16 != 0 || rd % (pool->dtype == PKV_F32 ? 8 : 16) != 0)
+        return PKV_ERR_UNSUPPORTED;
+    if (pool->dtype == PKV_FP8_E4M3 && !fp8_shape_built(pool)) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(pool->num_blocks) * pool->block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    // units of a row (rotated vector pairs and copied vectors): a CTA's threads hold a row at least
+    if (static_cast<int64_t>(pool->head_dim) * eb / 16 - rd * eb / 32 > 256) return PKV_ERR_UNSUPPORTED;
+    RopeParams p{};
+    p.q = q;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.q_out = q_out;
+    p.k_pool = pool->k;
+    p.v_pool = pool->v;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.status = dev_status;
+    p.q_stride = q_stride * eb / 16;
+    p.k_stride = k_stride * eb / 16;
+    p.v_stride = v_stride * eb / 16;
+    p.q_out_stride = q_out_stride * eb / 16;
+    p.pos_stride = pos_stride;
+    p.num_tokens = num_tokens;
+    p.hq = num_q_heads;
+    p.hkv = pool->num_kv_heads;
+    p.block_size = pool->block_size;
+    p.head_dim = pool->head_dim;
+    p.num_slots = pool->num_blocks * pool->block_size;
+    p.rotary_dim = rd;
+    p.interleaved = rope->interleaved;
+    p.factor = rope->factor;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    std::memcpy(p.freq, rope->freq, sizeof(uint64_t) * (rd / 2));
+    std::memcpy(p.axis, rope->axis, rd / 2);
+    return launch_append_rope(p, pool->dtype, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+pkv_status paged_copy_blocks(const pkv_pool *src, const pkv_pool *dst, int32_t n_pools,
+                             const int32_t *src_blocks, const int32_t *dst_blocks, int32_t n,
+                             int32_t *dev_status, pkv_stream_t stream)
+{
+    if (src == nullptr || n_pools < 0 || n < 0) return PKV_ERR_INVALID_ARG;
+    if (dst == nullptr) dst = src;
+    for (int32_t l = 0; l < n_pools; ++l) {
+        const pkv_pool &a = src[l], &b = dst[l], &f = src[0];
+        if (!valid_pool(&a) || !valid_pool(&b)) return PKV_ERR_INVALID_ARG;
+        for (const pkv_pool *x : {&a, &b})
+            if (x->dtype != f.dtype || x->block_size != f.block_size || x->num_kv_heads != f.num_kv_heads ||
+                x->head_dim != f.head_dim)
+                return PKV_ERR_INVALID_ARG;
+    }
+    if (n_pools == 0 || n == 0) return PKV_OK;
+    if (src_blocks == nullptr || dst_blocks == nullptr) return PKV_ERR_INVALID_ARG;
+    const int64_t row_bytes = static_cast<int64_t>(src[0].head_dim) * elem_bytes(src[0].dtype);
+    const int64_t page_bytes = row_bytes * src[0].block_size * src[0].num_kv_heads;
+    if (page_bytes % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    for (int32_t l0 = 0; l0 < n_pools; l0 += PKV_MAX_COPY_POOLS) {
+        const int32_t nl = std::min(n_pools - l0, PKV_MAX_COPY_POOLS);
+        CopyParams p{};
+        p.src_blocks = src_blocks;
+        p.dst_blocks = dst_blocks;
+        p.status = dev_status;
+        p.page_vecs = page_bytes / 16;
+        p.n = n;
+        p.n_tensors = 2 * nl;
+        for (int32_t l = 0; l < nl; ++l) {
+            p.src[2 * l] = src[l0 + l].k;
+            p.src[2 * l + 1] = src[l0 + l].v;
+            p.dst[2 * l] = dst[l0 + l].k;
+            p.dst[2 * l + 1] = dst[l0 + l].v;
+            p.src_num_blocks[l] = src[l0 + l].num_blocks;
+            p.dst_num_blocks[l] = dst[l0 + l].num_blocks;
+        }
+        if (launch_copy_blocks(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    return PKV_OK;
 }
 
 }  // extern "C"

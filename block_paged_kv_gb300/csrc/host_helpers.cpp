@@ -57,6 +57,37 @@ extern "C" pkv_status pkv_slot_mapping_check_host(const int32_t *slots, int32_t 
     return PKV_OK;
 }
 
+extern "C" pkv_status pkv_block_copies_check_host(const int32_t *src_blocks, const int32_t *dst_blocks,
+                                                  int32_t n, int32_t src_num_blocks,
+                                                  int32_t dst_num_blocks, int32_t same_pool,
+                                                  int32_t *first_bad)
+try {
+    if (first_bad != nullptr) *first_bad = -1;
+    if (n < 0 || src_num_blocks <= 0 || dst_num_blocks <= 0 ||
+        (n > 0 && (src_blocks == nullptr || dst_blocks == nullptr)))
+        return PKV_ERR_INVALID_ARG;
+    std::unordered_set<int32_t> read, written;
+    for (int32_t i = 0; i < n; ++i) {
+        const int32_t s = src_blocks[i], d = dst_blocks[i];
+        if (s < 0 || d < 0) continue;  // skipped by the copy
+        bool bad = s >= src_num_blocks || d >= dst_num_blocks;
+        if (!bad && same_pool && s == d) {
+            // the copy leaves it alone, but no other pair may write it
+            bad = written.count(d) != 0;
+        } else if (!bad) {
+            bad = !written.insert(d).second || (same_pool && (read.count(d) != 0 || written.count(s) != 0));
+        }
+        read.insert(s);
+        if (bad) {
+            if (first_bad != nullptr) *first_bad = i;
+            return PKV_ERR_INVALID_ARG;
+        }
+    }
+    return PKV_OK;
+} catch (...) {
+    return PKV_ERR_HOST_MEMORY;
+}
+
 extern "C" int32_t pkv_prefix_groups_host(const int32_t *block_tables, int32_t max_blocks_per_seq,
                                           const int32_t *seq_lens, int32_t batch, int32_t block_size,
                                           int32_t *group_of_row, int32_t *prefix_blocks)

@@ -41,6 +41,37 @@ struct AppendParams {
     int32_t heads_per_warp;  // FP8: kv heads one warp quantizes for a token (divides hkv)
 };
 
+// Rotary append: strides in 16-byte vectors between tokens; the descriptor's
+// tables travel in the launch parameters.
+constexpr int kRopeMaxPairs = PKV_ROPE_MAX_PAIRS;
+constexpr int kRopeMaxTokens = 8;  // tokens of a CTA
+struct RopeParams {
+    const void *q, *k_new, *v_new;
+    void *q_out, *k_pool, *v_pool;
+    const int32_t *slot_mapping;
+    const int32_t *positions;  // [axes][pos_stride]
+    int32_t *status;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, pos_stride;
+    int32_t num_tokens, hq, hkv, block_size, head_dim, num_slots;
+    int32_t rotary_dim, interleaved;
+    int32_t tokens_per_cta, rows_per_cta;  // set by the launch
+    float factor, k_scale, v_scale;
+    uint64_t freq[kRopeMaxPairs];
+    uint8_t axis[kRopeMaxPairs];
+};
+
+// Page copies of up to PKV_MAX_COPY_POOLS pools; tensor 2l is pool l's K, 2l + 1 its V.
+struct CopyParams {
+    const int32_t *src_blocks, *dst_blocks;
+    int32_t *status;
+    int64_t page_vecs;  // 16-byte vectors of one block (all kv heads) of one tensor
+    int32_t n, n_tensors;
+    const void *src[2 * PKV_MAX_COPY_POOLS];
+    void *dst[2 * PKV_MAX_COPY_POOLS];
+    int32_t src_num_blocks[PKV_MAX_COPY_POOLS];
+    int32_t dst_num_blocks[PKV_MAX_COPY_POOLS];
+};
+
 // Split plan of one decode call.  A row's key range [lo, L) covers the blocks
 // b_first .. b_end-1; split s of the row's suffix covers blocks
 // b_first + s*split_blocks .. (capped at b_end).  Rows of a shared-prefix
@@ -168,6 +199,8 @@ void drill_settings(uint64_t *wait_ns, uint32_t *flags);
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_append_fp8(const AppendParams &p, cudaStream_t stream);
+cudaError_t launch_append_rope(const RopeParams &p, pkv_dtype dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
 bool prefill_shape_built(pkv_dtype dtype, int32_t D, int32_t bs, int32_t G);
 int32_t prefill_queries_per_cta(pkv_dtype dtype, int32_t G);
 // Key-range split of the bf16 prefill for short chunks (all of a row's

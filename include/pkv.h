@@ -57,7 +57,8 @@ typedef enum {
     PKV_ERR_UNSUPPORTED = 2,
     PKV_ERR_CUDA = 3,
     PKV_ERR_WORKSPACE = 4,
-    PKV_ERR_OUT_OF_BLOCKS = 5 /* block allocator: the pool (at its maximum) cannot hold the request */
+    PKV_ERR_OUT_OF_BLOCKS = 5, /* block allocator: the pool (at its maximum) cannot hold the request */
+    PKV_ERR_HOST_MEMORY = 6    /* fork, truncate, compact, copy-list check: host memory ran out */
 } pkv_status;
 
 /*
@@ -132,6 +133,87 @@ typedef struct {
 pkv_status paged_kv_append(const pkv_pool *pool, const int32_t *slot_mapping, int32_t num_tokens,
                            const void *k_new, const void *v_new, int32_t *dev_status,
                            pkv_stream_t stream);
+
+/*
+ * Rotary positions with several axes (one for text; time, height and width for
+ * images and video).  Pair i of the rotary_dim / 2 pairs of a head turns by
+ * positions[axis[i]][t] * inv_freq[i] radians:
+ *   y1 = factor * (x1 cos - x2 sin),  y2 = factor * (x2 cos + x1 sin)
+ * with (x1, x2) the dims (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved; the dims from rotary_dim on are copied as they are.  The
+ * descriptor is host memory, filled by pkv_rope_init and passed by value into
+ * every launch: it needs no device memory and may be discarded after the call.
+ * freq holds the frequencies in turns per position, as fractions of 2^64 (whole
+ * turns dropped), so that the angle of any int32 position, negative ones
+ * included, keeps its full accuracy.
+ */
+#define PKV_ROPE_MAX_AXES 4
+#define PKV_ROPE_MAX_PAIRS 128
+
+typedef struct {
+    int32_t rotary_dim;   /* rotated dims, 2 .. 256, even */
+    int32_t num_axes;     /* rows of positions, 1 .. PKV_ROPE_MAX_AXES */
+    int32_t interleaved;  /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+    float factor;         /* multiplies the rotated dims (1 for none), finite */
+    uint64_t freq[PKV_ROPE_MAX_PAIRS];
+    uint8_t axis[PKV_ROPE_MAX_PAIRS];
+} pkv_rope;
+
+/* Fills a descriptor (host).  inv_freq: [rotary_dim / 2] radians per position
+ * (finite); axis_of_pair: [rotary_dim / 2], each 0 .. num_axes - 1, or NULL for
+ * axis 0 throughout. */
+pkv_status pkv_rope_init(pkv_rope *rope, int32_t rotary_dim, const double *inv_freq,
+                         int32_t num_axes, const int32_t *axis_of_pair, int32_t interleaved,
+                         float factor);
+
+/*
+ * Rotate and append in one launch: q_out gets the rotated q rows of every
+ * token, and each token with a slot >= 0 has its rotated k row and its v row
+ * written there as by paged_kv_append (bf16 and f32 pools: the fp32 result
+ * rounded once to the pool's type; FP8 pools: rotated k in fp32 stored as the
+ * E4M3 code nearest to the float32 quotient by k_scale).  A token whose slot is
+ * negative still gets its q rotated; one whose slot lies past the pool too
+ * (PKV_DEV_BAD_SLOT).
+ *   q:      device [num_tokens][num_q_heads][head_dim], tokens q_stride elements
+ *           apart (rows may be cut from a wider projection output); num_q_heads
+ *           0 rotates k alone (q, q_out NULL)
+ *   k_new, v_new: device [num_tokens][num_kv_heads][head_dim], strides likewise
+ *   q_out:  as q, with its own stride; may be q itself with the same stride
+ *   positions: device int32 [num_axes][num_tokens], axes pos_stride elements apart
+ * Types as for paged_kv_append (q and q_out: bf16 beside FP8 pools, else the
+ * pool's).  Pointers 16-byte aligned and strides a multiple of 16 bytes, at
+ * least a token's rows.  Built: rotary_dim a multiple of 16 (f32: 8) up to
+ * head_dim; rows a multiple of 16 bytes.
+ */
+pkv_status paged_kv_append_rope(const pkv_pool *pool, const int32_t *slot_mapping,
+                                int32_t num_tokens, const void *q, int64_t q_stride,
+                                int32_t num_q_heads, const void *k_new, int64_t k_stride,
+                                const void *v_new, int64_t v_stride, const int32_t *positions,
+                                int64_t pos_stride, const pkv_rope *rope, void *q_out,
+                                int64_t q_out_stride, int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * Copy pages: for every pair i and every pool l, all kv heads' K and V of block
+ * dst_blocks[i] of dst[l] become those of block src_blocks[i] of src[l], byte
+ * for byte.  Block ids are shared by a model's layers, so that one call (one
+ * launch per PKV_MAX_COPY_POOLS pools) serves a fork, a rollback or a
+ * compaction in all of them.
+ *   src, dst:  host arrays of n_pools pools; dst NULL copies within src.  All
+ *              share dtype, block_size, num_kv_heads and head_dim; dst[l] may
+ *              have another num_blocks (growing or moving a pool)
+ *   src_blocks, dst_blocks: device int32 [n]; a pair with a negative id is
+ *              skipped, one with an id past its pool too (PKV_DEV_BAD_BLOCK)
+ * Within one call no block may be written twice, nor be written and read (a
+ * pair with src == dst of one pool does nothing and is allowed): the copies of
+ * a call run in no order.  pkv_block_copies_check_host checks a host list.
+ * A page (num_kv_heads * block_size * head_dim elements) is a multiple of 16
+ * bytes, else PKV_ERR_UNSUPPORTED.
+ */
+#define PKV_MAX_COPY_POOLS 64
+
+pkv_status paged_copy_blocks(const pkv_pool *src, const pkv_pool *dst, int32_t n_pools,
+                             const int32_t *src_blocks, const int32_t *dst_blocks, int32_t n,
+                             int32_t *dev_status, pkv_stream_t stream);
 
 /*
  * Bytes of device workspace paged_decode_attention needs for these sizes on the
@@ -330,6 +412,19 @@ pkv_status pkv_slot_mapping_check_host(const int32_t *slots, int32_t n, int32_t 
                                        int32_t block_size, int32_t *first_bad);
 
 /*
+ * Host helper, a debug check of a page copy list: every id >= 0 lies inside its
+ * pool, no block is a destination twice, and no block is both a source and a
+ * destination (unless src == dst of the pair itself; same_pool 0: source and
+ * destination pools differ, so only repeated destinations count).  Pairs with a
+ * negative id are skipped.  Returns PKV_OK, or PKV_ERR_INVALID_ARG with
+ * *first_bad (may be NULL) the first pair at fault (-1 when the arguments
+ * themselves are invalid).  Host arrays; allocates host scratch.
+ */
+pkv_status pkv_block_copies_check_host(const int32_t *src_blocks, const int32_t *dst_blocks,
+                                       int32_t n, int32_t src_num_blocks, int32_t dst_num_blocks,
+                                       int32_t same_pool, int32_t *first_bad);
+
+/*
  * Host helper: shared-prefix groups read off the block tables (host arrays).
  * Rows whose first entry is the same physical block form a group when there
  * are at least two of them; the group's prefix is the longest run of leading
@@ -387,7 +482,8 @@ typedef enum {
     PKV_KERNEL_DECODE_SPLIT = 2,  /* per-row split-KV decode */
     PKV_KERNEL_DECODE_COMBINE = 3,
     PKV_KERNEL_PREFILL = 4,
-    PKV_KERNEL_KINDS = 5
+    PKV_KERNEL_COPY = 5,
+    PKV_KERNEL_KINDS = 6
 } pkv_kernel_kind;
 
 /* Bit k of kind_mask enables timing of kernel kind k: each such launch is
@@ -483,6 +579,43 @@ pkv_status pkv_allocator_publish(pkv_allocator *a, int32_t req, const int32_t *t
  * request's reference (as in release) and its table entry becomes -1, the
  * sentinel the decode never reads.  Table positions are kept (absolute). */
 pkv_status pkv_allocator_expire(pkv_allocator *a, int32_t req, int32_t first_live_token);
+
+/* Sliding window with sink tokens: as pkv_allocator_expire, but the blocks
+ * holding any of the first `sinks` tokens stay. */
+pkv_status pkv_allocator_expire_window(pkv_allocator *a, int32_t req, int32_t first_live_token,
+                                       int32_t sinks);
+
+/* Fork: a new request whose first n_tokens tokens are req's (n_tokens <= req's
+ * table's capacity).  It shares req's full blocks (refcount + 1; expired
+ * entries stay -1); a block it holds only a part of cannot be shared, as both
+ * would go on writing into it, so it gets one of its own: *src, *dst name the
+ * page copy the caller makes (paged_copy_blocks) before either writes there,
+ * -1, -1 when n_tokens ends on a block boundary or that entry has expired.
+ * PKV_ERR_OUT_OF_BLOCKS changes nothing. */
+pkv_status pkv_allocator_fork(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *new_req,
+                              int32_t *src, int32_t *dst);
+
+/* Roll a request back to its first n_tokens tokens (rejected speculation, an
+ * edited prompt): the blocks past them lose its reference, as in release.  A
+ * last block that becomes partial and that another request holds or the prefix
+ * table names is replaced by one of its own, and *src, *dst name the page copy
+ * (else -1, -1): the next tokens would overwrite shared ones.
+ * PKV_ERR_OUT_OF_BLOCKS changes nothing. */
+pkv_status pkv_allocator_truncate(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *src,
+                                  int32_t *dst);
+
+/* Compaction: the pool becomes num_blocks blocks (at most the present count).
+ * Every block held by a request or cached moves below that: the lowest free ids
+ * take, in ascending order, the blocks at or past num_blocks, in ascending
+ * order.  Cache-only blocks are evicted, least recently released first, while
+ * in-use and cached blocks outnumber num_blocks.  Tables, refcounts, prefix
+ * table and eviction order follow the moves; *n_moves pairs go to src and dst
+ * (host, capacity cap), for paged_copy_blocks: no id is both a source and a
+ * destination.  Nothing changes on PKV_ERR_OUT_OF_BLOCKS (more blocks in use than
+ * num_blocks) and on PKV_ERR_INVALID_ARG (cap below the moves there are, which
+ * *n_moves then says).  The pool may grow again later. */
+pkv_status pkv_allocator_compact(pkv_allocator *a, int32_t num_blocks, int32_t *src, int32_t *dst,
+                                 int32_t cap, int32_t *n_moves);
 
 /* release_request: every block of the table loses a reference; a published
  * block at refcount 0 becomes cache-only (LRU tail), an unpublished one free.
