@@ -154,6 +154,91 @@ class AllocatorModel:
                 self._drop(t[i])
                 t[i] = -1
 
+    def expire_window(self, r: int, first_live_token: int, sinks: int) -> None:
+        """As expire, but blocks holding any of the first ``sinks`` tokens stay."""
+        t = self.tables[r]
+        for i in range(min(first_live_token // self.bs, len(t))):
+            if t[i] >= 0 and i * self.bs >= sinks:
+                self._drop(t[i])
+                t[i] = -1
+
+    # -- fork, rollback, compaction ------------------------------------------
+    def _own_block(self) -> int:
+        """One more block, by the reservation's rule (through a request of its own)."""
+        n, keep = self.next_req, (dict(self.tables), dict(self.chains), dict(self.done), dict(self.fresh))
+        r = self.begin()
+        try:
+            self.reserve(r, 1)
+            return self.tables[r][0]
+        finally:
+            self.next_req = n
+            self.tables, self.chains, self.done, self.fresh = keep
+
+    def fork(self, r: int, n_tokens: int):
+        """A request sharing r's first n_tokens tokens: (id, page copy or None)."""
+        assert 0 <= n_tokens <= len(self.tables[r]) * self.bs
+        full, copy, table = n_tokens // self.bs, None, []
+        if n_tokens % self.bs:
+            b = self.tables[r][full]
+            if b >= 0:
+                copy = (b, self._own_block())
+            table = [copy[1] if copy else -1]
+        c = self.begin()
+        self.fresh[c] = False
+        for b in self.tables[r][:full]:
+            if b >= 0:
+                self.refcount[b] += 1
+        self.tables[c] = self.tables[r][:full] + table
+        self.chains[c] = self.chains[r][:full]
+        self.done[c] = min(self.done[r], full)
+        return c, copy
+
+    def truncate(self, r: int, n_tokens: int):
+        """Roll r back to its first n_tokens tokens; the page copy, or None."""
+        t = self.tables[r]
+        assert 0 <= n_tokens <= len(t) * self.bs
+        full, copy = n_tokens // self.bs, None
+        keep = -(-n_tokens // self.bs)
+        if keep > full and t[full] >= 0:
+            b = t[full]
+            if self.refcount[b] > 1 or b in self.hash_of_block:
+                copy = (b, self._own_block())
+                self._drop(b)
+                t[full] = copy[1]
+        for b in t[keep:]:
+            if b >= 0:
+                self._drop(b)
+        del t[keep:]
+        del self.chains[r][full:]
+        self.done[r] = min(self.done[r], full)
+        self.fresh[r] = False
+        return copy
+
+    def compact(self, num_blocks: int):
+        """Shrink to num_blocks blocks: the moves [(src, dst)]."""
+        assert 0 <= num_blocks <= self.num_blocks
+        evict = max(0, self.num_blocks - len(self.free) - num_blocks)
+        if evict > len(self.lru):
+            raise OutOfBlocks()
+        for b in self.lru[:evict]:
+            del self.block_of_hash[self.hash_of_block.pop(b)]
+        self.free = sorted(self.free + self.lru[:evict])
+        self.lru = self.lru[evict:]
+        high = [b for b in range(num_blocks, self.num_blocks) if b not in self.free]
+        moves = list(zip(high, self.free))
+        to = dict(moves)
+        for b, d in moves:
+            self.refcount[d] = self.refcount[b]
+            if b in self.hash_of_block:
+                h = self.hash_of_block.pop(b)
+                self.hash_of_block[d], self.block_of_hash[h] = h, d
+        self.lru = [to.get(b, b) for b in self.lru]
+        self.tables = {r: [to.get(b, b) for b in t] for r, t in self.tables.items()}
+        self.free = [b for b in self.free[len(moves):] if b < num_blocks]
+        del self.refcount[num_blocks:]
+        self.num_blocks = num_blocks
+        return moves
+
     def release(self, r: int) -> None:
         for b in self.tables.pop(r):
             if b >= 0:
