@@ -143,9 +143,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //     the items' tiles in item order form one sequence of W tiles
 //     (sk_prefix, written by prefill_sk_plan_kernel).  CTA c first runs item
 //     c whole (the CTAs of one (row, kv head) then start together and share
-//     its K/V through L2), then takes the tiles [B + c R / n, B + (c + 1) R
-//     / n) of the rest (B = the first n items' tiles, R = W - B), item by
-//     item.  Only the first and the last segment of that run can cut an
+//     its K/V through L2), then takes the tiles [B + c R / m, B + (c + 1) R
+//     / m) of the rest (B = the first n items' tiles, R = W - B, m = min(n, R):
+//     the CTAs from m on take none, so that no CTA between two pieces of an
+//     item is without one), item by item.  Only the first and the last segment of that run can cut an
 //     item; a cut segment writes a partial to slot 0 (first) or 1 (last) of
 //     the CTA, and the warp that completes an item's pieces merges them.
 // ---------------------------------------------------------------------------
@@ -167,8 +168,9 @@ struct SegWalk {
 // start of CTA c's balanced run (c = n: the end of the sequence)
 __device__ __forceinline__ int32_t sk_run_start(const PrefillParams &p, int32_t c)
 {
-    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), W = __ldg(p.sk_prefix + p.sk_items);
-    return static_cast<int32_t>(B + static_cast<int64_t>(c) * (W - B) / p.sk_ctas);
+    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), R = __ldg(p.sk_prefix + p.sk_items) - B;
+    const int32_t m = static_cast<int32_t>(min(static_cast<int64_t>(p.sk_ctas), R));
+    return static_cast<int32_t>(m > 0 ? B + min(c, m) * R / m : B);
 }
 
 // the item holding tile pos: the largest u with prefix[u] <= pos
@@ -185,10 +187,11 @@ __device__ __forceinline__ int32_t sk_item_of(const PrefillParams &p, int32_t po
 // the CTA whose balanced run holds tile pos (pos past the first n items)
 __device__ __forceinline__ int32_t sk_cta_of(const PrefillParams &p, int32_t pos)
 {
-    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), W = __ldg(p.sk_prefix + p.sk_items);
-    int32_t c = W > B ? static_cast<int32_t>((pos - B) * static_cast<int64_t>(p.sk_ctas) / (W - B)) : 0;
-    c = min(max(c, 0), p.sk_ctas - 1);
-    while (c + 1 < p.sk_ctas && sk_run_start(p, c + 1) <= pos) ++c;
+    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), R = __ldg(p.sk_prefix + p.sk_items) - B;
+    const int32_t m = static_cast<int32_t>(max(min(static_cast<int64_t>(p.sk_ctas), R), static_cast<int64_t>(1)));
+    int32_t c = R > 0 ? static_cast<int32_t>((pos - B) * m / R) : 0;
+    c = min(max(c, 0), m - 1);
+    while (c + 1 < m && sk_run_start(p, c + 1) <= pos) ++c;
     while (c > 0 && sk_run_start(p, c) > pos) --c;
     return c;
 }
