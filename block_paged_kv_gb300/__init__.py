@@ -128,6 +128,20 @@ _lib.paged_copy_blocks.restype = ctypes.c_int
 _i32p = ctypes.POINTER(ctypes.c_int32)
 _lib.pkv_slot_mapping_check_host.argtypes = [_vp, _i32, _i32, _i32, _i32p]
 _lib.pkv_slot_mapping_check_host.restype = ctypes.c_int
+_lib.paged_decode_sinks_workspace_size.argtypes = [_i32] * 8
+_lib.paged_decode_sinks_workspace_size.restype = _sz
+_lib.paged_decode_attention_sinks.argtypes = [_vp, _i32, _PP, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                              ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
+_lib.paged_decode_attention_sinks.restype = ctypes.c_int
+_lib.paged_decode_groups_sinks_workspace_size.argtypes = [_GP, _vp, _i32, _i32, _i32]
+_lib.paged_decode_groups_sinks_workspace_size.restype = _sz
+_lib.paged_decode_attention_groups_sinks.argtypes = [_GP, _vp, _i32, _i32, _i32, _vp, _sz, _vp, _vp]
+_lib.paged_decode_attention_groups_sinks.restype = ctypes.c_int
+_lib.paged_prefill_sinks_workspace_size.argtypes = [_i32] * 9
+_lib.paged_prefill_sinks_workspace_size.restype = _sz
+_lib.paged_prefill_chunk_attention_sinks.argtypes = [_vp, _vp, _i32, _PP, _vp, _i32, _vp, _i32, _i32, _i32,
+                                                     _i32, _i32, ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
+_lib.paged_prefill_chunk_attention_sinks.restype = ctypes.c_int
 _lib.pkv_block_copies_check_host.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _i32p]
 _lib.pkv_block_copies_check_host.restype = ctypes.c_int
 _lib.pkv_allocator_expire_window.argtypes = [_vp, _i32, _i32, _i32]
@@ -175,6 +189,9 @@ EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_atte
             "pkv_allocator_release",
             "pkv_allocator_table", "pkv_allocator_refcount", "pkv_allocator_stats",
             "pkv_rope_init", "paged_kv_append_rope", "paged_copy_blocks", "pkv_block_copies_check_host",
+            "paged_decode_sinks_workspace_size", "paged_decode_attention_sinks",
+            "paged_decode_groups_sinks_workspace_size", "paged_decode_attention_groups_sinks",
+            "paged_prefill_sinks_workspace_size", "paged_prefill_chunk_attention_sinks",
             "pkv_allocator_expire_window", "pkv_allocator_fork", "pkv_allocator_truncate",
             "pkv_allocator_compact"]
 
@@ -541,7 +558,10 @@ def check_block_copies(src_blocks, dst_blocks, num_blocks: int,
 
 def decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                           block_size: int, max_seq_len: int, window: int = 0,
-                          prefix: Optional[PrefixDesc] = None) -> int:
+                          prefix: Optional[PrefixDesc] = None, sinks: int = 0) -> int:
+    if sinks and prefix is None:
+        return int(_lib.paged_decode_sinks_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                          block_size, max_seq_len, window, sinks))
     px = ctypes.byref(prefix._c()) if prefix is not None else None
     return int(_lib.paged_decode_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
                                                 block_size, max_seq_len, window, px))
@@ -560,12 +580,14 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
                            prefix: Optional[PrefixDesc] = None,
                            status: Optional[torch.Tensor] = None,
                            k_scale: Optional[float] = None,
-                           v_scale: Optional[float] = None) -> torch.Tensor:
+                           v_scale: Optional[float] = None, sinks: int = 0) -> torch.Tensor:
     """Batched paged decode attention; returns ``out`` [B, Hq, D].
 
     ``max_seq_len`` is a host bound on ``seq_lens`` (default: the block-table
     capacity); ``workspace`` defaults to a fresh buffer of the queried size.
     FP8 pools (uint8) take bf16 queries and their ``k_scale``/``v_scale``.
+    With a ``window``, the first ``sinks`` positions of a row stay visible
+    (not together with ``prefix``).
     """
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
     dev = k_pool.device
@@ -587,10 +609,21 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     _status_ok(status, dev)
     _prefix_ok(prefix, dev)
     with _on(dev):  # the plan reads the SM count of the current device
-        need = decode_workspace_size(B, hq, pool.num_kv_heads, D, pool.block_size, max_seq_len,
-                                     window, prefix)
         if workspace is None:
-            workspace = alloc_workspace(need, dev)
+            workspace = alloc_workspace(
+                decode_workspace_size(B, hq, pool.num_kv_heads, D, pool.block_size, max_seq_len, window,
+                                      prefix, sinks), dev)
+        if sinks:
+            if prefix is not None and (window or sinks < 0):
+                raise PkvError("paged_decode_attention (sinks with a shared prefix)",
+                               PKV_ERR_UNSUPPORTED if sinks > 0 else PKV_ERR_INVALID_ARG)
+            if prefix is None:
+                _check("paged_decode_attention_sinks", _lib.paged_decode_attention_sinks(
+                    q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width,
+                    seq_lens.data_ptr(), B, max_seq_len, window, sinks, scale, out.data_ptr(),
+                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status),
+                    _stream(dev)))
+                return out
         px = ctypes.byref(prefix._c()) if prefix is not None else None
         _check("paged_decode_attention", _lib.paged_decode_attention(
             q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width,
@@ -602,7 +635,11 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
 
 def prefill_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                            block_size: int, max_q_len: int, max_seq_len: int,
-                           window: int = 0) -> int:
+                           window: int = 0, sinks: int = 0) -> int:
+    if sinks:
+        return int(_lib.paged_prefill_sinks_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                           block_size, max_q_len, max_seq_len, window,
+                                                           sinks))
     return int(_lib.paged_prefill_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
                                                  block_size, max_q_len, max_seq_len, window))
 
@@ -615,8 +652,9 @@ def paged_prefill_chunk_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, k_po
                                   max_seq_len: Optional[int] = None,
                                   status: Optional[torch.Tensor] = None,
                                   k_scale: Optional[float] = None,
-                                  v_scale: Optional[float] = None) -> torch.Tensor:
-    """Chunked prefill against the paged prefix; returns ``out`` [sum C, Hq, D]."""
+                                  v_scale: Optional[float] = None, sinks: int = 0) -> torch.Tensor:
+    """Chunked prefill against the paged prefix; returns ``out`` [sum C, Hq, D].
+    With a ``window``, the first ``sinks`` positions of a row stay visible."""
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
     dev = k_pool.device
     _require(q.dim() == 3 and q.shape[2] == pool.head_dim and q.dtype == _act_dtype(k_pool.dtype) and
@@ -638,10 +676,17 @@ def paged_prefill_chunk_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, k_po
     _status_ok(status, dev)
     hq = q.shape[1]
     with _on(dev):  # the plan reads the SM count of the current device
-        need = prefill_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, pool.block_size,
-                                      max_q_len, max_seq_len, window)
         if workspace is None:
-            workspace = alloc_workspace(need, dev)
+            workspace = alloc_workspace(
+                prefill_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, pool.block_size,
+                                       max_q_len, max_seq_len, window, sinks), dev)
+        if sinks:
+            _check("paged_prefill_chunk_attention_sinks", _lib.paged_prefill_chunk_attention_sinks(
+                q.data_ptr(), cu_q_lens.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(),
+                width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, sinks, scale,
+                out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                _ptr(status), _stream(dev)))
+            return out
         _check("paged_prefill_chunk_attention", _lib.paged_prefill_chunk_attention(
             q.data_ptr(), cu_q_lens.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(),
             width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, float(scale),
@@ -732,6 +777,11 @@ class DecodeGroup:
     max_seq_len: Optional[int] = None
     k_scale: Optional[float] = None
     v_scale: Optional[float] = None
+    sinks: int = 0
+
+
+def _sinks_c(groups):
+    return (ctypes.c_int32 * len(groups))(*[int(g.sinks) for g in groups])
 
 
 def _group_c(g: DecodeGroup) -> _Group:
@@ -772,11 +822,12 @@ def paged_decode_attention_groups(groups, workspace: Optional[torch.Tensor] = No
     _on_device(workspace, "workspace", dev)
     _status_ok(status, dev)
     with _on(dev):  # the plan reads the SM count of the current device
-        need = int(_lib.paged_decode_groups_workspace_size(arr, len(groups), B, hq))
+        sinks = _sinks_c(groups)
         if workspace is None:
-            workspace = alloc_workspace(need, dev)
-        _check("paged_decode_attention_groups", _lib.paged_decode_attention_groups(
-            arr, len(groups), B, hq, workspace.data_ptr(),
+            workspace = alloc_workspace(
+                int(_lib.paged_decode_groups_sinks_workspace_size(arr, sinks, len(groups), B, hq)), dev)
+        _check("paged_decode_attention_groups", _lib.paged_decode_attention_groups_sinks(
+            arr, sinks, len(groups), B, hq, workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _ptr(status), _stream(dev)))
     return [g.out for g in groups]
 
@@ -784,8 +835,8 @@ def paged_decode_attention_groups(groups, workspace: Optional[torch.Tensor] = No
 def decode_groups_workspace_size(groups) -> int:
     groups = list(groups)
     arr = (_Group * len(groups))(*[_group_c(g) for g in groups])
-    return int(_lib.paged_decode_groups_workspace_size(arr, len(groups), groups[0].q.shape[0],
-                                                       groups[0].q.shape[1]))
+    return int(_lib.paged_decode_groups_sinks_workspace_size(arr, _sinks_c(groups), len(groups),
+                                                             groups[0].q.shape[0], groups[0].q.shape[1]))
 
 
 def paged_decode_attention_no_alloc(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,

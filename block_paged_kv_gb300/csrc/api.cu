@@ -108,12 +108,12 @@ bool decode_shape_built(pkv_dtype dtype, int32_t D, int32_t bs, int32_t G)
 // The split plan: a pure function of the sizes and the SM count.
 DecodePlan make_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
                      int32_t max_len, int32_t window, const pkv_prefix_desc *prefix,
-                     pkv_dtype dtype, int num_sms)
+                     pkv_dtype dtype, int num_sms, int32_t sinks = 0)
 {
     DecodePlan pl{};
     const int32_t G = hq / hkv;
     int64_t nblk_max = ceil_div64(max_len, bs);
-    if (window > 0) nblk_max = std::min<int64_t>(nblk_max, ceil_div64(window, bs) + 1);
+    if (window > 0) nblk_max = std::min<int64_t>(nblk_max, ceil_div64(window, bs) + 1 + ceil_div64(sinks, bs));
     nblk_max = std::max<int64_t>(nblk_max, 1);
     const int64_t tiles_ub = static_cast<int64_t>(batch) * nblk_max * hkv;
     // Split size over the upper bound of (block, kv head) tiles, a multiple of
@@ -255,11 +255,13 @@ pkv_status decode_setup(const void *q, int32_t num_q_heads, const pkv_pool *pool
                         const int32_t *block_tables, int32_t max_blocks_per_seq,
                         const int32_t *seq_lens, int32_t batch, int32_t max_seq_len,
                         int32_t window, float scale, void *out, void *workspace, size_t ws_bytes,
-                        const pkv_prefix_desc *prefix, int32_t *dev_status, DecodeParams *pp)
+                        const pkv_prefix_desc *prefix, int32_t *dev_status, DecodeParams *pp,
+                        int32_t sinks = 0)
 {
     if (!valid_pool(pool) || batch < 0 || num_q_heads <= 0 || max_seq_len < 0 || window < 0 ||
-        !std::isfinite(scale))
+        sinks < 0 || !std::isfinite(scale))
         return PKV_ERR_INVALID_ARG;
+    if (window == 0) sinks = 0;  // full attention sees every position
     if (num_q_heads % pool->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     if (batch == 0) return PKV_OK;
     if (q == nullptr || out == nullptr || block_tables == nullptr || seq_lens == nullptr ||
@@ -276,7 +278,7 @@ pkv_status decode_setup(const void *q, int32_t num_q_heads, const pkv_pool *pool
 
     const DecodePlan pl = make_plan(batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
                                     pool->block_size, max_len, window,
-                                    use_prefix ? prefix : nullptr, pool->dtype, num_sms_current());
+                                    use_prefix ? prefix : nullptr, pool->dtype, num_sms_current(), sinks);
     if (pl.n_suffix_ctas > INT32_MAX || pl.n_prefix_ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     const size_t need = ws_total_bytes(batch, num_q_heads, pool->head_dim, pl);
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
@@ -310,6 +312,7 @@ pkv_status decode_setup(const void *q, int32_t num_q_heads, const pkv_pool *pool
     p.num_blocks = pool->num_blocks;
     p.max_len = max_len;
     p.window = window;
+    p.sinks = sinks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.v_scale = 1.f;
     if (pool->dtype == PKV_FP8_E4M3) {
@@ -319,6 +322,41 @@ pkv_status decode_setup(const void *q, int32_t num_q_heads, const pkv_pool *pool
     drill_settings(&p.wait_ns, &p.drill);
     p.plan = pl;
     return PKV_OK;
+}
+
+// One validated decode call's launches: the split kernel of its pool type, then the merge.
+pkv_status decode_launch(const DecodeParams &p, const pkv_pool *pool, pkv_stream_t stream)
+{
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (pool->dtype == PKV_FP8_E4M3) {
+        err = launch_decode_fp8(p, st);
+    } else if (pool->dtype == PKV_BF16) {
+        if (!encode_fn_ready()) return PKV_ERR_CUDA;
+        CUtensorMap kmap, vmap;
+        if (!encode_pool_map_tile(&kmap, pool->k, *pool) ||
+            !encode_pool_map_tile(&vmap, pool->v, *pool))
+            return PKV_ERR_UNSUPPORTED;
+        err = launch_decode_bf16(p, kmap, vmap, st);
+    } else {
+        err = launch_decode_f32(p, st);
+    }
+    if (err != cudaSuccess) return PKV_ERR_CUDA;
+    err = launch_decode_combine(p, out_dtype(pool->dtype), st);
+    return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status decode_call(const void *q, int32_t num_q_heads, const pkv_pool *pool,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                       int32_t batch, int32_t max_seq_len, int32_t window, int32_t sinks, float scale,
+                       void *out, void *workspace, size_t ws_bytes, const pkv_prefix_desc *prefix,
+                       int32_t *dev_status, pkv_stream_t stream)
+{
+    DecodeParams p{};
+    const pkv_status stt = decode_setup(q, num_q_heads, pool, block_tables, max_blocks_per_seq,
+                                        seq_lens, batch, max_seq_len, window, scale, out,
+                                        workspace, ws_bytes, prefix, dev_status, &p, sinks);
+    return stt != PKV_OK || batch == 0 ? stt : decode_launch(p, pool, stream);
 }
 
 // Groups of one fused call must share what fixes the kernel instantiation.
@@ -554,95 +592,133 @@ pkv_status paged_decode_attention(const void *q, int32_t num_q_heads, const pkv_
                                   size_t ws_bytes, const pkv_prefix_desc *prefix,
                                   int32_t *dev_status, pkv_stream_t stream)
 {
-    DecodeParams p{};
-    const pkv_status stt = decode_setup(q, num_q_heads, pool, block_tables, max_blocks_per_seq,
-                                        seq_lens, batch, max_seq_len, window, scale, out,
-                                        workspace, ws_bytes, prefix, dev_status, &p);
-    if (stt != PKV_OK || batch == 0) return stt;
-
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t err;
-    if (pool->dtype == PKV_FP8_E4M3) {
-        err = launch_decode_fp8(p, st);
-    } else if (pool->dtype == PKV_BF16) {
-        if (!encode_fn_ready()) return PKV_ERR_CUDA;
-        CUtensorMap kmap, vmap;
-        if (!encode_pool_map_tile(&kmap, pool->k, *pool) ||
-            !encode_pool_map_tile(&vmap, pool->v, *pool))
-            return PKV_ERR_UNSUPPORTED;
-        err = launch_decode_bf16(p, kmap, vmap, st);
-    } else {
-        err = launch_decode_f32(p, st);
-    }
-    if (err != cudaSuccess) return PKV_ERR_CUDA;
-    err = launch_decode_combine(p, out_dtype(pool->dtype), st);
-    return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return decode_call(q, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch,
+                       max_seq_len, window, 0, scale, out, workspace, ws_bytes, prefix, dev_status,
+                       stream);
 }
 
-size_t paged_decode_groups_workspace_size(const pkv_decode_group *groups, int32_t n_groups,
-                                          int32_t batch, int32_t num_q_heads)
+size_t paged_decode_sinks_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int32_t max_seq_len,
+                                         int32_t window, int32_t sinks)
+{
+    if (batch < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        head_dim <= 0 || block_size <= 0 || max_seq_len < 0 || window < 0 || sinks < 0)
+        return 0;
+    const DecodePlan pl = make_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                    max_seq_len, window, nullptr, PKV_BF16, num_sms_current(),
+                                    window > 0 ? sinks : 0);
+    return ws_total_bytes(batch, num_q_heads, head_dim, pl);
+}
+
+pkv_status paged_decode_attention_sinks(const void *q, int32_t num_q_heads, const pkv_pool *pool,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, int32_t batch, int32_t max_seq_len,
+                                        int32_t window, int32_t sinks, float scale, void *out,
+                                        void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                        pkv_stream_t stream)
+{
+    return decode_call(q, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch,
+                       max_seq_len, window, sinks, scale, out, workspace, ws_bytes, nullptr,
+                       dev_status, stream);
+}
+
+size_t paged_decode_groups_sinks_workspace_size(const pkv_decode_group *groups, const int32_t *sinks,
+                                                int32_t n_groups, int32_t batch, int32_t num_q_heads)
 {
     if (groups == nullptr || n_groups < 1 || n_groups > PKV_MAX_DECODE_GROUPS || batch < 0)
         return 0;
     size_t total = 0;
     for (int32_t i = 0; i < n_groups; ++i) {
         const pkv_decode_group &g = groups[i];
-        const size_t one = paged_decode_workspace_size(
+        const size_t one = paged_decode_sinks_workspace_size(
             batch, num_q_heads, g.pool.num_kv_heads, g.pool.head_dim, g.pool.block_size,
-            g.max_seq_len, g.window, nullptr);
+            g.max_seq_len, g.window, sinks != nullptr ? sinks[i] : 0);
         if (one == 0) return 0;
         total += (one + 255) & ~static_cast<size_t>(255);
     }
     return total;
 }
 
-pkv_status paged_decode_attention_groups(const pkv_decode_group *groups, int32_t n_groups,
-                                         int32_t batch, int32_t num_q_heads, void *workspace,
-                                         size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
+size_t paged_decode_groups_workspace_size(const pkv_decode_group *groups, int32_t n_groups,
+                                          int32_t batch, int32_t num_q_heads)
+{
+    return paged_decode_groups_sinks_workspace_size(groups, nullptr, n_groups, batch, num_q_heads);
+}
+
+pkv_status paged_decode_attention_groups_sinks(const pkv_decode_group *groups, const int32_t *sinks,
+                                               int32_t n_groups, int32_t batch, int32_t num_q_heads,
+                                               void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                               pkv_stream_t stream)
 {
     if (groups == nullptr || n_groups < 1 || n_groups > PKV_MAX_DECODE_GROUPS || batch < 0 ||
         num_q_heads <= 0)
         return PKV_ERR_INVALID_ARG;
     for (int32_t i = 0; i < n_groups; ++i)
-        if (!valid_pool(&groups[i].pool)) return PKV_ERR_INVALID_ARG;
+        if (!valid_pool(&groups[i].pool) || (sinks != nullptr && sinks[i] < 0)) return PKV_ERR_INVALID_ARG;
     if (!groups_compatible(groups, n_groups)) return PKV_ERR_INVALID_ARG;
     const pkv_dtype dt = groups[0].pool.dtype;
     if (dt == PKV_F32) return PKV_ERR_UNSUPPORTED;  // the CUDA-core f32 kernel runs per call
     if (batch == 0) return PKV_OK;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-        ws_bytes < paged_decode_groups_workspace_size(groups, n_groups, batch, num_q_heads))
+        ws_bytes < paged_decode_groups_sinks_workspace_size(groups, sinks, n_groups, batch, num_q_heads))
         return PKV_ERR_WORKSPACE;
     if (dt == PKV_BF16 && !encode_fn_ready()) return PKV_ERR_CUDA;
 
+    // groups without sinks share the launches; one with sinks gets its own call's
     GroupedDecode gd{};
-    gd.n = n_groups;
+    DecodeParams own[PKV_MAX_DECODE_GROUPS];
+    const pkv_pool *own_pool[PKV_MAX_DECODE_GROUPS];
+    int32_t n_own = 0;
     char *ws = static_cast<char *>(workspace);
     size_t left = ws_bytes;
     int64_t ctas = 0;
     for (int32_t i = 0; i < n_groups; ++i) {
         const pkv_decode_group &g = groups[i];
+        DecodeParams p{};
         const pkv_status stt = decode_setup(g.q, num_q_heads, &g.pool, g.block_tables,
                                             g.max_blocks_per_seq, g.seq_lens, batch, g.max_seq_len,
                                             g.window, g.scale, g.out, ws, left, nullptr,
-                                            dev_status, &gd.g[i]);
+                                            dev_status, &p, sinks != nullptr ? sinks[i] : 0);
         if (stt != PKV_OK) return stt;
-        const size_t used = (ws_total_bytes(batch, num_q_heads, g.pool.head_dim, gd.g[i].plan) + 255) &
+        const size_t used = (ws_total_bytes(batch, num_q_heads, g.pool.head_dim, p.plan) + 255) &
                             ~static_cast<size_t>(255);
         ws += used;
         left -= used;
-        ctas += gd.g[i].plan.n_prefix_ctas + gd.g[i].plan.n_suffix_ctas;
-        gd.cta_end[i] = ctas;
-        if (dt == PKV_BF16 && (!encode_pool_map_tile(&gd.kmap[i], g.pool.k, g.pool) ||
-                               !encode_pool_map_tile(&gd.vmap[i], g.pool.v, g.pool)))
+        if (p.sinks > 0) {
+            own[n_own] = p;
+            own_pool[n_own++] = &g.pool;
+            continue;
+        }
+        const int32_t j = gd.n++;
+        gd.g[j] = p;
+        ctas += p.plan.n_prefix_ctas + p.plan.n_suffix_ctas;
+        gd.cta_end[j] = ctas;
+        if (dt == PKV_BF16 && (!encode_pool_map_tile(&gd.kmap[j], g.pool.k, g.pool) ||
+                               !encode_pool_map_tile(&gd.vmap[j], g.pool.v, g.pool)))
             return PKV_ERR_UNSUPPORTED;
     }
     if (ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t err = dt == PKV_FP8_E4M3 ? launch_decode_fp8_grouped(gd, st)
-                                         : launch_decode_bf16_grouped(gd, st);
-    if (err != cudaSuccess) return PKV_ERR_CUDA;
-    err = launch_decode_combine_grouped(gd, out_dtype(dt), st);
-    return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    if (gd.n > 0) {
+        cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+        cudaError_t err = dt == PKV_FP8_E4M3 ? launch_decode_fp8_grouped(gd, st)
+                                             : launch_decode_bf16_grouped(gd, st);
+        if (err != cudaSuccess) return PKV_ERR_CUDA;
+        err = launch_decode_combine_grouped(gd, out_dtype(dt), st);
+        if (err != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    for (int32_t i = 0; i < n_own; ++i) {
+        const pkv_status stt = decode_launch(own[i], own_pool[i], stream);
+        if (stt != PKV_OK) return stt;
+    }
+    return PKV_OK;
+}
+
+pkv_status paged_decode_attention_groups(const pkv_decode_group *groups, int32_t n_groups,
+                                         int32_t batch, int32_t num_q_heads, void *workspace,
+                                         size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
+{
+    return paged_decode_attention_groups_sinks(groups, nullptr, n_groups, batch, num_q_heads, workspace,
+                                               ws_bytes, dev_status, stream);
 }
 
 }  // extern "C"
@@ -669,10 +745,36 @@ int32_t prefill_items(int32_t batch, int32_t hq, int32_t hkv, int32_t max_q_len)
 // The decode plan for a verify step: the key range of a row spans its
 // queries' windows.
 DecodePlan verify_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
-                       int32_t max_len, int32_t window, int32_t max_q_len)
+                       int32_t max_len, int32_t window, int32_t max_q_len, int32_t sinks)
 {
-    return make_plan(batch, hq, hkv, D, bs, max_len, window > 0 ? window + max_q_len - 1 : 0,
-                     nullptr, PKV_BF16, num_sms_current());
+    const int32_t span = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(window) + max_q_len - 1, INT32_MAX));
+    return make_plan(batch, hq, hkv, D, bs, max_len, window > 0 ? span : 0, nullptr, PKV_BF16,
+                     num_sms_current(), sinks);
+}
+
+// Bytes of one prefill call's workspace (sinks count with a window only).
+size_t prefill_ws(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                  int32_t block_size, int32_t max_q_len, int32_t max_seq_len, int32_t window, int32_t sinks)
+{
+    if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        max_q_len <= 0 || max_seq_len < 0 || window < 0 || sinks < 0)
+        return 0;
+    if (window == 0) sinks = 0;
+    // scratch only for short bf16 chunks: the decode kernel's split partials
+    // (a few queries per row), or the prefill kernel's key-range runs
+    const int32_t G = num_q_heads / num_kv_heads;
+    if (verify_on_decode(G, head_dim, block_size, max_q_len)) {
+        const DecodePlan pl = verify_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                          max_seq_len, window, max_q_len, sinks);
+        return ws_total_bytes(batch * max_q_len, num_q_heads, head_dim, pl);
+    }
+    const int sms = num_sms_current();
+    const PrefillSplit sp = prefill_split_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                               max_q_len, max_seq_len, window, sinks, sms);
+    const int32_t sk = prefill_sk_ctas(PKV_BF16, batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                       max_q_len, sms);
+    return std::max(prefill_split_ws_bytes(batch, num_q_heads, max_q_len, sp),
+                    prefill_sk_ws_bytes(prefill_items(batch, num_q_heads, num_kv_heads, max_q_len), sk));
 }
 
 }  // namespace
@@ -683,37 +785,32 @@ size_t paged_prefill_workspace_size(int32_t batch, int32_t num_q_heads, int32_t 
                                     int32_t head_dim, int32_t block_size, int32_t max_q_len,
                                     int32_t max_seq_len, int32_t window)
 {
-    if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
-        max_q_len <= 0 || max_seq_len < 0 || window < 0)
-        return 0;
-    // scratch only for short bf16 chunks: the decode kernel's split partials
-    // (a few queries per row), or the prefill kernel's key-range runs
-    const int32_t G = num_q_heads / num_kv_heads;
-    if (verify_on_decode(G, head_dim, block_size, max_q_len)) {
-        const DecodePlan pl = verify_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                          max_seq_len, window, max_q_len);
-        return ws_total_bytes(batch * max_q_len, num_q_heads, head_dim, pl);
-    }
-    const int sms = num_sms_current();
-    const PrefillSplit sp = prefill_split_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                               max_q_len, max_seq_len, window, sms);
-    const int32_t sk = prefill_sk_ctas(PKV_BF16, batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                       max_q_len, sms);
-    return std::max(prefill_split_ws_bytes(batch, num_q_heads, max_q_len, sp),
-                    prefill_sk_ws_bytes(prefill_items(batch, num_q_heads, num_kv_heads, max_q_len), sk));
+    return prefill_ws(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_seq_len,
+                      window, 0);
 }
 
-pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens,
-                                         int32_t num_q_heads, const pkv_pool *pool,
-                                         const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                         const int32_t *seq_lens, int32_t batch, int32_t max_q_len,
-                                         int32_t max_seq_len, int32_t window, float scale,
-                                         void *out, void *workspace, size_t ws_bytes,
-                                         int32_t *dev_status, pkv_stream_t stream)
+size_t paged_prefill_sinks_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                          int32_t max_seq_len, int32_t window, int32_t sinks)
+{
+    return prefill_ws(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_seq_len,
+                      window, sinks);
+}
+
+}  // extern "C"
+
+namespace {
+
+pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_heads, const pkv_pool *pool,
+                        const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                        int32_t batch, int32_t max_q_len, int32_t max_seq_len, int32_t window,
+                        int32_t sinks, float scale, void *out, void *workspace, size_t ws_bytes,
+                        int32_t *dev_status, pkv_stream_t stream)
 {
     if (!valid_pool(pool) || batch < 0 || num_q_heads <= 0 || max_q_len < 0 || max_seq_len < 0 ||
-        window < 0 || !std::isfinite(scale))
+        window < 0 || sinks < 0 || !std::isfinite(scale))
         return PKV_ERR_INVALID_ARG;
+    if (window == 0) sinks = 0;  // full attention sees every position
     if (num_q_heads % pool->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     if (batch == 0 || max_q_len == 0) return PKV_OK;
     if (q == nullptr || out == nullptr || cu_q_lens == nullptr || block_tables == nullptr ||
@@ -727,7 +824,7 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
         // M-rows, then its merge
         const int32_t max_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, cap));
         const DecodePlan pl = verify_plan(batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
-                                          pool->block_size, max_len, window, max_q_len);
+                                          pool->block_size, max_len, window, max_q_len, sinks);
         if (pl.n_suffix_ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
         const int32_t prow = batch * max_q_len;
         const size_t need = ws_total_bytes(prow, num_q_heads, pool->head_dim, pl);
@@ -760,6 +857,7 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
         d.num_blocks = pool->num_blocks;
         d.max_len = max_len;
         d.window = window;
+        d.sinks = sinks;
         d.scale_log2 = scale * 1.4426950408889634f;
         d.v_scale = 1.f;
         drill_settings(&d.wait_ns, &d.drill);
@@ -803,6 +901,7 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
     p.max_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, cap));
     p.max_q_len = max_q_len;
     p.window = window;
+    p.sinks = sinks;
     const int32_t qpt = prefill_queries_per_cta(pool->dtype, G);
     p.q_tiles = static_cast<int32_t>(ceil_div64(max_q_len, qpt));
     p.kv_splits = 1;
@@ -810,7 +909,7 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
     if (pool->dtype != PKV_F32) {
         const PrefillSplit sp = prefill_split_plan(batch, num_q_heads, pool->num_kv_heads,
                                                    pool->head_dim, pool->block_size, max_q_len,
-                                                   p.max_len, window, num_sms_current());
+                                                   p.max_len, window, sinks, num_sms_current());
         if (sp.splits > 1) {
             const size_t need = prefill_split_ws_bytes(batch, num_q_heads, max_q_len, sp);
             if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
@@ -871,6 +970,34 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
         err = launch_prefill_f32(p, st);
     }
     return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens,
+                                         int32_t num_q_heads, const pkv_pool *pool,
+                                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t *seq_lens, int32_t batch, int32_t max_q_len,
+                                         int32_t max_seq_len, int32_t window, float scale,
+                                         void *out, void *workspace, size_t ws_bytes,
+                                         int32_t *dev_status, pkv_stream_t stream)
+{
+    return prefill_call(q, cu_q_lens, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch,
+                        max_q_len, max_seq_len, window, 0, scale, out, workspace, ws_bytes, dev_status,
+                        stream);
+}
+
+pkv_status paged_prefill_chunk_attention_sinks(
+    const void *q, const int32_t *cu_q_lens, int32_t num_q_heads, const pkv_pool *pool,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t batch,
+    int32_t max_q_len, int32_t max_seq_len, int32_t window, int32_t sinks, float scale, void *out,
+    void *workspace, size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
+{
+    return prefill_call(q, cu_q_lens, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch,
+                        max_q_len, max_seq_len, window, sinks, scale, out, workspace, ws_bytes, dev_status,
+                        stream);
 }
 
 }  // extern "C"

@@ -12,7 +12,7 @@ namespace pkv {
 // block (decode_coop.cuh).
 static bool coop_fits(const DecodeParams &p)
 {
-    return p.plan.coop && p.cu_q_lens == nullptr && p.plan.n_prefix_ctas == 0 && p.group <= 8 &&
+    return p.plan.coop && p.sinks == 0 && p.cu_q_lens == nullptr && p.plan.n_prefix_ctas == 0 && p.group <= 8 &&
            (p.head_dim == 128 || p.head_dim == 256);
 }
 
@@ -25,15 +25,23 @@ cudaError_t launch_decode_bf16(const DecodeParams &p, const CUtensorMap &kmap,
     const bool mq = p.cu_q_lens != nullptr;  // several queries per row
     // query n-tiles: the rows of a split item (G, or G x max_q for a verify step)
     const bool two = query_ntiles(static_cast<int64_t>(p.group) * (mq ? p.max_q : 1)) == 2;
-#define PKV_BF16_LAUNCH(DIM)                                                             \
-    return mq ? (two ? launch_split<DIM, true, false, 2>(p, kmap, vmap, stream)           \
-                     : launch_split<DIM, true, false, 1>(p, kmap, vmap, stream))          \
-              : (two ? launch_split<DIM, false, false, 2>(p, kmap, vmap, stream)          \
-                     : launch_split<DIM, false, false, 1>(p, kmap, vmap, stream))
+#define PKV_BF16_LAUNCH(DIM, SINK)                                                       \
+    return mq ? (two ? launch_split<DIM, true, false, 2, SINK>(p, kmap, vmap, stream)     \
+                     : launch_split<DIM, true, false, 1, SINK>(p, kmap, vmap, stream))    \
+              : (two ? launch_split<DIM, false, false, 2, SINK>(p, kmap, vmap, stream)    \
+                     : launch_split<DIM, false, false, 1, SINK>(p, kmap, vmap, stream))
+    if (p.sinks > 0) {
+        switch (p.head_dim) {
+        case 64: PKV_BF16_LAUNCH(64, true);
+        case 128: PKV_BF16_LAUNCH(128, true);
+        case 256: PKV_BF16_LAUNCH(256, true);
+        default: return cudaErrorInvalidValue;
+        }
+    }
     switch (p.head_dim) {
-    case 64: PKV_BF16_LAUNCH(64);
-    case 128: PKV_BF16_LAUNCH(128);
-    case 256: PKV_BF16_LAUNCH(256);
+    case 64: PKV_BF16_LAUNCH(64, false);
+    case 128: PKV_BF16_LAUNCH(128, false);
+    case 256: PKV_BF16_LAUNCH(256, false);
     default: return cudaErrorInvalidValue;
     }
 #undef PKV_BF16_LAUNCH

@@ -11,9 +11,10 @@ struct RowRange {
     int32_t L;        // clamped sequence length
     int32_t C;        // queries of the row (1 for decode), at positions L - C .. L - 1
     int32_t q0;       // index of the row's first query in the packed q / out
-    int32_t lo;       // first position any of its queries attends
+    int32_t lo;       // first position any of its queries attends (sinks aside)
     int32_t b_first;  // first block of the row's own (suffix) splits
     int32_t b_end;    // one past the last block holding a position < L
+    int32_t nsb;      // sink blocks before them: blocks 0 .. nsb-1 (0 without sinks)
     int32_t grp;      // shared-prefix group, -1 = none
     int32_t P;        // prefix blocks of the group (0 = none)
 };
@@ -48,6 +49,9 @@ __device__ __forceinline__ RowRange row_range(const DecodeParams &p, int32_t r, 
     rr.lo = p.window > 0 ? max(0, L - rr.C + 1 - p.window) : 0;
     rr.b_first = rr.lo / p.block_size;
     rr.b_end = ceil_div_i(L, p.block_size);
+    // sinks: the row's splits run over the sink blocks, then the window's; a
+    // block that holds the last sinks and the window's start counts with the window
+    rr.nsb = p.sinks > 0 ? min(ceil_div_i(min(p.sinks, rr.lo), p.block_size), rr.b_first) : 0;
     rr.grp = -1;
     rr.P = 0;
     if (p.group_of_row != nullptr) {
@@ -73,7 +77,7 @@ __device__ __forceinline__ RowRange row_range(const DecodeParams &p, int32_t r, 
 
 __device__ __forceinline__ int32_t row_suffix_splits(const DecodeParams &p, const RowRange &rr)
 {
-    return rr.b_end > rr.b_first ? ceil_div_i(rr.b_end - rr.b_first, p.plan.split_blocks) : 0;
+    return rr.b_end > rr.b_first ? ceil_div_i(rr.nsb + rr.b_end - rr.b_first, p.plan.split_blocks) : 0;
 }
 
 __device__ __forceinline__ int32_t row_prefix_splits(const DecodeParams &p, const RowRange &rr)

@@ -39,6 +39,8 @@ __global__ void __launch_bounds__(kF32Threads)
     pdl_wait();
     pdl_trigger();
     int32_t b0, nblk, slot, g;
+    // sinks: block v of the row's run is block v + (v >= nsb ? gap : 0) of the row
+    int32_t nsb = 0, gap = 0, sink = 0;
     if (!prefix_mode) {
         int64_t bid = blockIdx.x;
         const int32_t s = static_cast<int32_t>(bid % p.plan.n_suffix_splits);
@@ -46,8 +48,14 @@ __global__ void __launch_bounds__(kF32Threads)
         g = static_cast<int32_t>(bid % p.hkv);
         const int32_t r = static_cast<int32_t>(bid / p.hkv);
         const RowRange rr = row_range(p, r, s == 0 && g == 0);
-        b0 = rr.b_first + s * p.plan.split_blocks;
-        const int32_t b1 = min(b0 + p.plan.split_blocks, rr.b_end);
+        if (p.sinks > 0) {
+            nsb = rr.nsb;
+            gap = rr.b_first - nsb;
+            sink = p.sinks;
+        }
+        // numbered over the sink blocks and the window's (without sinks: from b_first)
+        b0 = (p.sinks > 0 ? 0 : rr.b_first) + s * p.plan.split_blocks;
+        const int32_t b1 = min(b0 + p.plan.split_blocks, rr.b_end - gap);
         if (b0 >= b1) return;
         nblk = b1 - b0;
         slot = p.plan.n_prefix_splits + s;
@@ -135,7 +143,7 @@ __global__ void __launch_bounds__(kF32Threads)
     const float *kpool = static_cast<const float *>(p.k_pool);
     const float *vpool = static_cast<const float *>(p.v_pool);
     for (int i = 0; i < nblk; ++i) {
-        const int32_t b = b0 + i;
+        const int32_t b = b0 + i >= nsb ? b0 + i + gap : b0 + i;
         const int32_t blk = __ldg(p.tables + static_cast<int64_t>(tab_row) * p.width + b);
         const bool ok = static_cast<uint32_t>(blk) < static_cast<uint32_t>(p.num_blocks);
         if (!ok && tid == 0) report(p.status, PKV_DEV_BAD_BLOCK);
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kF32Threads)
             const int k = j / bs, t = j % bs;
             const int pos = b * bs + t;
             float sv = -INFINITY;
-            if (ok && prow[k] >= 0 && pos >= plo[k] && pos < phi[k]) {
+            if (ok && prow[k] >= 0 && (pos >= plo[k] || pos < sink) && pos < phi[k]) {
                 float acc = 0.f;
                 for (int d = 0; d < D; ++d) acc = fmaf(qs[k * D + d], ks[t * D + d], acc);
                 sv = acc * p.scale_log2;

@@ -12,15 +12,23 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t stream)
     const bool mq = p.cu_q_lens != nullptr;
     // query n-tiles: the rows of a split item (G, or G x max_q for a verify step)
     const bool two = query_ntiles(static_cast<int64_t>(p.group) * (mq ? p.max_q : 1)) == 2;
-#define PKV_FP8_LAUNCH(DIM)                                                               \
-    return mq ? (two ? launch_split<DIM, true, true, 2>(p, none, none, stream)             \
-                     : launch_split<DIM, true, true, 1>(p, none, none, stream))            \
-              : (two ? launch_split<DIM, false, true, 2>(p, none, none, stream)            \
-                     : launch_split<DIM, false, true, 1>(p, none, none, stream))
+#define PKV_FP8_LAUNCH(DIM, SINK)                                                         \
+    return mq ? (two ? launch_split<DIM, true, true, 2, SINK>(p, none, none, stream)       \
+                     : launch_split<DIM, true, true, 1, SINK>(p, none, none, stream))      \
+              : (two ? launch_split<DIM, false, true, 2, SINK>(p, none, none, stream)      \
+                     : launch_split<DIM, false, true, 1, SINK>(p, none, none, stream))
+    if (p.sinks > 0) {
+        switch (p.head_dim) {
+        case 64: PKV_FP8_LAUNCH(64, true);
+        case 128: PKV_FP8_LAUNCH(128, true);
+        case 256: PKV_FP8_LAUNCH(256, true);
+        default: return cudaErrorInvalidValue;
+        }
+    }
     switch (p.head_dim) {
-    case 64: PKV_FP8_LAUNCH(64);
-    case 128: PKV_FP8_LAUNCH(128);
-    case 256: PKV_FP8_LAUNCH(256);
+    case 64: PKV_FP8_LAUNCH(64, false);
+    case 128: PKV_FP8_LAUNCH(128, false);
+    case 256: PKV_FP8_LAUNCH(256, false);
     default: return cudaErrorInvalidValue;
     }
 #undef PKV_FP8_LAUNCH

@@ -110,15 +110,21 @@ __device__ __forceinline__ uint32_t kv_chunk_addr(uint32_t tile, int tok, int d0
 
 // Block ids of a strided run, fetched 32 at a time ahead of use: index j of
 // the run is row[first + stride * j].  All lanes call next() with the same,
-// increasing j; the id comes back on every lane.
-struct BlockIds {
+// increasing j; the id comes back on every lane.  kSink: the run is numbered
+// over the sink blocks and the window's, and `gap` blocks lie unread between
+// block nsb - 1 and the next.
+template <bool kSink>
+struct BlockIdsT {
     const int32_t *row;
     int32_t first, stride, n, batch_no;
     int32_t cur, nxt;
+    int32_t nsb, gap;
     __device__ __forceinline__ int32_t fetch(int32_t j, int lane) const
     {
         const int32_t k = j + lane;
-        return k < n ? __ldg(row + first + stride * k) : -1;
+        int32_t b = first + stride * k;
+        if (kSink && b >= nsb) b += gap;
+        return k < n ? __ldg(row + b) : -1;
     }
     __device__ __forceinline__ void init(const int32_t *r, int32_t f, int32_t s, int32_t count,
                                          int lane)
@@ -141,10 +147,12 @@ struct BlockIds {
         return __shfl_sync(0xffffffffu, cur, j & 31);
     }
 };
+using BlockIds = BlockIdsT<false>;
 
 // The work of CTA `cta` of one decode call (p), its K/V tensor maps (bf16)
-// given by reference to kernel-parameter memory.
-template <int D, bool kMQ, bool kF8, int NQ>
+// given by reference to kernel-parameter memory.  kSink (split items only): the
+// row's blocks are its sink blocks, then its window's.
+template <int D, bool kMQ, bool kF8, int NQ, bool kSink = false>
 __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                                   const DecodeParams &p, const int64_t cta)
 {
@@ -191,7 +199,11 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
     const int R = kMQ ? G * p.max_q : G;
     // the block ids of the run (this warp's share of a split item; the whole
     // run for a prefix item, fetched by warp 0)
-    BlockIds ids;
+    BlockIdsT<kSink> ids;
+    // sinks: block v of the row's run is block v + (v >= nsb ? gap : 0) of the
+    // row, and positions below `sink` are attended beside [lo, hi)
+    int32_t nsb = 0, gap = 0;
+    const int32_t sink = kSink ? p.sinks : 0;
     // B fragments of Q^T (query rows on N, NQ n-tiles of 8):
     // b0 = Q[row 8n + lane/4][16kk + 2(lane%4), +1], b1 = the same 8 dims further.
     // A split item whose query fits in registers loads them straight from
@@ -234,13 +246,23 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
         // attention, no shared prefix), so that the two fetches overlap; a
         // decode step's query loads go out with them.
         const int32_t b_guess = s * p.plan.split_blocks;
-        const int32_t n_guess =
-            max(0, (min(p.plan.split_blocks, p.width - b_guess) - warp + NW - 1) / NW);
-        ids.init(table_row + (n_guess > 0 ? b_guess : 0), warp, NW, n_guess, lane);
+        if constexpr (!kSink) {
+            const int32_t n_guess =
+                max(0, (min(p.plan.split_blocks, p.width - b_guess) - warp + NW - 1) / NW);
+            ids.init(table_row + (n_guess > 0 ? b_guess : 0), warp, NW, n_guess, lane);
+        }
         if constexpr (C::kQInRegs && !kMQ) load_q_direct();
         const RowRange rr = row_range(p, row_r, s == 0 && g == 0);
-        b0 = rr.b_first + s * p.plan.split_blocks;
-        const int32_t b1 = min(b0 + p.plan.split_blocks, rr.b_end);
+        int32_t b1;
+        if constexpr (kSink) {  // numbered over the sink blocks and the window's
+            nsb = rr.nsb;
+            gap = rr.b_first - nsb;
+            b0 = b_guess;
+            b1 = min(b0 + p.plan.split_blocks, nsb + rr.b_end - rr.b_first);
+        } else {
+            b0 = rr.b_first + s * p.plan.split_blocks;
+            b1 = min(b0 + p.plan.split_blocks, rr.b_end);
+        }
         if (b0 >= b1) return;
         nblk = b1 - b0;
         slot = p.plan.n_prefix_splits + s;
@@ -252,7 +274,11 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
         tiles = 1;
         if constexpr (C::kQInRegs && kMQ) load_q_direct();
         const int32_t nbw = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;
-        if (rr.b_first != 0)
+        if constexpr (kSink) {
+            ids.nsb = nsb;
+            ids.gap = gap;
+            ids.init(table_row, b0 + warp, NW, nbw, lane);
+        } else if (rr.b_first != 0)
             ids.init(table_row + b0, warp, NW, nbw, lane);  // the guess was wrong
         else
             ids.n = nbw;  // fetched ids past the run are never used
@@ -550,7 +576,9 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
         for (int i = 0; i < BPS; ++i) {
             okb[i] = stage_ok[st * BPS + i] != 0;
             const int32_t j = k * BPS + i;
-            base_tok[i] = (b0 + (prefix_item ? j : warp + NW * j)) * bs;
+            int32_t b = b0 + (prefix_item ? j : warp + NW * j);
+            if (kSink && b >= nsb) b += gap;
+            base_tok[i] = b * bs;
         }
 
         // S^T = K Q^T: rows = the block's tokens g8 (first half) and
@@ -622,7 +650,8 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     in = in && (chi[n][e] == 0 ||
-                                (base_tok[i] >= clo[n][e] && base_tok[i] + bs <= chi[n][e]));
+                                ((base_tok[i] >= clo[n][e] || (kSink && base_tok[i] + bs <= sink)) &&
+                                 base_tok[i] + bs <= chi[n][e]));
             inside = inside && in;
         }
         if (__all_sync(0xffffffffu, inside)) {
@@ -641,7 +670,7 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
                     for (int e = 0; e < 4; ++e) {
                         const int pos = base_tok[i] + g8 + 8 * (e >> 1);
                         const int lo = clo[n][e & 1], hi = chi[n][e & 1];
-                        sv[i][n][e] = (okb[i] && pos >= lo && pos < hi)
+                        sv[i][n][e] = (okb[i] && (pos >= lo || (kSink && pos < sink)) && pos < hi)
                                           ? sT[i][n][e] * p.scale_log2
                                           : -INFINITY;
                     }
@@ -726,7 +755,9 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
             uint32_t mk0 = 0xffffffffu, mk1 = 0xffffffffu;
             const int bt = base_tok[i];
             if (bt < lo_all || bt + bs > hi_all) {
-                auto live = [&](int t) { return bt + t >= lo_all && bt + t < hi_all; };
+                auto live = [&](int t) {
+                    return (bt + t >= lo_all || (kSink && bt + t < sink)) && bt + t < hi_all;
+                };
                 mk0 = (live(2 * cc) ? 0x0000ffffu : 0u) | (live(2 * cc + 1) ? 0xffff0000u : 0u);
                 mk1 = (live(2 * cc + 8) ? 0x0000ffffu : 0u) | (live(2 * cc + 9) ? 0xffff0000u : 0u);
             }
@@ -876,12 +907,12 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
     }
 }
 
-template <int D, bool kMQ, bool kF8, int NQ>
+template <int D, bool kMQ, bool kF8, int NQ, bool kSink>
 __global__ void __launch_bounds__(kDecodeWarps * 32, KvCfg<D, kF8, NQ>::kCtasPerSm)
     decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const DecodeParams p)
 {
-    decode_split_body<D, kMQ, kF8, NQ>(kmap, vmap, p, blockIdx.x);
+    decode_split_body<D, kMQ, kF8, NQ, kSink>(kmap, vmap, p, blockIdx.x);
 }
 
 // Several decode calls in one launch (groups of a model's layers that share
@@ -916,13 +947,13 @@ static cudaError_t launch_split_grouped(const GroupedDecode &gd, cudaStream_t st
     return err;
 }
 
-template <int D, bool kMQ, bool kF8, int NQ = 1>
+template <int D, bool kMQ, bool kF8, int NQ = 1, bool kSink = false>
 static cudaError_t launch_split(const DecodeParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream)
 {
     const int64_t ctas = p.plan.n_prefix_ctas + p.plan.n_suffix_ctas;
     if (ctas == 0) return cudaSuccess;
-    auto kern = decode_split_kernel<D, kMQ, kF8, NQ>;
+    auto kern = decode_split_kernel<D, kMQ, kF8, NQ, kSink>;
     const int smem = KvSmem<D, kF8, NQ>::kLaunchBytes;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;

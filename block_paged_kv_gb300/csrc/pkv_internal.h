@@ -112,6 +112,7 @@ struct DecodeParams {
     int32_t batch, hq, hkv, group, head_dim, block_size, width, num_blocks;
     int32_t max_len;   // min(max_seq_len, width * block_size): lengths are clamped to it
     int32_t window;
+    int32_t sinks;     // with a window: the first positions that stay visible (0 = none)
     int32_t num_groups;
     float scale_log2;  // scale * log2(e) (* k_scale for FP8): scores are kept in base-2 units
     float v_scale;     // FP8: applied to each partial's weighted values
@@ -169,6 +170,7 @@ struct PrefillParams {
     int32_t max_len;    // min(max_seq_len, width * block_size)
     int32_t max_q_len;
     int32_t window;
+    int32_t sinks;      // with a window: the first positions that stay visible (0 = none)
     int32_t q_tiles;    // CTAs per (row, kv head): ceil(max_q_len / queries per CTA)
     // key-range split (bf16, short chunks only; 1 = none): each (row, kv head,
     // query tile) is cut into kv_splits runs of split_tiles 64-key tiles whose
@@ -211,7 +213,7 @@ struct PrefillSplit {
 };
 PrefillSplit prefill_split_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
                                 int32_t max_q_len, int32_t max_seq_len, int32_t window,
-                                int num_sms);
+                                int32_t sinks, int num_sms);
 size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, const PrefillSplit &sp);
 // The persistent balanced schedule of the tensor-core prefill: the CTA count
 // (0 = off: the grid then holds one CTA per item) and its workspace.

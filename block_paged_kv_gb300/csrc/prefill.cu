@@ -89,7 +89,27 @@ constexpr uint32_t kRescaleLog2 = 8;      // O is rescaled only when the max gro
 
 struct PrefillRowInfo {
     int32_t r, g, i0, nq, L, C, kv_lo, kv_hi, s;
+    // sinks (kSink): the item's key tiles are numbered from 0 over its nst sink
+    // tiles, then the window's; tile v >= nst is key tile v + gap.  Without
+    // sinks tiles carry their own number.
+    int32_t nst, gap;
 };
+
+// the first key tile of an item in its own numbering, and their number
+template <bool kSink>
+__device__ __forceinline__ int32_t item_first_tile(const PrefillRowInfo &w)
+{
+    return kSink ? 0 : w.kv_lo / pf::kKeys;
+}
+__device__ __forceinline__ int32_t item_tiles(const PrefillRowInfo &w)
+{
+    return w.nst + (w.kv_hi - 1) / pf::kKeys - w.kv_lo / pf::kKeys + 1;
+}
+template <bool kSink>
+__device__ __forceinline__ int32_t key_tile(const PrefillRowInfo &w, int32_t v)
+{
+    return kSink && v >= w.nst ? v + w.gap : v;
+}
 
 __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int64_t bid, int qpc,
                                              PrefillRowInfo &w)
@@ -120,6 +140,10 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int64_t bid
     const int32_t p_first = L - C + w.i0;
     w.kv_hi = p_first + w.nq;
     w.kv_lo = p.window > 0 ? max(0, p_first - p.window + 1) : 0;
+    // tiles wholly before the window's first one that hold sinks
+    const int32_t jw = w.kv_lo / pf::kKeys;
+    w.nst = p.sinks > 0 ? min((min(p.sinks, w.kv_lo) + pf::kKeys - 1) / pf::kKeys, jw) : 0;
+    w.gap = jw - w.nst;
     return true;
 }
 
@@ -153,7 +177,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 struct Seg {
     PrefillRowInfo w;
     int32_t item;
-    int32_t jt0;    // first key tile of the segment (in 64-key units)
+    int32_t jt0;    // first key tile of the segment (64-key units, the item's numbering)
     int32_t ntile;  // tiles of the segment
     bool whole;     // the item's whole key range
     int32_t slot;   // persistent schedule: partial slot of a cut segment
@@ -197,6 +221,7 @@ __device__ __forceinline__ int32_t sk_cta_of(const PrefillParams &p, int32_t pos
 }
 
 // Next segment of a persistent CTA's run (false at its end).
+template <bool kSink>
 __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk &sw, Seg &sg)
 {
     if (sw.pos >= sw.end) return false;
@@ -205,7 +230,7 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
     const int32_t seg_end = min(hi, sw.end);
     prefill_item(p, u, qpc, sg.w);  // an item with tiles has queries
     sg.item = u;
-    sg.jt0 = sg.w.kv_lo / pf::kKeys + (sw.pos - lo);
+    sg.jt0 = item_first_tile<kSink>(sg.w) + (sw.pos - lo);
     sg.ntile = seg_end - sw.pos;
     sg.whole = sw.pos == lo && seg_end == hi;
     sg.slot = sw.k == 0 ? 0 : 1;
@@ -221,6 +246,7 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
 
 // First segment of CTA `cta` (false: nothing to do).  One CTA per item: the
 // item (or its key-range run; an empty run sets ntile <= 0).
+template <bool kSink>
 __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64_t cta, SegWalk &sw,
                                           Seg &sg)
 {
@@ -234,18 +260,18 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
         if (hi > lo) {  // item c, whole
             prefill_item(p, c, qpc, sg.w);  // an item with tiles has queries
             sg.item = c;
-            sg.jt0 = sg.w.kv_lo / pf::kKeys;
+            sg.jt0 = item_first_tile<kSink>(sg.w);
             sg.ntile = hi - lo;
             sg.whole = true;
             sg.slot = 0;
             return true;
         }
-        return sk_next(p, qpc, sw, sg);
+        return sk_next<kSink>(p, qpc, sw, sg);
     }
     if (!prefill_item(p, cta, qpc, sg.w)) return false;
     sg.item = static_cast<int32_t>(cta);
-    sg.jt0 = sg.w.kv_lo / pf::kKeys;
-    sg.ntile = (sg.w.kv_hi - 1) / pf::kKeys - sg.jt0 + 1;
+    sg.jt0 = item_first_tile<kSink>(sg.w);
+    sg.ntile = item_tiles(sg.w);
     sg.whole = p.kv_splits <= 1;
     sg.slot = 0;
     if (!sg.whole) {
@@ -257,12 +283,14 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
     return true;
 }
 
+template <bool kSink>
 __device__ __forceinline__ bool seg_next(const PrefillParams &p, int qpc, SegWalk &sw, Seg &sg)
 {
-    return p.sk_ctas > 0 && sk_next(p, qpc, sw, sg);
+    return p.sk_ctas > 0 && sk_next<kSink>(p, qpc, sw, sg);
 }
 
 // The key tiles of a CTA in order, over its segments (producers).
+template <bool kSink>
 struct TileCursor {
     SegWalk sw;
     Seg sg;
@@ -282,9 +310,9 @@ struct TileCursor {
         if (!valid) return;
         if (++j < sg.ntile) return;
         j = 0;
-        valid = seg_next(p, qpc, sw, sg);
+        valid = seg_next<kSink>(p, qpc, sw, sg);
     }
-    __device__ __forceinline__ int32_t kt() const { return sg.jt0 + j; }  // absolute key tile
+    __device__ __forceinline__ int32_t kt() const { return key_tile<kSink>(sg.w, sg.jt0 + j); }  // absolute key tile
 };
 
 // One row of a query tile into shared memory (softmax thread ii = 0 .. 255:
@@ -329,7 +357,8 @@ __device__ __noinline__ void stage_q_row(const uint4 *q, const int32_t *cu_q_len
 // ---------------------------------------------------------------------------
 // bf16, tcgen05
 // ---------------------------------------------------------------------------
-template <bool kF8>
+// kSink: a window with sink tokens (their tiles first, then the window's)
+template <bool kF8, bool kSink>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PrefillParams p)
@@ -369,7 +398,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     const int qpc = kQTiles * qpt;  // queries per item
     SegWalk sw0;
     Seg seg0;
-    if (!seg_first(p, qpc, blockIdx.x, sw0, seg0)) return;
+    if (!seg_first<kSink>(p, qpc, blockIdx.x, sw0, seg0)) return;
     const bool split = p.kv_splits > 1;  // one CTA per key-range run of a short chunk
     if (split && seg0.ntile <= 0) {
         // an empty run: an empty partial (no weight) for every live row
@@ -448,12 +477,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         uint64_t *empty = is_k ? k_empty : v_empty;
         // lane < kBlocks: logical block kt * kBlocks + lane of the cursor's
         // tile, inside the table and the item's key range
-        auto in_range_of = [&](const TileCursor &c) {
+        auto in_range_of = [&](const TileCursor<kSink> &c) {
             const int32_t kb = c.kt() * kBlocks + lane;
             return c.valid && lane < kBlocks && kb < p.width && kb * 16 < c.sg.w.kv_hi &&
-                   (kb + 1) * 16 > c.sg.w.kv_lo;
+                   ((kb + 1) * 16 > c.sg.w.kv_lo || (kSink && kb * 16 < p.sinks));
         };
-        auto load_id = [&](const TileCursor &c) {
+        auto load_id = [&](const TileCursor<kSink> &c) {
             return in_range_of(c) ? __ldg(p.tables + static_cast<int64_t>(c.sg.w.r) * p.width +
                                           c.kt() * kBlocks + lane)
                                   : -1;
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             int32_t nf = 0;  // tiles 0 .. nf-1 fetched into the staging buffers
             // fetch tile nf at cursor c (block ids read one tile before);
             // whole warp; returns the mask of loaded blocks
-            auto fetch = [&](const TileCursor &c, int32_t id) {
+            auto fetch = [&](const TileCursor<kSink> &c, int32_t id) {
                 const bool in_range = in_range_of(c);
                 const bool good = in_range && static_cast<uint32_t>(id) < static_cast<uint32_t>(p.num_blocks);
                 if (is_k && in_range && !good) report(p.status, PKV_DEV_BAD_BLOCK);
@@ -503,7 +532,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             };
             // bulk copies only, two tiles ahead; the softmax warps widen each
             // tile into the ring and release the staging buffer
-            TileCursor cf, ci;
+            TileCursor<kSink> cf, ci;
             cf.start(p, qpc, sw0, seg0);
             ci = cf;
             int32_t id_next = load_id(ci);
@@ -526,7 +555,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         } else {
             const CUtensorMap *map = is_k ? &kmap : &vmap;
             const uint64_t policy = l2_evict_last_policy();  // re-read by the row's other CTAs
-            TileCursor cur;
+            TileCursor<kSink> cur;
             cur.start(p, qpc, sw0, seg0);
             int32_t T = 0;
             for (; cur.valid; ++T, cur.advance(p, qpc)) {
@@ -658,7 +687,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             }
             if (!ok) break;
             T0 += n;
-            if (!seg_next(p, qpc, sw, sg)) break;
+            if (!seg_next<kSink>(p, qpc, sw, sg)) break;
         }
         // every product this warp issued has completed before the CTA frees
         // tensor memory (after a wait ran out, some may still be running)
@@ -774,7 +803,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         for (int32_t jj = 0; jj < ntile; ++jj) {
             const int32_t T = T0 + jj;
             const int ks = T % kStages, buf = T & 1;
-            const int32_t tbase = (jt0 + jj) * kKeys;
+            const int32_t tbase = (kSink ? key_tile<true>(ss->sg.w, jt0 + jj) : jt0 + jj) * kKeys;
             const uint32_t sx = tS(x, buf) + lane_base;
             if constexpr (kF8) {
                 if (do_k && T + 2 < T_total && !widen_k(T + 2)) {
@@ -800,7 +829,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 const uint32_t vm = smask[2 + sb];
                 const uint32_t src = smem_u32(smem + L::kStagingOff + 2 * kF8StageTile + sb * kF8StageTile);
                 const uint32_t dst = smem_u32(v_s + ks * kTileBytes);
-                const bool vedge = tbase < kv_lo || tbase + kKeys > kv_hi;
+                const bool vedge = (tbase < kv_lo && !(kSink && tbase + kKeys <= p.sinks)) || tbase + kKeys > kv_hi;
                 // A warp takes the 32 chunks of one (block, 32-dim group): lane
                 // l holds dim 32g + 8jn + l/4 (jn = 0..3) for keys 16b + 2(l%4)
                 // + {0, 1, 8, 9}, i.e. the 8x8 matrices (dims 32g + 8jn .. + 7)
@@ -821,7 +850,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                         if (vedge) {
                             auto live = [&](int k) {
                                 const int32_t kp = tbase + b * 16 + k;
-                                return kp >= kv_lo && kp < kv_hi;
+                                return (kp >= kv_lo || (kSink && kp < p.sinks)) && kp < kv_hi;
                             };
                             const uint32_t mk0 = (live(2 * c) ? 0x0000ffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
                             const uint32_t mk1 = (live(2 * c + 8) ? 0x0000ffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
@@ -877,15 +906,19 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // a tile with any key outside this row's range takes the masked
                 // path: key column e is attended iff e - lo is in [0, qpos - qlo]
                 // and its block was loaded
-                const bool full = mask == (1u << kBlocks) - 1u && tbase >= qlo &&
+                const bool full = mask == (1u << kBlocks) - 1u &&
+                                  (tbase >= qlo || (kSink && tbase + kKeys <= p.sinks)) &&
                                   tbase + kKeys - 1 <= qpos && valid_row;
                 if (!full) {
                     const int32_t lo = qlo - tbase;
                     const uint32_t span = static_cast<uint32_t>(qpos - qlo);  // qlo <= qpos
                     const uint32_t bm = valid_row ? mask : 0u;
+                    // sink columns of the tile: e < sk (positions up to the query's own)
+                    const int32_t sk = kSink ? min(p.sinks, qpos + 1) - tbase : 0;
     #pragma unroll
                     for (int e = 0; e < 64; ++e) {
-                        const bool ok = static_cast<uint32_t>(e - lo) <= span && ((bm >> (e >> 4)) & 1u);
+                        const bool ok = (static_cast<uint32_t>(e - lo) <= span || (kSink && e < sk)) &&
+                                        ((bm >> (e >> 4)) & 1u);
                         s[e] = ok ? s[e] : -INFINITY;
                     }
                 }
@@ -990,14 +1023,15 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 break;
             }
             // (FP8: the V producer wrote those columns as zeros)
-            const bool edge = !kF8 && (mask != (1u << kBlocks) - 1u || tbase < kv_lo ||
+            const bool edge = !kF8 && (mask != (1u << kBlocks) - 1u ||
+                                       (tbase < kv_lo && !(kSink && tbase + kKeys <= p.sinks)) ||
                                        tbase + kKeys > kv_hi);
             if (edge) {
                 // thread row r < 64 zeroes key row r's first 64 dims, r >= 64
                 // the second 64 dims of key row r - 64
                 const int kr = row & (kKeys - 1), half = row >> 6;
                 const int32_t kp = tbase + kr;
-                if (!(kp >= kv_lo && kp < kv_hi && ((mask >> (kr >> 4)) & 1u))) {
+                if (!((kp >= kv_lo || (kSink && kp < p.sinks)) && kp < kv_hi && ((mask >> (kr >> 4)) & 1u))) {
                     uint8_t *vs = v_s + ks * kTileBytes + half * kKVRegion + kr * 128;
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
@@ -1164,7 +1198,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         if (lane == 0) {
             SegWalk sw = ss->sw;
             Seg sg;
-            more = seg_next(p, qpc, sw, sg);
+            more = seg_next<kSink>(p, qpc, sw, sg);
             if (more) {
                 ss->sw = sw;
                 ss->sg = sg;
@@ -1224,7 +1258,11 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
     const float *kpool = static_cast<const float *>(p.k_pool);
     const float *vpool = static_cast<const float *>(p.v_pool);
     const int32_t *trow = p.tables + static_cast<int64_t>(w.r) * p.width;
-    for (int32_t b = w.kv_lo / bs; b * bs < w.kv_hi; ++b) {
+    // the sink blocks before the window's first block, then the window's
+    const int32_t b_win = w.kv_lo / bs;
+    const int32_t nsb = p.sinks > 0 ? min((min(p.sinks, w.kv_lo) + bs - 1) / bs, b_win) : 0;
+    const int32_t sink = p.sinks;
+    for (int32_t b = nsb > 0 ? 0 : b_win; b * bs < w.kv_hi; b = b + 1 == nsb ? b_win : b + 1) {
         const int32_t blk = b < p.width ? __ldg(trow + b) : -1;
         const bool ok = static_cast<uint32_t>(blk) < static_cast<uint32_t>(p.num_blocks);
         if (!ok && tid == 0) report(p.status, PKV_DEV_BAD_BLOCK);
@@ -1240,7 +1278,7 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
             const int k = j / bs, tt = j % bs;
             const int pos = b * bs + tt;
             float sv = -INFINITY;
-            if (ok && pos >= plo[k] && pos < phi[k]) {
+            if (ok && (pos >= plo[k] || pos < sink) && pos < phi[k]) {
                 float acc = 0.f;
                 for (int d = 0; d < D; ++d) acc = fmaf(qs[k * D + d], ks[tt * D + d], acc);
                 sv = acc * p.scale_log2;
@@ -1363,7 +1401,7 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         int32_t n = 0;
         PrefillRowInfo w;
         if (u < p.sk_items && prefill_item(p, u, qpc, w))
-            n = (w.kv_hi - 1) / pf::kKeys - w.kv_lo / pf::kKeys + 1;
+            n = item_tiles(w);
         // inclusive scan: within the warp, then over the warps' sums
         int32_t v = n;
 #pragma unroll
@@ -1408,7 +1446,8 @@ int32_t prefill_queries_per_cta(pkv_dtype dtype, int32_t G)
 }
 
 PrefillSplit prefill_split_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
-                                int32_t max_q_len, int32_t max_seq_len, int32_t window, int num_sms)
+                                int32_t max_q_len, int32_t max_seq_len, int32_t window, int32_t sinks,
+                                int num_sms)
 {
     PrefillSplit sp{1, 0};
     if (hkv <= 0 || hq % hkv != 0 || batch <= 0 || max_q_len <= 0) return sp;
@@ -1419,7 +1458,8 @@ PrefillSplit prefill_split_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t 
     const int64_t keys = window > 0 ? std::min<int64_t>(max_seq_len, static_cast<int64_t>(window) + max_q_len)
                                     : max_seq_len;
     // +1: a CTA's range may start inside a tile
-    const int64_t tiles = (keys + pf::kKeys - 1) / pf::kKeys + 1;
+    int64_t tiles = (keys + pf::kKeys - 1) / pf::kKeys + 1;
+    if (sinks > 0) tiles += (static_cast<int64_t>(std::min(sinks, max_seq_len)) + pf::kKeys - 1) / pf::kKeys;
     // about four CTAs per SM over the grid, at least 8 tiles (512 keys) per run
     int64_t s = (4ll * std::max(num_sms, 1) + ctas - 1) / ctas;
     s = std::min<int64_t>(s, tiles / 8);
@@ -1464,7 +1504,7 @@ size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, cons
     return o + n * 2 * sizeof(float);
 }
 
-template <bool kF8>
+template <bool kF8, bool kSink>
 static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &kmap,
                                     const CUtensorMap &vmap, cudaStream_t stream)
 {
@@ -1472,14 +1512,14 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
                                        : static_cast<int64_t>(p.batch) * p.hkv * p.q_tiles * p.kv_splits;
     if (ctas == 0) return cudaSuccess;
     constexpr int smem = pf::Layout<kF8>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8>,
+    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_PREFILL, stream);
     if (p.sk_ctas > 0)
         err = launch_pdl(prefill_sk_plan_kernel, dim3(1), dim3(kSkPlanThreads), 0, stream, p);
     if (err == cudaSuccess)
-        err = launch_pdl(prefill_kernel<kF8>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
+        err = launch_pdl(prefill_kernel<kF8, kSink>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
                          stream, kmap, vmap, p);
     if (err == cudaSuccess && p.kv_splits > 1) {
         const int64_t items = static_cast<int64_t>(p.batch) * p.max_q_len * p.hq;
@@ -1494,13 +1534,15 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
 cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream)
 {
-    return launch_prefill_tc<false>(p, kmap, vmap, stream);
+    return p.sinks > 0 ? launch_prefill_tc<false, true>(p, kmap, vmap, stream)
+                       : launch_prefill_tc<false, false>(p, kmap, vmap, stream);
 }
 
 cudaError_t launch_prefill_fp8(const PrefillParams &p, cudaStream_t stream)
 {
     const CUtensorMap none{};  // the FP8 producers read the pools by bulk copy
-    return launch_prefill_tc<true>(p, none, none, stream);
+    return p.sinks > 0 ? launch_prefill_tc<true, true>(p, none, none, stream)
+                       : launch_prefill_tc<true, false>(p, none, none, stream);
 }
 
 cudaError_t launch_prefill_f32(const PrefillParams &p, cudaStream_t stream)

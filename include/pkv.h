@@ -382,6 +382,48 @@ pkv_status paged_prefill_chunk_attention(const void *q, const int32_t *cu_q_lens
                                          void *out, void *workspace, size_t ws_bytes,
                                          int32_t *dev_status, pkv_stream_t stream);
 
+/*
+ * Sliding window with sink tokens: the first `sinks` positions of a row stay
+ * visible to every later query.  A query at position p attends
+ *   { j : 0 <= j <= p and (j > p - window or j < sinks) }.
+ * The calls below are the ones above with that key set: same layouts, types,
+ * workspaces (their own size queries), errors and determinism.  sinks 0, or
+ * window 0 (full attention, where every position is visible), is the call
+ * above, bit for bit.  Blocks between the sinks and the window are never
+ * read: their table entries may be -1 (pkv_allocator_expire_window).
+ */
+size_t paged_decode_sinks_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size,
+                                         int32_t max_seq_len, int32_t window, int32_t sinks);
+
+pkv_status paged_decode_attention_sinks(const void *q, int32_t num_q_heads, const pkv_pool *pool,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, int32_t batch,
+                                        int32_t max_seq_len, int32_t window, int32_t sinks,
+                                        float scale, void *out, void *workspace, size_t ws_bytes,
+                                        int32_t *dev_status, pkv_stream_t stream);
+
+/* sinks: host [n_groups], or NULL for none.  Groups without sinks share the
+ * fused launches; a group with sinks gets its own call's launches. */
+size_t paged_decode_groups_sinks_workspace_size(const pkv_decode_group *groups, const int32_t *sinks,
+                                                int32_t n_groups, int32_t batch, int32_t num_q_heads);
+
+pkv_status paged_decode_attention_groups_sinks(const pkv_decode_group *groups, const int32_t *sinks,
+                                               int32_t n_groups, int32_t batch, int32_t num_q_heads,
+                                               void *workspace, size_t ws_bytes,
+                                               int32_t *dev_status, pkv_stream_t stream);
+
+size_t paged_prefill_sinks_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                          int32_t max_seq_len, int32_t window, int32_t sinks);
+
+pkv_status paged_prefill_chunk_attention_sinks(
+    const void *q, const int32_t *cu_q_lens, int32_t num_q_heads, const pkv_pool *pool,
+    const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t batch, int32_t max_q_len, int32_t max_seq_len, int32_t window, int32_t sinks,
+    float scale, void *out, void *workspace, size_t ws_bytes, int32_t *dev_status,
+    pkv_stream_t stream);
+
 /* Static text for a status code. */
 const char *pkv_status_string(pkv_status status);
 
