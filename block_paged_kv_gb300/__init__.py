@@ -238,14 +238,19 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(device.index)
+
+
+_NULL = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on(device: torch.device):
     """Make `device` current for a library call (the library plans for, and
     takes scratch from, the current device); a no-op when it already is."""
-    if device.index is None or torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
+    if _current_device() == device.index:
+        return _NULL
     return torch.cuda.device(device)
 
 
@@ -254,23 +259,30 @@ def _require(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
+# Host cost of a call matters at decode sizes (a launch takes 3 us): the checks
+# below read each attribute once, in one expression per call, and only a call
+# that fails one goes through the messages.
 def _pool(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: Optional[float] = None,
           v_scale: Optional[float] = None) -> _Pool:
-    _require(k_pool.dtype == v_pool.dtype and k_pool.shape == v_pool.shape,
-             "K and V pools share a dtype and a shape")
-    _require(k_pool.is_cuda and v_pool.is_cuda, "pools live on the GPU")
-    _require(k_pool.is_contiguous() and v_pool.is_contiguous(), "pools are contiguous")
-    if k_pool.dtype == torch.uint8:
-        _require(k_pool.dim() == 3 and k_pool.shape[2] % FP8_BLOCK_SIZE == 0,
+    dt, shape = k_pool.dtype, k_pool.shape
+    if not (dt is v_pool.dtype and shape == v_pool.shape and k_pool.is_cuda and
+            v_pool.get_device() == k_pool.get_device() and k_pool.is_contiguous() and
+            v_pool.is_contiguous()):
+        _require(dt is v_pool.dtype and shape == v_pool.shape, "K and V pools share a dtype and a shape")
+        _require(k_pool.is_cuda and v_pool.is_cuda, "pools live on the GPU")
+        _require(v_pool.device == k_pool.device, "K and V pools live on one GPU")
+        raise ValueError("pools are contiguous")
+    if dt is torch.uint8:
+        _require(len(shape) == 3 and shape[2] % FP8_BLOCK_SIZE == 0,
                  "FP8 pools are [num_blocks, num_kv_heads, 16 * head_dim] uint8")
         _require(k_scale is not None and v_scale is not None, "FP8 pools need k_scale and v_scale")
-        nb, hkv, n = k_pool.shape
+        nb, hkv, n = shape
         return _Pool(k_pool.data_ptr(), v_pool.data_ptr(), nb, FP8_BLOCK_SIZE, hkv,
-                     n // FP8_BLOCK_SIZE, PKV_FP8_E4M3, float(k_scale), float(v_scale))
-    _require(k_pool.dim() == 4, "pools are [num_blocks, num_kv_heads, block_size, head_dim]")
-    nb, hkv, bs, d = k_pool.shape
-    return _Pool(k_pool.data_ptr(), v_pool.data_ptr(), nb, bs, hkv, d, _dtype_code(k_pool.dtype),
-                 0.0, 0.0)
+                     n // FP8_BLOCK_SIZE, PKV_FP8_E4M3, k_scale, v_scale)
+    _require(len(shape) == 4, "pools are [num_blocks, num_kv_heads, block_size, head_dim]")
+    nb, hkv, bs, d = shape
+    return _Pool(k_pool.data_ptr(), v_pool.data_ptr(), nb, bs, hkv, d,
+                 PKV_BF16 if dt is torch.bfloat16 else _dtype_code(dt), 0.0, 0.0)
 
 
 def _on_device(t: Optional[torch.Tensor], name: str, device) -> None:
@@ -431,12 +443,36 @@ def make_rope(inv_freq, axis_of_pair=None, num_axes: Optional[int] = None, inter
     return RopeDesc(c)
 
 
-def _token_stride(t: torch.Tensor, rows: int, dim: int, name: str) -> int:
-    """Elements between a [T, rows, dim] operand's tokens; each token's rows are contiguous."""
-    s = t.stride()
-    if not ((s[2] == 1 or dim == 1) and (s[1] == dim or rows == 1)):
-        raise ValueError(f"{name}: each token's [heads, head_dim] rows are contiguous")
-    return s[0] if t.shape[0] > 1 else rows * dim
+def _token_stride(t: torch.Tensor, rows: int, dim: int) -> int:
+    """Elements between a [T, rows, dim] operand's tokens, -1 when a token's rows are not contiguous."""
+    a, b, c = t.stride()
+    if (c != 1 and dim != 1) or (b != dim and rows != 1):
+        return -1
+    return a if t.shape[0] > 1 else rows * dim
+
+
+def _rope_refuse(pool, dev, act, slot_mapping, q, k_new, v_new, positions, rope, q_out, status):
+    """The messages of paged_kv_append_rope's checks."""
+    hkv, D = pool.num_kv_heads, pool.head_dim
+    _i32_dev(slot_mapping, "slot_mapping", dev)
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    for t, name in ((k_new, "k_new"), (v_new, "v_new"), (q, "q"), (q_out, "q_out")):
+        if t is None:
+            continue
+        _on_device(t, name, dev)
+        _require(t.dtype == act, f"{name} matches the pool dtype (bf16 for FP8)")
+        _require(t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and
+                 (name[0] == "q" or t.shape[1] == hkv),
+                 f"{name} is [T, heads, head_dim], one slot per token")
+        _require(_token_stride(t, t.shape[1], D) >= 0 or t.numel() == 0,
+                 f"{name}: each token's [heads, head_dim] rows are contiguous")
+    _require(q is not None or q_out is None, "q_out without q")
+    _require(q_out is None or q_out.shape == q.shape, "q_out matches q")
+    _require(positions.dtype == torch.int32 and positions.device == dev and
+             (positions.shape == (rope.num_axes, T) or (rope.num_axes == 1 and positions.shape == (T,))) and
+             (positions.stride(-1) == 1 or T <= 1),
+             "positions are int32 [num_axes, T] (or [T]) on the pools' GPU, each axis contiguous")
+    _status_ok(status, dev)
 
 
 def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mapping: torch.Tensor,
@@ -450,44 +486,48 @@ def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mappin
     ``slot_mapping`` [T]; returns the rotated q (``q_out``, which may be ``q``).
     Token rows may be cut from a wider projection output.  ``q`` None: k alone."""
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    hkv, D = pool.num_kv_heads, pool.head_dim
-    act = _act_dtype(k_pool.dtype)
-    _i32_dev(slot_mapping, "slot_mapping", dev)
-    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
-    _require(k_new.shape == (T, hkv, D) and v_new.shape == (T, hkv, D),
-             "k_new/v_new are [T, num_kv_heads, head_dim], one slot per token")
-    _require(k_new.dtype == act and v_new.dtype == act, "new rows match the pool dtype (bf16 for FP8)")
-    _on_device(k_new, "k_new", dev)
-    _on_device(v_new, "v_new", dev)
-    _require(positions.dtype == torch.int32 and positions.device == dev and
-             (positions.shape == (rope.num_axes, T) or (rope.num_axes == 1 and positions.shape == (T,))) and
-             (positions.stride(-1) == 1 or T <= 1),
-             "positions are int32 [num_axes, T] (or [T]) on the pools' GPU, each axis contiguous")
-    # one axis has no stride to speak of
-    pos_stride = positions.stride(0) if rope.num_axes > 1 else T
-    _status_ok(status, dev)
-    hq = qs = os_ = 0
-    if q is not None:
-        _require(q.dim() == 3 and q.shape[0] == T and q.shape[2] == D and q.dtype == act,
-                 "q is [T, num_q_heads, head_dim], pool dtype (bf16 for FP8)")
-        _on_device(q, "q", dev)
-        hq = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=act, device=dev)
+    gpu, pdt = k_pool.get_device(), k_pool.dtype
+    act = torch.float32 if pdt is torch.float32 else torch.bfloat16
+    hkv, D, T, axes, i32 = pool.num_kv_heads, pool.head_dim, slot_mapping.numel(), rope._c.num_axes, torch.int32
+    kshape, pshape = k_new.shape, positions.shape
+    ok = (slot_mapping.dtype is i32 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous() and
+          slot_mapping.get_device() == gpu and kshape == (T, hkv, D) and v_new.shape == kshape and
+          k_new.dtype is act and v_new.dtype is act and k_new.get_device() == gpu and
+          v_new.get_device() == gpu and positions.dtype is i32 and positions.get_device() == gpu and
+          (pshape == (axes, T) or (axes == 1 and pshape == (T,))) and
+          (positions.stride(-1) == 1 or T <= 1) and
+          (status is None or (status.get_device() == gpu and status.dtype is i32 and status.numel() >= 1)))
+    ks = vs = qs = os_ = 0
+    hq, qp, op = 0, None, None
+    if ok:
+        ks, vs = _token_stride(k_new, hkv, D), _token_stride(v_new, hkv, D)
+        if q is None:
+            ok = q_out is None
         else:
-            _require(q_out.shape == q.shape and q_out.dtype == act, "q_out matches q")
-            _on_device(q_out, "q_out", dev)
-        if hq:
-            qs, os_ = _token_stride(q, hq, D, "q"), _token_stride(q_out, hq, D, "q_out")
+            qshape = q.shape
+            ok = len(qshape) == 3 and qshape[0] == T and qshape[2] == D and q.dtype is act and \
+                q.get_device() == gpu and \
+                (q_out is None or (q_out.shape == qshape and q_out.dtype is act and q_out.get_device() == gpu))
+            if ok:
+                if q_out is None:
+                    q_out = torch.empty(qshape, dtype=act, device=q.device)
+                hq, qp, op = qshape[1], q.data_ptr(), q_out.data_ptr()
+                if hq:
+                    qs, os_ = _token_stride(q, hq, D), _token_stride(q_out, hq, D)
+        ok = ok and (T == 0 or (ks >= 0 and vs >= 0 and qs >= 0 and os_ >= 0))
+    if not ok:
+        _rope_refuse(pool, k_pool.device, act, slot_mapping, q, k_new, v_new, positions, rope, q_out, status)
+        raise ValueError("paged_kv_append_rope: invalid arguments")
+    args = (ctypes.byref(pool), slot_mapping.data_ptr(), T, qp, qs, hq, k_new.data_ptr(), ks,
+            v_new.data_ptr(), vs, positions.data_ptr(), positions.stride(0) if axes > 1 else T,
+            ctypes.byref(rope._c), op, os_, None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = _lib.paged_kv_append_rope(*args)
     else:
-        _require(q_out is None, "q_out without q")
-    with _on(dev):
-        _check("paged_kv_append_rope", _lib.paged_kv_append_rope(
-            ctypes.byref(pool), slot_mapping.data_ptr(), T, _ptr(q), qs, hq,
-            k_new.data_ptr(), _token_stride(k_new, hkv, D, "k_new"), v_new.data_ptr(),
-            _token_stride(v_new, hkv, D, "v_new"), positions.data_ptr(), pos_stride,
-            ctypes.byref(rope._c), _ptr(q_out), os_, _ptr(status), _stream(dev)))
+        with torch.cuda.device(gpu):
+            code = _lib.paged_kv_append_rope(*args)
+    if code != PKV_OK:
+        raise PkvError("paged_kv_append_rope", code)
     return q_out
 
 
@@ -498,7 +538,8 @@ class PoolSet:
     def __init__(self, pools):
         self.pools = [(k, v) for k, v in pools]
         _require(len(self.pools) > 0, "at least one pool")
-        self.device = self.pools[0][0].device
+        self.device, self.n = self.pools[0][0].device, len(self.pools)
+        self.gpu = self.pools[0][0].get_device()
         # page copies move bytes: FP8 scales play no part
         self._c = (_Pool * len(self.pools))(*[_pool(k, v, 1.0, 1.0) for k, v in self.pools])
         f = self._c[0]
@@ -509,7 +550,7 @@ class PoolSet:
                      "the pools share dtype, block size, kv heads and head_dim")
 
     def __len__(self) -> int:
-        return len(self.pools)
+        return self.n
 
 
 def paged_copy_blocks(pools: PoolSet, src_blocks: torch.Tensor, dst_blocks: torch.Tensor,
@@ -519,20 +560,28 @@ def paged_copy_blocks(pools: PoolSet, src_blocks: torch.Tensor, dst_blocks: torc
     [n]) of the same pool, or of ``dst_pools``'; negative ids are skipped.  Within
     a call no page may be written twice, nor written and read
     (``check_block_copies``)."""
-    dev = pools.device
-    _i32_dev(src_blocks, "src_blocks", dev)
-    _i32_dev(dst_blocks, "dst_blocks", dev)
-    _require(src_blocks.dim() == 1 and src_blocks.shape == dst_blocks.shape,
-             "one destination page per source page")
-    if dst_pools is not None:
-        _require(dst_pools.device == dev and len(dst_pools) == len(pools),
-                 "as many destination pools as source pools, on one GPU")
-    _status_ok(status, dev)
-    with _on(dev):
-        _check("paged_copy_blocks", _lib.paged_copy_blocks(
-            pools._c, dst_pools._c if dst_pools is not None else None, len(pools),
-            src_blocks.data_ptr(), dst_blocks.data_ptr(), src_blocks.shape[0], _ptr(status),
-            _stream(dev)))
+    gpu, n, i32 = pools.gpu, src_blocks.numel(), torch.int32
+    if not (src_blocks.dtype is i32 and dst_blocks.dtype is i32 and src_blocks.dim() == 1 and
+            dst_blocks.shape == src_blocks.shape and src_blocks.get_device() == gpu and
+            dst_blocks.get_device() == gpu and src_blocks.is_contiguous() and dst_blocks.is_contiguous() and
+            (dst_pools is None or (dst_pools.gpu == gpu and dst_pools.n == pools.n)) and
+            (status is None or (status.get_device() == gpu and status.dtype is i32 and status.numel() >= 1))):
+        dev = pools.device
+        _i32_dev(src_blocks, "src_blocks", dev)
+        _i32_dev(dst_blocks, "dst_blocks", dev)
+        _require(src_blocks.dim() == 1 and src_blocks.shape == dst_blocks.shape,
+                 "one destination page per source page")
+        _status_ok(status, dev)
+        raise ValueError("as many destination pools as source pools, on one GPU")
+    args = (pools._c, None if dst_pools is None else dst_pools._c, pools.n, src_blocks.data_ptr(),
+            dst_blocks.data_ptr(), n, None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = _lib.paged_copy_blocks(*args)
+    else:
+        with torch.cuda.device(gpu):
+            code = _lib.paged_copy_blocks(*args)
+    if code != PKV_OK:
+        raise PkvError("paged_copy_blocks", code)
 
 
 def check_block_copies(src_blocks, dst_blocks, num_blocks: int,
@@ -590,46 +639,59 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
     (not together with ``prefix``).
     """
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
-    dev = k_pool.device
-    _require(q.dim() == 3 and q.shape[2] == pool.head_dim and q.dtype == _act_dtype(k_pool.dtype) and
-             q.is_contiguous() and q.device == dev, "q is [B, Hq, D], contiguous, pool dtype")
-    B, hq, D = q.shape
-    _i32_dev(block_tables, "block_tables", dev)
-    _i32_dev(seq_lens, "seq_lens", dev)
-    _require(block_tables.dim() == 2 and block_tables.shape[0] == B and seq_lens.shape == (B,),
-             "block_tables [B, max_blocks], seq_lens [B]")
-    width = block_tables.shape[1]
+    gpu, i32, qshape, tshape = k_pool.get_device(), torch.int32, q.shape, block_tables.shape
+    if not (len(qshape) == 3 and qshape[2] == pool.head_dim and q.is_contiguous() and
+            q.get_device() == gpu and q.dtype is (torch.float32 if pool.dtype == PKV_F32 else torch.bfloat16) and
+            block_tables.dtype is i32 and block_tables.is_contiguous() and
+            block_tables.get_device() == gpu and len(tshape) == 2 and tshape[0] == qshape[0] and
+            seq_lens.dtype is i32 and seq_lens.is_contiguous() and seq_lens.get_device() == gpu and
+            seq_lens.shape == qshape[:1] and
+            (out is None or (out.shape == qshape and out.dtype is q.dtype and out.is_contiguous() and
+                             out.get_device() == gpu)) and
+            (workspace is None or workspace.get_device() == gpu) and
+            (status is None or (status.get_device() == gpu and status.dtype is i32 and status.numel() >= 1))):
+        dev = k_pool.device
+        _require(q.dim() == 3 and q.shape[2] == pool.head_dim and q.dtype == _act_dtype(k_pool.dtype) and
+                 q.is_contiguous() and q.device == dev, "q is [B, Hq, D], contiguous, pool dtype")
+        _i32_dev(block_tables, "block_tables", dev)
+        _i32_dev(seq_lens, "seq_lens", dev)
+        _require(block_tables.dim() == 2 and block_tables.shape[0] == q.shape[0] and
+                 seq_lens.shape == q.shape[:1], "block_tables [B, max_blocks], seq_lens [B]")
+        _on_device(out, "out", dev)
+        _require(out is None or (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()),
+                 "out matches q")
+        _on_device(workspace, "workspace", dev)
+        _status_ok(status, dev)
+        raise ValueError("paged_decode_attention: invalid arguments")
+    B, hq, D = qshape
+    width = tshape[1]
     if max_seq_len is None:
         max_seq_len = width * pool.block_size
-    if out is None:
-        out = torch.empty_like(q)
-    _require(out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous(), "out matches q")
-    _on_device(out, "out", dev)
-    _on_device(workspace, "workspace", dev)
-    _status_ok(status, dev)
-    _prefix_ok(prefix, dev)
-    with _on(dev):  # the plan reads the SM count of the current device
+    if prefix is not None:
+        _prefix_ok(prefix, k_pool.device)
+        if sinks and (window or sinks < 0):
+            raise PkvError("paged_decode_attention (sinks with a shared prefix)",
+                           PKV_ERR_UNSUPPORTED if sinks > 0 else PKV_ERR_INVALID_ARG)
+    with _on(k_pool.device):  # the plan reads the SM count of the current device
+        if out is None:
+            out = torch.empty_like(q)
         if workspace is None:
             workspace = alloc_workspace(
                 decode_workspace_size(B, hq, pool.num_kv_heads, D, pool.block_size, max_seq_len, window,
-                                      prefix, sinks), dev)
-        if sinks:
-            if prefix is not None and (window or sinks < 0):
-                raise PkvError("paged_decode_attention (sinks with a shared prefix)",
-                               PKV_ERR_UNSUPPORTED if sinks > 0 else PKV_ERR_INVALID_ARG)
-            if prefix is None:
-                _check("paged_decode_attention_sinks", _lib.paged_decode_attention_sinks(
-                    q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width,
-                    seq_lens.data_ptr(), B, max_seq_len, window, sinks, scale, out.data_ptr(),
-                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(status),
-                    _stream(dev)))
-                return out
-        px = ctypes.byref(prefix._c()) if prefix is not None else None
-        _check("paged_decode_attention", _lib.paged_decode_attention(
-            q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width,
-            seq_lens.data_ptr(), B, max_seq_len, window, float(scale), out.data_ptr(),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), px, _ptr(status),
-            _stream(dev)))
+                                      prefix, sinks), k_pool.device)
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        st = None if status is None else status.data_ptr()
+        if sinks and prefix is None:
+            code = _lib.paged_decode_attention_sinks(
+                q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width, seq_lens.data_ptr(),
+                B, max_seq_len, window, sinks, scale, out.data_ptr(), ws, nbytes, st, _raw_stream(gpu))
+        else:
+            code = _lib.paged_decode_attention(
+                q.data_ptr(), hq, ctypes.byref(pool), block_tables.data_ptr(), width, seq_lens.data_ptr(),
+                B, max_seq_len, window, scale, out.data_ptr(), ws, nbytes,
+                ctypes.byref(prefix._c()) if prefix is not None else None, st, _raw_stream(gpu))
+    if code != PKV_OK:
+        raise PkvError("paged_decode_attention_sinks" if sinks else "paged_decode_attention", code)
     return out
 
 
