@@ -1100,6 +1100,7 @@ pkv_status paged_kv_append_rope(const pkv_pool *pool, const int32_t *slot_mappin
     p.num_slots = pool->num_blocks * pool->block_size;
     p.rotary_dim = rd;
     p.interleaved = rope->interleaved;
+    p.num_axes = rope->num_axes;
     p.factor = rope->factor;
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;

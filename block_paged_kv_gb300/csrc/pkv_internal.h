@@ -44,7 +44,7 @@ struct AppendParams {
 // Rotary append: strides in 16-byte vectors between tokens; the descriptor's
 // tables travel in the launch parameters.
 constexpr int kRopeMaxPairs = PKV_ROPE_MAX_PAIRS;
-constexpr int kRopeMaxTokens = 8;  // tokens of a CTA
+constexpr int kRopeMaxTokens = 16;  // tokens of a CTA
 struct RopeParams {
     const void *q, *k_new, *v_new;
     void *q_out, *k_pool, *v_pool;
@@ -53,7 +53,7 @@ struct RopeParams {
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, q_out_stride, pos_stride;
     int32_t num_tokens, hq, hkv, block_size, head_dim, num_slots;
-    int32_t rotary_dim, interleaved;
+    int32_t rotary_dim, interleaved, num_axes;
     int32_t tokens_per_cta, rows_per_cta;  // set by the launch
     float factor, k_scale, v_scale;
     uint64_t freq[kRopeMaxPairs];
