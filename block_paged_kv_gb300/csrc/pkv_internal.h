@@ -157,6 +157,8 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 void prof_begin(int kind, cudaStream_t stream);
 void prof_end(int kind, cudaStream_t stream);
 
+constexpr int kSkItemBytes = 64;  // one item's record of the persistent schedule
+
 struct PrefillParams {
     const void *q;
     void *out;
@@ -185,10 +187,11 @@ struct PrefillParams {
     // partial to one of its CTA's two slots
     int32_t sk_ctas, sk_items;
     int32_t *sk_prefix;  // [sk_items + 1]: tiles of items 0 .. u-1 (written by the plan kernel)
+    void *sk_rec;        // [sk_items] records of kSkItemBytes (written by the plan kernel)
     int32_t *sk_count;   // [sk_ctas][2 query tiles][4 warps]: pieces done of the item cut
                          // after the CTA's first tile (zeroed by the plan kernel)
-    float *sk_o;         // [sk_ctas][2][256 rows][128] unnormalised weighted values
-    float *sk_ml;        // [sk_ctas][2][256 rows][2]: reference max (log2 units), weight sum
+    float *sk_o;         // [sk_ctas][2][2 query tiles][4 warps][32 dim groups][32 rows][4] unnormalised weighted values
+    float *sk_ml;        // [sk_ctas][2][2 query tiles][4 warps][32 rows][2]: reference max (log2 units), weight sum
     float scale_log2;  // scale * log2(e) (* k_scale for FP8 pools)
     float v_scale;     // FP8 pools: applied to the weighted values
     uint64_t wait_ns;  // limit of the pipeline's data waits (kWaitLimitNs unless a drill)

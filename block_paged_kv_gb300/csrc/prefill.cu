@@ -181,6 +181,7 @@ struct Seg {
     int32_t ntile;  // tiles of the segment
     bool whole;     // the item's whole key range
     int32_t slot;   // persistent schedule: partial slot of a cut segment
+    int32_t lo, hi; // persistent schedule: the item's tiles in the sequence
 };
 
 struct SegWalk {
@@ -220,27 +221,47 @@ __device__ __forceinline__ int32_t sk_cta_of(const PrefillParams &p, int32_t pos
     return c;
 }
 
+// An item of the persistent schedule as the plan kernel recorded it (one read
+// in place of the row's lengths, the prefix sums and the search for the next
+// item with tiles, one after another).
+struct alignas(16) SkItem {
+    PrefillRowInfo w;
+    int32_t lo, hi;  // its tiles in the sequence
+    int32_t next;    // the next item with tiles
+    int32_t pad[2];
+};
+static_assert(sizeof(SkItem) == kSkItemBytes, "the workspace holds one per item");
+
+__device__ __forceinline__ SkItem sk_load(const PrefillParams &p, int32_t u)
+{
+    union {
+        SkItem it;
+        int4 v[sizeof(SkItem) / 16];
+    } r;
+    const int4 *src = reinterpret_cast<const int4 *>(p.sk_rec) + static_cast<int64_t>(u) * (sizeof(SkItem) / 16);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(SkItem) / 16); ++i) r.v[i] = __ldg(src + i);
+    return r.it;
+}
+
 // Next segment of a persistent CTA's run (false at its end).
 template <bool kSink>
 __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk &sw, Seg &sg)
 {
     if (sw.pos >= sw.end) return false;
-    const int32_t u = sw.u;
-    const int32_t lo = __ldg(p.sk_prefix + u), hi = __ldg(p.sk_prefix + u + 1);
-    const int32_t seg_end = min(hi, sw.end);
-    prefill_item(p, u, qpc, sg.w);  // an item with tiles has queries
-    sg.item = u;
-    sg.jt0 = item_first_tile<kSink>(sg.w) + (sw.pos - lo);
+    const SkItem it = sk_load(p, sw.u);
+    const int32_t seg_end = min(it.hi, sw.end);
+    sg.w = it.w;
+    sg.item = sw.u;
+    sg.jt0 = item_first_tile<kSink>(sg.w) + (sw.pos - it.lo);
     sg.ntile = seg_end - sw.pos;
-    sg.whole = sw.pos == lo && seg_end == hi;
+    sg.whole = sw.pos == it.lo && seg_end == it.hi;
     sg.slot = sw.k == 0 ? 0 : 1;
+    sg.lo = it.lo;
+    sg.hi = it.hi;
     ++sw.k;
     sw.pos = seg_end;
-    if (seg_end == hi) {
-        int32_t v = u + 1;  // skip items without tiles (no queries)
-        while (v < p.sk_items && __ldg(p.sk_prefix + v + 1) == __ldg(p.sk_prefix + v)) ++v;
-        sw.u = v;
-    }
+    if (seg_end == it.hi) sw.u = it.next;
     return true;
 }
 
@@ -256,14 +277,16 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
         sw.end = sk_run_start(p, c + 1);
         sw.k = 0;
         sw.u = sw.pos < sw.end ? sk_item_of(p, sw.pos) : 0;
-        const int32_t lo = __ldg(p.sk_prefix + c), hi = __ldg(p.sk_prefix + c + 1);
-        if (hi > lo) {  // item c, whole
-            prefill_item(p, c, qpc, sg.w);  // an item with tiles has queries
+        const SkItem it = sk_load(p, c);
+        if (it.hi > it.lo) {  // item c, whole
+            sg.w = it.w;
             sg.item = c;
             sg.jt0 = item_first_tile<kSink>(sg.w);
-            sg.ntile = hi - lo;
+            sg.ntile = it.hi - it.lo;
             sg.whole = true;
             sg.slot = 0;
+            sg.lo = it.lo;
+            sg.hi = it.hi;
             return true;
         }
         return sk_next<kSink>(p, qpc, sw, sg);
@@ -274,6 +297,7 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
     sg.ntile = item_tiles(sg.w);
     sg.whole = p.kv_splits <= 1;
     sg.slot = 0;
+    sg.lo = sg.hi = 0;
     if (!sg.whole) {
         const int32_t tb = sg.w.s * p.split_tiles;
         sg.ntile = min(sg.ntile, tb + p.split_tiles) - tb;
@@ -315,40 +339,45 @@ struct TileCursor {
     __device__ __forceinline__ int32_t kt() const { return key_tile<kSink>(sg.w, sg.jt0 + j); }  // absolute key tile
 };
 
-// One row of a query tile into shared memory (softmax thread ii = 0 .. 255:
-// tile ii / 128, row i = ii % 128 = (query x*qpt + i/G, head i%G)), 128-byte
-// swizzled for the tensor cores.  FP8 pools take f16 products (bf16 -> f16 is
-// exact inside the f16 range; a magnitude past 65504 sets PKV_DEV_Q_RANGE); a
-// negative scale is staged as -q (`flip` toggles the sign bits), so that the
-// scores the tensor cores produce always take a positive factor.  Not inlined:
-// a segment's staging then leaves the registers of the softmax loop around
-// it alone.
+// A softmax warp's 32 rows of a query tile into shared memory (warp wi = 0 .. 7:
+// tile wi / 4, rows 32 (wi % 4) ..; row i = (query x*qpt + i/G, head i%G)),
+// 128-byte swizzled for the tensor cores.  Sixteen lanes take one row's 256
+// bytes, so that a load instruction covers two whole rows.  FP8 pools take f16
+// products (bf16 -> f16 is exact inside the f16 range; a magnitude past 65504
+// sets PKV_DEV_Q_RANGE); a negative scale is staged as -q (`flip` toggles the
+// sign bits), so that the scores the tensor cores produce always take a
+// positive factor.  Not inlined: a segment's staging then leaves the registers
+// of the softmax loop around it alone.
 template <bool kF8>
-__device__ __noinline__ void stage_q_row(const uint4 *q, const int32_t *cu_q_lens, int32_t hq, int G,
-                                         int qpt, int32_t r, int32_t i0, int32_t nq, int32_t g,
-                                         uint32_t flip, int32_t *status, uint8_t *q_s, int ii)
+__device__ __noinline__ void stage_q_rows(const uint4 *q, const int32_t *cu_q_lens, int32_t hq, int glog,
+                                          int qpt, int32_t r, int32_t i0, int32_t nq, int32_t g,
+                                          uint32_t flip, int32_t *status, uint8_t *q_s, int wi, int lane)
 {
     constexpr int kD = pf::kD, kRows = pf::kRows;
-    const int x = ii / kRows, i = ii % kRows;
-    const int t = x * qpt + i / G, h = i % G;
-    const bool valid = i < qpt * G && t < nq;
-    const uint4 *src = q + ((static_cast<int64_t>(__ldg(cu_q_lens + r)) + i0 + t) * hq + g * G + h) * (kD / 8);
-    uint8_t *qt_s = q_s + x * pf::kQBytes;
+    const int x = wi >> 2, c = lane & 15, first = 32 * (wi & 3) + (lane >> 4);
+    const uint4 *src = q + ((static_cast<int64_t>(__ldg(cu_q_lens + r)) + i0) * hq + (g << glog)) * (kD / 8) + c;
+    uint8_t *qt_s = q_s + x * pf::kQBytes + (c >> 3) * (kRows * 128);
+    uint4 v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        const int i = first + 2 * k, t = x * qpt + (i >> glog), h = i & ((1 << glog) - 1);
+        v[k] = t < nq ? __ldg(src + (static_cast<int64_t>(t) * hq + h) * (kD / 8)) : make_uint4(0, 0, 0, 0);
+    }
     bool qbad = false;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 16; ++k) {
+        const int i = first + 2 * k;
         if constexpr (kF8) {
-            v.x = bf16x2_to_f16x2(v.x, qbad);
-            v.y = bf16x2_to_f16x2(v.y, qbad);
-            v.z = bf16x2_to_f16x2(v.z, qbad);
-            v.w = bf16x2_to_f16x2(v.w, qbad);
+            v[k].x = bf16x2_to_f16x2(v[k].x, qbad);
+            v[k].y = bf16x2_to_f16x2(v[k].y, qbad);
+            v[k].z = bf16x2_to_f16x2(v[k].z, qbad);
+            v[k].w = bf16x2_to_f16x2(v[k].w, qbad);
         }
-        v.x ^= flip;
-        v.y ^= flip;
-        v.z ^= flip;
-        v.w ^= flip;
-        *reinterpret_cast<uint4 *>(qt_s + (c >> 3) * (kRows * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v;
+        v[k].x ^= flip;
+        v[k].y ^= flip;
+        v[k].z ^= flip;
+        v[k].w ^= flip;
+        *reinterpret_cast<uint4 *>(qt_s + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = v[k];
     }
     if (qbad) report(status, PKV_DEV_Q_RANGE);
     fence_proxy_async_smem();  // read by the tensor cores (async proxy)
@@ -448,16 +477,17 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
 
     // query tiles: tile x row i = (query t = x * qpt + i / G, head h = i % G);
-    // the 256 softmax threads load one row each (the first segment's here,
+    // the 8 softmax warps load 32 rows each (the first segment's here,
     // the next segments' after each epilogue)
     // a negative scale: stage -q (sign bits flipped, exact), so that the
     // scores the tensor cores produce always take a positive factor
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-    auto load_q_row = [&](const PrefillRowInfo &w) {
-        stage_q_row<kF8>(static_cast<const uint4 *>(p.q), p.cu_q_lens, p.hq, G, qpt, w.r, w.i0, w.nq,
-                         w.g, flip, p.status, q_s, threadIdx.x - 128);
+    const int glog = __ffs(G) - 1;  // G divides the tile's 128 rows
+    auto load_q_rows = [&](const PrefillRowInfo &w) {
+        stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.cu_q_lens, p.hq, glog, qpt, w.r, w.i0, w.nq,
+                          w.g, flip, p.status, q_s, warp - 4, lane);
     };
-    if (warp >= 4) load_q_row(seg0.w);
+    if (warp >= 4) load_q_rows(seg0.w);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -792,7 +822,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int32_t kv_lo = ss->sg.w.kv_lo, kv_hi = ss->sg.w.kv_hi;
         // the segment's query tile: staged (the first in the prologue), then
         // handed to the MMA-issue warp
-        if (k > 0) load_q_row(ss->sg.w);
+        if (k > 0) load_q_rows(ss->sg.w);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
         const bool valid_row = row < qpt * G && t < ss->sg.w.nq;
@@ -1060,31 +1090,34 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 break;
             } else if (p.sk_ctas > 0 && !ss->sg.whole) {
                 // a piece of an item cut by this CTA's run: a partial in the
-                // CTA's slot (first or last segment), merged afterwards
+                // CTA's slot (first or last segment), merged afterwards.  Each
+                // warp's 32 rows lie dim-group major (float4 d4 of row `lane`
+                // at d4 * 32 + lane), so that every access below is 512
+                // consecutive bytes a warp (with rows contiguous a merge of two
+                // or three pieces took 20 us)
                 tc::fence_after();
-                const size_t pr = (static_cast<size_t>(blockIdx.x) * 2 + ss->sg.slot) * (kQTiles * kRows) +
-                                  x * kRows + row;
-                float4 *dst = reinterpret_cast<float4 *>(p.sk_o + pr * kD);
+                const auto piece_at = [&](int32_t c, int32_t slot) {
+                    return ((static_cast<size_t>(c) * 2 + slot) * kQTiles + x) * 4 + (warp & 3);
+                };
+                const size_t own = piece_at(blockIdx.x, ss->sg.slot);
+                float4 *dst = reinterpret_cast<float4 *>(p.sk_o) + own * (32 * kD / 4) + lane;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r32[32];
                     tc::ld32(ox + c * 32, r32);
                     tc::wait_ld();
-                    if (valid_row) {
-                        const float vs = kF8 ? p.v_scale : 1.f;
+                    const float vs = kF8 ? p.v_scale : 1.f;
 #pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            dst[c * 8 + v] = make_float4(__uint_as_float(r32[4 * v]) * vs, __uint_as_float(r32[4 * v + 1]) * vs,
-                                                         __uint_as_float(r32[4 * v + 2]) * vs, __uint_as_float(r32[4 * v + 3]) * vs);
-                    }
+                    for (int v = 0; v < 8; ++v)
+                        dst[(c * 8 + v) * 32] = make_float4(__uint_as_float(r32[4 * v]) * vs, __uint_as_float(r32[4 * v + 1]) * vs,
+                                                            __uint_as_float(r32[4 * v + 2]) * vs, __uint_as_float(r32[4 * v + 3]) * vs);
                 }
-                if (valid_row) *reinterpret_cast<float2 *>(p.sk_ml + pr * 2) = make_float2(m_ref, l);
+                reinterpret_cast<float2 *>(p.sk_ml)[own * 32 + lane] = make_float2(m_ref, l);
                 // the item's pieces: CTAs cf .. cl; per (query tile, warp) the
                 // warp whose piece completes last merges their 32 rows (no
                 // waiting: the others published theirs before counting)
                 __syncwarp();
-                const int32_t u = ss->sg.item;
-                const int32_t lo = __ldg(p.sk_prefix + u), hi = __ldg(p.sk_prefix + u + 1);
+                const int32_t lo = ss->sg.lo, hi = ss->sg.hi;
                 const int32_t cf = sk_cta_of(p, lo), cl = sk_cta_of(p, hi - 1);
                 int last = 0;
                 if (lane == 0) {
@@ -1094,53 +1127,65 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     if (last) __threadfence();
                 }
                 last = __shfl_sync(0xffffffffu, last, 0);
-                if (last && valid_row) {
-                    auto piece = [&](int32_t c) {  // slot 1: the item is not c's first segment
-                        const int32_t slot = (c == cf && sk_run_start(p, c) < lo) ? 1 : 0;
-                        return (static_cast<size_t>(c) * 2 + slot) * (kQTiles * kRows) + x * kRows + row;
-                    };
+                if (last) {
+                    // slot 1: the item is not c's first segment
+                    const int32_t slot_f = sk_run_start(p, cf) < lo ? 1 : 0;
+                    const auto piece = [&](int32_t c) { return piece_at(c, c == cf ? slot_f : 0); };
+                    const float2 *ml = reinterpret_cast<const float2 *>(p.sk_ml) + lane;
+                    const float4 *po = reinterpret_cast<const float4 *>(p.sk_o) + lane;
                     float M = -INFINITY, lsum = 0.f;
-                    for (int32_t c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(p.sk_ml + piece(c) * 2));
-                    if (M != -INFINITY)
-                        for (int32_t c = cf; c <= cl; ++c) {
-                            const size_t pc = piece(c);
-                            const float mc = __ldcg(p.sk_ml + pc * 2);
-                            if (mc != -INFINITY) lsum = fmaf(fast_exp2(mc - M), __ldcg(p.sk_ml + pc * 2 + 1), lsum);
-                        }
+#pragma unroll 4
+                    for (int32_t c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(ml + piece(c) * 32).x);
+                    // a piece without weight (nothing seen) takes the factor 0
+                    const auto weight = [&](float m) { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
+#pragma unroll 4
+                    for (int32_t c = cf; c <= cl; ++c) {
+                        const float2 v = __ldcg(ml + piece(c) * 32);
+                        lsum = fmaf(weight(v.x), v.y, lsum);
+                    }
                     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out) +
                                  ((static_cast<int64_t>(__ldg(p.cu_q_lens + w.r)) + w.i0 + t) * p.hq +
                                   w.g * G + row % G) * (kD / 8);
-                    // 32 dims at a time
+                    // 32 dims at a time, two pieces' loads in flight
 #pragma unroll 1
                     for (int d0 = 0; d0 < kD; d0 += 32) {
                         float acc[32];
 #pragma unroll
                         for (int d = 0; d < 32; ++d) acc[d] = 0.f;
-                        if (M != -INFINITY)
-                            for (int32_t c = cf; c <= cl; ++c) {
-                                const size_t pc = piece(c);
-                                const float mc = __ldcg(p.sk_ml + pc * 2);
-                                if (mc == -INFINITY) continue;
-                                const float wgt = fast_exp2(mc - M);
-                                const float4 *src = reinterpret_cast<const float4 *>(p.sk_o + pc * kD + d0);
+#pragma unroll 1
+                        for (int32_t c = cf; c <= cl; c += 2) {
+                            const size_t p0 = piece(c), p1 = piece(min(c + 1, cl));
+                            float4 o0[8], o1[8];
+#pragma unroll
+                            for (int v = 0; v < 8; ++v) o0[v] = __ldcg(po + p0 * (32 * kD / 4) + (d0 / 4 + v) * 32);
+#pragma unroll
+                            for (int v = 0; v < 8; ++v) o1[v] = __ldcg(po + p1 * (32 * kD / 4) + (d0 / 4 + v) * 32);
+                            const float w0 = weight(__ldcg(ml + p0 * 32).x);
+                            const float w1 = c < cl ? weight(__ldcg(ml + p1 * 32).x) : 0.f;
+                            const auto add = [&](float wgt, const float4 (&o)[8]) {
+                                if (wgt == 0.f) return;  // (a piece that saw nothing)
 #pragma unroll
                                 for (int v = 0; v < 8; ++v) {
-                                    const float4 o4 = __ldcg(src + v);
-                                    acc[4 * v] = fmaf(wgt, o4.x, acc[4 * v]);
-                                    acc[4 * v + 1] = fmaf(wgt, o4.y, acc[4 * v + 1]);
-                                    acc[4 * v + 2] = fmaf(wgt, o4.z, acc[4 * v + 2]);
-                                    acc[4 * v + 3] = fmaf(wgt, o4.w, acc[4 * v + 3]);
+                                    acc[4 * v] = fmaf(wgt, o[v].x, acc[4 * v]);
+                                    acc[4 * v + 1] = fmaf(wgt, o[v].y, acc[4 * v + 1]);
+                                    acc[4 * v + 2] = fmaf(wgt, o[v].z, acc[4 * v + 2]);
+                                    acc[4 * v + 3] = fmaf(wgt, o[v].w, acc[4 * v + 3]);
                                 }
-                            }
+                            };
+                            add(w0, o0);
+                            add(w1, o1);
+                        }
+                        if (valid_row) {
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint4 o;
-                            o.x = pack_bf16x2(acc[8 * v + 0] * inv, acc[8 * v + 1] * inv);
-                            o.y = pack_bf16x2(acc[8 * v + 2] * inv, acc[8 * v + 3] * inv);
-                            o.z = pack_bf16x2(acc[8 * v + 4] * inv, acc[8 * v + 5] * inv);
-                            o.w = pack_bf16x2(acc[8 * v + 6] * inv, acc[8 * v + 7] * inv);
-                            dst[d0 / 8 + v] = o;
+                            for (int v = 0; v < 4; ++v) {
+                                uint4 o;
+                                o.x = pack_bf16x2(acc[8 * v + 0] * inv, acc[8 * v + 1] * inv);
+                                o.y = pack_bf16x2(acc[8 * v + 2] * inv, acc[8 * v + 3] * inv);
+                                o.z = pack_bf16x2(acc[8 * v + 4] * inv, acc[8 * v + 5] * inv);
+                                o.w = pack_bf16x2(acc[8 * v + 6] * inv, acc[8 * v + 7] * inv);
+                                dst[d0 / 8 + v] = o;
+                            }
                         }
                     }
                 }
@@ -1167,27 +1212,40 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             } else {
                 tc::fence_after();
                 const float inv = (l > 0.f ? 1.f / l : 0.f) * (kF8 ? p.v_scale : 1.f);
-                const int h = row % G;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out) +
-                             ((static_cast<int64_t>(__ldg(p.cu_q_lens + w.r)) + w.i0 + t) * p.hq +
-                              w.g * G + h) * (kD / 8);
+                // the warp's rows go through its part of the query tile, which
+                // every product of the segment has read: 16-byte chunks
+                // swizzled by the row, then whole rows to global memory
+                uint8_t *stage = q_s + x * kQBytes + 32 * (warp & 3) * 128;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r32[32];
                     tc::ld32(ox + c * 32, r32);
                     tc::wait_ld();
-                    if (valid_row) {
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            uint4 o;
-                            o.x = pack_bf16x2(__uint_as_float(r32[8 * v + 0]) * inv, __uint_as_float(r32[8 * v + 1]) * inv);
-                            o.y = pack_bf16x2(__uint_as_float(r32[8 * v + 2]) * inv, __uint_as_float(r32[8 * v + 3]) * inv);
-                            o.z = pack_bf16x2(__uint_as_float(r32[8 * v + 4]) * inv, __uint_as_float(r32[8 * v + 5]) * inv);
-                            o.w = pack_bf16x2(__uint_as_float(r32[8 * v + 6]) * inv, __uint_as_float(r32[8 * v + 7]) * inv);
-                            dst[c * 4 + v] = o;
-                        }
+                    for (int v = 0; v < 4; ++v) {
+                        uint4 o;
+                        o.x = pack_bf16x2(__uint_as_float(r32[8 * v + 0]) * inv, __uint_as_float(r32[8 * v + 1]) * inv);
+                        o.y = pack_bf16x2(__uint_as_float(r32[8 * v + 2]) * inv, __uint_as_float(r32[8 * v + 3]) * inv);
+                        o.z = pack_bf16x2(__uint_as_float(r32[8 * v + 4]) * inv, __uint_as_float(r32[8 * v + 5]) * inv);
+                        o.w = pack_bf16x2(__uint_as_float(r32[8 * v + 6]) * inv, __uint_as_float(r32[8 * v + 7]) * inv);
+                        const int ch = c * 4 + v;  // dims 8ch .. 8ch + 7
+                        *reinterpret_cast<uint4 *>(stage + (ch >> 3) * (kRows * 128) + lane * 128 +
+                                                   (((ch & 7) ^ (lane & 7)) << 4)) = o;
                     }
                 }
+                __syncwarp();
+                const int ch = lane & 15;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out) +
+                             ((static_cast<int64_t>(__ldg(p.cu_q_lens + w.r)) + w.i0) * p.hq + w.g * G) * (kD / 8) + ch;
+#pragma unroll 4
+                for (int k = 0; k < 16; ++k) {
+                    const int rr = 2 * k + (lane >> 4), i = 32 * (warp & 3) + rr;  // row of the warp, of the tile
+                    const int tq = x * qpt + (i >> glog), h = i & (G - 1);
+                    const uint4 o = *reinterpret_cast<const uint4 *>(stage + (ch >> 3) * (kRows * 128) + rr * 128 +
+                                                                     (((ch & 7) ^ (rr & 7)) << 4));
+                    if (tq < w.nq) dst[(static_cast<int64_t>(tq) * p.hq + h) * (kD / 8)] = o;
+                }
+                __syncwarp();  // the rows are read before the next query tile lands there
             }
         }
         // the next segment: its query tile replaces this one once every
@@ -1422,9 +1480,37 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         }
         __syncthreads();
         const int32_t incl = v + (warp > 0 ? warp_sum[warp - 1] : 0) + carry;
-        if (u < p.sk_items) p.sk_prefix[u + 1] = incl;
+        if (u < p.sk_items) {
+            p.sk_prefix[u + 1] = incl;
+            SkItem *it = reinterpret_cast<SkItem *>(p.sk_rec) + u;
+            if (n > 0) it->w = w;
+            it->lo = incl - n;
+            it->hi = incl;
+        }
         __syncthreads();
         if (threadIdx.x == kSkPlanThreads - 1) carry = incl;
+        __syncthreads();
+    }
+    // each item's next one with tiles, from the last run of threads to the first
+    __shared__ int32_t warp_first[kSkPlanThreads / 32], after;
+    if (threadIdx.x == 0) after = p.sk_items;
+    __syncthreads();
+    for (int32_t base = (p.sk_items - 1) / kSkPlanThreads * kSkPlanThreads; base >= 0; base -= kSkPlanThreads) {
+        const int32_t u = base + threadIdx.x;
+        SkItem *it = reinterpret_cast<SkItem *>(p.sk_rec) + u;  // this thread's own writes above
+        const uint32_t m = __ballot_sync(0xffffffffu, u < p.sk_items && it->hi > it->lo);
+        if (lane == 0) warp_first[warp] = m != 0 ? base + warp * 32 + __ffs(m) - 1 : -1;
+        __syncthreads();
+        const uint32_t rest = lane < 31 ? m >> (lane + 1) : 0u;
+        int32_t next = rest != 0 ? u + __ffs(rest) : -1;
+        for (int i = warp + 1; next < 0 && i < kSkPlanThreads / 32; ++i) next = warp_first[i];
+        if (next < 0) next = after;
+        if (u < p.sk_items) it->next = next;
+        int32_t first = -1;
+        if (threadIdx.x == 0)
+            for (int i = 0; first < 0 && i < kSkPlanThreads / 32; ++i) first = warp_first[i];
+        __syncthreads();
+        if (threadIdx.x == 0 && first >= 0) after = first;
         __syncthreads();
     }
 }
@@ -1490,6 +1576,7 @@ size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas)
 {
     if (ctas <= 0) return 0;
     const size_t pre = ((static_cast<size_t>(items + 1) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255)) +
+                       ((static_cast<size_t>(items) * kSkItemBytes + 255) & ~static_cast<size_t>(255)) +
                        ((static_cast<size_t>(ctas) * 8 * sizeof(int32_t) + 255) & ~static_cast<size_t>(255));
     const size_t rows = static_cast<size_t>(ctas) * 2 * pf::kQTiles * pf::kRows;
     const size_t o = (rows * pf::kD * sizeof(float) + 255) & ~static_cast<size_t>(255);
