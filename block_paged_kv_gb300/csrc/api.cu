@@ -944,8 +944,8 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
             p.sk_ctas = sk;
             p.sk_items = items;
             char *ws = static_cast<char *>(workspace);
-            p.sk_prefix = reinterpret_cast<int32_t *>(ws);
-            ws += (static_cast<size_t>(items + 1) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255);
+            p.sk_plan = reinterpret_cast<int32_t *>(ws);
+            ws += (static_cast<size_t>(sk) * 3 * sizeof(int32_t) + 4 + 255) & ~static_cast<size_t>(255);
             p.sk_rec = ws;
             ws += (static_cast<size_t>(items) * kSkItemBytes + 255) & ~static_cast<size_t>(255);
             p.sk_count = reinterpret_cast<int32_t *>(ws);

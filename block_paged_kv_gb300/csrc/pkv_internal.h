@@ -186,7 +186,8 @@ struct PrefillParams {
     // (row, kv head, query-tile pair); a run that cuts an item writes a
     // partial to one of its CTA's two slots
     int32_t sk_ctas, sk_items;
-    int32_t *sk_prefix;  // [sk_items + 1]: tiles of items 0 .. u-1 (written by the plan kernel)
+    int32_t *sk_plan;    // written by the plan kernel: starts of the CTAs' runs [sk_ctas + 1], the items
+                         // there [sk_ctas], the CTAs' whole items [sk_ctas]
     void *sk_rec;        // [sk_items] records of kSkItemBytes (written by the plan kernel)
     int32_t *sk_count;   // [sk_ctas][2 query tiles][4 warps]: pieces done of the item cut
                          // after the CTA's first tile (zeroed by the plan kernel)

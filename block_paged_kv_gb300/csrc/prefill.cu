@@ -163,16 +163,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 // its key range [kv_lo, kv_hi).
 //   one CTA per item (sk_ctas == 0): one segment, the item's whole range or,
 //     for the key-range runs of a short chunk, one run of it;
-//   persistent balanced schedule (sk_ctas = n > 0, fewer than the items):
-//     the items' tiles in item order form one sequence of W tiles
-//     (sk_prefix, written by prefill_sk_plan_kernel).  CTA c first runs item
-//     c whole (the CTAs of one (row, kv head) then start together and share
-//     its K/V through L2), then takes the tiles [B + c R / m, B + (c + 1) R
-//     / m) of the rest (B = the first n items' tiles, R = W - B, m = min(n, R):
-//     the CTAs from m on take none, so that no CTA between two pieces of an
-//     item is without one), item by item.  Only the first and the last segment of that run can cut an
-//     item; a cut segment writes a partial to slot 0 (first) or 1 (last) of
-//     the CTA, and the warp that completes an item's pieces merges them.
+//   persistent balanced schedule (sk_ctas = n > 0, fewer than the items),
+//     dealt by prefill_sk_plan_kernel: the items' tiles in item order form one
+//     sequence of W tiles.  CTA c first runs the c-th item with tiles whole
+//     (the CTAs of one (row, kv head) then start together and share its K/V
+//     through L2), then a run of consecutive tiles of the rest (R = W - B, B
+//     the tiles of the first n such items), item by item.  The runs level the
+//     CTAs: with w_c = max(0, level - the c-th item's tiles), CTA c's run
+//     starts at B + R (w_0 + .. + w_(c-1)) / (w_0 + .. + w_(n-1)).  Only the
+//     first and the last segment of a run can cut an item; a cut segment
+//     writes a partial to slot 0 (first) or 1 (last) of the CTA, and the warp
+//     that completes an item's pieces merges them.
 // ---------------------------------------------------------------------------
 struct Seg {
     PrefillRowInfo w;
@@ -181,7 +182,8 @@ struct Seg {
     int32_t ntile;  // tiles of the segment
     bool whole;     // the item's whole key range
     int32_t slot;   // persistent schedule: partial slot of a cut segment
-    int32_t lo, hi; // persistent schedule: the item's tiles in the sequence
+    int32_t lo, cf, cl;  // persistent schedule: the item's first tile in the sequence,
+                         // the first and the last CTA whose runs hold its tiles
 };
 
 struct SegWalk {
@@ -190,36 +192,11 @@ struct SegWalk {
     int32_t k;         // segments returned so far
 };
 
-// start of CTA c's balanced run (c = n: the end of the sequence)
-__device__ __forceinline__ int32_t sk_run_start(const PrefillParams &p, int32_t c)
-{
-    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), R = __ldg(p.sk_prefix + p.sk_items) - B;
-    const int32_t m = static_cast<int32_t>(min(static_cast<int64_t>(p.sk_ctas), R));
-    return static_cast<int32_t>(m > 0 ? B + min(c, m) * R / m : B);
-}
-
-// the item holding tile pos: the largest u with prefix[u] <= pos
-__device__ __forceinline__ int32_t sk_item_of(const PrefillParams &p, int32_t pos)
-{
-    int32_t lo = 0, hi = p.sk_items;
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (__ldg(p.sk_prefix + mid) <= pos) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
-// the CTA whose balanced run holds tile pos (pos past the first n items)
-__device__ __forceinline__ int32_t sk_cta_of(const PrefillParams &p, int32_t pos)
-{
-    const int64_t B = __ldg(p.sk_prefix + p.sk_ctas), R = __ldg(p.sk_prefix + p.sk_items) - B;
-    const int32_t m = static_cast<int32_t>(max(min(static_cast<int64_t>(p.sk_ctas), R), static_cast<int64_t>(1)));
-    int32_t c = R > 0 ? static_cast<int32_t>((pos - B) * m / R) : 0;
-    c = min(max(c, 0), m - 1);
-    while (c + 1 < m && sk_run_start(p, c + 1) <= pos) ++c;
-    while (c > 0 && sk_run_start(p, c) > pos) --c;
-    return c;
-}
+// the plan's arrays: start of CTA c's run (c = n: the end of the sequence), the
+// item that holds it, the item CTA c runs whole (-1: none)
+__device__ __forceinline__ int32_t sk_run_start(const PrefillParams &p, int32_t c) { return __ldg(p.sk_plan + c); }
+__device__ __forceinline__ int32_t sk_run_item(const PrefillParams &p, int32_t c) { return __ldg(p.sk_plan + p.sk_ctas + 1 + c); }
+__device__ __forceinline__ int32_t sk_whole_item(const PrefillParams &p, int32_t c) { return __ldg(p.sk_plan + 2 * p.sk_ctas + 1 + c); }
 
 // An item of the persistent schedule as the plan kernel recorded it (one read
 // in place of the row's lengths, the prefix sums and the search for the next
@@ -228,7 +205,7 @@ struct alignas(16) SkItem {
     PrefillRowInfo w;
     int32_t lo, hi;  // its tiles in the sequence
     int32_t next;    // the next item with tiles
-    int32_t pad[2];
+    int32_t cf, cl;  // first and last CTA whose runs hold its tiles
 };
 static_assert(sizeof(SkItem) == kSkItemBytes, "the workspace holds one per item");
 
@@ -258,7 +235,8 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
     sg.whole = sw.pos == it.lo && seg_end == it.hi;
     sg.slot = sw.k == 0 ? 0 : 1;
     sg.lo = it.lo;
-    sg.hi = it.hi;
+    sg.cf = it.cf;
+    sg.cl = it.cl;
     ++sw.k;
     sw.pos = seg_end;
     if (seg_end == it.hi) sw.u = it.next;
@@ -273,20 +251,21 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
 {
     if (p.sk_ctas > 0) {
         const int32_t c = static_cast<int32_t>(cta);
+        const int32_t whole = sk_whole_item(p, c);
         sw.pos = sk_run_start(p, c);
         sw.end = sk_run_start(p, c + 1);
         sw.k = 0;
-        sw.u = sw.pos < sw.end ? sk_item_of(p, sw.pos) : 0;
-        const SkItem it = sk_load(p, c);
-        if (it.hi > it.lo) {  // item c, whole
+        sw.u = sk_run_item(p, c);
+        if (whole >= 0) {
+            const SkItem it = sk_load(p, whole);
             sg.w = it.w;
-            sg.item = c;
+            sg.item = whole;
             sg.jt0 = item_first_tile<kSink>(sg.w);
             sg.ntile = it.hi - it.lo;
             sg.whole = true;
             sg.slot = 0;
             sg.lo = it.lo;
-            sg.hi = it.hi;
+            sg.cf = sg.cl = 0;
             return true;
         }
         return sk_next<kSink>(p, qpc, sw, sg);
@@ -297,7 +276,7 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
     sg.ntile = item_tiles(sg.w);
     sg.whole = p.kv_splits <= 1;
     sg.slot = 0;
-    sg.lo = sg.hi = 0;
+    sg.lo = sg.cf = sg.cl = 0;
     if (!sg.whole) {
         const int32_t tb = sg.w.s * p.split_tiles;
         sg.ntile = min(sg.ntile, tb + p.split_tiles) - tb;
@@ -793,7 +772,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         };
         // the CTA's tiles over all its segments
         const int32_t T_total =
-            p.sk_ctas > 0 ? __ldg(p.sk_prefix + blockIdx.x + 1) - __ldg(p.sk_prefix + blockIdx.x) +
+            p.sk_ctas > 0 ? (seg0.whole && sk_whole_item(p, blockIdx.x) >= 0 ? seg0.ntile : 0) +
                                 sk_run_start(p, blockIdx.x + 1) - sk_run_start(p, blockIdx.x)
                           : seg0.ntile;
         if constexpr (kF8) {
@@ -820,6 +799,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         for (int32_t k = 0; !abort; ++k) {
         const int32_t ntile = ss->sg.ntile, jt0 = ss->sg.jt0;
         const int32_t kv_lo = ss->sg.w.kv_lo, kv_hi = ss->sg.w.kv_hi;
+        const int32_t nst = ss->sg.w.nst, gap = ss->sg.w.gap;
         // the segment's query tile: staged (the first in the prologue), then
         // handed to the MMA-issue warp
         if (k > 0) load_q_rows(ss->sg.w);
@@ -833,7 +813,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         for (int32_t jj = 0; jj < ntile; ++jj) {
             const int32_t T = T0 + jj;
             const int ks = T % kStages, buf = T & 1;
-            const int32_t tbase = (kSink ? key_tile<true>(ss->sg.w, jt0 + jj) : jt0 + jj) * kKeys;
+            const int32_t tbase = (jt0 + jj + (kSink && jt0 + jj >= nst ? gap : 0)) * kKeys;
             const uint32_t sx = tS(x, buf) + lane_base;
             if constexpr (kF8) {
                 if (do_k && T + 2 < T_total && !widen_k(T + 2)) {
@@ -940,17 +920,21 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                                   (tbase >= qlo || (kSink && tbase + kKeys <= p.sinks)) &&
                                   tbase + kKeys - 1 <= qpos && valid_row;
                 if (!full) {
-                    const int32_t lo = qlo - tbase;
-                    const uint32_t span = static_cast<uint32_t>(qpos - qlo);  // qlo <= qpos
+                    // attended columns as bits: the window's from qlo to qpos, the
+                    // sinks' up to the query's own, both within loaded blocks
+                    const auto below = [](int32_t n) {  // bits 0 .. n-1
+                        return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+                    };
+                    uint64_t bits = below(qpos + 1 - tbase);
+                    bits &= kSink ? ~below(qlo - tbase) | below(p.sinks - tbase) : ~below(qlo - tbase);
                     const uint32_t bm = valid_row ? mask : 0u;
-                    // sink columns of the tile: e < sk (positions up to the query's own)
-                    const int32_t sk = kSink ? min(p.sinks, qpos + 1) - tbase : 0;
+                    uint64_t blocks = 0;
     #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const bool ok = (static_cast<uint32_t>(e - lo) <= span || (kSink && e < sk)) &&
-                                        ((bm >> (e >> 4)) & 1u);
-                        s[e] = ok ? s[e] : -INFINITY;
-                    }
+                    for (int b = 0; b < kBlocks; ++b) blocks |= ((bm >> b) & 1u) ? 0xFFFFull << (16 * b) : 0ull;
+                    bits &= blocks;
+                    const uint32_t b0 = static_cast<uint32_t>(bits), b1 = static_cast<uint32_t>(bits >> 32);
+    #pragma unroll
+                    for (int e = 0; e < 64; ++e) s[e] = (((e < 32 ? b0 : b1) >> (e & 31)) & 1u) ? s[e] : -INFINITY;
                 }
                 float mt;
                 {
@@ -1117,29 +1101,33 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // warp whose piece completes last merges their 32 rows (no
                 // waiting: the others published theirs before counting)
                 __syncwarp();
-                const int32_t lo = ss->sg.lo, hi = ss->sg.hi;
-                const int32_t cf = sk_cta_of(p, lo), cl = sk_cta_of(p, hi - 1);
+                const int32_t cf = ss->sg.cf, cl = ss->sg.cl;
+                // CTAs between them may have empty runs
+                const auto piece_from = [&](int32_t c) {
+                    while (c < cl && sk_run_start(p, c + 1) == sk_run_start(p, c)) ++c;
+                    return c;
+                };
                 int last = 0;
                 if (lane == 0) {
+                    int others = 0;
+                    for (int32_t c = cf; c < cl; ++c) others += sk_run_start(p, c + 1) > sk_run_start(p, c) ? 1 : 0;
                     __threadfence();
                     const int old = atomicAdd(p.sk_count + (cf * 2 + x) * 4 + (warp & 3), 1);
-                    last = old == cl - cf;
+                    last = old == others;
                     if (last) __threadfence();
                 }
                 last = __shfl_sync(0xffffffffu, last, 0);
                 if (last) {
                     // slot 1: the item is not c's first segment
-                    const int32_t slot_f = sk_run_start(p, cf) < lo ? 1 : 0;
+                    const int32_t slot_f = sk_run_start(p, cf) < ss->sg.lo ? 1 : 0;
                     const auto piece = [&](int32_t c) { return piece_at(c, c == cf ? slot_f : 0); };
                     const float2 *ml = reinterpret_cast<const float2 *>(p.sk_ml) + lane;
                     const float4 *po = reinterpret_cast<const float4 *>(p.sk_o) + lane;
                     float M = -INFINITY, lsum = 0.f;
-#pragma unroll 4
-                    for (int32_t c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(ml + piece(c) * 32).x);
+                    for (int32_t c = cf; c <= cl; c = piece_from(c + 1)) M = fmaxf(M, __ldcg(ml + piece(c) * 32).x);
                     // a piece without weight (nothing seen) takes the factor 0
                     const auto weight = [&](float m) { return m == -INFINITY ? 0.f : fast_exp2(m - M); };
-#pragma unroll 4
-                    for (int32_t c = cf; c <= cl; ++c) {
+                    for (int32_t c = cf; c <= cl; c = piece_from(c + 1)) {
                         const float2 v = __ldcg(ml + piece(c) * 32);
                         lsum = fmaf(weight(v.x), v.y, lsum);
                     }
@@ -1154,15 +1142,17 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
                         for (int d = 0; d < 32; ++d) acc[d] = 0.f;
 #pragma unroll 1
-                        for (int32_t c = cf; c <= cl; c += 2) {
-                            const size_t p0 = piece(c), p1 = piece(min(c + 1, cl));
+                        for (int32_t c = cf; c <= cl;) {
+                            const int32_t c1 = c < cl ? piece_from(c + 1) : c;  // (the last piece alone: loaded twice)
+                            const size_t p0 = piece(c), p1 = piece(c1);
                             float4 o0[8], o1[8];
 #pragma unroll
                             for (int v = 0; v < 8; ++v) o0[v] = __ldcg(po + p0 * (32 * kD / 4) + (d0 / 4 + v) * 32);
 #pragma unroll
                             for (int v = 0; v < 8; ++v) o1[v] = __ldcg(po + p1 * (32 * kD / 4) + (d0 / 4 + v) * 32);
                             const float w0 = weight(__ldcg(ml + p0 * 32).x);
-                            const float w1 = c < cl ? weight(__ldcg(ml + p1 * 32).x) : 0.f;
+                            const float w1 = c1 > c ? weight(__ldcg(ml + p1 * 32).x) : 0.f;
+                            c = c1 < cl ? piece_from(c1 + 1) : cl + 1;
                             const auto add = [&](float wgt, const float4 (&o)[8]) {
                                 if (wgt == 0.f) return;  // (a piece that saw nothing)
 #pragma unroll
@@ -1435,83 +1425,174 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
 }
 
 // ---------------------------------------------------------------------------
-// persistent balanced schedule: the plan (tile prefix sums of the items; the
-// cut items' arrival counters zeroed)
+// persistent balanced schedule: the plan (the items' records, the CTAs' whole
+// items and runs, the cut items' arrival counters zeroed), one CTA
 // ---------------------------------------------------------------------------
 constexpr int kSkPlanThreads = 1024;
+constexpr int kSkMaxCtas = 512;
 
 __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const PrefillParams p)
 {
-    __shared__ int32_t warp_sum[kSkPlanThreads / 32];
-    __shared__ int32_t carry;
+    constexpr int kWarps = kSkPlanThreads / 32;
+    __shared__ int32_t warp_sum[kWarps], warp_cnt[kWarps], warp_first[kWarps];
+    __shared__ int32_t carry, carry_cnt, after;
+    __shared__ int32_t whole[kSkMaxCtas], tiles[kSkMaxCtas], run[kSkMaxCtas + 1], run_item[kSkMaxCtas];
     pdl_wait();  // lengths may come from the previous kernel on the stream
     pdl_trigger();
     const int qpc = pf::kQTiles * (pf::kRows / p.group);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t ctas = p.sk_ctas;
+    SkItem *rec = reinterpret_cast<SkItem *>(p.sk_rec);
     if (threadIdx.x == 0) {
-        carry = 0;
-        p.sk_prefix[0] = 0;
+        carry = carry_cnt = 0;
+        after = p.sk_items;
     }
-    for (int32_t i = threadIdx.x; i < p.sk_ctas * 8; i += kSkPlanThreads) p.sk_count[i] = 0;
+    for (int32_t i = threadIdx.x; i < ctas; i += kSkPlanThreads) {
+        whole[i] = -1;
+        tiles[i] = 0;
+        run_item[i] = 0;
+    }
+    for (int32_t i = threadIdx.x; i < ctas * 8; i += kSkPlanThreads) p.sk_count[i] = 0;
     __syncthreads();
     for (int32_t base = 0; base < p.sk_items; base += kSkPlanThreads) {
         const int32_t u = base + threadIdx.x;
         int32_t n = 0;
         PrefillRowInfo w;
-        if (u < p.sk_items && prefill_item(p, u, qpc, w))
-            n = item_tiles(w);
-        // inclusive scan: within the warp, then over the warps' sums
+        if (u < p.sk_items && prefill_item(p, u, qpc, w)) n = item_tiles(w);
+        // inclusive scans of the tiles and of the items with tiles: within the
+        // warp, then over the warps' sums
+        const uint32_t has = __ballot_sync(0xffffffffu, n > 0);
         int32_t v = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
             if (lane >= d) v += o;
         }
-        if (lane == 31) warp_sum[warp] = v;
+        if (lane == 31) {
+            warp_sum[warp] = v;
+            warp_cnt[warp] = __popc(has);
+        }
         __syncthreads();
         if (warp == 0) {
-            int32_t ws = warp_sum[lane];
+            int32_t ws = warp_sum[lane], wc = warp_cnt[lane];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int32_t o = __shfl_up_sync(0xffffffffu, ws, d);
-                if (lane >= d) ws += o;
+                const int32_t o = __shfl_up_sync(0xffffffffu, ws, d), oc = __shfl_up_sync(0xffffffffu, wc, d);
+                if (lane >= d) {
+                    ws += o;
+                    wc += oc;
+                }
             }
             warp_sum[lane] = ws;  // inclusive over the warps
+            warp_cnt[lane] = wc;
         }
         __syncthreads();
         const int32_t incl = v + (warp > 0 ? warp_sum[warp - 1] : 0) + carry;
+        const int32_t rank = __popc(has & ((1u << lane) - 1u)) + (warp > 0 ? warp_cnt[warp - 1] : 0) + carry_cnt;
         if (u < p.sk_items) {
-            p.sk_prefix[u + 1] = incl;
-            SkItem *it = reinterpret_cast<SkItem *>(p.sk_rec) + u;
-            if (n > 0) it->w = w;
-            it->lo = incl - n;
-            it->hi = incl;
+            if (n > 0) rec[u].w = w;
+            rec[u].lo = incl - n;
+            rec[u].hi = incl;
+            if (n > 0 && rank < ctas) {
+                whole[rank] = u;
+                tiles[rank] = n;
+            }
         }
         __syncthreads();
-        if (threadIdx.x == kSkPlanThreads - 1) carry = incl;
+        if (threadIdx.x == kSkPlanThreads - 1) {
+            carry = incl;
+            carry_cnt += warp_cnt[kWarps - 1];
+        }
         __syncthreads();
     }
-    // each item's next one with tiles, from the last run of threads to the first
-    __shared__ int32_t warp_first[kSkPlanThreads / 32], after;
-    if (threadIdx.x == 0) after = p.sk_items;
+    // the runs: the least level at which the CTAs take the R tiles left
+    if (warp == 0) {
+        int32_t B = 0, most = 0;
+        for (int32_t c = lane; c < ctas; c += 32) {
+            B += tiles[c];
+            most = max(most, tiles[c]);
+        }
+        B = __reduce_add_sync(0xffffffffu, B);
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int64_t R = carry - B;
+        int64_t lo = 0, hi = most + (R + ctas - 1) / ctas;  // room(hi) >= R
+        const auto room = [&](int64_t level) {
+            int64_t sum = 0;
+            for (int32_t c = lane; c < ctas; c += 32) sum += max(static_cast<int64_t>(0), level - tiles[c]);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            return sum;
+        };
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (room(mid) >= R) hi = mid; else lo = mid + 1;
+        }
+        const int64_t total = room(lo);
+        int64_t before = 0;  // room of the CTAs before this group of 32
+        for (int32_t c0 = 0; c0 < ctas; c0 += 32) {
+            const int32_t c = c0 + lane;
+            int64_t v = c < ctas ? max(static_cast<int64_t>(0), lo - tiles[c]) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+                if (lane >= d) v += o;
+            }
+            if (c < ctas) run[c + 1] = static_cast<int32_t>(B + (total > 0 ? R * (before + v) / total : 0));
+            before += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) run[0] = B;
+    }
     __syncthreads();
+    // each item's next one with tiles, from the last run of threads to the
+    // first; the CTAs that hold its tiles; the item at each run's start
     for (int32_t base = (p.sk_items - 1) / kSkPlanThreads * kSkPlanThreads; base >= 0; base -= kSkPlanThreads) {
         const int32_t u = base + threadIdx.x;
-        SkItem *it = reinterpret_cast<SkItem *>(p.sk_rec) + u;  // this thread's own writes above
-        const uint32_t m = __ballot_sync(0xffffffffu, u < p.sk_items && it->hi > it->lo);
+        int32_t lo = 0, hi = 0;
+        if (u < p.sk_items) {  // this thread's own writes above
+            lo = rec[u].lo;
+            hi = rec[u].hi;
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, hi > lo);
         if (lane == 0) warp_first[warp] = m != 0 ? base + warp * 32 + __ffs(m) - 1 : -1;
         __syncthreads();
         const uint32_t rest = lane < 31 ? m >> (lane + 1) : 0u;
         int32_t next = rest != 0 ? u + __ffs(rest) : -1;
-        for (int i = warp + 1; next < 0 && i < kSkPlanThreads / 32; ++i) next = warp_first[i];
+        for (int i = warp + 1; next < 0 && i < kWarps; ++i) next = warp_first[i];
         if (next < 0) next = after;
-        if (u < p.sk_items) it->next = next;
+        if (u < p.sk_items) {
+            int32_t cf = 0, cl = 0;
+            if (hi > lo && hi > run[0]) {
+                const auto cta_of = [&](int32_t pos) {  // the last c with run[c] <= pos: its run holds pos
+                    int32_t a = 0, b = ctas;
+                    while (b - a > 1) {
+                        const int32_t mid = (a + b) >> 1;
+                        if (run[mid] <= pos) a = mid; else b = mid;
+                    }
+                    return a;
+                };
+                cf = cta_of(lo);
+                cl = cta_of(hi - 1);
+                // the runs that start inside this item
+                for (int32_t c = run[cf] >= lo ? cf : cf + 1; c <= cl; ++c) run_item[c] = u;
+                for (int32_t c = cf; c >= 0 && run[c] >= lo; --c) run_item[c] = u;
+            }
+            rec[u].next = next;
+            rec[u].cf = cf;
+            rec[u].cl = cl;
+        }
         int32_t first = -1;
         if (threadIdx.x == 0)
-            for (int i = 0; first < 0 && i < kSkPlanThreads / 32; ++i) first = warp_first[i];
+            for (int i = 0; first < 0 && i < kWarps; ++i) first = warp_first[i];
         __syncthreads();
         if (threadIdx.x == 0 && first >= 0) after = first;
         __syncthreads();
+    }
+    for (int32_t c = threadIdx.x; c <= ctas; c += kSkPlanThreads) {
+        p.sk_plan[c] = run[c];
+        if (c < ctas) {
+            p.sk_plan[ctas + 1 + c] = run_item[c];
+            p.sk_plan[2 * ctas + 1 + c] = whole[c];
+        }
     }
 }
 
@@ -1568,14 +1649,14 @@ int32_t prefill_sk_ctas(pkv_dtype dtype, int32_t batch, int32_t hq, int32_t hkv,
     const int64_t items = static_cast<int64_t>(batch) * hkv * ((max_q_len + qpc - 1) / qpc);
     // more items than SMs (else one wave of one CTA per item already fits),
     // and a plan the one-CTA plan kernel scans quickly
-    if (items <= num_sms || items > 65536) return 0;
+    if (items <= num_sms || items > 65536 || num_sms > kSkMaxCtas) return 0;
     return num_sms;
 }
 
 size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas)
 {
     if (ctas <= 0) return 0;
-    const size_t pre = ((static_cast<size_t>(items + 1) * sizeof(int32_t) + 255) & ~static_cast<size_t>(255)) +
+    const size_t pre = ((static_cast<size_t>(ctas) * 3 * sizeof(int32_t) + 4 + 255) & ~static_cast<size_t>(255)) +
                        ((static_cast<size_t>(items) * kSkItemBytes + 255) & ~static_cast<size_t>(255)) +
                        ((static_cast<size_t>(ctas) * 8 * sizeof(int32_t) + 255) & ~static_cast<size_t>(255));
     const size_t rows = static_cast<size_t>(ctas) * 2 * pf::kQTiles * pf::kRows;
