@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         for (int32_t k = 0; !abort; ++k) {
         const int32_t ntile = ss->sg.ntile, jt0 = ss->sg.jt0;
         const int32_t kv_lo = ss->sg.w.kv_lo, kv_hi = ss->sg.w.kv_hi;
-        const int32_t nst = ss->sg.w.nst, gap = ss->sg.w.gap;
+        const int32_t nst = kSink ? ss->sg.w.nst : 0, gap = kSink ? ss->sg.w.gap : 0;
         // the segment's query tile: staged (the first in the prologue), then
         // handed to the MMA-issue warp
         if (k > 0) load_q_rows(ss->sg.w);
@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // path: key column e is attended iff e - lo is in [0, qpos - qlo]
                 // and its block was loaded
                 const bool full = mask == (1u << kBlocks) - 1u &&
-                                  (tbase >= qlo || (kSink && tbase + kKeys <= p.sinks)) &&
+                                  tbase >= qlo &&
                                   tbase + kKeys - 1 <= qpos && valid_row;
                 if (!full) {
                     // attended columns as bits: the window's from qlo to qpos, the
@@ -1514,24 +1514,26 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         }
         B = __reduce_add_sync(0xffffffffu, B);
         most = __reduce_max_sync(0xffffffffu, most);
-        const int64_t R = carry - B;
-        int64_t lo = 0, hi = most + (R + ctas - 1) / ctas;  // room(hi) >= R
-        const auto room = [&](int64_t level) {
-            int64_t sum = 0;
-            for (int32_t c = lane; c < ctas; c += 32) sum += max(static_cast<int64_t>(0), level - tiles[c]);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            return sum;
+        const int32_t R = carry - B;
+        // room(level) >= ctas * level - B, with equality while no whole item
+        // passes the level: the even level is enough, and exact when it holds
+        // every whole item (fewer than 2^30 tiles: 65536 items of 16384 at most)
+        const auto room = [&](int32_t level) {
+            int32_t sum = 0;
+            for (int32_t c = lane; c < ctas; c += 32) sum += max(0, level - tiles[c]);
+            return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, sum));
         };
+        int32_t lo = 0, hi = (R + B + ctas - 1) / ctas;
+        if (most <= hi) lo = hi;
         while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
+            const int32_t mid = (lo + hi) >> 1;
             if (room(mid) >= R) hi = mid; else lo = mid + 1;
         }
         const int64_t total = room(lo);
         int64_t before = 0;  // room of the CTAs before this group of 32
         for (int32_t c0 = 0; c0 < ctas; c0 += 32) {
             const int32_t c = c0 + lane;
-            int64_t v = c < ctas ? max(static_cast<int64_t>(0), lo - tiles[c]) : 0;
+            int64_t v = c < ctas ? max(0, lo - tiles[c]) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
