@@ -14,18 +14,32 @@ namespace pkv {
 
 constexpr int kF32Threads = 128;
 
+// Blocks of one online-softmax step.  Calls with sinks take as many as keep a
+// tile within 4096 elements (64 tokens of 64 dims: four barriers and one pass
+// of the softmax for four blocks); the others one, which fixes the order of
+// their sums.
+__host__ __device__ __forceinline__ int f32_blocks_per_step(int32_t sinks, int bs, int D)
+{
+    const int n = sinks > 0 ? 4096 / (bs * D) : 1;
+    return n < 1 ? 1 : n > 8 ? 8 : n;
+}
+
 __global__ void __launch_bounds__(kF32Threads)
     decode_f32_kernel(const DecodeParams p, int prefix_mode)
 {
     constexpr int NQ = kF32Rows;
-    extern __shared__ float fsm[];
-    const int D = p.head_dim, bs = p.block_size;
+    extern __shared__ __align__(16) float fsm[];
+    const int D = p.head_dim, bs = p.block_size, dlog = 31 - __clz(D);
     float *qs = fsm;                   // [NQ][D]
     float *os = qs + NQ * D;           // [NQ][D]
-    float *ks = os + NQ * D;           // [bs][D]
-    float *vs = ks + bs * D;           // [bs][D]
-    float *sc = vs + bs * D;           // [NQ][bs]
-    float *mrow = sc + NQ * bs;        // [NQ]
+    const int ksd = D + 1;             // a token's K row, padded: lanes on 16 tokens hit distinct banks
+    const int bps = f32_blocks_per_step(p.sinks, bs, D);
+    const int ts = bs * bps;           // tokens of a step
+    const int kpart = (ts * ksd + 3) & ~3;  // the V rows start on 16 bytes
+    const int tile = kpart + ts * D;
+    float *kv = os + NQ * D;           // [2][K rows [ts][D + 1], V rows [ts][D]]
+    float *sc = kv + 2 * tile;         // [NQ][ts]
+    float *mrow = sc + NQ * ts;        // [NQ]
     float *lrow = mrow + NQ;           // [NQ]
     float *alpha = lrow + NQ;          // [NQ]
     int32_t *prow = reinterpret_cast<int32_t *>(alpha + NQ);  // [NQ] row, -1 = unused
@@ -129,7 +143,8 @@ __global__ void __launch_bounds__(kF32Threads)
         }
     }
     const float *qg = static_cast<const float *>(p.q);
-    for (int i = tid; i < NQ * D; i += kF32Threads) {
+    const int rows = prefix_mode ? NQ : G;  // query rows of this CTA
+    for (int i = tid; i < rows * D; i += kF32Threads) {
         const int k = i / D, d = i % D;
         qs[i] = prow[k] >= 0 ? qg[(static_cast<int64_t>(prow[k]) * p.hq + phead[k]) * D + d] : 0.f;
         os[i] = 0.f;
@@ -142,60 +157,91 @@ __global__ void __launch_bounds__(kF32Threads)
 
     const float *kpool = static_cast<const float *>(p.k_pool);
     const float *vpool = static_cast<const float *>(p.v_pool);
-    for (int i = 0; i < nblk; ++i) {
-        const int32_t b = b0 + i >= nsb ? b0 + i + gap : b0 + i;
-        const int32_t blk = __ldg(p.tables + static_cast<int64_t>(tab_row) * p.width + b);
-        const bool ok = static_cast<uint32_t>(blk) < static_cast<uint32_t>(p.num_blocks);
-        if (!ok && tid == 0) report(p.status, PKV_DEV_BAD_BLOCK);
-        if (ok) {
-            const int64_t base = (static_cast<int64_t>(blk) * p.hkv + g) * bs * D;
-            for (int j = tid; j < bs * D; j += kF32Threads) {
-                ks[j] = __ldg(kpool + base + j);
-                vs[j] = __ldg(vpool + base + j);
+    // step i's rows into buffer i % 2 by asynchronous copies (K rows are padded:
+    // 4 bytes each), one step ahead of the compute; the mask of its blocks that exist
+    auto block_of = [&](int j) { return b0 + j >= nsb ? b0 + j + gap : b0 + j; };
+    auto stage = [&](int i) {
+        uint32_t okm = 0;
+        for (int e = 0; e < bps && i * bps + e < nblk; ++e) {
+            const int32_t blk = __ldg(p.tables + static_cast<int64_t>(tab_row) * p.width + block_of(i * bps + e));
+            const bool ok = static_cast<uint32_t>(blk) < static_cast<uint32_t>(p.num_blocks);
+            if (!ok) {
+                if (tid == 0) report(p.status, PKV_DEV_BAD_BLOCK);
+                continue;
             }
+            okm |= 1u << e;
+            const int64_t base = (static_cast<int64_t>(blk) * p.hkv + g) * bs * D;
+            const uint32_t ks = smem_u32(kv + (i & 1) * tile) + 4 * e * bs * ksd;
+            const uint32_t vs = smem_u32(kv + (i & 1) * tile + kpart) + 4 * e * bs * D;
+            // head_dim is a power of two
+            for (int j = tid; j < bs * D; j += kF32Threads)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ks + 4 * (j + (j >> dlog))),
+                             "l"(kpool + base + j)
+                             : "memory");
+            for (int j = 4 * tid; j < bs * D; j += 4 * kF32Threads)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(vs + 4 * j), "l"(vpool + base + j)
+                             : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return okm;
+    };
+    uint32_t okm = stage(0);
+    const int nstep = (nblk + bps - 1) / bps;
+    for (int i = 0; i < nstep; ++i) {
+        const uint32_t ok_next = stage(i + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        for (int j = tid; j < NQ * bs; j += kF32Threads) {
-            const int k = j / bs, t = j % bs;
-            const int pos = b * bs + t;
+        const float *ks = kv + (i & 1) * tile, *vs = ks + kpart;
+        for (int j = tid; j < rows * ts; j += kF32Threads) {
+            const int k = j / ts, t = j - k * ts, e = t / bs;
+            const int pos = block_of(i * bps + e) * bs + (t - e * bs);
             float sv = -INFINITY;
-            if (ok && prow[k] >= 0 && (pos >= plo[k] || pos < sink) && pos < phi[k]) {
+            if (((okm >> e) & 1u) && prow[k] >= 0 && (pos >= plo[k] || pos < sink) && pos < phi[k]) {
                 float acc = 0.f;
-                for (int d = 0; d < D; ++d) acc = fmaf(qs[k * D + d], ks[t * D + d], acc);
+#pragma unroll 16
+                for (int d = 0; d < D; ++d) acc = fmaf(qs[k * D + d], ks[t * ksd + d], acc);
                 sv = acc * p.scale_log2;
             }
             sc[j] = sv;
         }
         __syncthreads();
-        if (tid < NQ) {
+        // a warp per query row: maximum and exponentials over the lanes, the
+        // sum in token order
+        for (int k = tid >> 5; k < rows; k += kF32Threads / 32) {
+            const int lane = tid & 31;
             float mx = -INFINITY;
-            for (int t = 0; t < bs; ++t) mx = fmaxf(mx, sc[tid * bs + t]);
-            const float mn = fmaxf(mrow[tid], mx);
+            for (int t = lane; t < ts; t += 32) mx = fmaxf(mx, sc[k * ts + t]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float mn = fmaxf(mrow[k], mx);
             const float mu = mn == -INFINITY ? 0.f : mn;
-            const float al = fast_exp2(mrow[tid] - mu);
-            float sum = 0.f;
-            for (int t = 0; t < bs; ++t) {
-                const float e = fast_exp2(sc[tid * bs + t] - mu);
-                sc[tid * bs + t] = e;
-                sum += e;
+            for (int t = lane; t < ts; t += 32) sc[k * ts + t] = fast_exp2(sc[k * ts + t] - mu);
+            __syncwarp();
+            if (lane == 0) {
+                const float al = fast_exp2(mrow[k] - mu);
+                float sum = 0.f;
+#pragma unroll 8
+                for (int t = 0; t < ts; ++t) sum += sc[k * ts + t];
+                lrow[k] = lrow[k] * al + sum;
+                mrow[k] = mn;
+                alpha[k] = al;
             }
-            lrow[tid] = lrow[tid] * al + sum;
-            mrow[tid] = mn;
-            alpha[tid] = al;
         }
         __syncthreads();
-        for (int j = tid; j < NQ * D; j += kF32Threads) {
-            const int k = j / D, d = j % D;
+        for (int j = tid; j < rows * D; j += kF32Threads) {
+            const int k = j >> dlog, d = j & (D - 1);
             float acc = os[j] * alpha[k];
-            for (int t = 0; t < bs; ++t) {
-                const float w = sc[k * bs + t];
-                if (w != 0.f) acc = fmaf(w, vs[t * D + d], acc);  // masked slots may hold NaN
+#pragma unroll 8
+            for (int t = 0; t < ts; ++t) {
+                const float w = sc[k * ts + t], v = vs[t * D + d];
+                if (w != 0.f) acc = fmaf(w, v, acc);  // masked slots may hold NaN
             }
             os[j] = acc;
         }
         __syncthreads();
+        okm = ok_next;
     }
-    for (int j = tid; j < NQ * D; j += kF32Threads) {
+    for (int j = tid; j < rows * D; j += kF32Threads) {
         const int k = j / D, d = j % D;
         if (prow[k] < 0) continue;
         const size_t pi = partial_index(p, prow[k], phead[k], slot);
@@ -207,15 +253,16 @@ __global__ void __launch_bounds__(kF32Threads)
     }
 }
 
-size_t f32_smem_bytes(int D, int bs)
+size_t f32_smem_bytes(int D, int bs, int32_t sinks)
 {
-    return sizeof(float) * (2 * kF32Rows * D + 2 * bs * D + kF32Rows * bs + 3 * kF32Rows) +
+    const int ts = bs * f32_blocks_per_step(sinks, bs, D);
+    return sizeof(float) * (2 * kF32Rows * D + 2 * (ts * (2 * D + 1) + 3) + kF32Rows * ts + 3 * kF32Rows) +
            sizeof(int32_t) * (4 * kF32Rows + 4);
 }
 
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t stream)
 {
-    const size_t smem = f32_smem_bytes(p.head_dim, p.block_size);
+    const size_t smem = f32_smem_bytes(p.head_dim, p.block_size, p.sinks);
     cudaError_t err = cudaFuncSetAttribute(decode_f32_kernel,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(smem));

@@ -374,3 +374,21 @@ def test_refusals(pkv):
             fn()
         assert e.value.code == code
     assert pkv.launch_count() == n0
+
+
+@pytest.mark.parametrize("bs,d", [(1, 64), (5, 32), (7, 128), (24, 64), (64, 32), (16, 256)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 0), (30, 9), (200, 70)])
+def test_f32_other_block_sizes(pkv, orc, bs, d, window, sinks):
+    w = gen.decode_workload(seed=395 + bs, dtype="f32", num_q_heads=6, num_kv_heads=2, head_dim=d,
+                            context_lens=[0, 3, 40, 333, 600], block_size=bs, window=window)
+    if window:
+        return check(pkv, orc, w, sinks)
+    d_ = Dev(w)
+    append(pkv, d_)
+    out = call(pkv, w, d_, 0)
+    torch.cuda.synchronize()
+    kp, vp = w.k_pool.copy(), w.v_pool.copy()
+    slots = pkv.slot_mapping_host(w.block_tables, w.num_blocks, w.new_rows, w.new_pos, bs)
+    orc.append(kp, vp, "f32", slots, w.k_new, w.v_new)
+    assert_close(to_f64(out), orc.decode(w.q, kp, vp, "f32", w.block_tables, w.seq_lens, 0, w.scale), "f32",
+                 f"block size {bs}")
