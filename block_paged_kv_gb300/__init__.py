@@ -809,13 +809,15 @@ def profile_times(kind: int) -> list:
 
 
 DRILL_WITHHOLD_FIRST_LOAD = 1
+DRILL_LATE_CONSUMERS = 4
 
 
 def set_wait_drill(wait_limit_ns: int = 0, flags: int = 0) -> None:
     """Diagnostic fail-closed drill for the launches that follow: the limit of
     each pipeline data wait (0 = the 2 s default) and, with
     DRILL_WITHHOLD_FIRST_LOAD, every pipeline's first load left unissued so
-    that the wait for it runs out.  set_wait_drill() restores normal operation."""
+    that the wait for it runs out, or, with DRILL_LATE_CONSUMERS, the prefill's
+    softmax warps late at each item's output.  set_wait_drill() restores normal operation."""
     _check("pkv_set_wait_drill", _lib.pkv_set_wait_drill(int(wait_limit_ns), int(flags)))
 
 

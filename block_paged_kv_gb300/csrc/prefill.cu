@@ -68,8 +68,8 @@ struct Layout {
     static constexpr int kBarOff = kStagingOff + kStagingBytes;
     // barriers: k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[tile][buf],
     // p_full[tile][buf], pv_done[tile], mma_drain[tile], q_full[tile],
-    // FP8: staged[K/V][2], stg_free[K/V][2]
-    static constexpr int kNumBars = 4 * kStages + 4 + 4 + 2 + 2 + 2 + (kF8 ? 8 : 0);
+    // o_done[tile], FP8: staged[K/V][2], stg_free[K/V][2]
+    static constexpr int kNumBars = 4 * kStages + 4 + 4 + 2 + 2 + 2 + 2 + (kF8 ? 8 : 0);
     // kmask[kStages], FP8: smask[K/V][2] (blocks loaded of each staging buffer)
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kTmemOff = kMaskOff + (kStages + 4) * 4;
@@ -387,8 +387,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     uint64_t *pv_done = bars + 4 * kStages + 8; // [tile]
     uint64_t *mma_drain = bars + 4 * kStages + 10;  // [tile]: the issuer's last products
     uint64_t *q_full = bars + 4 * kStages + 12;     // [tile]: a segment's query tile staged
-    uint64_t *staged = bars + 4 * kStages + 14;  // FP8: [K/V * 2 + buffer]
-    uint64_t *stg_free = bars + 4 * kStages + 18;  // FP8: [K/V * 2 + buffer] widened by the softmax warps
+    uint64_t *o_done = bars + 4 * kStages + 14;  // [tile]: a segment's last P.V product
+    uint64_t *staged = bars + 4 * kStages + 16;  // FP8: [K/V * 2 + buffer]
+    uint64_t *stg_free = bars + 4 * kStages + 20;  // FP8: [K/V * 2 + buffer] widened by the softmax warps
     uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);
     uint32_t *smask = kmask + kStages;  // FP8: [K/V * 2 + buffer] blocks loaded of a staging buffer
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemOff);
@@ -445,6 +446,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         mbar_init(&pv_done[1], 1);
         mbar_init(&mma_drain[0], 1);
         mbar_init(&mma_drain[1], 1);
+        mbar_init(&o_done[0], 1);
+        mbar_init(&o_done[1], 1);
         mbar_init(&q_full[0], kSoftmaxWarps / kQTiles);
         mbar_init(&q_full[1], kSoftmaxWarps / kQTiles);
         if (kF8) {
@@ -690,6 +693,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 tc::fence_after();
                 if (elect_one()) {
                     pv_issue(T, j == 0);
+                    if (j == n - 1) tc::commit(&o_done[x]);
                     if (more) s_issue(T + 2);
                 }
                 __syncwarp();
@@ -1060,14 +1064,15 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         }
         if (abort) break;
         const PrefillRowInfo &w = ss->sg.w;
-        // epilogue: O / l once the segment's last P.V product is in.  Phases
-        // up to its last tile - 3 are known complete here (S of its last tile
-        // was issued after P.V of the tile two before), and those of earlier
-        // segments too, so wait for the last tile - 1 first: a parity names
-        // one phase only when the one before it has completed
+        if (p.drill & kDrillLate) __nanosleep(20000 + 4000 * (warp & 3));
+        // epilogue: O / l once the segment's last P.V product is in.  A parity
+        // names one phase only while no later one can have completed: o_done
+        // completes once a segment, and its next phase needs this warp.
+        // pv_done alone cannot tell: a warp that comes late finds the last two
+        // products done, where a wait for the first of them never ends
         {
             const int32_t Tl = T0 + ntile - 1;
-            bool done = ntile < 2 || mbar_wait(&pv_done[x], (Tl - 1) & 1, p.wait_ns);
+            bool done = mbar_wait(&o_done[x], k & 1, p.wait_ns);
             done = done && mbar_wait(&pv_done[x], Tl & 1, p.wait_ns);
             if (__any_sync(0xffffffffu, !done)) {
                 if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);

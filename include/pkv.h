@@ -499,7 +499,10 @@ int32_t pkv_set_decode_split_blocks(int32_t blocks_per_split);
  *                  (2 s); values above the default are cut to it;
  *   flags:         0, or PKV_DRILL_WITHHOLD_FIRST_LOAD: every pipeline
  *                  leaves its first load unissued, so that the wait for it
- *                  runs out after wait_limit_ns.
+ *                  runs out after wait_limit_ns;
+ *                  PKV_DRILL_LATE_CONSUMERS: the tensor-core prefill's
+ *                  softmax warps come to each item's output some 20 us late
+ *                  (results are the same, calls are slower).
  * A wait that runs out sets PKV_DEV_TIMEOUT in the status word; the CTA then
  * waits (with the 2 s default limit) for every copy it did issue to land
  * and for its tensor-core products to finish, and exits.  The call's output
@@ -507,6 +510,7 @@ int32_t pkv_set_decode_split_blocks(int32_t blocks_per_split);
  * Returns PKV_ERR_INVALID_ARG for unknown flags.
  */
 #define PKV_DRILL_WITHHOLD_FIRST_LOAD 1u
+#define PKV_DRILL_LATE_CONSUMERS 4u
 pkv_status pkv_set_wait_drill(uint64_t wait_limit_ns, uint32_t flags);
 
 /* Number of splits per row and blocks per split the automatic plan picks for
