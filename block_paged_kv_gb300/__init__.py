@@ -411,15 +411,7 @@ class RopeDesc:
     """Rotary descriptor (host memory, passed by value into every launch)."""
 
     def __init__(self, c: _Rope):
-        self._c = c
-
-    @property
-    def rotary_dim(self) -> int:
-        return int(self._c.rotary_dim)
-
-    @property
-    def num_axes(self) -> int:
-        return int(self._c.num_axes)
+        self._c, self.rotary_dim, self.num_axes = c, int(c.rotary_dim), int(c.num_axes)
 
 
 def make_rope(inv_freq, axis_of_pair=None, num_axes: Optional[int] = None, interleaved: bool = False,
@@ -443,12 +435,12 @@ def make_rope(inv_freq, axis_of_pair=None, num_axes: Optional[int] = None, inter
     return RopeDesc(c)
 
 
-def _token_stride(t: torch.Tensor, rows: int, dim: int) -> int:
-    """Elements between a [T, rows, dim] operand's tokens, -1 when a token's rows are not contiguous."""
-    a, b, c = t.stride()
+def _token_stride(strides, tokens: int, rows: int, dim: int) -> int:
+    """Elements between a [tokens, rows, dim] operand's tokens, -1 when a token's rows are not contiguous."""
+    a, b, c = strides
     if (c != 1 and dim != 1) or (b != dim and rows != 1):
         return -1
-    return a if t.shape[0] > 1 else rows * dim
+    return a if tokens > 1 else rows * dim
 
 
 def _rope_refuse(pool, dev, act, slot_mapping, q, k_new, v_new, positions, rope, q_out, status):
@@ -464,7 +456,7 @@ def _rope_refuse(pool, dev, act, slot_mapping, q, k_new, v_new, positions, rope,
         _require(t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and
                  (name[0] == "q" or t.shape[1] == hkv),
                  f"{name} is [T, heads, head_dim], one slot per token")
-        _require(_token_stride(t, t.shape[1], D) >= 0 or t.numel() == 0,
+        _require(_token_stride(t.stride(), t.shape[0], t.shape[1], D) >= 0 or t.numel() == 0,
                  f"{name}: each token's [heads, head_dim] rows are contiguous")
     _require(q is not None or q_out is None, "q_out without q")
     _require(q_out is None or q_out.shape == q.shape, "q_out matches q")
@@ -488,19 +480,20 @@ def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mappin
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
     gpu, pdt = k_pool.get_device(), k_pool.dtype
     act = torch.float32 if pdt is torch.float32 else torch.bfloat16
-    hkv, D, T, axes, i32 = pool.num_kv_heads, pool.head_dim, slot_mapping.numel(), rope._c.num_axes, torch.int32
+    hkv, D, T, axes, i32 = pool.num_kv_heads, pool.head_dim, slot_mapping.numel(), rope.num_axes, torch.int32
     kshape, pshape = k_new.shape, positions.shape
-    ok = (slot_mapping.dtype is i32 and slot_mapping.dim() == 1 and slot_mapping.is_contiguous() and
+    ok = (slot_mapping.dtype is i32 and slot_mapping.ndim == 1 and slot_mapping.is_contiguous() and
           slot_mapping.get_device() == gpu and kshape == (T, hkv, D) and v_new.shape == kshape and
           k_new.dtype is act and v_new.dtype is act and k_new.get_device() == gpu and
           v_new.get_device() == gpu and positions.dtype is i32 and positions.get_device() == gpu and
           (pshape == (axes, T) or (axes == 1 and pshape == (T,))) and
-          (positions.stride(-1) == 1 or T <= 1) and
+          (positions.is_contiguous() or positions.stride(-1) == 1 or T <= 1) and
           (status is None or (status.get_device() == gpu and status.dtype is i32 and status.numel() >= 1)))
     ks = vs = qs = os_ = 0
     hq, qp, op = 0, None, None
     if ok:
-        ks, vs = _token_stride(k_new, hkv, D), _token_stride(v_new, hkv, D)
+        ks = _token_stride(k_new.stride(), T, hkv, D)
+        vs = _token_stride(v_new.stride(), T, hkv, D)
         if q is None:
             ok = q_out is None
         else:
@@ -513,7 +506,8 @@ def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mappin
                     q_out = torch.empty(qshape, dtype=act, device=q.device)
                 hq, qp, op = qshape[1], q.data_ptr(), q_out.data_ptr()
                 if hq:
-                    qs, os_ = _token_stride(q, hq, D), _token_stride(q_out, hq, D)
+                    qs = _token_stride(q.stride(), T, hq, D)
+                    os_ = _token_stride(q_out.stride(), T, hq, D)
         ok = ok and (T == 0 or (ks >= 0 and vs >= 0 and qs >= 0 and os_ >= 0))
     if not ok:
         _rope_refuse(pool, k_pool.device, act, slot_mapping, q, k_new, v_new, positions, rope, q_out, status)
@@ -672,14 +666,15 @@ def paged_decode_attention(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.
         if sinks and (window or sinks < 0):
             raise PkvError("paged_decode_attention (sinks with a shared prefix)",
                            PKV_ERR_UNSUPPORTED if sinks > 0 else PKV_ERR_INVALID_ARG)
-    with _on(k_pool.device):  # the plan reads the SM count of the current device
+    # the plan reads the SM count of the current device
+    with _NULL if _current_device() == gpu else torch.cuda.device(gpu):
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
             workspace = alloc_workspace(
                 decode_workspace_size(B, hq, pool.num_kv_heads, D, pool.block_size, max_seq_len, window,
                                       prefix, sinks), k_pool.device)
-        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws, nbytes = workspace.data_ptr(), workspace.nbytes
         st = None if status is None else status.data_ptr()
         if sinks and prefix is None:
             code = _lib.paged_decode_attention_sinks(
