@@ -280,14 +280,28 @@ try {
     const bool part = n_tokens % a->bs != 0;
     Request c;
     c.fresh = false;
+    c.table.reserve(full + (part ? 1 : 0));
     c.table.assign(r.table.begin(), r.table.begin() + static_cast<ptrdiff_t>(full));
     c.hashes.assign(r.hashes.begin(), r.hashes.begin() + static_cast<ptrdiff_t>(std::min(full, r.hashes.size())));
     c.published = static_cast<int32_t>(std::min<size_t>(full, static_cast<size_t>(r.published)));
+    // the request's entry comes first: past the block that take() gives, nothing allocates
+    const int32_t id = a->next_req;
+    const auto entry = a->reqs.emplace(id, Request{}).first;
     int32_t from = -1, to = -1;
     if (part) {
-        std::vector<int32_t> got;
         if (r.table[full] >= 0) {
-            if (!a->take(1, got)) return PKV_ERR_OUT_OF_BLOCKS;
+            bool taken = false;
+            std::vector<int32_t> got;
+            try {
+                taken = a->take(1, got);
+            } catch (...) {
+                a->reqs.erase(entry);
+                throw;
+            }
+            if (!taken) {
+                a->reqs.erase(entry);
+                return PKV_ERR_OUT_OF_BLOCKS;
+            }
             from = r.table[full];
             to = got[0];
         }
@@ -295,8 +309,8 @@ try {
     }
     for (size_t i = 0; i < full; ++i)
         if (c.table[i] >= 0) ++a->blocks[c.table[i]].refcount;
-    const int32_t id = a->next_req++;
-    a->reqs.emplace(id, std::move(c));
+    entry->second = std::move(c);
+    ++a->next_req;
     *new_req = id;
     *src = from;
     *dst = to;
