@@ -730,7 +730,6 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         // regions, as the bf16 path lays them out); keys of blocks not loaded
         // are left as they are (their scores are masked).  The stage is free
         // once tile Tk - kStages's S products and mask reads are done.
-        const int nthr = kRows;
         const bool do_k = nqt == 1 || x == 0, do_v = nqt == 1 || x == 1;
         const int wq0 = (threadIdx.x - 128) & (kRows - 1);  // this thread's first chunk
         auto widen_k = [&](int32_t Tk) {
@@ -749,16 +748,20 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             // Matrix 2kk + h is 16-byte chunk 2kk + h of each key's 128-byte
             // row, swizzled by the key row.
             const int mr = lane & 7, mm = lane >> 3;  // this lane's row address: row mr of matrix mm
-            for (int q = wq0; q < kBlocks * 128; q += nthr) {
-                const int b = q >> 7, ch = q & 127;  // warp-uniform but for ch % 32
+            // The four blocks' chunks are read first, so that the reads are in
+            // flight together (a block not loaded reads stale bytes, unused).
+            const int ch = wq0, grp = ch >> 6, half = (ch >> 5) & 1;  // warp-uniform but for ch % 32
+            uint4 q4[kBlocks];
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) q4[b] = lds128(src + b * kF8BlockBytes + ch * 16);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
                 if (!((km >> b) & 1u)) continue;
-                const int grp = ch >> 6, half = (ch >> 5) & 1;
-                const uint4 q4 = lds128(src + b * kF8BlockBytes + ch * 16);
                 uint32_t f[8];  // f[2kk + h]: matrix (kk, h)
-                e4m3x4_to_f16x2x2(q4.x, f[0], f[1]);
-                e4m3x4_to_f16x2x2(q4.y, f[2], f[3]);
-                e4m3x4_to_f16x2x2(q4.z, f[4], f[5]);
-                e4m3x4_to_f16x2x2(q4.w, f[6], f[7]);
+                e4m3x4_to_f16x2x2(q4[b].x, f[0], f[1]);
+                e4m3x4_to_f16x2x2(q4[b].y, f[2], f[3]);
+                e4m3x4_to_f16x2x2(q4[b].z, f[4], f[5]);
+                e4m3x4_to_f16x2x2(q4[b].w, f[6], f[7]);
                 const int krow = b * 16 + half * 8 + mr;
                 const uint32_t rowa = dst + grp * kKVRegion + krow * 128;
                 stsm_x4(rowa + ((mm ^ mr) << 4), f[0], f[1], f[2], f[3]);
@@ -851,16 +854,18 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // (jn, h) is 16-byte chunk 2b + h of each dim row, swizzled by
                 // the dim row.
                 const int mr = lane & 7, mm = lane >> 3, c = lane & 3;
-                for (int q = wq0; q < kBlocks * 128; q += nthr) {
-                    const int b = q >> 7, ch = q & 127;  // warp-uniform but for ch % 32
-                    const int g32 = ch >> 5;
+                const int ch = wq0, g32 = ch >> 5;  // warp-uniform but for ch % 32
+                uint4 q4[kBlocks];
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) q4[b] = lds128(src + b * kF8BlockBytes + ch * 16);
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
                     uint32_t f[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};  // f[2jn + h]: matrix (jn, h)
                     if ((vm >> b) & 1u) {
-                        const uint4 q4 = lds128(src + b * kF8BlockBytes + ch * 16);
-                        e4m3x4_to_f16x2x2(q4.x, f[0], f[1]);
-                        e4m3x4_to_f16x2x2(q4.y, f[2], f[3]);
-                        e4m3x4_to_f16x2x2(q4.z, f[4], f[5]);
-                        e4m3x4_to_f16x2x2(q4.w, f[6], f[7]);
+                        e4m3x4_to_f16x2x2(q4[b].x, f[0], f[1]);
+                        e4m3x4_to_f16x2x2(q4[b].y, f[2], f[3]);
+                        e4m3x4_to_f16x2x2(q4[b].z, f[4], f[5]);
+                        e4m3x4_to_f16x2x2(q4[b].w, f[6], f[7]);
                         if (vedge) {
                             auto live = [&](int k) {
                                 const int32_t kp = tbase + b * 16 + k;
