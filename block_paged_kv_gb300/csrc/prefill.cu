@@ -167,10 +167,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //     dealt by prefill_sk_plan_kernel: the items' tiles in item order form one
 //     sequence of W tiles.  CTA c first runs the c-th item with tiles whole
 //     (the CTAs of one (row, kv head) then start together and share its K/V
-//     through L2), then a run of consecutive tiles of the rest (R = W - B, B
-//     the tiles of the first n such items), item by item.  The runs level the
-//     CTAs: with w_c = max(0, level - the c-th item's tiles), CTA c's run
-//     starts at B + R (w_0 + .. + w_(c-1)) / (w_0 + .. + w_(n-1)).  Only the
+//     through L2), then a run of consecutive tiles of the rest, item by item.
+//     The runs level the CTAs' costs, an item counting kSkItemCost tiles more
+//     than it has: with w_c = max(0, level - the c-th item's cost), B the cost
+//     of the first n such items and R that of the rest, CTA c's run starts
+//     at cost B + R (w_0 + .. + w_(c-1)) / (w_0 + .. + w_(n-1)).  Only the
 //     first and the last segment of a run can cut an item; a cut segment
 //     writes a partial to slot 0 (first) or 1 (last) of the CTA, and the warp
 //     that completes an item's pieces merges them.
@@ -1440,13 +1441,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
 // ---------------------------------------------------------------------------
 constexpr int kSkPlanThreads = 1024;
 constexpr int kSkMaxCtas = 512;
+// What an item costs a CTA beside its tiles, in tiles (its query tile staged, the
+// first products, the epilogue: about 7 us against 1.2 a tile), and the fewest
+// tiles worth a cut (a piece's partial is written and merged).  Against 0 and 1:
+// 8 ragged chunks on FP8 pools (16/4 heads, window 1000) 87.7 -> 73.4 us, 4
+// chunks of 512 with a window of 512 61.8 -> 51.0 (bf16), 2 chunks of 4096 with
+// one of 4096 470 -> 465; 4 to 8 and 2 to 4 lie within 5 % of each other.
+constexpr int32_t kSkItemCost = 6;
+constexpr int32_t kSkLeastPiece = 4;
 
 __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const PrefillParams p)
 {
     constexpr int kWarps = kSkPlanThreads / 32;
     __shared__ int32_t warp_sum[kWarps], warp_cnt[kWarps], warp_first[kWarps];
     __shared__ int32_t carry, carry_cnt, after;
-    __shared__ int32_t whole[kSkMaxCtas], tiles[kSkMaxCtas], run[kSkMaxCtas + 1], run_item[kSkMaxCtas];
+    __shared__ int32_t whole[kSkMaxCtas], cost[kSkMaxCtas], run[kSkMaxCtas + 1], run_item[kSkMaxCtas];
+    __shared__ int32_t run_cost[kSkMaxCtas + 1];  // the runs' starts, each item counted kSkItemCost longer
     pdl_wait();  // lengths may come from the previous kernel on the stream
     pdl_trigger();
     const int qpc = pf::kQTiles * (pf::kRows / p.group);
@@ -1459,7 +1469,7 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
     }
     for (int32_t i = threadIdx.x; i < ctas; i += kSkPlanThreads) {
         whole[i] = -1;
-        tiles[i] = 0;
+        cost[i] = 0;
         run_item[i] = 0;
     }
     for (int32_t i = threadIdx.x; i < ctas * 8; i += kSkPlanThreads) p.sk_count[i] = 0;
@@ -1503,9 +1513,10 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
             if (n > 0) rec[u].w = w;
             rec[u].lo = incl - n;
             rec[u].hi = incl;
+            rec[u].next = rank;  // until the next items are known
             if (n > 0 && rank < ctas) {
                 whole[rank] = u;
-                tiles[rank] = n;
+                cost[rank] = n + kSkItemCost;
             }
         }
         __syncthreads();
@@ -1515,25 +1526,26 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         }
         __syncthreads();
     }
-    // the runs: the least level at which the CTAs take the R tiles left
+    // the runs: the least level at which the CTAs take the cost R that is left
+    const int32_t W = carry + carry_cnt * kSkItemCost;
     if (warp == 0) {
         int32_t B = 0, most = 0;
         for (int32_t c = lane; c < ctas; c += 32) {
-            B += tiles[c];
-            most = max(most, tiles[c]);
+            B += cost[c];
+            most = max(most, cost[c]);
         }
         B = __reduce_add_sync(0xffffffffu, B);
         most = __reduce_max_sync(0xffffffffu, most);
-        const int32_t R = carry - B;
+        const int32_t R = W - B;
         // room(level) >= ctas * level - B, with equality while no whole item
         // passes the level: the even level is enough, and exact when it holds
-        // every whole item (fewer than 2^30 tiles: 65536 items of 16384 at most)
+        // every whole item (costs below 2^30: 65536 items of 16384 tiles at most)
         const auto room = [&](int32_t level) {
             int32_t sum = 0;
-            for (int32_t c = lane; c < ctas; c += 32) sum += max(0, level - tiles[c]);
+            for (int32_t c = lane; c < ctas; c += 32) sum += max(0, level - cost[c]);
             return static_cast<int32_t>(__reduce_add_sync(0xffffffffu, sum));
         };
-        int32_t lo = 0, hi = (R + B + ctas - 1) / ctas;
+        int32_t lo = 0, hi = (W + ctas - 1) / ctas;
         if (most <= hi) lo = hi;
         while (lo < hi) {
             const int32_t mid = (lo + hi) >> 1;
@@ -1543,16 +1555,34 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         int64_t before = 0;  // room of the CTAs before this group of 32
         for (int32_t c0 = 0; c0 < ctas; c0 += 32) {
             const int32_t c = c0 + lane;
-            int64_t v = c < ctas ? max(0, lo - tiles[c]) : 0;
+            int64_t v = c < ctas ? max(0, lo - cost[c]) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
                 if (lane >= d) v += o;
             }
-            if (c < ctas) run[c + 1] = static_cast<int32_t>(B + (total > 0 ? R * (before + v) / total : 0));
+            if (c < ctas) run_cost[c + 1] = static_cast<int32_t>(B + (total > 0 ? R * (before + v) / total : 0));
             before += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) run[0] = B;
+        if (lane == 0) run_cost[0] = B;
+    }
+    for (int32_t c = threadIdx.x; c <= ctas; c += kSkPlanThreads) run[c] = carry;  // the runs past the last item
+    __syncthreads();
+    // the runs' starts in tiles: the item whose cost holds a start places it, on
+    // its end where fewer than kSkLeastPiece tiles would lie on one side
+    for (int32_t u = threadIdx.x; u < p.sk_items; u += kSkPlanThreads) {  // this thread's own writes above
+        const int32_t tlo = rec[u].lo, n = rec[u].hi - tlo;
+        const int32_t clo = tlo + rec[u].next * kSkItemCost, chi = clo + n + kSkItemCost;
+        if (n == 0 || chi <= run_cost[0]) continue;
+        int32_t a = -1, b = ctas + 1;  // the last c with run_cost[c] < clo, the first past it
+        while (b - a > 1) {
+            const int32_t mid = (a + b) >> 1;
+            if (run_cost[mid] < clo) a = mid; else b = mid;
+        }
+        for (int32_t c = b; c <= ctas && run_cost[c] < chi; ++c) {
+            const int32_t at = run_cost[c] - clo;
+            run[c] = tlo + (at < kSkLeastPiece ? 0 : n - at < kSkLeastPiece ? n : at);
+        }
     }
     __syncthreads();
     // each item's next one with tiles, from the last run of threads to the
