@@ -111,15 +111,16 @@ __device__ __forceinline__ int32_t key_tile(const PrefillRowInfo &w, int32_t v)
     return kSink && v >= w.nst ? v + w.gap : v;
 }
 
-__device__ __forceinline__ bool prefill_item(const PrefillParams &p, int64_t bid, int qpc,
+// (a call has at most INT32_MAX items)
+__device__ __forceinline__ bool prefill_item(const PrefillParams &p, int32_t bid, int qpc,
                                              PrefillRowInfo &w)
 {
-    w.s = static_cast<int32_t>(bid % p.kv_splits);
+    w.s = bid % p.kv_splits;
     bid /= p.kv_splits;
-    const int32_t qt = static_cast<int32_t>(bid % p.q_tiles);
+    const int32_t qt = bid % p.q_tiles;
     bid /= p.q_tiles;
-    w.g = static_cast<int32_t>(bid % p.hkv);
-    w.r = static_cast<int32_t>(bid / p.hkv);
+    w.g = bid % p.hkv;
+    w.r = bid / p.hkv;
     const int32_t c0 = __ldg(p.cu_q_lens + w.r), c1 = __ldg(p.cu_q_lens + w.r + 1);
     int32_t C = c1 - c0;
     int32_t L = __ldg(p.seq_lens + w.r);
@@ -247,11 +248,10 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
 // First segment of CTA `cta` (false: nothing to do).  One CTA per item: the
 // item (or its key-range run; an empty run sets ntile <= 0).
 template <bool kSink>
-__device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64_t cta, SegWalk &sw,
+__device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int32_t c, SegWalk &sw,
                                           Seg &sg)
 {
     if (p.sk_ctas > 0) {
-        const int32_t c = static_cast<int32_t>(cta);
         const int32_t whole = sk_whole_item(p, c);
         sw.pos = sk_run_start(p, c);
         sw.end = sk_run_start(p, c + 1);
@@ -271,8 +271,8 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int64
         }
         return sk_next<kSink>(p, qpc, sw, sg);
     }
-    if (!prefill_item(p, cta, qpc, sg.w)) return false;
-    sg.item = static_cast<int32_t>(cta);
+    if (!prefill_item(p, c, qpc, sg.w)) return false;
+    sg.item = c;
     sg.jt0 = item_first_tile<kSink>(sg.w);
     sg.ntile = item_tiles(sg.w);
     sg.whole = p.kv_splits <= 1;
@@ -460,8 +460,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
 
     // query tiles: tile x row i = (query t = x * qpt + i / G, head h = i % G);
-    // the 8 softmax warps load 32 rows each (the first segment's here,
-    // the next segments' after each epilogue)
+    // the softmax warps load 32 rows each (a segment's before its first tile)
     // a negative scale: stage -q (sign bits flipped, exact), so that the
     // scores the tensor cores produce always take a positive factor
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -470,7 +469,6 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.cu_q_lens, p.hq, glog, qpt, w.r, w.i0, w.nq,
                           w.g, flip, p.status, q_s, warp - 4, lane);
     };
-    if (warp >= 4) load_q_rows(seg0.w);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -783,6 +781,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             p.sk_ctas > 0 ? (seg0.whole && sk_whole_item(p, blockIdx.x) >= 0 ? seg0.ntile : 0) +
                                 sk_run_start(p, blockIdx.x + 1) - sk_run_start(p, blockIdx.x)
                           : seg0.ntile;
+        load_q_rows(seg0.w);  // while the producers' first copies are under way
         if constexpr (kF8) {
             for (int32_t Tk = 0; do_k && Tk < min(2, T_total) && !abort; ++Tk)
                 if (!widen_k(Tk)) {
@@ -808,8 +807,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int32_t ntile = ss->sg.ntile, jt0 = ss->sg.jt0;
         const int32_t kv_lo = ss->sg.w.kv_lo, kv_hi = ss->sg.w.kv_hi;
         const int32_t nst = kSink ? ss->sg.w.nst : 0, gap = kSink ? ss->sg.w.gap : 0;
-        // the segment's query tile: staged (the first in the prologue), then
-        // handed to the MMA-issue warp
+        // the segment's query tile: staged (the first above), then handed to
+        // the MMA-issue warp
         if (k > 0) load_q_rows(ss->sg.w);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
@@ -1454,7 +1453,7 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
 {
     constexpr int kWarps = kSkPlanThreads / 32;
     __shared__ int32_t warp_sum[kWarps], warp_cnt[kWarps], warp_first[kWarps];
-    __shared__ int32_t carry, carry_cnt, after;
+    __shared__ int32_t carry, carry_cnt, after, whole_cost;
     __shared__ int32_t whole[kSkMaxCtas], cost[kSkMaxCtas], run[kSkMaxCtas + 1], run_item[kSkMaxCtas];
     __shared__ int32_t run_cost[kSkMaxCtas + 1];  // the runs' starts, each item counted kSkItemCost longer
     pdl_wait();  // lengths may come from the previous kernel on the stream
@@ -1474,6 +1473,9 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
     }
     for (int32_t i = threadIdx.x; i < ctas * 8; i += kSkPlanThreads) p.sk_count[i] = 0;
     __syncthreads();
+    // this thread's item of the first kSkPlanThreads stays in registers, later
+    // ones are read back
+    int32_t lo0 = 0, hi0 = 0, rank0 = 0;
     for (int32_t base = 0; base < p.sk_items; base += kSkPlanThreads) {
         const int32_t u = base + threadIdx.x;
         int32_t n = 0;
@@ -1514,6 +1516,11 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
             rec[u].lo = incl - n;
             rec[u].hi = incl;
             rec[u].next = rank;  // until the next items are known
+            if (base == 0) {
+                lo0 = incl - n;
+                hi0 = incl;
+                rank0 = rank;
+            }
             if (n > 0 && rank < ctas) {
                 whole[rank] = u;
                 cost[rank] = n + kSkItemCost;
@@ -1551,28 +1558,38 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
             const int32_t mid = (lo + hi) >> 1;
             if (room(mid) >= R) hi = mid; else lo = mid + 1;
         }
-        const int64_t total = room(lo);
-        int64_t before = 0;  // room of the CTAs before this group of 32
+        int32_t before = 0;  // room of the CTAs before this group of 32
         for (int32_t c0 = 0; c0 < ctas; c0 += 32) {
             const int32_t c = c0 + lane;
-            int64_t v = c < ctas ? max(0, lo - cost[c]) : 0;
+            int32_t v = c < ctas ? max(0, lo - cost[c]) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+                const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
                 if (lane >= d) v += o;
             }
-            if (c < ctas) run_cost[c + 1] = static_cast<int32_t>(B + (total > 0 ? R * (before + v) / total : 0));
+            if (c < ctas) run_cost[c + 1] = before + v;
             before += __shfl_sync(0xffffffffu, v, 31);
         }
-        if (lane == 0) run_cost[0] = B;
+        if (lane == 0) {
+            run_cost[0] = 0;
+            whole_cost = B;
+        }
     }
-    for (int32_t c = threadIdx.x; c <= ctas; c += kSkPlanThreads) run[c] = carry;  // the runs past the last item
+    __syncthreads();
+    // the rooms' running sums to costs, in proportion (the last one last)
+    const int64_t room_all = run_cost[ctas], R = W - whole_cost;
+    __syncthreads();
+    for (int32_t c = threadIdx.x; c <= ctas; c += kSkPlanThreads) {
+        run_cost[c] = static_cast<int32_t>(whole_cost + (room_all > 0 ? R * run_cost[c] / room_all : 0));
+        run[c] = carry;  // a run past the last item
+    }
     __syncthreads();
     // the runs' starts in tiles: the item whose cost holds a start places it, on
     // its end where fewer than kSkLeastPiece tiles would lie on one side
     for (int32_t u = threadIdx.x; u < p.sk_items; u += kSkPlanThreads) {  // this thread's own writes above
-        const int32_t tlo = rec[u].lo, n = rec[u].hi - tlo;
-        const int32_t clo = tlo + rec[u].next * kSkItemCost, chi = clo + n + kSkItemCost;
+        const bool mine = u < kSkPlanThreads;
+        const int32_t tlo = mine ? lo0 : rec[u].lo, n = (mine ? hi0 : rec[u].hi) - tlo;
+        const int32_t clo = tlo + (mine ? rank0 : rec[u].next) * kSkItemCost, chi = clo + n + kSkItemCost;
         if (n == 0 || chi <= run_cost[0]) continue;
         int32_t a = -1, b = ctas + 1;  // the last c with run_cost[c] < clo, the first past it
         while (b - a > 1) {
@@ -1590,7 +1607,10 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
     for (int32_t base = (p.sk_items - 1) / kSkPlanThreads * kSkPlanThreads; base >= 0; base -= kSkPlanThreads) {
         const int32_t u = base + threadIdx.x;
         int32_t lo = 0, hi = 0;
-        if (u < p.sk_items) {  // this thread's own writes above
+        if (base == 0) {
+            lo = lo0;
+            hi = hi0;
+        } else if (u < p.sk_items) {  // this thread's own writes above
             lo = rec[u].lo;
             hi = rec[u].hi;
         }
