@@ -61,6 +61,7 @@ constexpr int kVOff = kKOff + kStages * kTileBytes;
 constexpr int kF8BlockBytes = 16 * kD;                 // one (block, kv head) E4M3 tile
 constexpr int kF8StageTile = kBlocks * kF8BlockBytes;  // 8 KiB
 constexpr int kSoftmaxWarps = 8;  // 4-7 softmax of query tile A, 8-11 of tile B
+constexpr int kSegBytes = 160;    // a softmax warp's segment walk, current and next segment
 template <bool kF8>
 struct Layout {
     static constexpr int kStagingOff = kVOff + kStages * kTileBytes;
@@ -74,7 +75,7 @@ struct Layout {
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kTmemOff = kMaskOff + (kStages + 4) * 4;
     static constexpr int kSegOff = kTmemOff + 16;  // per softmax warp: its segment walk
-    static constexpr int kBytes = kSegOff + kSoftmaxWarps * 96;
+    static constexpr int kBytes = kSegOff + kSoftmaxWarps * kSegBytes;
     static constexpr int kLaunchBytes = kBytes + 1024;
     static_assert(kLaunchBytes <= 227 * 1024, "shared memory of one CTA");
 };
@@ -88,7 +89,9 @@ constexpr uint32_t kRescaleLog2 = 8;      // O is rescaled only when the max gro
 }  // namespace pf
 
 struct PrefillRowInfo {
-    int32_t r, g, i0, nq, L, C, kv_lo, kv_hi, s;
+    int32_t r, g, i0, nq;  // queries i0 .. i0 + nq - 1 of row r's chunk, at positions kv_hi - nq ..
+    int32_t q0;            // row of query i0 in q and out
+    int32_t kv_lo, kv_hi, s;
     // sinks (kSink): the item's key tiles are numbered from 0 over its nst sink
     // tiles, then the window's; tile v >= nst is key tile v + gap.  Without
     // sinks tiles carry their own number.
@@ -133,10 +136,9 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int32_t bid
         if (report_bad) report(p.status, PKV_DEV_BAD_LEN);
         C = c0 < 0 || C < 0 ? 0 : min(min(C, p.max_q_len), L);
     }
-    w.C = C;
-    w.L = L;
     w.i0 = qt * qpc;
     if (w.i0 >= C) return false;
+    w.q0 = c0 + w.i0;
     w.nq = min(qpc, C - w.i0);
     const int32_t p_first = L - C + w.i0;
     w.kv_hi = p_first + w.nq;
@@ -179,7 +181,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 // ---------------------------------------------------------------------------
 struct Seg {
     PrefillRowInfo w;
-    int32_t item;
     int32_t jt0;    // first key tile of the segment (64-key units, the item's numbering)
     int32_t ntile;  // tiles of the segment
     bool whole;     // the item's whole key range
@@ -231,7 +232,6 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
     const SkItem it = sk_load(p, sw.u);
     const int32_t seg_end = min(it.hi, sw.end);
     sg.w = it.w;
-    sg.item = sw.u;
     sg.jt0 = item_first_tile<kSink>(sg.w) + (sw.pos - it.lo);
     sg.ntile = seg_end - sw.pos;
     sg.whole = sw.pos == it.lo && seg_end == it.hi;
@@ -260,7 +260,6 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int32
         if (whole >= 0) {
             const SkItem it = sk_load(p, whole);
             sg.w = it.w;
-            sg.item = whole;
             sg.jt0 = item_first_tile<kSink>(sg.w);
             sg.ntile = it.hi - it.lo;
             sg.whole = true;
@@ -272,7 +271,6 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int32
         return sk_next<kSink>(p, qpc, sw, sg);
     }
     if (!prefill_item(p, c, qpc, sg.w)) return false;
-    sg.item = c;
     sg.jt0 = item_first_tile<kSink>(sg.w);
     sg.ntile = item_tiles(sg.w);
     sg.whole = p.kv_splits <= 1;
@@ -329,13 +327,13 @@ struct TileCursor {
 // positive factor.  Not inlined: a segment's staging then leaves the registers
 // of the softmax loop around it alone.
 template <bool kF8>
-__device__ __noinline__ void stage_q_rows(const uint4 *q, const int32_t *cu_q_lens, int32_t hq, int glog,
-                                          int qpt, int32_t r, int32_t i0, int32_t nq, int32_t g,
+__device__ __noinline__ void stage_q_rows(const uint4 *q, int32_t hq, int glog,
+                                          int qpt, int32_t q0, int32_t nq, int32_t g,
                                           uint32_t flip, int32_t *status, uint8_t *q_s, int wi, int lane)
 {
     constexpr int kD = pf::kD, kRows = pf::kRows;
     const int x = wi >> 2, c = lane & 15, first = 32 * (wi & 3) + (lane >> 4);
-    const uint4 *src = q + ((static_cast<int64_t>(__ldg(cu_q_lens + r)) + i0) * hq + (g << glog)) * (kD / 8) + c;
+    const uint4 *src = q + (static_cast<int64_t>(q0) * hq + (g << glog)) * (kD / 8) + c;
     uint8_t *qt_s = q_s + x * pf::kQBytes + (c >> 3) * (kRows * 128);
     uint4 v[16];
 #pragma unroll
@@ -466,8 +464,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     const int glog = __ffs(G) - 1;  // G divides the tile's 128 rows
     auto load_q_rows = [&](const PrefillRowInfo &w) {
-        stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.cu_q_lens, p.hq, glog, qpt, w.r, w.i0, w.nq,
-                          w.g, flip, p.status, q_s, warp - 4, lane);
+        stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.hq, glog, qpt, w.q0, w.nq, w.g, flip, p.status, q_s, warp - 4, lane);
     };
     tc::fence_before();
     __syncthreads();
@@ -789,31 +786,32 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     abort = true;
                 }
         }
-        // this warp's segment walk and current segment live in shared memory
-        // (lane 0 writes them): the tile loop keeps its registers
+        // this warp's segment walk, its current segment and the next one live in
+        // shared memory (lane 0 writes them): the tile loop keeps its registers
         struct SegSmem {
             SegWalk sw;
-            Seg sg;
+            Seg sg[2];  // segment k at k & 1
         };
-        static_assert(sizeof(SegSmem) <= 96, "the per-warp segment slot");
+        static_assert(sizeof(SegSmem) <= kSegBytes, "the per-warp segment slot");
         SegSmem *ss = reinterpret_cast<SegSmem *>(smem + L::kSegOff) + (warp - 4);
         if (lane == 0) {
             ss->sw = sw0;
-            ss->sg = seg0;
+            ss->sg[0] = seg0;
         }
         __syncwarp();
         int32_t T0 = 0;  // the segment's first tile in the running count
         for (int32_t k = 0; !abort; ++k) {
-        const int32_t ntile = ss->sg.ntile, jt0 = ss->sg.jt0;
-        const int32_t kv_lo = ss->sg.w.kv_lo, kv_hi = ss->sg.w.kv_hi;
-        const int32_t nst = kSink ? ss->sg.w.nst : 0, gap = kSink ? ss->sg.w.gap : 0;
+        const Seg &cs = ss->sg[k & 1];
+        const int32_t ntile = cs.ntile, jt0 = cs.jt0;
+        const int32_t kv_lo = cs.w.kv_lo, kv_hi = cs.w.kv_hi;
+        const int32_t nst = kSink ? cs.w.nst : 0, gap = kSink ? cs.w.gap : 0;
         // the segment's query tile: staged (the first above), then handed to
         // the MMA-issue warp
-        if (k > 0) load_q_rows(ss->sg.w);
+        if (k > 0) load_q_rows(cs.w);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
-        const bool valid_row = row < qpt * G && t < ss->sg.w.nq;
-        const int32_t qpos = ss->sg.w.L - ss->sg.w.C + ss->sg.w.i0 + t;
+        const bool valid_row = row < qpt * G && t < cs.w.nq;
+        const int32_t qpos = cs.w.kv_hi - cs.w.nq + t;
         const int32_t qlo = p.window > 0 ? max(0, qpos - p.window + 1) : 0;
         float m_ref = -INFINITY, l = 0.f;
         const bool warp_live = __any_sync(0xffffffffu, valid_row);
@@ -1068,8 +1066,20 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             if (lane == 0) mbar_arrive(&p_full[x * 2 + buf]);
         }
         if (abort) break;
-        const PrefillRowInfo &w = ss->sg.w;
+        const PrefillRowInfo &w = cs.w;
         if (p.drill & kDrillLate) __nanosleep(20000 + 4000 * (warp & 3));
+        // the next segment, read while the last product runs
+        bool more = false;
+        if (lane == 0) {
+            SegWalk sw = ss->sw;
+            Seg sg;
+            more = seg_next<kSink>(p, qpc, sw, sg);
+            if (more) {
+                ss->sw = sw;
+                ss->sg[(k + 1) & 1] = sg;
+            }
+        }
+        __syncwarp();
         // epilogue: O / l once the segment's last P.V product is in.  A parity
         // names one phase only while no later one can have completed: o_done
         // completes once a segment, and its next phase needs this warp.
@@ -1082,7 +1092,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             if (__any_sync(0xffffffffu, !done)) {
                 if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                 break;
-            } else if (p.sk_ctas > 0 && !ss->sg.whole) {
+            } else if (p.sk_ctas > 0 && !cs.whole) {
                 // a piece of an item cut by this CTA's run: a partial in the
                 // CTA's slot (first or last segment), merged afterwards.  Each
                 // warp's 32 rows lie dim-group major (float4 d4 of row `lane`
@@ -1093,7 +1103,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 const auto piece_at = [&](int32_t c, int32_t slot) {
                     return ((static_cast<size_t>(c) * 2 + slot) * kQTiles + x) * 4 + (warp & 3);
                 };
-                const size_t own = piece_at(blockIdx.x, ss->sg.slot);
+                const size_t own = piece_at(blockIdx.x, cs.slot);
                 float4 *dst = reinterpret_cast<float4 *>(p.sk_o) + own * (32 * kD / 4) + lane;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -1111,7 +1121,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // warp whose piece completes last merges their 32 rows (no
                 // waiting: the others published theirs before counting)
                 __syncwarp();
-                const int32_t cf = ss->sg.cf, cl = ss->sg.cl;
+                const int32_t cf = cs.cf, cl = cs.cl;
                 // CTAs between them may have empty runs
                 const auto piece_from = [&](int32_t c) {
                     while (c < cl && sk_run_start(p, c + 1) == sk_run_start(p, c)) ++c;
@@ -1129,7 +1139,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 last = __shfl_sync(0xffffffffu, last, 0);
                 if (last) {
                     // slot 1: the item is not c's first segment
-                    const int32_t slot_f = sk_run_start(p, cf) < ss->sg.lo ? 1 : 0;
+                    const int32_t slot_f = sk_run_start(p, cf) < cs.lo ? 1 : 0;
                     const auto piece = [&](int32_t c) { return piece_at(c, c == cf ? slot_f : 0); };
                     const float2 *ml = reinterpret_cast<const float2 *>(p.sk_ml) + lane;
                     const float4 *po = reinterpret_cast<const float4 *>(p.sk_o) + lane;
@@ -1143,7 +1153,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     }
                     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
                     uint4 *dst = reinterpret_cast<uint4 *>(p.out) +
-                                 ((static_cast<int64_t>(__ldg(p.cu_q_lens + w.r)) + w.i0 + t) * p.hq +
+                                 ((static_cast<int64_t>(w.q0) + t) * p.hq +
                                   w.g * G + row % G) * (kD / 8);
                     // 32 dims at a time, two pieces' loads in flight
 #pragma unroll 1
@@ -1236,7 +1246,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 __syncwarp();
                 const int ch = lane & 15;
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out) +
-                             ((static_cast<int64_t>(__ldg(p.cu_q_lens + w.r)) + w.i0) * p.hq + w.g * G) * (kD / 8) + ch;
+                             (static_cast<int64_t>(w.q0) * p.hq + w.g * G) * (kD / 8) + ch;
 #pragma unroll 4
                 for (int k = 0; k < 16; ++k) {
                     const int rr = 2 * k + (lane >> 4), i = 32 * (warp & 3) + rr;  // row of the warp, of the tile
@@ -1252,16 +1262,6 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         // product that read it has completed (the waits above)
         tc::fence_before();
         T0 += ntile;
-        bool more = false;
-        if (lane == 0) {
-            SegWalk sw = ss->sw;
-            Seg sg;
-            more = seg_next<kSink>(p, qpc, sw, sg);
-            if (more) {
-                ss->sw = sw;
-                ss->sg = sg;
-            }
-        }
         more = __shfl_sync(0xffffffffu, more, 0);
         __syncwarp();
         if (!more) break;
@@ -1295,11 +1295,11 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
     pdl_trigger();
     PrefillRowInfo w;
     if (!prefill_item(p, blockIdx.x, qpt, w)) return;
-    const int32_t row0 = __ldg(p.cu_q_lens + w.r) + w.i0;
+    const int32_t row0 = w.q0;
     if (tid < NQ) {
         const int t = tid / G;
         const bool valid = tid < qpt * G && t < w.nq;
-        const int32_t qpos = w.L - w.C + w.i0 + t;
+        const int32_t qpos = w.kv_hi - w.nq + t;
         phi[tid] = valid ? qpos + 1 : 0;
         plo[tid] = p.window > 0 ? max(0, qpos - p.window + 1) : 0;
         mrow[tid] = -INFINITY;
