@@ -10,7 +10,7 @@ Layouts (see ``include/pkv.h``): pools ``[num_blocks, num_kv_heads,
 block_size, head_dim]``; ``q``/``out`` ``[batch, num_q_heads, head_dim]``
 (prefill: ``[sum C, num_q_heads, head_dim]``); block tables int32
 ``[batch, max_blocks_per_seq]``; ``seq_lens`` int32 ``[batch]`` counting the
-tokens appended this step.
+tokens appended this step; rotary ``positions`` int32 ``[num_axes, tokens]``.
 """
 from __future__ import annotations
 

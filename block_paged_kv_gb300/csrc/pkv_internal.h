@@ -186,8 +186,8 @@ struct PrefillParams {
     int32_t split_tiles;
     float *ws_o;   // [batch][max_q_len][hq][kv_splits][128] unnormalised weighted values
     float *ws_ml;  // [batch][max_q_len][hq][kv_splits][2]: reference max (log2 units), weight sum
-    // persistent balanced schedule ("stream-K"; 0 = off): sk_ctas CTAs take
-    // equal runs of the (item, 64-key tile) sequence of the sk_items items
+    // persistent balanced schedule (0 = off): sk_ctas CTAs take
+    // level runs of the (item, 64-key tile) sequence of the sk_items items
     // (row, kv head, query-tile pair); a run that cuts an item writes a
     // partial to one of its CTA's two slots
     int32_t sk_ctas, sk_items;

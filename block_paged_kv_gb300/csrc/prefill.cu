@@ -2,7 +2,8 @@
 // a prefill chunk attends its cached prefix through the pages; "paged-cache.md":
 // chunk boundaries change the reduction order, not the result).  Query i of a
 // row's chunk sits at absolute position p = L - C + i and attends positions
-// max(0, p - W + 1) .. p: the whole prefix and the chunk causally.
+// max(0, p - W + 1) .. p (the whole prefix and the chunk causally for W = 0), and
+// with sinks the first S positions beside them.
 //
 // Tensor-core kernel (bf16 pools; FP8 pools the same kernel with widening),
 // work item = (row, kv head, two tiles of 128/G queries).  A tile's 128 M-rows
@@ -29,8 +30,8 @@
 //             term), and the epilogue O / l.  FP8 pools: tile A's warps also
 //             widen the staged K tiles to f16, tile B's the V tiles.
 // Schedules: one CTA per item while the items fit one wave; more items than
-// SMs: one persistent CTA per SM (a whole item, then an equal run of the
-// remaining items' tiles, cut pieces merged in the kernel).  A short chunk
+// SMs: one persistent CTA per SM (a whole item, then a run of the remaining
+// items' tiles that levels the CTAs, cut pieces merged in the kernel).  A short chunk
 // fills tile A only (tile B's warps stay idle, warps whose rows hold no query
 // skip the softmax work); on a grid too small for the GPU its key range is
 // cut into runs whose fp32 partials prefill_merge_kernel merges.
