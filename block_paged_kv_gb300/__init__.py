@@ -1008,7 +1008,8 @@ class BlockAllocator:
 
     def fork(self, req: int, n_tokens: int):
         """A new request that shares ``req``'s first ``n_tokens`` tokens: its id and
-        the page copy to make, ``(src, dst)``, or None when none is needed."""
+        the page copy to make, ``(src, dst)``, or None when none is needed.  Inside
+        a block that has expired it is refused (PKV_ERR_OUT_OF_BLOCKS)."""
         v = [ctypes.c_int32(-1) for _ in range(3)]
         _check("pkv_allocator_fork", _lib.pkv_allocator_fork(
             self._a, req, int(n_tokens), *[ctypes.byref(x) for x in v]))
@@ -1016,7 +1017,8 @@ class BlockAllocator:
 
     def truncate(self, req: int, n_tokens: int):
         """Roll ``req`` back to its first ``n_tokens`` tokens; the page copy to make,
-        ``(src, dst)``, or None."""
+        ``(src, dst)``, or None.  Into a block that has expired it is refused
+        (PKV_ERR_OUT_OF_BLOCKS)."""
         v = [ctypes.c_int32(-1) for _ in range(2)]
         _check("pkv_allocator_truncate", _lib.pkv_allocator_truncate(
             self._a, req, int(n_tokens), *[ctypes.byref(x) for x in v]))

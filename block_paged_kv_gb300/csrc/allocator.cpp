@@ -278,6 +278,7 @@ try {
     if (n_tokens > static_cast<int64_t>(r.table.size()) * a->bs) return PKV_ERR_INVALID_ARG;
     const size_t full = static_cast<size_t>(n_tokens / a->bs);
     const bool part = n_tokens % a->bs != 0;
+    if (part && r.table[full] < 0) return PKV_ERR_OUT_OF_BLOCKS;  // expired: nowhere to go on writing
     Request c;
     c.fresh = false;
     c.table.reserve(full + (part ? 1 : 0));
@@ -289,22 +290,20 @@ try {
     const auto entry = a->reqs.emplace(id, Request{}).first;
     int32_t from = -1, to = -1;
     if (part) {
-        if (r.table[full] >= 0) {
-            bool taken = false;
-            std::vector<int32_t> got;
-            try {
-                taken = a->take(1, got);
-            } catch (...) {
-                a->reqs.erase(entry);
-                throw;
-            }
-            if (!taken) {
-                a->reqs.erase(entry);
-                return PKV_ERR_OUT_OF_BLOCKS;
-            }
-            from = r.table[full];
-            to = got[0];
+        bool taken = false;
+        std::vector<int32_t> got;
+        try {
+            taken = a->take(1, got);
+        } catch (...) {
+            a->reqs.erase(entry);
+            throw;
         }
+        if (!taken) {
+            a->reqs.erase(entry);
+            return PKV_ERR_OUT_OF_BLOCKS;
+        }
+        from = r.table[full];
+        to = got[0];
         c.table.push_back(to);
     }
     for (size_t i = 0; i < full; ++i)
@@ -328,8 +327,9 @@ try {
     if (n_tokens > static_cast<int64_t>(r.table.size()) * a->bs) return PKV_ERR_INVALID_ARG;
     const size_t full = static_cast<size_t>(n_tokens / a->bs);
     const bool part = n_tokens % a->bs != 0;
+    if (part && r.table[full] < 0) return PKV_ERR_OUT_OF_BLOCKS;  // expired: nowhere to go on writing
     int32_t from = -1, to = -1;
-    if (part && r.table[full] >= 0) {
+    if (part) {
         const Block &tail = a->blocks[r.table[full]];
         if (tail.refcount > 1 || tail.published) {
             std::vector<int32_t> got;

@@ -57,7 +57,8 @@ typedef enum {
     PKV_ERR_UNSUPPORTED = 2,
     PKV_ERR_CUDA = 3,
     PKV_ERR_WORKSPACE = 4,
-    PKV_ERR_OUT_OF_BLOCKS = 5, /* block allocator: the pool (at its maximum) cannot hold the request */
+    PKV_ERR_OUT_OF_BLOCKS = 5, /* block allocator: the pool (at its maximum) cannot hold the request,
+                                  or the block that the call would go on in has expired */
     PKV_ERR_HOST_MEMORY = 6    /* fork, truncate, compact, copy-list check: host memory ran out */
 } pkv_status;
 
@@ -636,8 +637,12 @@ pkv_status pkv_allocator_expire_window(pkv_allocator *a, int32_t req, int32_t fi
  * entries stay -1); a block it holds only a part of cannot be shared, as both
  * would go on writing into it, so it gets one of its own: *src, *dst name the
  * page copy the caller makes (paged_copy_blocks) before either writes there,
- * -1, -1 when n_tokens ends on a block boundary or that entry has expired.
- * PKV_ERR_OUT_OF_BLOCKS changes nothing. */
+ * -1, -1 when n_tokens ends on a block boundary.  A fork inside a block that has
+ * expired is refused with PKV_ERR_OUT_OF_BLOCKS: there is no block that its next
+ * token could be written to, and reserve adds none where the table already
+ * reaches.  Expiry is not undone: the fork's attention from n_tokens on needs the
+ * blocks of its window (and sinks) to be there still.  PKV_ERR_OUT_OF_BLOCKS
+ * changes nothing. */
 pkv_status pkv_allocator_fork(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *new_req,
                               int32_t *src, int32_t *dst);
 
@@ -645,8 +650,10 @@ pkv_status pkv_allocator_fork(pkv_allocator *a, int32_t req, int32_t n_tokens, i
  * edited prompt): the blocks past them lose its reference, as in release.  A
  * last block that becomes partial and that another request holds or the prefix
  * table names is replaced by one of its own, and *src, *dst name the page copy
- * (else -1, -1): the next tokens would overwrite shared ones.
- * PKV_ERR_OUT_OF_BLOCKS changes nothing. */
+ * (else -1, -1): the next tokens would overwrite shared ones.  Rolling back into
+ * a block that has expired is refused with PKV_ERR_OUT_OF_BLOCKS, as for a fork;
+ * a request that may be rolled back is expired by the window of the position
+ * that it may return to.  PKV_ERR_OUT_OF_BLOCKS changes nothing. */
 pkv_status pkv_allocator_truncate(pkv_allocator *a, int32_t req, int32_t n_tokens, int32_t *src,
                                   int32_t *dst);
 

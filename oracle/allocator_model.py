@@ -180,9 +180,10 @@ class AllocatorModel:
         full, copy, table = n_tokens // self.bs, None, []
         if n_tokens % self.bs:
             b = self.tables[r][full]
-            if b >= 0:
-                copy = (b, self._own_block())
-            table = [copy[1] if copy else -1]
+            if b < 0:           # expired: no block to go on writing into
+                raise OutOfBlocks()
+            copy = (b, self._own_block())
+            table = [copy[1]]
         c = self.begin()
         self.fresh[c] = False
         for b in self.tables[r][:full]:
@@ -199,8 +200,10 @@ class AllocatorModel:
         assert 0 <= n_tokens <= len(t) * self.bs
         full, copy = n_tokens // self.bs, None
         keep = -(-n_tokens // self.bs)
-        if keep > full and t[full] >= 0:
+        if keep > full:
             b = t[full]
+            if b < 0:           # expired: no block to go on writing into
+                raise OutOfBlocks()
             if self.refcount[b] > 1 or b in self.hash_of_block:
                 copy = (b, self._own_block())
                 self._drop(b)
