@@ -332,12 +332,25 @@ try {
     if (part) {
         const Block &tail = a->blocks[r.table[full]];
         if (tail.refcount > 1 || tail.published) {
+            // a block of its own: a free one; where the pool would have to evict
+            // or to grow for it, the lowest private block that this call releases
+            size_t own = r.table.size();
+            if (a->free_set.empty() && (!a->lru.empty() || a->num_blocks() < a->max_blocks))
+                for (size_t i = full + 1; i < r.table.size(); ++i)
+                    if (r.table[i] >= 0 && a->blocks[r.table[i]].refcount == 1 && !a->blocks[r.table[i]].published &&
+                        (own == r.table.size() || r.table[i] < r.table[own]))
+                        own = i;
             std::vector<int32_t> got;
-            if (!a->take(1, got)) return PKV_ERR_OUT_OF_BLOCKS;
+            if (own < r.table.size())
+                to = r.table[own];
+            else if (a->take(1, got))
+                to = got[0];
+            else
+                return PKV_ERR_OUT_OF_BLOCKS;
             from = r.table[full];
-            to = got[0];
             a->drop_ref(from);
             r.table[full] = to;
+            if (own < r.table.size()) r.table[own] = -1;  // moved, not released
         }
     }
     const size_t keep = full + (part ? 1 : 0);

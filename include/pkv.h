@@ -650,7 +650,11 @@ pkv_status pkv_allocator_fork(pkv_allocator *a, int32_t req, int32_t n_tokens, i
  * edited prompt): the blocks past them lose its reference, as in release.  A
  * last block that becomes partial and that another request holds or the prefix
  * table names is replaced by one of its own, and *src, *dst name the page copy
- * (else -1, -1): the next tokens would overwrite shared ones.  Rolling back into
+ * (else -1, -1): the next tokens would overwrite shared ones.  That block is
+ * taken as a reservation takes it, but where the reservation would evict a cached
+ * block or grow the pool, an unpublished block that this call releases from req
+ * alone (the lowest id) serves instead; the copy's *dst may thus be a block of
+ * req's old table.  Where the reservation would be refused, so is the call.  Rolling back into
  * a block that has expired is refused with PKV_ERR_OUT_OF_BLOCKS, as for a fork;
  * a request that may be rolled back is expired by the window of the position
  * that it may return to.  PKV_ERR_OUT_OF_BLOCKS changes nothing. */

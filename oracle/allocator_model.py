@@ -205,7 +205,14 @@ class AllocatorModel:
             if b < 0:           # expired: no block to go on writing into
                 raise OutOfBlocks()
             if self.refcount[b] > 1 or b in self.hash_of_block:
-                copy = (b, self._own_block())
+                # rather than evict or grow: the lowest private block that goes anyway
+                own = sorted(x for x in t[keep:] if x >= 0 and self.refcount[x] == 1 and
+                             x not in self.hash_of_block)
+                if own and not self.free and (self.lru or self.num_blocks < self.max_blocks):
+                    copy = (b, own[0])
+                    t[t.index(own[0])] = -1
+                else:
+                    copy = (b, self._own_block())
                 self._drop(b)
                 t[full] = copy[1]
         for b in t[keep:]:

@@ -44,3 +44,34 @@ def test_places_beside_the_expired_ones_are_not(make, n):
     for q in (r, c):
         m.reserve(q, n + 1)                         # token n has a block
         assert m.table(q)[n // 4] >= 0
+
+
+def test_a_rollback_evicts_and_grows_nothing_while_it_frees_blocks(make):
+    m = make(4, 5, 10)
+    s = m.begin()
+    m.reserve(s, 4)
+    m.publish(s, [9] * 4)
+    m.release(s)                                    # block 0 cached
+    r, toks = m.begin(), list(range(16))
+    m.reserve(r, 16)                                # blocks 1 .. 4: none is free now
+    m.publish(r, toks[:8])                          # 1, 2 published, 3 and 4 private
+    assert m.truncate(r, 7) == (2, 3)               # 3 goes with the rollback: it holds the copy
+    assert m.table(r) == [1, 3] and m.refs(5) == [0, 1, 0, 1, 0]
+    assert m.stats() == (5, 1, 2, 0)                # 4 free; 0 and 2 cached; no growth
+    t = m.begin()
+    assert m.find_cached_prefix(t, [9] * 4) == 4    # the cached prefix is still there
+
+
+def test_a_rollback_grows_where_it_frees_nothing_private(make):
+    m = make(4, 3, 6)
+    r, toks = m.begin(), list(range(12))
+    m.reserve(r, 12)
+    m.publish(r, toks)                              # all three published
+    assert m.truncate(r, 6) == (1, 3)               # the pool doubles
+    assert m.table(r) == [0, 3] and m.stats() == (6, 2, 2, 1)
+    c, _ = m.fork(r, 8)                             # shares 0 and 3
+    m.reserve(r, 12)                                # 4 is private ...
+    m.reserve(c, 16)                                # ... 5 is c's, and 1 is evicted for it
+    assert m.table(r) == [0, 3, 4] and m.table(c) == [0, 3, 1, 5] and m.stats() == (6, 0, 1, 1)
+    assert m.truncate(r, 5) == (3, 4) and m.table(r) == [0, 4]   # 2 stays cached
+    assert m.stats() == (6, 0, 1, 1) and m.refs(6) == [2, 1, 0, 1, 1, 1]
