@@ -105,6 +105,27 @@ bool decode_shape_built(pkv_dtype dtype, int32_t D, int32_t bs, int32_t G)
     return (D == 32 || D == 64 || D == 128 || D == 256) && bs <= 64 && bs * D <= 4096;
 }
 
+// The most blocks a row's key range can have.
+int64_t plan_blocks(int32_t max_len, int32_t bs, int32_t window, int32_t sinks)
+{
+    int64_t n = ceil_div64(max_len, bs);
+    if (window > 0) n = std::min<int64_t>(n, ceil_div64(window, bs) + 1 + ceil_div64(sinks, bs));
+    return std::max<int64_t>(n, 1);
+}
+
+// How a plan cuts its rows: split sizes come to about `target` CTAs and at least
+// `least` blocks.
+struct SplitRule {
+    bool few;  // fewer (row, kv head) pairs than SMs
+    int64_t target, least;
+};
+
+SplitRule split_rule(int64_t pairs, int num_sms)
+{
+    const bool few = pairs < num_sms;
+    return {few, static_cast<int64_t>(std::max(num_sms, 1)) * (few ? 2 : 9), few ? 4 : 8};
+}
+
 // The split plan: a pure function of the sizes and the SM count.
 DecodePlan make_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
                      int32_t max_len, int32_t window, const pkv_prefix_desc *prefix,
@@ -112,9 +133,7 @@ DecodePlan make_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t 
 {
     DecodePlan pl{};
     const int32_t G = hq / hkv;
-    int64_t nblk_max = ceil_div64(max_len, bs);
-    if (window > 0) nblk_max = std::min<int64_t>(nblk_max, ceil_div64(window, bs) + 1 + ceil_div64(sinks, bs));
-    nblk_max = std::max<int64_t>(nblk_max, 1);
+    const int64_t nblk_max = plan_blocks(max_len, bs, window, sinks);
     const int64_t tiles_ub = static_cast<int64_t>(batch) * nblk_max * hkv;
     // Split size over the upper bound of (block, kv head) tiles, a multiple of
     // the consumer warp count.  Many (row, kv head) pairs: about nine CTAs
@@ -124,11 +143,10 @@ DecodePlan make_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t 
     // query per row and for four).  Fewer pairs than SMs (a few long rows):
     // two CTAs per SM, one wave, since each CTA pays a fixed start-up cost
     // and the merge reads every partial; at least 4 blocks per split.
-    const int64_t pairs = static_cast<int64_t>(batch) * hkv;
-    const bool few = pairs < num_sms;
-    const int64_t target = static_cast<int64_t>(std::max(num_sms, 1)) * (few ? 2 : 9);
-    int64_t C = ceil_div64(tiles_ub, target);
-    C = std::max<int64_t>(C, few ? 4 : 8);
+    const SplitRule rule = split_rule(static_cast<int64_t>(batch) * hkv, num_sms);
+    const bool few = rule.few;
+    int64_t C = ceil_div64(tiles_ub, rule.target);
+    C = std::max<int64_t>(C, rule.least);
     C = ceil_div64(C, kDecodeWarps) * kDecodeWarps;
     const int32_t ov = g_split_override.load();
     if (ov > 0) C = ov;
@@ -183,6 +201,27 @@ size_t ws_o_bytes(int32_t batch, int32_t hq, int32_t D, const DecodePlan &pl)
 size_t ws_total_bytes(int32_t batch, int32_t hq, int32_t D, const DecodePlan &pl)
 {
     return ws_o_bytes(batch, hq, D, pl) + static_cast<size_t>(batch) * hq * pl.nslot * 2 * sizeof(float);
+}
+
+// Bytes to report for calls of these sizes: enough for every plan over lengths
+// up to max_len.  A call plans with its own bound (its table may hold less than
+// max_len), and a shorter row can take more splits than a longer one, as the
+// split size moves in steps: 76 blocks in splits of 12 are 7, 72 in splits of 8
+// are 9.  A plan of n blocks has splits of C >= max(least, n * pairs / target), so
+// at most min(ceil(n / least), ceil(target / pairs)) of them.
+size_t ws_query_bytes(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs, int32_t max_len,
+                      int32_t window, const pkv_prefix_desc *prefix, int32_t sinks, int32_t queries = 1)
+{
+    const int sms = num_sms_current();
+    DecodePlan pl = make_plan(batch, hq, hkv, D, bs, max_len, window, prefix, PKV_BF16, sms, sinks);
+    const int64_t pairs = static_cast<int64_t>(batch) * hkv;
+    if (pairs > 0 && g_split_override.load() == 0) {
+        const SplitRule rule = split_rule(pairs, sms);
+        pl.n_suffix_splits = static_cast<int32_t>(
+            std::min(ceil_div64(plan_blocks(max_len, bs, window, sinks), rule.least), ceil_div64(rule.target, pairs)));
+        pl.nslot = pl.n_prefix_splits + pl.n_suffix_splits;
+    }
+    return ws_total_bytes(batch * queries, hq, D, pl);
 }
 
 bool valid_prefix(const pkv_prefix_desc *prefix, int32_t batch, int32_t width)
@@ -580,9 +619,8 @@ size_t paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t n
     // the f32, bf16 and FP8 plans differ only in how many CTAs cover a
     // prefix group's rows, which does not change the slot count: the size
     // holds for every pool dtype
-    const DecodePlan pl = make_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                    max_seq_len, window, prefix, PKV_BF16, num_sms_current());
-    return ws_total_bytes(batch, num_q_heads, head_dim, pl);
+    return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window,
+                          prefix, 0);
 }
 
 pkv_status paged_decode_attention(const void *q, int32_t num_q_heads, const pkv_pool *pool,
@@ -604,10 +642,8 @@ size_t paged_decode_sinks_workspace_size(int32_t batch, int32_t num_q_heads, int
     if (batch < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
         head_dim <= 0 || block_size <= 0 || max_seq_len < 0 || window < 0 || sinks < 0)
         return 0;
-    const DecodePlan pl = make_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                    max_seq_len, window, nullptr, PKV_BF16, num_sms_current(),
-                                    window > 0 ? sinks : 0);
-    return ws_total_bytes(batch, num_q_heads, head_dim, pl);
+    return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len, window,
+                          nullptr, window > 0 ? sinks : 0);
 }
 
 pkv_status paged_decode_attention_sinks(const void *q, int32_t num_q_heads, const pkv_pool *pool,
@@ -744,11 +780,16 @@ int32_t prefill_items(int32_t batch, int32_t hq, int32_t hkv, int32_t max_q_len)
 
 // The decode plan for a verify step: the key range of a row spans its
 // queries' windows.
+int32_t verify_window(int32_t window, int32_t max_q_len)
+{
+    return window > 0 ? static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(window) + max_q_len - 1, INT32_MAX))
+                      : 0;
+}
+
 DecodePlan verify_plan(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t bs,
                        int32_t max_len, int32_t window, int32_t max_q_len, int32_t sinks)
 {
-    const int32_t span = static_cast<int32_t>(std::min<int64_t>(static_cast<int64_t>(window) + max_q_len - 1, INT32_MAX));
-    return make_plan(batch, hq, hkv, D, bs, max_len, window > 0 ? span : 0, nullptr, PKV_BF16,
+    return make_plan(batch, hq, hkv, D, bs, max_len, verify_window(window, max_q_len), nullptr, PKV_BF16,
                      num_sms_current(), sinks);
 }
 
@@ -763,11 +804,9 @@ size_t prefill_ws(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int3
     // scratch only for short bf16 chunks: the decode kernel's split partials
     // (a few queries per row), or the prefill kernel's key-range runs
     const int32_t G = num_q_heads / num_kv_heads;
-    if (verify_on_decode(G, head_dim, block_size, max_q_len)) {
-        const DecodePlan pl = verify_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
-                                          max_seq_len, window, max_q_len, sinks);
-        return ws_total_bytes(batch * max_q_len, num_q_heads, head_dim, pl);
-    }
+    if (verify_on_decode(G, head_dim, block_size, max_q_len))
+        return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                              verify_window(window, max_q_len), nullptr, sinks, max_q_len);
     const int sms = num_sms_current();
     const PrefillSplit sp = prefill_split_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
                                                max_q_len, max_seq_len, window, sinks, sms);

@@ -8,7 +8,6 @@
 // device and may fail under memory pressure).  For them this file keeps the
 // scratch in the library's own device image: a fixed array that exists on
 // every GPU that loads the library, from load until the process exits.
-#include <algorithm>
 #include <mutex>
 
 #include <cuda_runtime.h>
@@ -53,16 +52,9 @@ extern "C" pkv_status paged_decode_attention_no_alloc(
     void *scratch = nullptr;
     const pkv_status st = scratch_for_current_device(&scratch);
     if (st != PKV_OK) return st;
-    // the same plan the workspace entry point makes for these sizes
-    int64_t len = max_seq_len;
-    if (max_blocks_per_seq > 0 && pool->block_size > 0)
-        len = std::min<int64_t>(len, static_cast<int64_t>(max_blocks_per_seq) * pool->block_size);
-    const size_t need = paged_decode_workspace_size(batch, num_q_heads, pool->num_kv_heads,
-                                                    pool->head_dim, pool->block_size,
-                                                    static_cast<int32_t>(len), window, prefix);
-    if (need > PKV_NO_ALLOC_SCRATCH_BYTES) return PKV_ERR_WORKSPACE;
-    // the split partials are written before they are read, so the previous
-    // call's contents need no clearing
+    // the call itself refuses a plan that the scratch does not hold; the split
+    // partials are written before they are read, so the previous call's contents
+    // need no clearing
     return paged_decode_attention(q, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens,
                                   batch, max_seq_len, window, scale, out, scratch,
                                   PKV_NO_ALLOC_SCRATCH_BYTES, prefix, dev_status, stream);

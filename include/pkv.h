@@ -222,7 +222,10 @@ pkv_status paged_copy_blocks(const pkv_pool *src, const pkv_pool *dst, int32_t n
  * The size does not depend on the pool's dtype: f32, bf16 and FP8 pools of
  * the same sizes take the same workspace (the plan's partial slots per row do
  * not change with the dtype; only how many CTAs share a prefix group's rows
- * does).  Returns 0 for invalid sizes.
+ * does).  It holds for every shorter length too (a call whose table or
+ * max_seq_len is smaller may plan more splits): a workspace sized once for the
+ * longest context serves them all, here and in the other size queries.
+ * Returns 0 for invalid sizes.
  */
 size_t paged_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int32_t block_size, int32_t max_seq_len,
@@ -315,8 +318,9 @@ pkv_status paged_decode_attention_groups(const pkv_decode_group *groups, int32_t
  *     that first call before any stream capture.  After cudaDeviceReset the
  *     kept address is stale: do not call this entry point on that device
  *     again in the same process.
- *   - Sizes whose workspace (paged_decode_workspace_size) exceeds
- *     PKV_NO_ALLOC_SCRATCH_BYTES return PKV_ERR_WORKSPACE, nothing enqueued.
+ *   - Sizes whose partials exceed PKV_NO_ALLOC_SCRATCH_BYTES return
+ *     PKV_ERR_WORKSPACE, nothing enqueued (none whose
+ *     paged_decode_workspace_size fits it).
  *   - Every call on a device shares the one array and leaves its contents
  *     behind (nothing in it has to start at zero).  Calls that overlap on the
  *     GPU (different streams, or different host threads without ordering)
