@@ -264,8 +264,7 @@ cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t stream)
 {
     const size_t smem = f32_smem_bytes(p.head_dim, p.block_size, p.sinks);
     cudaError_t err = cudaFuncSetAttribute(decode_f32_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kF32SmemLimit);
     if (err != cudaSuccess) return err;
     if (p.plan.n_prefix_ctas > 0) {
         prof_begin(PKV_KERNEL_DECODE_PREFIX, stream);

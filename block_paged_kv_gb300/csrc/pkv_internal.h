@@ -208,6 +208,12 @@ struct PrefillParams {
 // the flags every decode / prefill launch carries.
 void drill_settings(uint64_t *wait_ns, uint32_t *flags);
 
+// Dynamic shared memory the f32 kernels may ask for (every built shape needs
+// less).  Set as one value whatever the call's shape: with each call's own size,
+// a second host thread's call could lower the limit between another's setting it
+// and its launch, which then failed.
+constexpr int kF32SmemLimit = 227 * 1024;
+
 cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_append_fp8(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_append_rope(const RopeParams &p, pkv_dtype dtype, int num_sms, cudaStream_t stream);

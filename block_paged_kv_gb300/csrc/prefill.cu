@@ -1784,8 +1784,7 @@ cudaError_t launch_prefill_f32(const PrefillParams &p, cudaStream_t stream)
     const size_t smem = sizeof(float) * (2 * NQ * D + 2 * bs * D + NQ * bs + 3 * NQ) +
                         sizeof(int32_t) * 2 * NQ;
     cudaError_t err = cudaFuncSetAttribute(prefill_f32_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(smem));
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kF32SmemLimit);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_PREFILL, stream);
     err = launch_pdl(prefill_f32_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPf32Threads),
