@@ -975,8 +975,8 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     if (pool->dtype != PKV_F32 && p.kv_splits == 1) {
         const int32_t sk = prefill_sk_ctas(pool->dtype, batch, num_q_heads, pool->num_kv_heads,
                                            pool->head_dim, pool->block_size, max_q_len, num_sms_current());
-        if (sk > 0) {
-            const int32_t items = prefill_items(batch, num_q_heads, pool->num_kv_heads, max_q_len);
+        const int32_t items = sk > 0 ? prefill_items(batch, num_q_heads, pool->num_kv_heads, max_q_len) : 0;
+        if (sk > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len, window, sinks)) {
             if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
                 ws_bytes < prefill_sk_ws_bytes(items, sk))
                 return PKV_ERR_WORKSPACE;

@@ -235,6 +235,10 @@ size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, cons
 int32_t prefill_sk_ctas(pkv_dtype dtype, int32_t batch, int32_t hq, int32_t hkv, int32_t D,
                         int32_t bs, int32_t max_q_len, int num_sms);
 size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas);
+// Whether the plan's 32-bit sums hold items of up to max_len keys (else the call
+// takes one CTA per item; past 65536 items of two million keys, say).
+bool prefill_sk_counts(int32_t items, int32_t max_q_len, int32_t group, int32_t max_len, int32_t window,
+                       int32_t sinks);
 cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream);
 cudaError_t launch_prefill_f32(const PrefillParams &p, cudaStream_t stream);

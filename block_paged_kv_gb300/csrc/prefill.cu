@@ -1547,7 +1547,7 @@ __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const P
         const int32_t R = W - B;
         // room(level) >= ctas * level - B, with equality while no whole item
         // passes the level: the even level is enough, and exact when it holds
-        // every whole item (costs below 2^30: 65536 items of 16384 tiles at most)
+        // every whole item (all costs together stay below 2^31: prefill_sk_counts)
         const auto room = [&](int32_t level) {
             int32_t sum = 0;
             for (int32_t c = lane; c < ctas; c += 32) sum += max(0, level - cost[c]);
@@ -1714,6 +1714,20 @@ int32_t prefill_sk_ctas(pkv_dtype dtype, int32_t batch, int32_t hq, int32_t hkv,
     // and a plan the one-CTA plan kernel scans quickly
     if (items <= num_sms || items > 65536 || num_sms > kSkMaxCtas) return 0;
     return num_sms;
+}
+
+bool prefill_sk_counts(int32_t items, int32_t max_q_len, int32_t group, int32_t max_len, int32_t window,
+                       int32_t sinks)
+{
+    const int64_t qpc = pf::kQTiles * (pf::kRows / group);
+    int64_t tiles = (static_cast<int64_t>(max_len) + pf::kKeys - 1) / pf::kKeys;
+    if (window > 0) {
+        // the window of the item's first query to its last one, and the sinks' tiles
+        const int64_t keys = static_cast<int64_t>(window) - 1 + std::min<int64_t>(qpc, max_q_len);
+        tiles = std::min(tiles, (keys + 2 * pf::kKeys - 2) / pf::kKeys +
+                                    (static_cast<int64_t>(sinks) + pf::kKeys - 1) / pf::kKeys);
+    }
+    return items * (tiles + kSkItemCost) <= INT32_MAX - (1 << 20);  // the margin: sums round up per CTA
 }
 
 size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas)
