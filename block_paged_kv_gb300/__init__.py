@@ -242,8 +242,12 @@ def _stream(device: torch.device) -> int:
 
 
 _NULL = contextlib.nullcontext()
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the bindings under torch.cuda's calls, which cost more than the library's own
+# checks; a torch built without CUDA lacks them (the allocator and the host
+# helpers work there all the same)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on(device: torch.device):
