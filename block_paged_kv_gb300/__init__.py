@@ -478,8 +478,9 @@ def paged_kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, slot_mappin
                          status: Optional[torch.Tensor] = None, k_scale: Optional[float] = None,
                          v_scale: Optional[float] = None) -> Optional[torch.Tensor]:
     """Rotate ``q`` [T, Hq, D] and ``k_new`` [T, Hkv, D] by ``positions`` ([T], or
-    [num_axes, T]; int32) and append the rotated k and ``v_new`` into the pools at
-    ``slot_mapping`` [T]; returns the rotated q (``q_out``, which may be ``q``).
+    [num_axes, T], which may be one row expanded; int32) and append the rotated k
+    and ``v_new`` into the pools at ``slot_mapping`` [T]; returns the rotated q
+    (``q_out``, which may be ``q``).
     Token rows may be cut from a wider projection output.  ``q`` None: k alone."""
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
     gpu, pdt = k_pool.get_device(), k_pool.dtype

@@ -1106,7 +1106,8 @@ pkv_status paged_kv_append_rope(const pkv_pool *pool, const int32_t *slot_mappin
     const int eb = elem_bytes(out_dtype(pool->dtype));
     const int64_t q_row = static_cast<int64_t>(num_q_heads) * pool->head_dim;
     const int64_t kv_row = static_cast<int64_t>(pool->num_kv_heads) * pool->head_dim;
-    if (slot_mapping == nullptr || positions == nullptr || (rope->num_axes > 1 && pos_stride < num_tokens) ||
+    if (slot_mapping == nullptr || positions == nullptr ||
+        (rope->num_axes > 1 && pos_stride != 0 && pos_stride < num_tokens) ||  // 0: one row for every axis
         !rope_rows_ok(k_new, k_stride, kv_row, eb) || !rope_rows_ok(v_new, v_stride, kv_row, eb))
         return PKV_ERR_INVALID_ARG;
     if (num_q_heads > 0 &&

@@ -181,6 +181,7 @@ pkv_status pkv_rope_init(pkv_rope *rope, int32_t rotary_dim, const double *inv_f
  *   k_new, v_new: device [num_tokens][num_kv_heads][head_dim], strides likewise
  *   q_out:  as q, with its own stride; may be q itself with the same stride
  *   positions: device int32 [num_axes][num_tokens], axes pos_stride elements apart
+ *           (0: one row of positions for every axis, as text has)
  * Types as for paged_kv_append (q and q_out: bf16 beside FP8 pools, else the
  * pool's).  Pointers 16-byte aligned and strides a multiple of 16 bytes, at
  * least a token's rows.  Built: rotary_dim a multiple of 16 (f32: 8) up to
