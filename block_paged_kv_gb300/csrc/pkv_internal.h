@@ -24,9 +24,9 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 // runs out with nothing in flight on its barrier.
 constexpr uint32_t kDrillWithholdFirst = PKV_DRILL_WITHHOLD_FIRST_LOAD;
 
-// Diagnostic drill flag: the softmax warps of the tensor-core prefill sleep
-// 20 us or more between handing over a segment's last weights and looking for
-// its output, long after the tensor cores have finished it.
+// Diagnostic drill flag: the softmax warps of the tensor-core prefill let 20 us
+// or more pass between handing over a segment's last weights and looking for its
+// output, long after the tensor cores have finished it.
 constexpr uint32_t kDrillLate = PKV_DRILL_LATE_CONSUMERS;
 
 struct AppendParams {
