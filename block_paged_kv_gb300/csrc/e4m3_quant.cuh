@@ -8,18 +8,22 @@ namespace pkv {
 // E4M3 codes of correctly rounded float32 quotients x / s (s > 0) without a
 // division, r = the correctly rounded reciprocal of s.
 //
-// q0 = RN(x * r) lies within one ulp of x / s (the rounding of the product
-// and r's own half ulp).  One correction step then gives the correctly
-// rounded quotient: e = x - s * q0 is exact (one fused multiply-add), and
-// RN(q0 + e * r) = RN(x / s) when r = RN(1/s) and q0 is within one ulp, in
-// the normal range (Markstein's theorem on the final step of an FMA
-// division: P. Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990).  The step is
-// taken where the last ulp can change the E4M3 code, 2^-11 <= |q0| <= 512:
-// below, the code is a zero of x's sign; above, E4M3 saturates (448); NaN
-// stays NaN.  Checked against the IEEE quotient on every bf16 input for
-// thousands of scales, codes compared, and against the oracle's codes in the
-// GPU tests.
+// q0 = RN(x * r) is off x / s by up to 1.5 ulp: half an ulp of the product's
+// rounding, up to one from r's (2^-24 relative).  One correction step, the final
+// step of an FMA division (P. Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990), brings the
+// quotient to its rounding but for rare last bits: e = x - s * q0 in one fused
+// multiply-add is exact or, at 25 bits, off by 2^-24 relative, and e * r by as
+// much again, so that q0 + e * r, before its rounding, is off x / s by at most
+// 1.5 ulp * 2^-23 = 3 * 2^-24 ulp.  The E4M3 code can differ from the quotient's
+// only where x / s lies that close to the rounding boundary beside a midpoint
+// between two codes; the significands of x and s for which it does are few, and
+// each of them was tried and gives the quotient's code (the CPU tests do it, for
+// any float32 x, beside every bf16 x at hundreds of scales; the GPU tests compare
+// with the oracle's codes).  The step is taken where the last ulp can change the
+// code, 2^-11 <= |q0| <= 512: below, the code is a zero of x's sign; above, E4M3
+// saturates (448); NaN stays NaN.  All this for scales of 2^-92 to 2^126, where
+// the last bits of e and r are normal.
 __device__ __forceinline__ float e4m3_quotient(float x, float s, float r)
 {
     const float q0 = __fmul_rn(x, r);
