@@ -565,7 +565,8 @@ static cudaError_t launch_rope_window(const RopeParams &p, cudaStream_t stream)
 
 // Calls of at least this many tokens into FP8 pools write whole tiles (measured
 // with 32 q and 8 kv heads of 128 dims, per token against windows: 512 tokens
-// 8.9 against 13.3 us, 1024 13.7 against 14.5, 2048 25 against 20, 8192 89 against 48).
+// 8.9 against 13.3 us, 1024 13.7 against 14.5, 2048 25 against 20, 8192 89 against 48:
+// they cross a little above it).  Other head counts and sizes were not measured.
 constexpr int32_t kRopeWindowTokens = 1024;
 
 cudaError_t launch_append_rope(const RopeParams &params, pkv_dtype dtype, int num_sms, cudaStream_t stream)

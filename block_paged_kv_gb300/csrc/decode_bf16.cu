@@ -9,7 +9,8 @@ namespace pkv {
 
 // A few long rows (the plan's coop flag), one query per row, no shared-prefix
 // items and one query n-tile: the cooperative kernel, whose warps share every
-// block (decode_coop.cuh).
+// block (decode_coop.cuh).  It does not number sink blocks: calls with sinks take
+// the many-row kernel at any size (not measured against a cooperative form).
 static bool coop_fits(const DecodeParams &p)
 {
     return p.plan.coop && p.sinks == 0 && p.cu_q_lens == nullptr && p.plan.n_prefix_ctas == 0 && p.group <= 8 &&

@@ -344,10 +344,11 @@ pkv_status paged_decode_attention_no_alloc(const void *q, int32_t num_q_heads,
  *     say) on grids too small to fill the GPU: their key ranges are cut into
  *     runs whose fp32 partials a second kernel merges;
  *   - longer chunks with more (row, kv head, 256-row query tile pair) items
- *     than SMs: one persistent CTA per SM takes an equal share of the items'
- *     64-key tiles (computed on the device from the actual lengths by a
- *     one-CTA plan kernel); an item cut by a CTA boundary is computed in
- *     pieces whose fp32 partials a merge kernel combines.
+ *     than SMs: one persistent CTA per SM takes a whole item and then a run of
+ *     the other items' 64-key tiles that levels the CTAs' costs (dealt on the
+ *     device from the actual lengths by a one-CTA plan kernel); the fp32
+ *     partials of an item that runs cut are merged by the warps that finish it.
+ *     Bounds that allow about 2^31 tiles in all turn it off (one CTA per item).
  * Both cuts depend only on the sizes, the lengths and the SM count, so a call
  * is bit-reproducible. */
 size_t paged_prefill_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -362,7 +363,10 @@ size_t paged_prefill_workspace_size(int32_t batch, int32_t num_q_heads, int32_t 
  * (C_r of them); its chunk's K/V must already be in the pool (paged_kv_append).
  * Query i of row r sits at p = seq_lens[r] - C_r + i and attends the positions
  * max(0, p - W + 1) .. p (W = 0: 0 .. p), i.e. the whole prefix and the chunk
- * causally.
+ * causally.  V rows that some query of a row's chunk attends are finite: in bf16
+ * and FP8 pools a NaN or infinity there may reach the chunk's other queries too
+ * (their weight for it is 0, and 0 times it is NaN).  Slots that no query of the
+ * row attends may hold anything, and so may K rows that a query does not.
  *   q, out:      device [cu_q_lens[batch]][num_q_heads][head_dim], pool.dtype
  *                (bf16 for FP8)
  *   cu_q_lens:   device int32 [batch + 1], non-decreasing, cu_q_lens[0] = 0
