@@ -1397,7 +1397,7 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
         const int k = j / D, d = j % D, t = k / G, h = k % G;
         if (k >= qpt * G || t >= w.nq) continue;
         const float l = lrow[k];
-        og[(static_cast<int64_t>(row0 + t) * p.hq + w.g * G + h) * D + d] = l > 0.f ? os[j] / l : 0.f;
+        og[(static_cast<int64_t>(row0 + t) * p.hq + w.g * G + h) * D + d] = l != 0.f ? os[j] / l : 0.f;  // (NaN stays NaN)
     }
 }
 

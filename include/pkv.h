@@ -26,7 +26,10 @@
  *   - window W > 0: a query at absolute position p attends positions
  *     max(0, p - W + 1) .. p; W = 0 is full attention;
  *   - an empty key range (seq_len 0) yields an all-zero output row;
- *   - softmax scores are scale * (q . k); accumulation is fp32.
+ *   - softmax scores are scale * (q . k); accumulation is fp32;
+ *   - a query with a NaN in q, or that attends one, has no defined output (the
+ *     other queries' outputs are not touched by it, but for V rows within a
+ *     prefill chunk, see there).
  *
  * Ownership and errors.  Every pointer named "device" is device memory owned
  * by the caller; the library allocates no device memory.  All calls are
