@@ -322,9 +322,9 @@ pkv_status paged_decode_attention_groups(const pkv_decode_group *groups, int32_t
  *     that first call before any stream capture.  After cudaDeviceReset the
  *     kept address is stale: do not call this entry point on that device
  *     again in the same process.
- *   - Sizes whose partials exceed PKV_NO_ALLOC_SCRATCH_BYTES return
- *     PKV_ERR_WORKSPACE, nothing enqueued (none whose
- *     paged_decode_workspace_size fits it).
+ *   - Calls whose partials exceed PKV_NO_ALLOC_SCRATCH_BYTES return
+ *     PKV_ERR_WORKSPACE, nothing enqueued; none is refused whose
+ *     paged_decode_workspace_size is within it.
  *   - Every call on a device shares the one array and leaves its contents
  *     behind (nothing in it has to start at zero).  Calls that overlap on the
  *     GPU (different streams, or different host threads without ordering)
