@@ -30,7 +30,7 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_WORKSPAC
 PKV_ERR_HOST_MEMORY = 6
 PKV_F32, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_BAD_PREFIX, DEV_TIMEOUT = 1, 2, 4, 8, 16
-DEV_Q_RANGE = 32
+DEV_Q_RANGE, DEV_BAD_PATH = 32, 64
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it first "
@@ -67,7 +67,13 @@ class _Rope(ctypes.Structure):
                 ("freq", ctypes.c_uint64 * ROPE_MAX_PAIRS), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS)]
 
 
+class _LatentPool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
 MAX_DECODE_GROUPS = 4
+MAX_TREE = 64
 
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _PP, _XP = ctypes.POINTER(_Pool), ctypes.POINTER(_Prefix)
@@ -174,8 +180,29 @@ _lib.pkv_allocator_refcount.argtypes = [_vp, _i32]
 _lib.pkv_allocator_refcount.restype = _i32
 _lib.pkv_allocator_stats.argtypes = [_vp, _i32p, _i32p, _i32p, _i32p]
 _lib.pkv_allocator_stats.restype = ctypes.c_int
+_LP = ctypes.POINTER(_LatentPool)
+_lib.paged_tree_workspace_size.argtypes = [_i32] * 8
+_lib.paged_tree_workspace_size.restype = _sz
+_lib.paged_tree_attention.argtypes = [_vp, _vp, _vp, _i32, _PP, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                      ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
+_lib.paged_tree_attention.restype = ctypes.c_int
+_lib.pkv_tree_masks_host.argtypes = [_vp, _vp, _i32, _vp]
+_lib.pkv_tree_masks_host.restype = ctypes.c_int
+_lib.paged_tree_commit.argtypes = [_PP, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.paged_tree_commit.restype = ctypes.c_int
+_lib.paged_latent_tree_commit.argtypes = [_LP, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.paged_latent_tree_commit.restype = ctypes.c_int
+_lib.paged_latent_append.argtypes = [_LP, _vp, _i32, _vp, _i64, _vp, _i64, _vp, ctypes.c_float, _vp, _i64, _i64,
+                                     _i32, _vp, _i64, _RP, _vp, _i64, _i64, _vp, _vp]
+_lib.paged_latent_append.restype = ctypes.c_int
+_lib.paged_latent_workspace_size.argtypes = [_i32] * 7
+_lib.paged_latent_workspace_size.restype = _sz
+_lib.paged_latent_attention.argtypes = [_vp, _vp, _vp, _i32, _LP, _vp, _i32, _vp, _i32, _i32, _i32,
+                                        ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
+_lib.paged_latent_attention.restype = ctypes.c_int
 
 KERNEL_APPEND, KERNEL_DECODE_PREFIX, KERNEL_DECODE_SPLIT, KERNEL_DECODE_COMBINE, KERNEL_PREFILL, KERNEL_COPY = range(6)
+KERNEL_LATENT = 6
 
 EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_attention",
             "paged_prefill_workspace_size", "paged_prefill_chunk_attention", "pkv_status_string",
@@ -193,7 +220,9 @@ EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_atte
             "paged_decode_groups_sinks_workspace_size", "paged_decode_attention_groups_sinks",
             "paged_prefill_sinks_workspace_size", "paged_prefill_chunk_attention_sinks",
             "pkv_allocator_expire_window", "pkv_allocator_fork", "pkv_allocator_truncate",
-            "pkv_allocator_compact"]
+            "pkv_allocator_compact", "paged_tree_workspace_size", "paged_tree_attention", "pkv_tree_masks_host",
+            "paged_tree_commit", "paged_latent_tree_commit", "paged_latent_append", "paged_latent_workspace_size",
+            "paged_latent_attention"]
 
 
 class PkvError(RuntimeError):
@@ -754,6 +783,344 @@ def paged_prefill_chunk_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, k_po
             width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, float(scale),
             out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             _ptr(status), _stream(dev)))
+    return out
+
+
+def tree_masks_host(parents, cu_q_lens) -> np.ndarray:
+    """Masks of drafted trees (library helper, host arrays): node i of row r, at
+    ``cu_q_lens[r] + i``, has parent ``parents[..]`` in -1 .. i - 1 (-1: the last
+    cached token) and attends its ancestors and itself.  int64 bit patterns, as
+    ``paged_tree_attention`` and ``paged_latent_attention`` take them."""
+    up = np.ascontiguousarray(np.asarray(parents, dtype=np.int32)).reshape(-1)
+    cu = np.ascontiguousarray(np.asarray(cu_q_lens, dtype=np.int32)).reshape(-1)
+    _require(cu.size >= 1 and cu[0] == 0 and cu[-1] == up.size, "cu_q_lens runs from 0 to the number of parents")
+    _require(bool((np.diff(cu) >= 0).all()), "cu_q_lens does not descend")
+    out = np.empty(up.size, dtype=np.int64)
+    _check("pkv_tree_masks_host", _lib.pkv_tree_masks_host(
+        up.ctypes.data if up.size else None, cu.ctypes.data, cu.size - 1, out.ctypes.data if up.size else None))
+    return out
+
+
+def tree_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                        max_q_len: int, max_seq_len: int, window: int = 0) -> int:
+    return int(_lib.paged_tree_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                              max_q_len, max_seq_len, window))
+
+
+def _workspace_ok(workspace, gpu) -> bool:
+    return workspace is None or (workspace.get_device() == gpu and workspace.is_contiguous())
+
+
+def _status_word(status, gpu) -> bool:
+    return status is None or (status.get_device() == gpu and status.dtype is torch.int32 and status.numel() >= 1)
+
+
+def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: torch.Tensor,
+                         k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Tensor,
+                         seq_lens: torch.Tensor, max_q_len: int, window: int, scale: float,
+                         out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                         max_seq_len: Optional[int] = None, status: Optional[torch.Tensor] = None,
+                         k_scale: Optional[float] = None, v_scale: Optional[float] = None) -> torch.Tensor:
+    """Attention of drafted trees against the paged cache; returns ``out`` [sum C, Hq, D].
+
+    Row r's ``C`` drafts sit at the last ``C`` positions of its ``seq_lens``; draft
+    i's query attends the cached tokens and the drafts whose bits ``tree_masks``
+    [sum C] (int64 bit patterns, ``tree_masks_host``) has set, j <= i.  With a
+    ``window`` (at least ``max_q_len``) a node counts from its depth in the tree.
+    ``max_q_len`` is at most ``MAX_TREE``."""
+    pool = _pool(k_pool, v_pool, k_scale, v_scale)
+    gpu, i32, qshape, tshape = k_pool.get_device(), torch.int32, q.shape, block_tables.shape
+    if not (len(qshape) == 3 and qshape[2] == pool.head_dim and q.is_contiguous() and q.get_device() == gpu and
+            q.dtype is (torch.float32 if pool.dtype == PKV_F32 else torch.bfloat16) and
+            block_tables.dtype is i32 and block_tables.is_contiguous() and block_tables.get_device() == gpu and
+            len(tshape) == 2 and seq_lens.dtype is i32 and seq_lens.is_contiguous() and
+            seq_lens.get_device() == gpu and seq_lens.shape == tshape[:1] and
+            cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
+            cu_q_lens.shape == (tshape[0] + 1,) and
+            tree_masks.dtype is torch.int64 and tree_masks.shape == qshape[:1] and tree_masks.is_contiguous() and
+            tree_masks.get_device() == gpu and
+            (out is None or (out.shape == qshape and out.dtype is q.dtype and out.is_contiguous() and
+                             out.get_device() == gpu)) and
+            _workspace_ok(workspace, gpu) and _status_word(status, gpu)):
+        dev = k_pool.device
+        _require(q.dim() == 3 and q.shape[2] == pool.head_dim and q.dtype == _act_dtype(k_pool.dtype) and
+                 q.is_contiguous() and q.device == dev, "q is [sum C, Hq, D], contiguous, pool dtype")
+        _i32_dev(cu_q_lens, "cu_q_lens", dev)
+        _i32_dev(block_tables, "block_tables", dev)
+        _i32_dev(seq_lens, "seq_lens", dev)
+        _require(block_tables.dim() == 2 and seq_lens.shape == block_tables.shape[:1] and
+                 cu_q_lens.shape == (block_tables.shape[0] + 1,),
+                 "block_tables [B, max_blocks], seq_lens [B], cu_q_lens [B+1]")
+        _require(tree_masks.dtype == torch.int64 and tree_masks.shape == q.shape[:1] and
+                 tree_masks.is_contiguous() and tree_masks.device == dev,
+                 f"tree_masks are contiguous int64 [sum C] on {dev}")
+        _on_device(out, "out", dev)
+        _require(out is None or (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()),
+                 "out matches q")
+        _on_device(workspace, "workspace", dev)
+        _status_ok(status, dev)
+        raise ValueError("paged_tree_attention: invalid arguments")
+    B, width = tshape
+    hq = qshape[1]
+    if max_seq_len is None:
+        max_seq_len = width * pool.block_size
+    # the plan reads the SM count of the current device
+    with _NULL if _current_device() == gpu else torch.cuda.device(gpu):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = alloc_workspace(
+                tree_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, pool.block_size, max_q_len,
+                                    max_seq_len, window), k_pool.device)
+        code = _lib.paged_tree_attention(
+            q.data_ptr(), cu_q_lens.data_ptr(), tree_masks.data_ptr(), hq, ctypes.byref(pool),
+            block_tables.data_ptr(), width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if code != PKV_OK:
+        raise PkvError("paged_tree_attention", code)
+    return out
+
+
+def _latent_pool(pool: torch.Tensor, latent_dim: int) -> _LatentPool:
+    shape, dt = pool.shape, pool.dtype
+    if not (len(shape) == 3 and pool.is_cuda and pool.is_contiguous() and 0 < latent_dim < shape[2]):
+        _require(len(shape) == 3, "a latent pool is [num_blocks, block_size, latent_dim + rope_dim]")
+        _require(pool.is_cuda, "pools live on the GPU")
+        _require(pool.is_contiguous(), "pools are contiguous")
+        raise ValueError("latent_dim lies below the pool's row")
+    return _LatentPool(pool.data_ptr(), shape[0], shape[1], latent_dim, shape[2] - latent_dim,
+                       PKV_BF16 if dt is torch.bfloat16 else _dtype_code(dt))
+
+
+class LatentPoolSet:
+    """The latent pools [num_blocks, block_size, latent_dim + rope_dim] of several
+    layers that share block ids, checked once: what ``paged_tree_commit`` moves
+    rows in.  Holds the tensors."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        _require(len(self.pools) > 0, "at least one pool")
+        self.device, self.n, self.gpu = self.pools[0].device, len(self.pools), self.pools[0].get_device()
+        # rows move whole: where the latent ends plays no part
+        self._c = (_LatentPool * self.n)(*[_latent_pool(t, t.shape[-1] - 1) for t in self.pools])
+        f = self.pools[0]
+        for t in self.pools:
+            _require(t.device == self.device, "every pool on one GPU")
+            _require(t.dtype == f.dtype and t.shape[1:] == f.shape[1:], "the pools share dtype, block size and row")
+
+    def __len__(self) -> int:
+        return self.n
+
+
+def paged_tree_commit(pools, block_tables: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor,
+                      path: torch.Tensor, path_lens: torch.Tensor, new_seq_lens: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Move the rows of an accepted path behind the cached tokens, in every pool of
+    ``pools`` (a ``PoolSet`` or a ``LatentPoolSet``); returns the rows' new lengths.
+
+    ``path`` [B, max_path] holds draft indexes, strictly ascending, of which row r's
+    first ``path_lens[r]`` count: draft ``path[r, i]``'s row goes to position n + i
+    (n: the row's tokens before its drafts)."""
+    gpu, i32 = pools.gpu, torch.int32
+    tshape, pshape = block_tables.shape, path.shape
+    if not (block_tables.dtype is i32 and seq_lens.dtype is i32 and cu_q_lens.dtype is i32 and path.dtype is i32 and
+            path_lens.dtype is i32 and block_tables.get_device() == gpu and seq_lens.get_device() == gpu and
+            cu_q_lens.get_device() == gpu and path.get_device() == gpu and path_lens.get_device() == gpu and
+            block_tables.is_contiguous() and seq_lens.is_contiguous() and cu_q_lens.is_contiguous() and
+            path.is_contiguous() and path_lens.is_contiguous() and len(tshape) == 2 and len(pshape) == 2 and
+            pshape[0] == tshape[0] and seq_lens.shape == tshape[:1] and path_lens.shape == tshape[:1] and
+            cu_q_lens.shape == (tshape[0] + 1,) and
+            (new_seq_lens is None or (new_seq_lens.dtype is i32 and new_seq_lens.shape == tshape[:1] and
+                                      new_seq_lens.is_contiguous() and new_seq_lens.get_device() == gpu)) and
+            _status_word(status, gpu)):
+        dev = pools.device
+        for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (cu_q_lens, "cu_q_lens"),
+                        (path, "path"), (path_lens, "path_lens"), (new_seq_lens, "new_seq_lens")):
+            if t is not None:
+                _i32_dev(t, name, dev)
+        _status_ok(status, dev)
+        raise ValueError("block_tables [B, max_blocks], path [B, max_path], seq_lens, path_lens and new_seq_lens "
+                         "[B], cu_q_lens [B+1]")
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty_like(seq_lens)
+    call = _lib.paged_latent_tree_commit if isinstance(pools, LatentPoolSet) else _lib.paged_tree_commit
+    args = (pools._c, pools.n, block_tables.data_ptr(), tshape[1], seq_lens.data_ptr(), cu_q_lens.data_ptr(),
+            tshape[0], path.data_ptr(), pshape[1], path_lens.data_ptr(), new_seq_lens.data_ptr(),
+            None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = call(*args)
+    else:
+        with torch.cuda.device(gpu):
+            code = call(*args)
+    if code != PKV_OK:
+        raise PkvError("paged_tree_commit", code)
+    return new_seq_lens
+
+
+def _latent_append_refuse(dev, dt, slot_mapping, latent_new, k_rope_new, positions, rope, q_rope, q_rope_out,
+                          norm_weight, status, row):
+    """The messages of paged_latent_append's checks."""
+    _i32_dev(slot_mapping, "slot_mapping", dev)
+    T = slot_mapping.shape[0] if slot_mapping.dim() == 1 else -1
+    for t, name in ((latent_new, "latent_new"), (k_rope_new, "k_rope_new"), (q_rope, "q_rope"),
+                    (q_rope_out, "q_rope_out"), (norm_weight, "norm_weight")):
+        if t is not None:
+            _on_device(t, name, dev)
+            _require(t.dtype == dt, f"{name} matches the pool dtype")
+            _require(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, f"{name}'s rows are contiguous")
+    _require(latent_new.dim() == 2 and k_rope_new.dim() == 2 and latent_new.shape[0] == T and
+             k_rope_new.shape[0] == T and latent_new.shape[1] + k_rope_new.shape[1] == row,
+             "latent_new [T, latent_dim] and k_rope_new [T, rope_dim] make up the pool's rows, one slot per token")
+    _require(norm_weight is None or norm_weight.shape == latent_new.shape[1:], "norm_weight is [latent_dim]")
+    _require(q_rope is not None or q_rope_out is None, "q_rope_out without q_rope")
+    _require(q_rope is None or (q_rope.dim() == 3 and q_rope.shape[0] == T and q_rope.shape[2] == k_rope_new.shape[1]),
+             "q_rope is [T, heads, rope_dim]")
+    _require(q_rope_out is None or q_rope_out.shape == q_rope.shape, "q_rope_out matches q_rope")
+    _require(positions.dtype == torch.int32 and positions.device == dev and
+             (positions.shape == (rope.num_axes, T) or (rope.num_axes == 1 and positions.shape == (T,))) and
+             (positions.stride(-1) == 1 or T <= 1),
+             "positions are int32 [num_axes, T] (or [T]) on the pool's GPU, each axis contiguous")
+    _status_ok(status, dev)
+
+
+def paged_latent_append(pool: torch.Tensor, slot_mapping: torch.Tensor, latent_new: torch.Tensor,
+                        k_rope_new: torch.Tensor, positions: torch.Tensor, rope: RopeDesc,
+                        q_rope: Optional[torch.Tensor] = None, q_rope_out: Optional[torch.Tensor] = None,
+                        norm_weight: Optional[torch.Tensor] = None, norm_eps: float = 1e-6,
+                        status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Write the rows [latent | rotated key] of ``latent_new`` [T, R] and ``k_rope_new``
+    [T, Dr] into the latent ``pool`` [num_blocks, block_size, R + Dr] at
+    ``slot_mapping`` [T], the latent normalised by its root mean square and
+    ``norm_weight`` [R] where that is given; returns ``q_rope`` [T, H, Dr] rotated
+    (``q_rope_out``, which may be ``q_rope`` or the tail of the absorbed queries).
+    Token rows may be cut from wider tensors.  ``positions`` as for
+    ``paged_kv_append_rope``; the descriptor's rotary_dim is Dr."""
+    shape, dt, gpu, i32 = latent_new.shape, pool.dtype, pool.get_device(), torch.int32
+    T, axes, kshape, pshape = slot_mapping.numel(), rope.num_axes, k_rope_new.shape, positions.shape
+    ok = (len(shape) == 2 and shape[0] == T and len(kshape) == 2 and kshape[0] == T and pool.dim() == 3 and
+          shape[1] + kshape[1] == pool.shape[2] and slot_mapping.dtype is i32 and slot_mapping.ndim == 1 and
+          slot_mapping.is_contiguous() and slot_mapping.get_device() == gpu and
+          latent_new.dtype is dt and k_rope_new.dtype is dt and latent_new.get_device() == gpu and
+          k_rope_new.get_device() == gpu and
+          (T == 0 or ((latent_new.stride(1) == 1 or shape[1] == 1) and (k_rope_new.stride(1) == 1 or kshape[1] == 1))) and
+          positions.dtype is i32 and positions.get_device() == gpu and
+          (pshape == (axes, T) or (axes == 1 and pshape == (T,))) and (positions.stride(-1) == 1 or T <= 1) and
+          (norm_weight is None or (norm_weight.dtype is dt and norm_weight.shape == shape[1:] and
+                                   norm_weight.get_device() == gpu and norm_weight.is_contiguous())) and
+          _status_word(status, gpu))
+    H, qp, op, qs, qh, os_, oh = 0, None, None, 0, 0, 0, 0
+    if ok:
+        if q_rope is None:
+            ok = q_rope_out is None
+        else:
+            qshape = q_rope.shape
+            ok = len(qshape) == 3 and qshape[0] == T and qshape[2] == kshape[1] and q_rope.dtype is dt and \
+                q_rope.get_device() == gpu and \
+                (q_rope_out is None or (q_rope_out.shape == qshape and q_rope_out.dtype is dt and
+                                        q_rope_out.get_device() == gpu))
+            if ok:
+                if q_rope_out is None:
+                    q_rope_out = torch.empty(qshape, dtype=dt, device=q_rope.device)
+                H, qp, op = qshape[1], q_rope.data_ptr(), q_rope_out.data_ptr()
+                (qs, qh, qd), (os_, oh, od) = q_rope.stride(), q_rope_out.stride()
+                if H == 1:
+                    qh = oh = qshape[2]
+                if T == 1:
+                    qs, os_ = H * qh, H * oh
+                ok = T == 0 or H == 0 or (qd == 1 and od == 1)
+    if not ok:
+        _latent_append_refuse(pool.device, dt, slot_mapping, latent_new, k_rope_new, positions, rope, q_rope,
+                              q_rope_out, norm_weight, status, pool.shape[-1])
+        raise ValueError("paged_latent_append: invalid arguments")
+    c = _latent_pool(pool, shape[1])
+    args = (ctypes.byref(c), slot_mapping.data_ptr(), T, latent_new.data_ptr(),
+            latent_new.stride(0) if T > 1 else shape[1], k_rope_new.data_ptr(),
+            k_rope_new.stride(0) if T > 1 else kshape[1], None if norm_weight is None else norm_weight.data_ptr(),
+            norm_eps, qp, qs, qh, H, positions.data_ptr(), positions.stride(0) if axes > 1 else T,
+            ctypes.byref(rope._c), op, os_, oh, None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = _lib.paged_latent_append(*args)
+    else:
+        with torch.cuda.device(gpu):
+            code = _lib.paged_latent_append(*args)
+    if code != PKV_OK:
+        raise PkvError("paged_latent_append", code)
+    return q_rope_out
+
+
+def latent_workspace_size(batch: int, num_q_heads: int, latent_dim: int, rope_dim: int, block_size: int,
+                          max_q_len: int, max_seq_len: int) -> int:
+    return int(_lib.paged_latent_workspace_size(batch, num_q_heads, latent_dim, rope_dim, block_size, max_q_len,
+                                                max_seq_len))
+
+
+def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int, block_tables: torch.Tensor,
+                           seq_lens: torch.Tensor, scale: float, cu_q_lens: Optional[torch.Tensor] = None,
+                           max_q_len: int = 1, tree_masks: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                           max_seq_len: Optional[int] = None,
+                           status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention over a latent ``pool`` [num_blocks, block_size, R + Dr] in the absorbed
+    form: ``q`` [queries, H, R + Dr] against whole rows, weighted sums of the rows'
+    latents into ``out`` [queries, H, R] (R = ``latent_dim``).
+
+    One query per row (decode) without ``cu_q_lens``; with it [B+1] the last C
+    positions of each row hold a chunk's queries, causally, or, with ``tree_masks``,
+    a drafted tree's (as for ``paged_tree_attention``)."""
+    c = _latent_pool(pool, latent_dim)
+    gpu, i32, dt, qshape, tshape = pool.get_device(), torch.int32, pool.dtype, q.shape, block_tables.shape
+    if not (len(qshape) == 3 and qshape[2] == pool.shape[2] and q.is_contiguous() and q.get_device() == gpu and
+            q.dtype is dt and block_tables.dtype is i32 and block_tables.is_contiguous() and
+            block_tables.get_device() == gpu and len(tshape) == 2 and seq_lens.dtype is i32 and
+            seq_lens.is_contiguous() and seq_lens.get_device() == gpu and seq_lens.shape == tshape[:1] and
+            (qshape[0] == tshape[0] and max_q_len == 1 if cu_q_lens is None else
+             (cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
+              cu_q_lens.shape == (tshape[0] + 1,))) and
+            (tree_masks is None or (cu_q_lens is not None and tree_masks.dtype is torch.int64 and
+                                    tree_masks.shape == qshape[:1] and tree_masks.is_contiguous() and
+                                    tree_masks.get_device() == gpu)) and
+            (out is None or (out.shape == (qshape[0], qshape[1], latent_dim) and out.dtype is dt and
+                             out.is_contiguous() and out.get_device() == gpu)) and
+            _workspace_ok(workspace, gpu) and _status_word(status, gpu)):
+        dev = pool.device
+        _require(q.dim() == 3 and q.shape[2] == pool.shape[2] and q.dtype == dt and q.is_contiguous() and
+                 q.device == dev, "q is [queries, H, latent_dim + rope_dim], contiguous, pool dtype")
+        _i32_dev(block_tables, "block_tables", dev)
+        _i32_dev(seq_lens, "seq_lens", dev)
+        _require(block_tables.dim() == 2 and seq_lens.shape == block_tables.shape[:1],
+                 "block_tables [B, max_blocks], seq_lens [B]")
+        if cu_q_lens is None:
+            _require(q.shape[0] == block_tables.shape[0] and max_q_len == 1, "one query per row without cu_q_lens")
+            _require(tree_masks is None, "tree_masks go with cu_q_lens")
+        else:
+            _i32_dev(cu_q_lens, "cu_q_lens", dev)
+            _require(cu_q_lens.shape == (block_tables.shape[0] + 1,), "cu_q_lens [B+1]")
+            _require(tree_masks is None or (tree_masks.dtype == torch.int64 and tree_masks.shape == q.shape[:1] and
+                                            tree_masks.is_contiguous() and tree_masks.device == dev),
+                     f"tree_masks are contiguous int64 [queries] on {dev}")
+        _on_device(out, "out", dev)
+        _on_device(workspace, "workspace", dev)
+        _status_ok(status, dev)
+        raise ValueError("out is [queries, H, latent_dim], contiguous, pool dtype")
+    B, width = tshape
+    H = qshape[1]
+    if max_seq_len is None:
+        max_seq_len = width * c.block_size
+    with _NULL if _current_device() == gpu else torch.cuda.device(gpu):
+        if out is None:
+            out = torch.empty((qshape[0], H, latent_dim), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = alloc_workspace(
+                latent_workspace_size(B, H, latent_dim, c.rope_dim, c.block_size, max_q_len, max_seq_len),
+                q.device)
+        code = _lib.paged_latent_attention(
+            q.data_ptr(), None if cu_q_lens is None else cu_q_lens.data_ptr(),
+            None if tree_masks is None else tree_masks.data_ptr(), H, ctypes.byref(c), block_tables.data_ptr(),
+            width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, scale, out.data_ptr(), workspace.data_ptr(),
+            workspace.nbytes, None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if code != PKV_OK:
+        raise PkvError("paged_latent_attention", code)
     return out
 
 

@@ -769,6 +769,17 @@ bool verify_on_decode(int32_t G, int32_t D, int32_t bs, int32_t max_q_len)
            decode_shape_built(PKV_BF16, D, bs, G);
 }
 
+// Queries of a row that a split item of a drafted tree takes: its 16 rows.
+int32_t tree_chunk(int32_t G, int32_t max_q_len) { return std::min(max_q_len, std::max(1, 16 / G)); }
+
+// Drafted trees on the split-KV decode kernel: those of 16 rows, and every one of
+// a head_dim that the tensor-core prefill is not built for.
+bool tree_on_decode(int32_t G, int32_t D, int32_t bs, int32_t max_q_len)
+{
+    return decode_shape_built(PKV_BF16, D, bs, G) &&
+           (static_cast<int64_t>(G) * max_q_len <= 16 || !prefill_shape_built(PKV_BF16, D, bs, G));
+}
+
 // Items of the tensor-core prefill: (row, kv head, query-tile pair).
 int32_t prefill_items(int32_t batch, int32_t hq, int32_t hkv, int32_t max_q_len)
 {
@@ -844,7 +855,7 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
                         const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
                         int32_t batch, int32_t max_q_len, int32_t max_seq_len, int32_t window,
                         int32_t sinks, float scale, void *out, void *workspace, size_t ws_bytes,
-                        int32_t *dev_status, pkv_stream_t stream)
+                        int32_t *dev_status, pkv_stream_t stream, const uint64_t *tree = nullptr)
 {
     if (!valid_pool(pool) || batch < 0 || num_q_heads <= 0 || max_q_len < 0 || max_seq_len < 0 ||
         window < 0 || sinks < 0 || !std::isfinite(scale))
@@ -858,12 +869,16 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     const int32_t G = num_q_heads / pool->num_kv_heads;
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * pool->block_size;
     if (pool->dtype != PKV_F32 &&
-        verify_on_decode(G, pool->head_dim, pool->block_size, max_q_len)) {
+        (tree != nullptr ? tree_on_decode(G, pool->head_dim, pool->block_size, max_q_len)
+                         : verify_on_decode(G, pool->head_dim, pool->block_size, max_q_len))) {
         // a few queries per row: the split-KV decode kernel with (query, head)
         // M-rows, then its merge
         const int32_t max_len = static_cast<int32_t>(std::min<int64_t>(max_seq_len, cap));
-        const DecodePlan pl = verify_plan(batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
-                                          pool->block_size, max_len, window, max_q_len, sinks);
+        DecodePlan pl = verify_plan(batch, num_q_heads, pool->num_kv_heads, pool->head_dim,
+                                    pool->block_size, max_len, window, max_q_len, sinks);
+        const int32_t q_chunk = tree != nullptr ? tree_chunk(G, max_q_len) : max_q_len;
+        const int32_t q_chunks = (max_q_len + q_chunk - 1) / q_chunk;
+        pl.n_suffix_ctas *= q_chunks;
         if (pl.n_suffix_ctas > INT32_MAX) return PKV_ERR_UNSUPPORTED;
         const int32_t prow = batch * max_q_len;
         const size_t need = ws_total_bytes(prow, num_q_heads, pool->head_dim, pl);
@@ -897,6 +912,9 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
         d.max_len = max_len;
         d.window = window;
         d.sinks = sinks;
+        d.tree = tree;
+        d.q_chunk = q_chunk;
+        d.q_chunks = q_chunks;
         d.scale_log2 = scale * 1.4426950408889634f;
         d.v_scale = 1.f;
         drill_settings(&d.wait_ns, &d.drill);
@@ -906,14 +924,14 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
         if (pool->dtype == PKV_FP8_E4M3) {
             d.scale_log2 *= pool->k_scale;
             d.v_scale = pool->v_scale;
-            err = launch_decode_fp8(d, st);
+            err = tree != nullptr ? launch_tree_fp8(d, st) : launch_decode_fp8(d, st);
         } else {
             if (!encode_fn_ready()) return PKV_ERR_CUDA;
             CUtensorMap kmap, vmap;
             if (!encode_pool_map_tile(&kmap, pool->k, *pool) ||
                 !encode_pool_map_tile(&vmap, pool->v, *pool))
                 return PKV_ERR_UNSUPPORTED;
-            err = launch_decode_bf16(d, kmap, vmap, st);
+            err = tree != nullptr ? launch_tree_bf16(d, kmap, vmap, st) : launch_decode_bf16(d, kmap, vmap, st);
         }
         if (err == cudaSuccess) err = launch_decode_combine(d, out_dtype(pool->dtype), st);
         return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -941,6 +959,7 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     p.max_q_len = max_q_len;
     p.window = window;
     p.sinks = sinks;
+    p.tree = tree;
     const int32_t qpt = prefill_queries_per_cta(pool->dtype, G);
     p.q_tiles = static_cast<int32_t>(ceil_div64(max_q_len, qpt));
     p.kv_splits = 1;
@@ -976,7 +995,8 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
         const int32_t sk = prefill_sk_ctas(pool->dtype, batch, num_q_heads, pool->num_kv_heads,
                                            pool->head_dim, pool->block_size, max_q_len, num_sms_current());
         const int32_t items = sk > 0 ? prefill_items(batch, num_q_heads, pool->num_kv_heads, max_q_len) : 0;
-        if (sk > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len, window, sinks)) {
+        if (sk > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len,
+                                        tree != nullptr ? verify_window(window, max_q_len) : window, sinks)) {
             if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
                 ws_bytes < prefill_sk_ws_bytes(items, sk))
                 return PKV_ERR_WORKSPACE;
@@ -1193,6 +1213,328 @@ pkv_status paged_copy_blocks(const pkv_pool *src, const pkv_pool *dst, int32_t n
         if (launch_copy_blocks(p, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// One launch's tensors (at most kCommitTensors); new_seq_lens: of the call's first launch alone.
+pkv_status commit_call(CommitParams &p, void *const *base, const int32_t *num_blocks, int32_t n_tensors, bool fp8,
+                       const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                       const int32_t *cu_q_lens, int32_t batch, const int32_t *path, int32_t max_path,
+                       const int32_t *path_lens, int32_t *new_seq_lens, int32_t *dev_status, pkv_stream_t stream)
+{
+    p.tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.cu_q_lens = cu_q_lens;
+    p.path = path;
+    p.path_lens = path_lens;
+    p.new_lens = new_seq_lens;
+    p.status = dev_status;
+    p.batch = batch;
+    p.width = max_blocks_per_seq;
+    p.max_path = max_path;
+    p.n_tensors = n_tensors;
+    for (int32_t z = 0; z < n_tensors; ++z) {
+        p.base[z] = base[z];
+        p.num_blocks[z] = num_blocks[z];
+    }
+    return launch_commit(p, fp8, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+bool commit_args_ok(const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                    const int32_t *cu_q_lens, const int32_t *path, int32_t max_path, const int32_t *path_lens,
+                    const int32_t *new_seq_lens)
+{
+    return block_tables != nullptr && max_blocks_per_seq > 0 && seq_lens != nullptr && cu_q_lens != nullptr &&
+           path != nullptr && max_path >= 1 && max_path <= PKV_MAX_TREE && path_lens != nullptr &&
+           new_seq_lens != nullptr && new_seq_lens != seq_lens && new_seq_lens != path_lens;
+}
+
+bool valid_latent_pool(const pkv_latent_pool *pool)
+{
+    return pool != nullptr && pool->data != nullptr && aligned16(pool->data) && pool->num_blocks > 0 &&
+           pool->block_size > 0 && pool->latent_dim > 0 && pool->rope_dim > 0 &&
+           (pool->dtype == PKV_F32 || pool->dtype == PKV_BF16 || pool->dtype == PKV_FP8_E4M3);
+}
+
+constexpr int32_t kCommitPools = PKV_MAX_COPY_POOLS;  // of one launch
+
+// rows cut from a wider tensor: aligned, whole 16-byte vectors apart
+bool cut_rows_ok(const void *ptr, int64_t stride, int64_t least, int eb)
+{
+    return ptr != nullptr && aligned16(ptr) && stride >= least && stride <= (1ll << 31) && (stride * eb) % 16 == 0;
+}
+
+bool latent_shape_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs)
+{
+    return dtype != PKV_FP8_E4M3 && latent % 16 == 0 && latent <= 512 && rope % 16 == 0 && rope <= 128 && bs <= 64;
+}
+
+// Workers and pairs of an item for these sizes on the current device.
+struct LatentPlan {
+    int32_t workers, rows;
+};
+LatentPlan latent_plan(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs, int num_sms)
+{
+    (void)dtype;
+    (void)latent;
+    (void)rope;
+    (void)bs;
+    return {2 * std::max(num_sms, 1), kLatentSimpleRows};
+}
+
+size_t latent_ws_bytes(const LatentPlan &pl, int32_t latent)
+{
+    const size_t pieces = static_cast<size_t>(pl.workers) * 2 * pl.rows;
+    const auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
+    return up(pieces * latent * sizeof(float)) + up(pieces * 2 * sizeof(float)) +
+           static_cast<size_t>(pl.workers) * 3 * sizeof(int32_t);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t block_size, int32_t max_q_len, int32_t max_seq_len, int32_t window)
+{
+    if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_q_len <= 0 ||
+        max_q_len > PKV_MAX_TREE || max_seq_len < 0 || window < 0 || head_dim <= 0 || block_size <= 0)
+        return 0;
+    if (tree_on_decode(num_q_heads / num_kv_heads, head_dim, block_size, max_q_len))
+        return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                              verify_window(window, max_q_len), nullptr, 0, max_q_len);
+    return prefill_ws(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_seq_len, window, 0);
+}
+
+pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
+                                int32_t num_q_heads, const pkv_pool *pool, const int32_t *block_tables,
+                                int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t batch,
+                                int32_t max_q_len, int32_t max_seq_len, int32_t window, float scale, void *out,
+                                void *workspace, size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (max_q_len > PKV_MAX_TREE || (batch > 0 && max_q_len > 0 && tree_masks == nullptr))
+        return PKV_ERR_INVALID_ARG;
+    if (window > 0 && window < max_q_len) return PKV_ERR_UNSUPPORTED;
+    // (a call without rows or queries launches nothing)
+    return prefill_call(q, cu_q_lens, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch, max_q_len,
+                        max_seq_len, window, 0, scale, out, workspace, ws_bytes, dev_status, stream, tree_masks);
+}
+
+pkv_status paged_tree_commit(const pkv_pool *pools, int32_t n_pools, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
+                             int32_t batch, const int32_t *path, int32_t max_path, const int32_t *path_lens,
+                             int32_t *new_seq_lens, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (pools == nullptr || n_pools < 1 || batch < 0) return PKV_ERR_INVALID_ARG;
+    const pkv_pool &f = pools[0];
+    for (int32_t l = 0; l < n_pools; ++l)
+        if (!valid_pool(&pools[l]) || pools[l].dtype != f.dtype || pools[l].block_size != f.block_size ||
+            pools[l].num_kv_heads != f.num_kv_heads || pools[l].head_dim != f.head_dim)
+            return PKV_ERR_INVALID_ARG;
+    if (batch == 0) return PKV_OK;
+    if (!commit_args_ok(block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, path, max_path, path_lens, new_seq_lens))
+        return PKV_ERR_INVALID_ARG;
+    const bool fp8 = f.dtype == PKV_FP8_E4M3;
+    const int64_t row_bytes = static_cast<int64_t>(f.head_dim) * elem_bytes(f.dtype);
+    if (row_bytes % 16 != 0 || (fp8 && !fp8_shape_built(&f)) || row_bytes / 16 * f.num_kv_heads > INT32_MAX / PKV_MAX_TREE)
+        return PKV_ERR_UNSUPPORTED;
+    for (int32_t l0 = 0; l0 < n_pools; l0 += kCommitPools) {
+        const int32_t nl = std::min(n_pools - l0, kCommitPools);
+        void *base[2 * kCommitPools];
+        int32_t blocks[2 * kCommitPools];
+        for (int32_t l = 0; l < nl; ++l) {
+            base[2 * l] = pools[l0 + l].k;
+            base[2 * l + 1] = pools[l0 + l].v;
+            blocks[2 * l] = blocks[2 * l + 1] = pools[l0 + l].num_blocks;
+        }
+        CommitParams p{};
+        p.block_size = f.block_size;
+        p.heads = f.num_kv_heads;
+        p.row_vecs = static_cast<int32_t>(row_bytes / 16);
+        const pkv_status st = commit_call(p, base, blocks, 2 * nl, fp8, block_tables, max_blocks_per_seq, seq_lens,
+                                          cu_q_lens, batch, path, max_path, path_lens, l0 == 0 ? new_seq_lens : nullptr,
+                                          dev_status, stream);
+        if (st != PKV_OK) return st;
+    }
+    return PKV_OK;
+}
+
+pkv_status paged_latent_tree_commit(const pkv_latent_pool *pools, int32_t n_pools, const int32_t *block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t *seq_lens, const int32_t *cu_q_lens,
+                                    int32_t batch, const int32_t *path, int32_t max_path, const int32_t *path_lens,
+                                    int32_t *new_seq_lens, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (pools == nullptr || n_pools < 1 || batch < 0) return PKV_ERR_INVALID_ARG;
+    const pkv_latent_pool &f = pools[0];
+    for (int32_t l = 0; l < n_pools; ++l)
+        if (!valid_latent_pool(&pools[l]) || pools[l].dtype != f.dtype || pools[l].block_size != f.block_size ||
+            pools[l].latent_dim != f.latent_dim || pools[l].rope_dim != f.rope_dim)
+            return PKV_ERR_INVALID_ARG;
+    if (batch == 0) return PKV_OK;
+    if (!commit_args_ok(block_tables, max_blocks_per_seq, seq_lens, cu_q_lens, path, max_path, path_lens, new_seq_lens))
+        return PKV_ERR_INVALID_ARG;
+    const int64_t row_bytes = (static_cast<int64_t>(f.latent_dim) + f.rope_dim) * elem_bytes(f.dtype);
+    if (f.dtype == PKV_FP8_E4M3 || row_bytes % 16 != 0 || row_bytes / 16 > INT32_MAX / PKV_MAX_TREE)
+        return PKV_ERR_UNSUPPORTED;
+    for (int32_t l0 = 0; l0 < n_pools; l0 += kCommitTensors) {
+        const int32_t nl = std::min(n_pools - l0, kCommitTensors);
+        void *base[kCommitTensors];
+        int32_t blocks[kCommitTensors];
+        for (int32_t l = 0; l < nl; ++l) {
+            base[l] = pools[l0 + l].data;
+            blocks[l] = pools[l0 + l].num_blocks;
+        }
+        CommitParams p{};
+        p.block_size = f.block_size;
+        p.heads = 1;
+        p.row_vecs = static_cast<int32_t>(row_bytes / 16);
+        const pkv_status st = commit_call(p, base, blocks, nl, false, block_tables, max_blocks_per_seq, seq_lens,
+                                          cu_q_lens, batch, path, max_path, path_lens, l0 == 0 ? new_seq_lens : nullptr,
+                                          dev_status, stream);
+        if (st != PKV_OK) return st;
+    }
+    return PKV_OK;
+}
+
+pkv_status paged_latent_append(const pkv_latent_pool *pool, const int32_t *slot_mapping, int32_t num_tokens,
+                               const void *latent_new, int64_t latent_stride, const void *k_rope_new,
+                               int64_t k_rope_stride, const void *norm_weight, float norm_eps, const void *q_rope,
+                               int64_t q_stride, int64_t q_head_stride, int32_t num_q_heads, const int32_t *positions,
+                               int64_t pos_stride, const pkv_rope *rope, void *q_rope_out, int64_t q_out_stride,
+                               int64_t q_out_head_stride, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (!valid_latent_pool(pool) || num_tokens < 0 || num_q_heads < 0 || rope == nullptr ||
+        !(norm_eps >= 0.f && std::isfinite(norm_eps)))
+        return PKV_ERR_INVALID_ARG;
+    const int32_t rd = rope->rotary_dim;
+    if (rd < 2 || rd % 2 != 0 || rd > 2 * PKV_ROPE_MAX_PAIRS || rd != pool->rope_dim || rope->num_axes < 1 ||
+        rope->num_axes > PKV_ROPE_MAX_AXES || !std::isfinite(rope->factor))
+        return PKV_ERR_INVALID_ARG;
+    for (int32_t i = 0; i < rd / 2; ++i)
+        if (rope->axis[i] >= rope->num_axes) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    const int eb = elem_bytes(pool->dtype);
+    if (slot_mapping == nullptr || positions == nullptr || !aligned16(norm_weight) ||
+        (rope->num_axes > 1 && pos_stride != 0 && pos_stride < num_tokens) ||  // 0: one row for every axis
+        !cut_rows_ok(latent_new, latent_stride, pool->latent_dim, eb) ||
+        !cut_rows_ok(k_rope_new, k_rope_stride, rd, eb))
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads > 0 &&
+        (!cut_rows_ok(q_rope, q_stride, 0, eb) || !cut_rows_ok(q_rope, q_head_stride, rd, eb) ||
+         !cut_rows_ok(q_rope_out, q_out_stride, 0, eb) || !cut_rows_ok(q_rope_out, q_out_head_stride, rd, eb) ||
+         (num_tokens > 1 && (q_stride < (num_q_heads - 1) * q_head_stride + rd ||
+                             q_out_stride < (num_q_heads - 1) * q_out_head_stride + rd)) ||
+         (q_rope == q_rope_out && (q_head_stride != q_out_head_stride || (num_tokens > 1 && q_stride != q_out_stride)))))
+        return PKV_ERR_INVALID_ARG;
+    if (pool->dtype == PKV_FP8_E4M3 || pool->latent_dim % 16 != 0 || pool->latent_dim > 512 ||
+        rd % (pool->dtype == PKV_F32 ? 8 : 16) != 0 ||
+        static_cast<int64_t>(pool->num_blocks) * pool->block_size > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    LatentAppendParams p{};
+    p.c_new = latent_new;
+    p.k_new = k_rope_new;
+    p.q = q_rope;
+    p.norm_weight = norm_weight;
+    p.pool = pool->data;
+    p.q_out = q_rope_out;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.status = dev_status;
+    p.c_stride = latent_stride * eb / 16;
+    p.k_stride = k_rope_stride * eb / 16;
+    p.q_stride = q_stride * eb / 16;
+    p.q_head_stride = q_head_stride * eb / 16;
+    p.q_out_stride = q_out_stride * eb / 16;
+    p.q_out_head_stride = q_out_head_stride * eb / 16;
+    p.pos_stride = pos_stride;
+    p.num_tokens = num_tokens;
+    p.heads = num_q_heads;
+    p.num_slots = pool->num_blocks * pool->block_size;
+    p.c_vecs = pool->latent_dim * eb / 16;
+    p.row_vecs = (pool->latent_dim + rd) * eb / 16;
+    p.rotary_dim = rd;
+    p.interleaved = rope->interleaved;
+    p.num_axes = rope->num_axes;
+    p.factor = rope->factor;
+    p.eps = norm_eps;
+    std::memcpy(p.freq, rope->freq, sizeof(uint64_t) * (rd / 2));
+    std::memcpy(p.axis, rope->axis, rd / 2);
+    return launch_latent_append(p, pool->dtype, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PKV_OK
+               : PKV_ERR_CUDA;
+}
+
+size_t paged_latent_workspace_size(int32_t batch, int32_t num_q_heads, int32_t latent_dim, int32_t rope_dim,
+                                   int32_t block_size, int32_t max_q_len, int32_t max_seq_len)
+{
+    if (batch < 0 || num_q_heads <= 0 || latent_dim <= 0 || rope_dim <= 0 || block_size <= 0 || max_q_len <= 0 ||
+        max_seq_len < 0)
+        return 0;
+    // the same for every type and length
+    const int sms = num_sms_current();
+    return std::max(latent_ws_bytes(latent_plan(PKV_F32, latent_dim, rope_dim, block_size, sms), latent_dim),
+                    latent_ws_bytes(latent_plan(PKV_BF16, latent_dim, rope_dim, block_size, sms), latent_dim));
+}
+
+pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
+                                  int32_t num_q_heads, const pkv_latent_pool *pool, const int32_t *block_tables,
+                                  int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t batch,
+                                  int32_t max_q_len, int32_t max_seq_len, float scale, void *out, void *workspace,
+                                  size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
+{
+    if (!valid_latent_pool(pool) || num_q_heads <= 0 || batch < 0 || max_q_len < 0 || max_seq_len < 0 ||
+        !std::isfinite(scale) || (cu_q_lens == nullptr && max_q_len != 1) ||
+        (tree_masks != nullptr && (cu_q_lens == nullptr || max_q_len > PKV_MAX_TREE)))
+        return PKV_ERR_INVALID_ARG;
+    if (batch == 0 || max_q_len == 0) return PKV_OK;
+    if (q == nullptr || out == nullptr || block_tables == nullptr || seq_lens == nullptr || max_blocks_per_seq <= 0 ||
+        !aligned16(q) || !aligned16(out))
+        return PKV_ERR_INVALID_ARG;
+    if (!latent_shape_built(pool->dtype, pool->latent_dim, pool->rope_dim, pool->block_size)) return PKV_ERR_UNSUPPORTED;
+    const LatentPlan pl = latent_plan(pool->dtype, pool->latent_dim, pool->rope_dim, pool->block_size, num_sms_current());
+    const int64_t per_row = ceil_div64(static_cast<int64_t>(max_q_len) * num_q_heads, pl.rows);
+    if (per_row * batch > INT32_MAX / 2 || static_cast<int64_t>(max_q_len) * num_q_heads > INT32_MAX / 2)
+        return PKV_ERR_UNSUPPORTED;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+        ws_bytes < latent_ws_bytes(pl, pool->latent_dim))
+        return PKV_ERR_WORKSPACE;
+    LatentParams p{};
+    p.q = q;
+    p.out = out;
+    p.pool = pool->data;
+    p.tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.cu_q_lens = cu_q_lens;
+    p.tree = tree_masks;
+    p.status = dev_status;
+    p.batch = batch;
+    p.heads = num_q_heads;
+    p.latent = pool->latent_dim;
+    p.rope = pool->rope_dim;
+    p.block_size = pool->block_size;
+    p.width = max_blocks_per_seq;
+    p.num_blocks = pool->num_blocks;
+    p.max_len = static_cast<int32_t>(
+        std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_blocks_per_seq) * pool->block_size));
+    p.max_q = max_q_len;
+    p.items_per_row = static_cast<int32_t>(per_row);
+    p.workers = pl.workers;
+    const size_t pieces = static_cast<size_t>(pl.workers) * 2 * pl.rows;
+    char *ws = static_cast<char *>(workspace);
+    p.ws_o = reinterpret_cast<float *>(ws);
+    ws += (pieces * p.latent * sizeof(float) + 255) & ~static_cast<size_t>(255);
+    p.ws_ml = reinterpret_cast<float *>(ws);
+    ws += (pieces * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
+    p.rec = reinterpret_cast<int32_t *>(ws);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    drill_settings(&p.wait_ns, &p.drill);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return launch_latent_simple(p, pool->dtype, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

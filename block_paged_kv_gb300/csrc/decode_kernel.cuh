@@ -152,7 +152,9 @@ using BlockIds = BlockIdsT<false>;
 // The work of CTA `cta` of one decode call (p), its K/V tensor maps (bf16)
 // given by reference to kernel-parameter memory.  kSink (split items only): the
 // row's blocks are its sink blocks, then its window's.
-template <int D, bool kMQ, bool kF8, int NQ, bool kSink = false>
+// kTree (kMQ only): the queries are a drafted tree's, each behind the cached
+// tokens and its own ancestors; an item takes q_chunk of the row's queries.
+template <int D, bool kMQ, bool kF8, int NQ, bool kSink = false, bool kTree = false>
 __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const CUtensorMap &vmap,
                                                   const DecodeParams &p, const int64_t cta)
 {
@@ -196,7 +198,8 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
     // query rows of a split item: the G heads of one query (decode), or
     // (query, head) pairs of a row's few queries (kMQ: a verify step); the
     // launch takes NQ so that R <= TR
-    const int R = kMQ ? G * p.max_q : G;
+    const int R = kMQ ? G * (kTree ? p.q_chunk : p.max_q) : G;
+    int32_t t0 = 0, first = 0;  // kTree: the item's first query, the position of the row's first draft
     // the block ids of the run (this warp's share of a split item; the whole
     // run for a prefix item, fetched by warp 0)
     BlockIdsT<kSink> ids;
@@ -236,6 +239,10 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
     };
     if (!prefix_item) {
         int64_t bid = cta - p.plan.n_prefix_ctas;
+        if constexpr (kTree) {  // chunks of one split side by side: they share its blocks through L2
+            t0 = static_cast<int32_t>(bid % p.q_chunks) * p.q_chunk;
+            bid /= p.q_chunks;
+        }
         const int32_t s = static_cast<int32_t>(bid % p.plan.n_suffix_splits);
         bid /= p.plan.n_suffix_splits;
         g = static_cast<int32_t>(bid % p.hkv);
@@ -252,7 +259,7 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
             ids.init(table_row + (n_guess > 0 ? b_guess : 0), warp, NW, n_guess, lane);
         }
         if constexpr (C::kQInRegs && !kMQ) load_q_direct();
-        const RowRange rr = row_range(p, row_r, s == 0 && g == 0);
+        const RowRange rr = row_range(p, row_r, s == 0 && g == 0 && t0 == 0);
         int32_t b1;
         if constexpr (kSink) {  // numbered over the sink blocks and the window's
             nsb = rr.nsb;
@@ -271,6 +278,12 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
         hi_all = rr.L;
         row_C = rr.C;
         row_q0 = rr.q0;
+        if constexpr (kTree) {
+            first = rr.L - rr.C;
+            row_C = min(rr.C - t0, p.q_chunk);
+            if (row_C <= 0) return;
+            row_q0 += t0;
+        }
         tiles = 1;
         if constexpr (C::kQInRegs && kMQ) load_q_direct();
         const int32_t nbw = nblk > warp ? (nblk - warp + NW - 1) / NW : 0;
@@ -528,6 +541,7 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
     const int va_tok = (lane >> 4) * 8 + (lane & 7), va_dof = ((lane >> 3) & 1) * 8;
     // key range of this lane's C columns: query rows 8n + 2cc + e
     int clo[NQ][2], chi[NQ][2];
+    uint64_t ctm[NQ][2];  // kTree: its mask
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
@@ -539,8 +553,15 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
                 hi = pair_row[kq] >= 0 ? pair_len[kq] : 0;
             } else if constexpr (kMQ) {
                 const int t = row / G;
-                hi = (row < R && t < row_C) ? hi_all - row_C + t + 1 : 0;
-                lo = (p.window > 0 && hi > 0) ? max(0, hi - p.window) : 0;
+                if constexpr (kTree) {
+                    const bool live = row < R && t < row_C;
+                    ctm[n][e] = live ? tree_mask(p.tree, row_q0 + t, t0 + t) : 0ull;
+                    hi = live ? first + t0 + t + 1 : 0;
+                    lo = (p.window > 0 && live) ? max(0, first + tree_depth(ctm[n][e]) + 1 - p.window) : 0;
+                } else {
+                    hi = (row < R && t < row_C) ? hi_all - row_C + t + 1 : 0;
+                    lo = (p.window > 0 && hi > 0) ? max(0, hi - p.window) : 0;
+                }
             } else if (row < R) {
                 lo = lo_all;
                 hi = hi_all;
@@ -651,7 +672,7 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
                 for (int e = 0; e < 2; ++e)
                     in = in && (chi[n][e] == 0 ||
                                 ((base_tok[i] >= clo[n][e] || (kSink && base_tok[i] + bs <= sink)) &&
-                                 base_tok[i] + bs <= chi[n][e]));
+                                 base_tok[i] + bs <= (kTree ? first : chi[n][e])));
             inside = inside && in;
         }
         if (__all_sync(0xffffffffu, inside)) {
@@ -670,7 +691,9 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
                     for (int e = 0; e < 4; ++e) {
                         const int pos = base_tok[i] + g8 + 8 * (e >> 1);
                         const int lo = clo[n][e & 1], hi = chi[n][e & 1];
-                        sv[i][n][e] = (okb[i] && (pos >= lo || (kSink && pos < sink)) && pos < hi)
+                        bool seen = okb[i] && (pos >= lo || (kSink && pos < sink)) && pos < hi;
+                        if constexpr (kTree) seen = seen && (pos < first || ((ctm[n][e & 1] >> (pos - first)) & 1u));
+                        sv[i][n][e] = seen
                                           ? sT[i][n][e] * p.scale_log2
                                           : -INFINITY;
                     }
@@ -900,19 +923,19 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
                 lsum += wgt * mlbuf[(w * R + row) * 2 + 1];
             }
         }
-        const size_t pi = kMQ ? partial_index(p, row_r, g * G + row % G, slot, row / G)
+        const size_t pi = kMQ ? partial_index(p, row_r, g * G + row % G, slot, row / G + t0)
                               : partial_index(p, row_r, g * G + row, slot);
         p.ws_o[pi * D + d] = acc;
         if (d == 0) *reinterpret_cast<float2 *>(p.ws_ml + pi * 2) = make_float2(M, lsum);
     }
 }
 
-template <int D, bool kMQ, bool kF8, int NQ, bool kSink>
+template <int D, bool kMQ, bool kF8, int NQ, bool kSink, bool kTree>
 __global__ void __launch_bounds__(kDecodeWarps * 32, KvCfg<D, kF8, NQ>::kCtasPerSm)
     decode_split_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap, const DecodeParams p)
 {
-    decode_split_body<D, kMQ, kF8, NQ, kSink>(kmap, vmap, p, blockIdx.x);
+    decode_split_body<D, kMQ, kF8, NQ, kSink, kTree>(kmap, vmap, p, blockIdx.x);
 }
 
 // Several decode calls in one launch (groups of a model's layers that share
@@ -947,13 +970,13 @@ static cudaError_t launch_split_grouped(const GroupedDecode &gd, cudaStream_t st
     return err;
 }
 
-template <int D, bool kMQ, bool kF8, int NQ = 1, bool kSink = false>
+template <int D, bool kMQ, bool kF8, int NQ = 1, bool kSink = false, bool kTree = false>
 static cudaError_t launch_split(const DecodeParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream)
 {
     const int64_t ctas = p.plan.n_prefix_ctas + p.plan.n_suffix_ctas;
     if (ctas == 0) return cudaSuccess;
-    auto kern = decode_split_kernel<D, kMQ, kF8, NQ, kSink>;
+    auto kern = decode_split_kernel<D, kMQ, kF8, NQ, kSink, kTree>;
     const int smem = KvSmem<D, kF8, NQ>::kLaunchBytes;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;

@@ -1,5 +1,5 @@
-// Host helpers of the C ABI: slot mapping, its debug check and shared-prefix
-// group derivation from block tables.  Plain C++ on host arrays.
+// Host helpers of the C ABI: slot mapping, its debug check, shared-prefix group
+// derivation from block tables and the masks of drafted trees.  Plain C++ on host arrays.
 #include <algorithm>
 #include <unordered_map>
 #include <unordered_set>
@@ -131,4 +131,27 @@ extern "C" int32_t pkv_prefix_groups_host(const int32_t *block_tables, int32_t m
         prefix_blocks[ngroups++] = run;
     }
     return ngroups;
+}
+
+extern "C" pkv_status pkv_tree_masks_host(const int32_t *parents, const int32_t *cu_q_lens, int32_t batch,
+                                          uint64_t *tree_masks)
+{
+    if (batch < 0 || (batch > 0 && cu_q_lens == nullptr)) return PKV_ERR_INVALID_ARG;
+    for (int32_t r = 0; r < batch; ++r) {
+        const int64_t n = static_cast<int64_t>(cu_q_lens[r + 1]) - cu_q_lens[r];
+        if (cu_q_lens[r] < 0 || n < 0 || n > PKV_MAX_TREE || (n > 0 && (parents == nullptr || tree_masks == nullptr)))
+            return PKV_ERR_INVALID_ARG;
+        for (int32_t i = 0; i < n; ++i) {
+            const int32_t up = parents[cu_q_lens[r] + i];
+            if (up < -1 || up >= i) return PKV_ERR_INVALID_ARG;
+        }
+    }
+    for (int32_t r = 0; r < batch; ++r) {
+        uint64_t *m = tree_masks + cu_q_lens[r];
+        for (int32_t i = 0; i < cu_q_lens[r + 1] - cu_q_lens[r]; ++i) {
+            const int32_t up = parents[cu_q_lens[r] + i];
+            m[i] = (up >= 0 ? m[up] : 0) | (1ull << i);
+        }
+    }
+    return PKV_OK;
 }

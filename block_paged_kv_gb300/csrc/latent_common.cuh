@@ -1,0 +1,271 @@
+// Work items, runs and partials of the attention over latent rows, shared by its
+// kernels and the merge.
+//
+// Item u = (row u / items_per_row, pairs kRows (u % items_per_row) .. of the row's
+// (query, head) pairs, query-major).  Its keys are the positions up to its last
+// query's, in tiles of kKeys.  The items' tiles in item order form one sequence;
+// worker c of n takes tiles T c / n .. T (c + 1) / n of the T there are, so that
+// every worker has the same work whatever the rows' lengths.  Only the first and
+// the last piece of a run can cut an item; a cut piece leaves a partial (maximum,
+// sum, weighted values) in slot 0 (first piece) or 1 of its worker, which the
+// merge kernel joins.
+#pragma once
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+struct LatentItem {
+    int32_t r;      // row
+    int32_t first;  // position of the row's first query
+    int32_t q0;     // its index in q
+    int32_t p0;     // the item's first pair of the row's
+    int32_t n;      // its pairs (0: the item is empty)
+    int32_t hi;     // keys 0 .. hi - 1
+    int32_t tiles;
+};
+
+template <int kRows, int kKeys>
+__device__ __forceinline__ LatentItem latent_item(const LatentParams &p, int32_t u, bool say = false)
+{
+    LatentItem it;
+    it.r = u / p.items_per_row;
+    it.p0 = (u - it.r * p.items_per_row) * kRows;
+    say = say && it.p0 == 0;
+    int32_t L = __ldg(p.seq_lens + it.r), C = 1;
+    it.q0 = it.r;
+    if (L < 0 || L > p.max_len) {
+        if (say) report(p.status, PKV_DEV_BAD_LEN);
+        L = L < 0 ? 0 : p.max_len;
+    }
+    if (p.cu_q_lens != nullptr) {
+        const int32_t c0 = __ldg(p.cu_q_lens + it.r), c1 = __ldg(p.cu_q_lens + it.r + 1);
+        C = c1 - c0;
+        if (c0 < 0 || C < 0 || C > p.max_q || C > L) {
+            if (say) report(p.status, PKV_DEV_BAD_LEN);
+            C = c0 < 0 || C < 0 ? 0 : min(min(C, p.max_q), L);
+        }
+        it.q0 = c0;
+    }
+    it.first = L - C;
+    it.n = max(0, min(kRows, C * p.heads - it.p0));
+    // a decode row of length 0 has a query and no key: one tile, fully masked
+    it.hi = it.n > 0 ? max(0, it.first + (it.p0 + it.n - 1) / p.heads + 1) : 0;
+    it.tiles = it.n > 0 ? max(1, (it.hi + kKeys - 1) / kKeys) : 0;
+    return it;
+}
+
+// Keys that a pair's query attends: positions below hi, and of those from `first`
+// on (drafts) the mask's alone (all bits set: a chain).
+struct LatentRange {
+    int32_t hi;
+    uint64_t mask;
+};
+__device__ __forceinline__ LatentRange latent_range(const LatentParams &p, const LatentItem &it, int32_t pair)
+{
+    LatentRange rg{0, ~0ull};
+    if (pair >= it.n) return rg;
+    const int32_t i = (it.p0 + pair) / p.heads;  // the row's query
+    rg.hi = max(0, it.first + i + 1);
+    if (p.tree != nullptr) rg.mask = tree_mask(p.tree, it.q0 + i, i);
+    return rg;
+}
+
+// A worker's run: it starts in item u, `lo` being that item's first tile.
+struct LatentRun {
+    int64_t pos, end;  // tiles still ahead, in the sequence
+    int64_t lo;
+    int32_t u;
+    int32_t k;         // pieces so far
+};
+struct LatentPiece {
+    LatentItem it;
+    int32_t u;
+    int32_t t0, n;     // tiles t0 .. t0 + n - 1 of the item
+    bool whole;        // all of them
+    int32_t slot;      // a cut piece's partial slot
+};
+
+// Every thread of the CTA (kThreads of them): worker `c`'s run, and the record of
+// the item that it begins and does not end; `sm`: kThreads / 32 + 4 words of
+// shared memory (64 bits).  An empty run has pos == end.
+template <int kRows, int kKeys, int kThreads>
+__device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c, int32_t least, bool record,
+                                                int64_t *sm)
+{
+    constexpr int kWarps = kThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t items = p.batch * p.items_per_row;
+    auto tiles_of = [&](int32_t u, bool say) {
+        return u < items ? static_cast<int64_t>(latent_item<kRows, kKeys>(p, u, say).tiles) : 0;
+    };
+    // tiles in all; with one pass of items, they are looked up once
+    const bool one = items <= kThreads;
+    int64_t mine = 0;
+    for (int32_t u = threadIdx.x; u < items; u += kThreads) mine += tiles_of(u, c == 0 && record);
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sm[warp] = sum;
+    __syncthreads();
+    int64_t T = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) T += sm[w];
+    const int64_t n = min(static_cast<int64_t>(p.workers), max(static_cast<int64_t>(1), T / least));
+    LatentRun run{0, 0, 0, 0, 0};
+    if (c < n) {
+        run.pos = T * c / n;
+        run.end = T * (c + 1) / n;
+    }
+    // items that hold the run's first and last tile
+    int64_t *found = sm + kWarps;  // first: item, lo; last: item, its end
+    __syncthreads();
+    if (threadIdx.x == 0) found[0] = found[2] = -1;
+    int64_t before = 0;
+    for (int32_t base = 0; base < items && run.pos < run.end; base += kThreads) {
+        const int64_t x = one ? mine : tiles_of(base + threadIdx.x, false);
+        int64_t inc = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += y;
+        }
+        __syncthreads();
+        if (lane == 31) sm[warp] = inc;
+        __syncthreads();
+        int64_t lo = before + inc - x;
+        int64_t all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) lo += sm[w];
+            all += sm[w];
+        }
+        if (lo <= run.pos && run.pos < lo + x) {
+            found[0] = base + threadIdx.x;
+            found[1] = lo;
+        }
+        if (lo <= run.end - 1 && run.end - 1 < lo + x) {
+            found[2] = base + threadIdx.x;
+            found[3] = lo + x;
+        }
+        before += all;
+        if (before >= run.end) break;
+    }
+    __syncthreads();
+    if (run.pos < run.end) {
+        run.u = static_cast<int32_t>(found[0]);
+        run.lo = found[1];
+    }
+    if (record && threadIdx.x == 0) {
+        // the item at the run's end goes on in later workers, and began here
+        int32_t u = -1, last = -1;
+        if (run.pos < run.end && found[3] > run.end) {
+            const int64_t E = found[3];
+            const bool began = found[2] != found[0] || run.pos == run.lo;
+            if (began) {
+                u = static_cast<int32_t>(found[2]);
+                last = static_cast<int32_t>((E * n + T - 1) / T - 1);  // the first worker that ends at or past E
+            }
+        }
+        p.rec[2 * c] = u;
+        p.rec[2 * c + 1] = last;
+        p.rec[2 * p.workers + c] = u >= 0 && found[2] != found[0] ? 1 : 0;  // its piece's slot
+    }
+    return run;
+}
+
+// Next piece of the run (false at its end).
+template <int kRows, int kKeys>
+__device__ __forceinline__ bool latent_next(const LatentParams &p, LatentRun &run, LatentPiece &pc)
+{
+    if (run.pos >= run.end) return false;
+    pc.it = latent_item<kRows, kKeys>(p, run.u);
+    while (run.lo + pc.it.tiles <= run.pos) {  // (items without a query have no tile)
+        run.lo += pc.it.tiles;
+        pc.it = latent_item<kRows, kKeys>(p, ++run.u);
+    }
+    const int64_t hi = run.lo + pc.it.tiles, stop = min(hi, run.end);
+    pc.u = run.u;
+    pc.t0 = static_cast<int32_t>(run.pos - run.lo);
+    pc.n = static_cast<int32_t>(stop - run.pos);
+    pc.whole = pc.n == pc.it.tiles;
+    pc.slot = run.k == 0 ? 0 : 1;
+    ++run.k;
+    run.pos = stop;
+    return true;
+}
+
+// Partials: value quad d4 of pair i of a piece, and its (maximum, sum).
+template <int kRows>
+__device__ __forceinline__ float4 *latent_part_o(const LatentParams &p, int32_t worker, int32_t slot)
+{
+    return reinterpret_cast<float4 *>(p.ws_o) + (static_cast<int64_t>(worker) * 2 + slot) * (p.latent / 4) * kRows;
+}
+template <int kRows>
+__device__ __forceinline__ float2 *latent_part_ml(const LatentParams &p, int32_t worker, int32_t slot)
+{
+    return reinterpret_cast<float2 *>(p.ws_ml) + (static_cast<int64_t>(worker) * 2 + slot) * kRows;
+}
+
+__device__ __forceinline__ int64_t latent_out_row(const LatentParams &p, const LatentItem &it, int32_t pair)
+{
+    return (static_cast<int64_t>(it.q0) * p.heads + it.p0 + pair) * p.latent;
+}
+
+// Joins the pieces of an item cut between workers: CTA (x, y) the item that
+// worker x's run begins, dims 64y .. 64y + 63.  A thread holds 16 dims of a pair.
+constexpr int kLatMergeThreads = 128;
+
+template <typename T, int kRows, int kKeys>
+__global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const LatentParams p)
+{
+    pdl_wait();  // the records and partials come from the kernel just before
+    const int32_t c = blockIdx.x, u = p.rec[2 * c], last = p.rec[2 * c + 1];
+    if (u < 0) return;
+    const LatentItem it = latent_item<kRows, kKeys>(p, u);
+    // the item began in the run's last piece: slot 0 if that was the first too
+    const int32_t s0 = p.rec[2 * p.workers + c];
+    for (int32_t idx = threadIdx.x; idx < 4 * kRows; idx += kLatMergeThreads) {
+        const int32_t pair = idx % kRows, d4 = blockIdx.y * 16 + (idx / kRows) * 4;
+        if (pair >= it.n || d4 * 4 >= p.latent) continue;
+        float M = -INFINITY;
+        for (int32_t w = c; w <= last; ++w) M = fmaxf(M, latent_part_ml<kRows>(p, w, w == c ? s0 : 0)[pair].x);
+        float4 acc[4] = {};
+        float l = 0.f;
+        if (M != -INFINITY)
+            for (int32_t w = c; w <= last; ++w) {
+                const float2 ml = latent_part_ml<kRows>(p, w, w == c ? s0 : 0)[pair];
+                const float4 *o = latent_part_o<kRows>(p, w, w == c ? s0 : 0) + d4 * kRows + pair;
+                const float f = fast_exp2(ml.x - M);
+                l = fmaf(f, ml.y, l);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 v = o[e * kRows];
+                    acc[e].x = fmaf(f, v.x, acc[e].x);
+                    acc[e].y = fmaf(f, v.y, acc[e].y);
+                    acc[e].z = fmaf(f, v.z, acc[e].z);
+                    acc[e].w = fmaf(f, v.w, acc[e].w);
+                }
+            }
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
+        T *out = static_cast<T *>(p.out) + latent_out_row(p, it, pair) + d4 * 4;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                reinterpret_cast<float4 *>(out)[e] =
+                    make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+        } else {
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
+                v[2 * e + 1] = pack_bf16x2(acc[e].z * inv, acc[e].w * inv);
+            }
+            reinterpret_cast<uint4 *>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4 *>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+}  // namespace pkv

@@ -56,6 +56,26 @@ __device__ __forceinline__ void pdl_trigger()
 }
 
 // ---------------------------------------------------------------------------
+// drafted trees: the mask of draft i of a row (bit j = it attends draft j)
+// ---------------------------------------------------------------------------
+// Drafts after i are not attended, whatever their bits.
+__device__ __forceinline__ uint64_t tree_mask(const uint64_t *tree, int64_t packed, int32_t i)
+{
+    return __ldg(tree + packed) & (i >= 63 ? ~0ull : (2ull << i) - 1ull);
+}
+// The draft's place behind the cached tokens: its ancestors, itself not counted.
+__device__ __forceinline__ int32_t tree_depth(uint64_t mask) { return max(__popcll(mask) - 1, 0); }
+// Bits of the 64 positions from `base` on that the mask allows, the row's drafts
+// starting at position `first`: every cached position, and the mask's drafts.
+__device__ __forceinline__ uint64_t tree_bits(uint64_t mask, int32_t base, int32_t first)
+{
+    const int32_t d = first - base;  // cached positions ahead
+    if (d >= 64) return ~0ull;
+    if (d >= 0) return ((1ull << d) - 1ull) | (mask << d);
+    return d <= -64 ? 0ull : mask >> -d;
+}
+
+// ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)

@@ -77,6 +77,66 @@ struct CopyParams {
     int32_t dst_num_blocks[PKV_MAX_COPY_POOLS];
 };
 
+// The accepted paths' rows moved behind the cached tokens, in up to
+// kCommitTensors tensors (K and V of a pool, or a latent pool each).
+constexpr int kCommitTensors = 2 * PKV_MAX_COPY_POOLS;
+struct CommitParams {
+    const int32_t *tables, *seq_lens, *cu_q_lens, *path, *path_lens;
+    int32_t *new_lens;  // nullptr: not wanted (later launches of a call)
+    int32_t *status;
+    int32_t batch, width, max_path, block_size, heads;
+    int32_t row_vecs;   // 16-byte vectors of one head's row (FP8: of one head's codes)
+    int32_t n_tensors;
+    int32_t tensors_per_cta;  // set by the launch
+    void *base[kCommitTensors];
+    int32_t num_blocks[kCommitTensors];
+};
+
+// Latent append: strides in 16-byte vectors; the rotary tables as in RopeParams.
+struct LatentAppendParams {
+    const void *c_new, *k_new, *q, *norm_weight;
+    void *pool, *q_out;
+    const int32_t *slot_mapping;
+    const int32_t *positions;
+    int32_t *status;
+    int64_t c_stride, k_stride, q_stride, q_head_stride, q_out_stride, q_out_head_stride, pos_stride;
+    int32_t num_tokens, heads, num_slots;
+    int32_t c_vecs, row_vecs;  // vectors of the latent part and of a whole row
+    int32_t rotary_dim, interleaved, num_axes;
+    int32_t tokens_per_cta;    // set by the launch
+    float factor, eps;
+    uint64_t freq[kRopeMaxPairs];
+    uint8_t axis[kRopeMaxPairs];
+};
+
+// Attention over latent rows.  The (query, head) pairs of a row's queries are
+// cut into items of `rows` pairs, each over the row's keys up to its last
+// query's; the items' key tiles in item order form one sequence, of which every
+// worker takes an equal run.
+struct LatentParams {
+    const void *q;
+    void *out;
+    const void *pool;
+    const int32_t *tables;
+    const int32_t *seq_lens;
+    const int32_t *cu_q_lens;  // nullptr: one query per row
+    const uint64_t *tree;      // nullptr: chains
+    int32_t *status;
+    int32_t batch, heads, latent, rope, block_size, width, num_blocks;
+    int32_t max_len, max_q;
+    int32_t items_per_row;     // item bound of a row: ceil(max_q * heads / pairs of an item)
+    int32_t workers;
+    float *ws_o;    // [workers][2][latent / 4][pairs of an item][4] unnormalised weighted values
+    float *ws_ml;   // [workers][2][pairs of an item][2]: reference max (log2 units), weight sum
+    int32_t *rec;   // [workers][2]: the item that a worker's run begins and does not end (-1: none),
+                    // the last worker that holds a piece of it; then [workers]: its partial's slot
+    float scale_log2;
+    uint64_t wait_ns;
+    uint32_t drill;
+};
+constexpr int kLatentSimpleRows = 16;  // pairs of an item: CUDA-core kernel
+constexpr int kLatentTcRows = 128;     // tensor-core kernel
+
 // Split plan of one decode call.  A row's key range [lo, L) covers the blocks
 // b_first .. b_end-1; split s of the row's suffix covers blocks
 // b_first + s*split_blocks .. (capped at b_end).  Rows of a shared-prefix
@@ -118,6 +178,11 @@ struct DecodeParams {
     int32_t max_len;   // min(max_seq_len, width * block_size): lengths are clamped to it
     int32_t window;
     int32_t sinks;     // with a window: the first positions that stay visible (0 = none)
+    // drafted trees: bit j of tree[i] = the packed query i attends its row's
+    // draft j (nullptr: chains).  A split item then takes q_chunk of a row's
+    // queries, q_chunks of them a row
+    const uint64_t *tree;
+    int32_t q_chunk, q_chunks;
     int32_t num_groups;
     float scale_log2;  // scale * log2(e) (* k_scale for FP8): scores are kept in base-2 units
     float v_scale;     // FP8: applied to each partial's weighted values
@@ -178,6 +243,7 @@ struct PrefillParams {
     int32_t max_q_len;
     int32_t window;
     int32_t sinks;      // with a window: the first positions that stay visible (0 = none)
+    const uint64_t *tree;  // drafted trees: bit j of tree[i] = the packed query i attends its row's draft j
     int32_t q_tiles;    // CTAs per (row, kv head): ceil(max_q_len / queries per CTA)
     // key-range split (bf16, short chunks only; 1 = none): each (row, kv head,
     // query tile) is cut into kv_splits runs of split_tiles 64-key tiles whose
@@ -218,6 +284,9 @@ cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_append_fp8(const AppendParams &p, cudaStream_t stream);
 cudaError_t launch_append_rope(const RopeParams &p, pkv_dtype dtype, int num_sms, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
+cudaError_t launch_commit(const CommitParams &p, bool fp8, int num_sms, cudaStream_t stream);
+cudaError_t launch_latent_append(const LatentAppendParams &p, pkv_dtype dtype, int num_sms, cudaStream_t stream);
+cudaError_t launch_latent_simple(const LatentParams &p, pkv_dtype dtype, cudaStream_t stream);
 bool prefill_shape_built(pkv_dtype dtype, int32_t D, int32_t bs, int32_t G);
 int32_t prefill_queries_per_cta(pkv_dtype dtype, int32_t G);
 // Key-range split of the bf16 prefill for short chunks (all of a row's
@@ -248,6 +317,10 @@ cudaError_t launch_prefill_fp8(const PrefillParams &p, cudaStream_t stream);
 // maps (64 dims, slot, 64-dim region, kv head, block), whole-tile boxes, 128B swizzle.
 cudaError_t launch_decode_bf16(const DecodeParams &p, const CUtensorMap &kmap,
                                const CUtensorMap &vmap, cudaStream_t stream);
+// drafted trees (p.tree, p.q_chunk) on the same kernel
+cudaError_t launch_tree_bf16(const DecodeParams &p, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                             cudaStream_t stream);
+cudaError_t launch_tree_fp8(const DecodeParams &p, cudaStream_t stream);
 // f32 pools: CUDA-core kernel.
 cudaError_t launch_decode_f32(const DecodeParams &p, cudaStream_t stream);
 cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t stream);

@@ -143,7 +143,8 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int32_t bid
     w.nq = min(qpc, C - w.i0);
     const int32_t p_first = L - C + w.i0;
     w.kv_hi = p_first + w.nq;
-    w.kv_lo = p.window > 0 ? max(0, p_first - p.window + 1) : 0;
+    // (a tree's queries may all sit right behind the cached tokens)
+    w.kv_lo = p.window > 0 ? max(0, (p.tree != nullptr ? L - C : p_first) - p.window + 1) : 0;
     // tiles wholly before the window's first one that hold sinks
     const int32_t jw = w.kv_lo / pf::kKeys;
     w.nst = p.sinks > 0 ? min((min(p.sinks, w.kv_lo) + pf::kKeys - 1) / pf::kKeys, jw) : 0;
@@ -385,7 +386,8 @@ __device__ __forceinline__ void come_late(uint32_t ns)
 // bf16, tcgen05
 // ---------------------------------------------------------------------------
 // kSink: a window with sink tokens (their tiles first, then the window's)
-template <bool kF8, bool kSink>
+// kTree: the queries are a drafted tree's, masked by their ancestors
+template <bool kF8, bool kSink, bool kTree>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PrefillParams p)
@@ -832,7 +834,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         if (lane == 0) mbar_arrive(&q_full[x]);
         const bool valid_row = row < qpt * G && t < cs.w.nq;
         const int32_t qpos = cs.w.kv_hi - cs.w.nq + t;
-        const int32_t qlo = p.window > 0 ? max(0, qpos - p.window + 1) : 0;
+        // kTree: positions below `first` hold the cached tokens, the drafts follow
+        const int32_t first = cs.w.kv_hi - cs.w.nq - cs.w.i0;
+        uint64_t tmask = 0;
+        if constexpr (kTree) tmask = valid_row ? tree_mask(p.tree, cs.w.q0 + t, cs.w.i0 + t) : 0ull;
+        const int32_t at = kTree ? first + tree_depth(tmask) : qpos;  // where its window ends
+        const int32_t qlo = p.window > 0 ? max(0, at - p.window + 1) : 0;
         float m_ref = -INFINITY, l = 0.f;
         const bool warp_live = __any_sync(0xffffffffu, valid_row);
         for (int32_t jj = 0; jj < ntile; ++jj) {
@@ -945,7 +952,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // and its block was loaded
                 const bool full = mask == (1u << kBlocks) - 1u &&
                                   tbase >= qlo &&
-                                  tbase + kKeys - 1 <= qpos && valid_row;
+                                  tbase + kKeys - 1 <= (kTree ? first - 1 : qpos) && valid_row;
                 if (!full) {
                     // attended columns as bits: the window's from qlo to qpos, the
                     // sinks' up to the query's own, both within loaded blocks
@@ -954,6 +961,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     };
                     uint64_t bits = below(qpos + 1 - tbase);
                     bits &= kSink ? ~below(qlo - tbase) | below(p.sinks - tbase) : ~below(qlo - tbase);
+                    if constexpr (kTree) bits &= tree_bits(tmask, tbase, first);
                     const uint32_t bm = valid_row ? mask : 0u;
                     uint64_t blocks = 0;
     #pragma unroll
@@ -1310,18 +1318,24 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
     float *qs = fsm, *os = qs + NQ * D, *ks = os + NQ * D, *vs = ks + bs * D, *sc = vs + bs * D;
     float *mrow = sc + NQ * bs, *lrow = mrow + NQ, *alpha = lrow + NQ;
     int32_t *phi = reinterpret_cast<int32_t *>(alpha + NQ), *plo = phi + NQ;
+    uint64_t *tm = reinterpret_cast<uint64_t *>(plo + NQ);  // drafted trees: the rows' masks (an even word)
     const int tid = threadIdx.x;
     pdl_wait();
     pdl_trigger();
     PrefillRowInfo w;
     if (!prefill_item(p, blockIdx.x, qpt, w)) return;
-    const int32_t row0 = w.q0;
+    const int32_t row0 = w.q0, first = w.kv_hi - w.nq - w.i0;
     if (tid < NQ) {
         const int t = tid / G;
         const bool valid = tid < qpt * G && t < w.nq;
         const int32_t qpos = w.kv_hi - w.nq + t;
         phi[tid] = valid ? qpos + 1 : 0;
-        plo[tid] = p.window > 0 ? max(0, qpos - p.window + 1) : 0;
+        int32_t at = qpos;  // where its window ends
+        if (p.tree != nullptr) {
+            tm[tid] = valid ? tree_mask(p.tree, w.q0 + t, w.i0 + t) : 0ull;
+            at = qpos - (w.i0 + t) + tree_depth(tm[tid]);
+        }
+        plo[tid] = p.window > 0 ? max(0, at - p.window + 1) : 0;
         mrow[tid] = -INFINITY;
         lrow[tid] = 0.f;
     }
@@ -1356,7 +1370,9 @@ __global__ void __launch_bounds__(kPf32Threads) prefill_f32_kernel(const Prefill
             const int k = j / bs, tt = j % bs;
             const int pos = b * bs + tt;
             float sv = -INFINITY;
-            if (ok && (pos >= plo[k] || pos < sink) && pos < phi[k]) {
+            const int dr = pos - first;  // a tree's draft (< 0: a cached token)
+            if (ok && (pos >= plo[k] || pos < sink) && pos < phi[k] &&
+                (p.tree == nullptr || dr < 0 || ((tm[k] >> dr) & 1u))) {
                 float acc = 0.f;
                 for (int d = 0; d < D; ++d) acc = fmaf(qs[k * D + d], ks[tt * D + d], acc);
                 sv = acc * p.scale_log2;
@@ -1768,7 +1784,7 @@ size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, cons
     return o + n * 2 * sizeof(float);
 }
 
-template <bool kF8, bool kSink>
+template <bool kF8, bool kSink, bool kTree = false>
 static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &kmap,
                                     const CUtensorMap &vmap, cudaStream_t stream)
 {
@@ -1776,14 +1792,14 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
                                        : static_cast<int64_t>(p.batch) * p.hkv * p.q_tiles * p.kv_splits;
     if (ctas == 0) return cudaSuccess;
     constexpr int smem = pf::Layout<kF8>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink>,
+    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink, kTree>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_PREFILL, stream);
     if (p.sk_ctas > 0)
         err = launch_pdl(prefill_sk_plan_kernel, dim3(1), dim3(kSkPlanThreads), 0, stream, p);
     if (err == cudaSuccess)
-        err = launch_pdl(prefill_kernel<kF8, kSink>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
+        err = launch_pdl(prefill_kernel<kF8, kSink, kTree>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
                          stream, kmap, vmap, p);
     if (err == cudaSuccess && p.kv_splits > 1) {
         const int64_t items = static_cast<int64_t>(p.batch) * p.max_q_len * p.hq;
@@ -1798,6 +1814,7 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
 cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream)
 {
+    if (p.tree != nullptr) return launch_prefill_tc<false, false, true>(p, kmap, vmap, stream);
     return p.sinks > 0 ? launch_prefill_tc<false, true>(p, kmap, vmap, stream)
                        : launch_prefill_tc<false, false>(p, kmap, vmap, stream);
 }
@@ -1805,6 +1822,7 @@ cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
 cudaError_t launch_prefill_fp8(const PrefillParams &p, cudaStream_t stream)
 {
     const CUtensorMap none{};  // the FP8 producers read the pools by bulk copy
+    if (p.tree != nullptr) return launch_prefill_tc<true, false, true>(p, none, none, stream);
     return p.sinks > 0 ? launch_prefill_tc<true, true>(p, none, none, stream)
                        : launch_prefill_tc<true, false>(p, none, none, stream);
 }
@@ -1815,7 +1833,7 @@ cudaError_t launch_prefill_f32(const PrefillParams &p, cudaStream_t stream)
     if (ctas == 0) return cudaSuccess;
     const int D = p.head_dim, bs = p.block_size, NQ = kPf32Pairs;
     const size_t smem = sizeof(float) * (2 * NQ * D + 2 * bs * D + NQ * bs + 3 * NQ) +
-                        sizeof(int32_t) * 2 * NQ;
+                        sizeof(int32_t) * 2 * NQ + sizeof(uint64_t) * NQ;
     cudaError_t err = cudaFuncSetAttribute(prefill_f32_kernel,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kF32SmemLimit);
     if (err != cudaSuccess) return err;

@@ -94,6 +94,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
                                 that call are not valid */
 #define PKV_DEV_Q_RANGE 32   /* FP8 pools: a query element's magnitude is past 65504, the f16
                                 range the FP8 path computes q . k in; outputs not valid */
+#define PKV_DEV_BAD_PATH 64  /* an accepted path that does not ascend or names a draft its row does
+                                not have: nothing of the row is moved or accepted */
 
 /* One layer's K/V block pool (device pointers, 16-byte aligned). */
 typedef struct {
@@ -437,6 +439,146 @@ pkv_status paged_prefill_chunk_attention_sinks(
     float scale, void *out, void *workspace, size_t ws_bytes, int32_t *dev_status,
     pkv_stream_t stream);
 
+/*
+ * Drafted trees (speculative decoding with several continuations at once).  A row
+ * of n cached tokens holds C drafts at positions n .. n + C - 1 of its pages (its
+ * seq_len is n + C; cu_q_lens gives the C of each row), each behind its parent.
+ * Query i is draft i's, and tree_masks[cu_q_lens[r] + i] says which drafts it
+ * attends: bit j (j <= i; higher bits count for nothing) for draft j, its
+ * ancestors and, as a rule, itself.  It attends
+ *   { p < n : window == 0 or p > n + a - window }  and  { n + j : bit j },
+ * a = max(0, its bits - 1): a node sits a tokens behind the cached ones, whatever
+ * its place in the row (rotate its key and query by n + a).  A window is at least
+ * max_q_len, so that no ancestor lies outside it (else PKV_ERR_UNSUPPORTED).  A
+ * query without any key gives zeros.
+ * Layouts, types, errors and the other rules are those of
+ * paged_prefill_chunk_attention, but every (head_dim, Hq / Hkv) of the paged decode
+ * is built for bf16 and FP8 pools.  The K and V rows of a row's drafts are finite,
+ * also of one that no query attends.
+ *   tree_masks: device uint64 [cu_q_lens[batch]]
+ *   max_q_len:  host upper bound on C, at most PKV_MAX_TREE
+ */
+#define PKV_MAX_TREE 64
+
+size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, int32_t block_size, int32_t max_q_len,
+                                 int32_t max_seq_len, int32_t window);
+
+pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
+                                int32_t num_q_heads, const pkv_pool *pool,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *seq_lens, int32_t batch, int32_t max_q_len,
+                                int32_t max_seq_len, int32_t window, float scale, void *out,
+                                void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                pkv_stream_t stream);
+
+/* Host helper: masks of drafted trees from their parents.  Node i of row r (at
+ * cu_q_lens[r] + i in both arrays) has parent parents[..] in -1 .. i - 1 (-1: the
+ * last cached token); its mask gets its parent's bits and its own.  All arrays are
+ * host memory.  PKV_ERR_INVALID_ARG (nothing written) for a parent outside that
+ * range, a row of more than PKV_MAX_TREE nodes or lengths that descend. */
+pkv_status pkv_tree_masks_host(const int32_t *parents, const int32_t *cu_q_lens, int32_t batch,
+                               uint64_t *tree_masks);
+
+/*
+ * Commit an accepted path: for every row r, every pool and i < path_lens[r], the K
+ * and V rows of position n + path[r][i] become those of position n + i (n =
+ * seq_lens[r] minus the row's drafts), and new_seq_lens[r] = n + path_lens[r].
+ * Rows behind that are left as they are.  One launch per PKV_MAX_COPY_POOLS pools.
+ *   pools:        host array of n_pools pools that share everything but num_blocks
+ *   block_tables, seq_lens, cu_q_lens: as the attention call's (drafts counted)
+ *   path:         device int32 [batch][max_path] (1 <= max_path <= PKV_MAX_TREE):
+ *                 draft indexes, strictly ascending, each below the row's drafts
+ *   path_lens:    device int32 [batch] (0: nothing accepted)
+ *   new_seq_lens: device int32 [batch], not seq_lens itself
+ * A path that breaks these rules sets PKV_DEV_BAD_PATH: nothing of its row is
+ * moved, and its new length is n.  A token whose page is missing is skipped
+ * (PKV_DEV_BAD_BLOCK).  The drafts' pages belong to one row each.  Rows of a head
+ * are a multiple of 16 bytes, else PKV_ERR_UNSUPPORTED.
+ */
+pkv_status paged_tree_commit(const pkv_pool *pools, int32_t n_pools, const int32_t *block_tables,
+                             int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                             const int32_t *cu_q_lens, int32_t batch, const int32_t *path,
+                             int32_t max_path, const int32_t *path_lens, int32_t *new_seq_lens,
+                             int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * Latent caches: a token's keys and values of all heads come from one vector, its
+ * latent c (latent_dim) beside a key k_r (rope_dim) that carries the position.
+ * With the heads' up-projections moved to the query and the output (absorbed form),
+ * attention needs [c | k_r] alone: q = [W_uk^T q_nope | q_rope], and out, a weighted
+ * sum of latents, is projected by W_uv afterwards.
+ * A pool is [num_blocks][block_size][latent_dim + rope_dim] (16-byte aligned), bf16
+ * or f32 (FP8: PKV_ERR_UNSUPPORTED); slots, tables and lengths as for K/V pools.
+ */
+typedef struct {
+    void *data;
+    int32_t num_blocks;
+    int32_t block_size;
+    int32_t latent_dim;
+    int32_t rope_dim;
+    pkv_dtype dtype;
+} pkv_latent_pool;
+
+/*
+ * Append latent rows in one launch: for token t with slot s >= 0 the pool's row s is
+ *   [norm_weight * c / sqrt(mean(c^2) + norm_eps) | R(position) k]
+ * (norm_weight NULL: c as it is), and q_rope_out gets every token's q_rope rotated
+ * the same way.  fp32 arithmetic, one rounding to the row's type.
+ *   latent_new:  device [num_tokens][latent_dim], tokens latent_stride elements apart
+ *   k_rope_new:  device [num_tokens][rope_dim], stride likewise (both may be cut from
+ *                one projection's output)
+ *   q_rope:      device [num_tokens][num_q_heads][rope_dim] with strides between tokens
+ *                and heads (cut from the queries); num_q_heads 0: none (NULL)
+ *   q_rope_out:  likewise; may be q_rope itself with the same strides, or the tail of
+ *                absorbed query rows; no other overlap
+ *   norm_weight: device [latent_dim] of the pool's type, or NULL
+ *   positions:   as for paged_kv_append_rope; rope: rotary_dim == rope_dim
+ * Types are the pool's.  Pointers 16-byte aligned, strides multiples of 16 bytes.
+ * Built: latent_dim a multiple of 16 up to 512, rope_dim a multiple of 16 (f32: 8)
+ * up to 256.
+ */
+pkv_status paged_latent_append(const pkv_latent_pool *pool, const int32_t *slot_mapping,
+                               int32_t num_tokens, const void *latent_new, int64_t latent_stride,
+                               const void *k_rope_new, int64_t k_rope_stride,
+                               const void *norm_weight, float norm_eps, const void *q_rope,
+                               int64_t q_stride, int64_t q_head_stride, int32_t num_q_heads,
+                               const int32_t *positions, int64_t pos_stride, const pkv_rope *rope,
+                               void *q_rope_out, int64_t q_out_stride, int64_t q_out_head_stride,
+                               int32_t *dev_status, pkv_stream_t stream);
+
+/*
+ * Attention over latent rows, absorbed form: for every query and head
+ *   out = softmax_p(scale * q . [c_p | k_p]) . c_p
+ * over the positions that the query attends: decode (cu_q_lens NULL: one query a row
+ * at seq_lens[r] - 1), chunks (cu_q_lens: query i of C at seq_lens[r] - C + i,
+ * causally) or drafted trees (tree_masks, max_q_len <= PKV_MAX_TREE; without a
+ * window).  A query without a key gives zeros.
+ *   q:   device [queries][num_q_heads][latent_dim + rope_dim], contiguous
+ *   out: device [queries][num_q_heads][latent_dim], contiguous
+ *   workspace: device, >= paged_latent_workspace_size(...) bytes, 256-byte aligned
+ * Types are the pool's.  Rows that no query of a row attends may hold anything; the
+ * rows of a chunk or tree are finite.  Built: latent_dim a multiple of 16 up to 512,
+ * rope_dim a multiple of 16 up to 128, any number of heads, block_size up to 64.
+ */
+size_t paged_latent_workspace_size(int32_t batch, int32_t num_q_heads, int32_t latent_dim,
+                                   int32_t rope_dim, int32_t block_size, int32_t max_q_len,
+                                   int32_t max_seq_len);
+
+pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
+                                  int32_t num_q_heads, const pkv_latent_pool *pool,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t *seq_lens, int32_t batch, int32_t max_q_len,
+                                  int32_t max_seq_len, float scale, void *out, void *workspace,
+                                  size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream);
+
+/* paged_tree_commit over latent pools (that share everything but num_blocks). */
+pkv_status paged_latent_tree_commit(const pkv_latent_pool *pools, int32_t n_pools,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *seq_lens, const int32_t *cu_q_lens, int32_t batch,
+                                    const int32_t *path, int32_t max_path, const int32_t *path_lens,
+                                    int32_t *new_seq_lens, int32_t *dev_status, pkv_stream_t stream);
+
 /* Static text for a status code. */
 const char *pkv_status_string(pkv_status status);
 
@@ -541,8 +683,9 @@ typedef enum {
     PKV_KERNEL_DECODE_SPLIT = 2,  /* per-row split-KV decode */
     PKV_KERNEL_DECODE_COMBINE = 3,
     PKV_KERNEL_PREFILL = 4,
-    PKV_KERNEL_COPY = 5,
-    PKV_KERNEL_KINDS = 6
+    PKV_KERNEL_COPY = 5,          /* page copies, commits */
+    PKV_KERNEL_LATENT = 6,        /* attention over latent rows */
+    PKV_KERNEL_KINDS = 7
 } pkv_kernel_kind;
 
 /* Bit k of kind_mask enables timing of kernel kind k: each such launch is
