@@ -1274,17 +1274,28 @@ bool latent_shape_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t b
     return dtype != PKV_FP8_E4M3 && latent % 16 == 0 && latent <= 512 && rope % 16 == 0 && rope <= 128 && bs <= 64;
 }
 
+// 3-D map over a latent pool [num_blocks][bs][row], box 64 dims x bs slots, 128-byte swizzle.
+bool encode_latent_map(CUtensorMap *map, const pkv_latent_pool &pool)
+{
+    const cuuint64_t W = static_cast<cuuint64_t>(pool.latent_dim) + pool.rope_dim, bs = pool.block_size;
+    cuuint64_t dims[3] = {W, bs, static_cast<cuuint64_t>(pool.num_blocks)};
+    cuuint64_t strides[2] = {W * 2, bs * W * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bs), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool.data, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Workers and pairs of an item for these sizes on the current device.
 struct LatentPlan {
     int32_t workers, rows;
 };
 LatentPlan latent_plan(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs, int num_sms)
 {
-    (void)dtype;
-    (void)latent;
-    (void)rope;
-    (void)bs;
-    return {2 * std::max(num_sms, 1), kLatentSimpleRows};
+    const int sms = std::max(num_sms, 1);
+    if (latent_tc_built(dtype, latent, rope, bs)) return {std::max(sms / 2, 1), kLatentTcRows};
+    return {2 * sms, kLatentSimpleRows};
 }
 
 size_t latent_ws_bytes(const LatentPlan &pl, int32_t latent)
@@ -1534,7 +1545,12 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     p.scale_log2 = scale * 1.4426950408889634f;
     drill_settings(&p.wait_ns, &p.drill);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return launch_latent_simple(p, pool->dtype, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    if (!latent_tc_built(pool->dtype, p.latent, p.rope, p.block_size))
+        return launch_latent_simple(p, pool->dtype, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    if (!encode_fn_ready()) return PKV_ERR_CUDA;
+    CUtensorMap map;
+    if (!encode_latent_map(&map, *pool)) return PKV_ERR_UNSUPPORTED;
+    return launch_latent_tc(p, map, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"
