@@ -214,56 +214,99 @@ __device__ __forceinline__ int64_t latent_out_row(const LatentParams &p, const L
 }
 
 // Joins the pieces of an item cut between workers: CTA (x, y) the item that
-// worker x's run begins, dims 64y .. 64y + 63.  A thread holds 16 dims of a pair.
-constexpr int kLatMergeThreads = 128;
+// worker x's run begins, dims 64y .. 64y + 63.
+// The pieces' weights are worked out once a CTA (a thread per pair and piece), and
+// four pieces' values are in flight at a time: one piece after another, each read
+// waiting for the last, joined 20 pieces in 20 us.
+constexpr int kLatMergeThreads = 256;
+constexpr int kLatMergePieces = 32;  // of a pass
 
 template <typename T, int kRows, int kKeys>
 __global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const LatentParams p)
 {
+    __shared__ float wgt[kLatMergePieces][kRows];
     pdl_wait();  // the records and partials come from the kernel just before
     const int32_t c = blockIdx.x, u = p.rec[2 * c], last = p.rec[2 * c + 1];
+    // the piece that the item begins with: slot 0 if it was its worker's first
+    const int32_t s0 = p.rec[2 * p.workers + c];
     if (u < 0) return;
     const LatentItem it = latent_item<kRows, kKeys>(p, u);
-    // the item began in the run's last piece: slot 0 if that was the first too
-    const int32_t s0 = p.rec[2 * p.workers + c];
-    for (int32_t idx = threadIdx.x; idx < 4 * kRows; idx += kLatMergeThreads) {
-        const int32_t pair = idx % kRows, d4 = blockIdx.y * 16 + (idx / kRows) * 4;
-        if (pair >= it.n || d4 * 4 >= p.latent) continue;
-        float M = -INFINITY;
-        for (int32_t w = c; w <= last; ++w) M = fmaxf(M, latent_part_ml<kRows>(p, w, w == c ? s0 : 0)[pair].x);
-        float4 acc[4] = {};
-        float l = 0.f;
-        if (M != -INFINITY)
-            for (int32_t w = c; w <= last; ++w) {
-                const float2 ml = latent_part_ml<kRows>(p, w, w == c ? s0 : 0)[pair];
-                const float4 *o = latent_part_o<kRows>(p, w, w == c ? s0 : 0) + d4 * kRows + pair;
-                const float f = fast_exp2(ml.x - M);
-                l = fmaf(f, ml.y, l);
+    // this thread's pair, and 4 of the CTA's 64 dims (16 dims of 128 pairs)
+    constexpr int kGroups = kLatMergeThreads / kRows;        // threads of a pair
+    constexpr int kD4 = kGroups >= 16 ? 1 : 16 / kGroups;    // value quads of a thread
+    const int pair = threadIdx.x % kRows, grp = threadIdx.x / kRows;
+    const int d4 = blockIdx.y * 16 + grp * kD4;
+    const bool live = pair < it.n && d4 * 4 < p.latent;
+    float M = -INFINITY, l = 0.f;
+    float4 acc[kD4] = {};
+    const int32_t np = last - c + 1;
+    const auto slot = [&](int32_t i) { return i == 0 ? s0 : 0; };
+    for (int32_t i0 = 0; i0 < np; i0 += kLatMergePieces) {
+        const int32_t n = min(np - i0, kLatMergePieces);
+        __syncthreads();  // the last pass's weights are read
+        for (int32_t i = grp; i < n; i += kGroups)
+            wgt[i][pair] = pair < it.n ? latent_part_ml<kRows>(p, c + i0 + i, slot(i0 + i))[pair].x : -INFINITY;
+        __syncthreads();
+        float mn = M;
+        for (int32_t i = 0; i < n; ++i) mn = fmaxf(mn, wgt[i][pair]);
+        if (!live || mn == -INFINITY) continue;
+        const float f0 = fast_exp2(M - mn);
+        M = mn;
+        l *= f0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float4 v = o[e * kRows];
-                    acc[e].x = fmaf(f, v.x, acc[e].x);
-                    acc[e].y = fmaf(f, v.y, acc[e].y);
-                    acc[e].z = fmaf(f, v.z, acc[e].z);
-                    acc[e].w = fmaf(f, v.w, acc[e].w);
+        for (int e = 0; e < kD4; ++e) {
+            acc[e].x *= f0;
+            acc[e].y *= f0;
+            acc[e].z *= f0;
+            acc[e].w *= f0;
+        }
+        constexpr int kFly = kD4 >= 8 ? 2 : kD4 >= 4 ? 4 : 8;  // pieces in flight
+        for (int32_t i = 0; i < n; i += kFly) {
+            float4 v[kFly][kD4];
+            float sum[kFly];
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                if (i + j >= n) continue;
+                const int32_t w = c + i0 + i + j, s = slot(i0 + i + j);
+                sum[j] = latent_part_ml<kRows>(p, w, s)[pair].y;
+                const float4 *o = latent_part_o<kRows>(p, w, s) + d4 * kRows + pair;
+#pragma unroll
+                for (int e = 0; e < kD4; ++e) v[j][e] = o[e * kRows];
+            }
+#pragma unroll
+            for (int j = 0; j < kFly; ++j) {
+                if (i + j >= n) continue;
+                const float f = fast_exp2(wgt[i + j][pair] - M);
+                l = fmaf(f, sum[j], l);
+#pragma unroll
+                for (int e = 0; e < kD4; ++e) {
+                    acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
+                    acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
+                    acc[e].z = fmaf(f, v[j][e].z, acc[e].z);
+                    acc[e].w = fmaf(f, v[j][e].w, acc[e].w);
                 }
             }
-        const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
-        T *out = static_cast<T *>(p.out) + latent_out_row(p, it, pair) + d4 * 4;
-        if constexpr (sizeof(T) == 4) {
+        }
+    }
+    if (!live) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
+    T *out = static_cast<T *>(p.out) + latent_out_row(p, it, pair) + d4 * 4;
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                reinterpret_cast<float4 *>(out)[e] =
-                    make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+        for (int e = 0; e < kD4; ++e)
+            reinterpret_cast<float4 *>(out)[e] =
+                make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
+    } else {
+        uint2 v[kD4];
+#pragma unroll
+        for (int e = 0; e < kD4; ++e)
+            v[e] = make_uint2(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv));
+        if constexpr (kD4 >= 2) {
+#pragma unroll
+            for (int e = 0; e < kD4; e += 2)
+                reinterpret_cast<uint4 *>(out)[e / 2] = make_uint4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
         } else {
-            uint32_t v[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                v[2 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
-                v[2 * e + 1] = pack_bf16x2(acc[e].z * inv, acc[e].w * inv);
-            }
-            reinterpret_cast<uint4 *>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<uint4 *>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<uint2 *>(out) = v[0];
         }
     }
 }
