@@ -1509,7 +1509,10 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     if (!latent_shape_built(pool->dtype, pool->latent_dim, pool->rope_dim, pool->block_size)) return PKV_ERR_UNSUPPORTED;
     const LatentPlan pl = latent_plan(pool->dtype, pool->latent_dim, pool->rope_dim, pool->block_size, num_sms_current());
     const int64_t per_row = ceil_div64(static_cast<int64_t>(max_q_len) * num_q_heads, pl.rows);
-    if (per_row * batch > INT32_MAX / 2 || static_cast<int64_t>(max_q_len) * num_q_heads > INT32_MAX / 2)
+    const int64_t max_len = std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_blocks_per_seq) * pool->block_size);
+    // the runs' sums are 32 bits: key tiles of all items, and some beside them
+    const int64_t item_tiles = max_len / (pl.rows == kLatentTcRows ? 64 : 16) + 8;
+    if (static_cast<int64_t>(max_q_len) * num_q_heads > INT32_MAX / 2 || per_row > INT32_MAX / item_tiles / batch)
         return PKV_ERR_UNSUPPORTED;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         ws_bytes < latent_ws_bytes(pl, pool->latent_dim))
@@ -1530,8 +1533,7 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     p.block_size = pool->block_size;
     p.width = max_blocks_per_seq;
     p.num_blocks = pool->num_blocks;
-    p.max_len = static_cast<int32_t>(
-        std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_blocks_per_seq) * pool->block_size));
+    p.max_len = static_cast<int32_t>(max_len);
     p.max_q = max_q_len;
     p.items_per_row = static_cast<int32_t>(per_row);
     p.workers = pl.workers;

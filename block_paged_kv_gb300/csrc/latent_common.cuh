@@ -4,7 +4,7 @@
 // Item u = (row u / items_per_row, pairs kRows (u % items_per_row) .. of the row's
 // (query, head) pairs, query-major).  Its keys are the positions up to its last
 // query's, in tiles of kKeys.  The items' tiles in item order form one sequence;
-// worker c of n takes tiles T c / n .. T (c + 1) / n of the T there are, so that
+// worker c of n takes units T c / n .. T (c + 1) / n of the T there are, so that
 // every worker has the same work whatever the rows' lengths.  Only the first and
 // the last piece of a run can cut an item; a cut piece leaves a partial (maximum,
 // sum, weighted values) in slot 0 (first piece) or 1 of its worker, which the
@@ -72,11 +72,13 @@ __device__ __forceinline__ LatentRange latent_range(const LatentParams &p, const
     return rg;
 }
 
-// A worker's run: it starts in item u, `lo` being that item's first tile.
+// A worker's run, in units: an item counts its tiles and `over` units before them
+// (what a piece costs beside its tiles: queries staged, first products, epilogue).
 struct LatentRun {
-    int64_t pos, end;  // tiles still ahead, in the sequence
-    int64_t lo;
-    int32_t u;
+    int32_t pos, end;  // units still ahead, in the sequence
+    int32_t lo;        // item u's first unit
+    int32_t u;         // the item that holds pos
+    int32_t over;
     int32_t k;         // pieces so far
 };
 struct LatentPiece {
@@ -87,90 +89,102 @@ struct LatentPiece {
     int32_t slot;      // a cut piece's partial slot
 };
 
-// Every thread of the CTA (kThreads of them): worker `c`'s run, and the record of
-// the item that it begins and does not end; `sm`: kThreads / 32 + 4 words of
-// shared memory (64 bits).  An empty run has pos == end.
+// Every thread of the CTA (kThreads of them, at least 128): worker `c`'s run, and the
+// record of the item that it begins and does not end; `sm`: kThreads / 32 + 4 words
+// of shared memory (64 bits).  An empty run has pos == end.  The runs have `least`
+// units at least; where they have `level` tiles or more, items count `over` units
+// beside their tiles (`level` > `over`, so that every run holds a tile).
 template <int kRows, int kKeys, int kThreads>
-__device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c, int32_t least, bool record,
-                                                int64_t *sm)
+__device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c, int32_t least, int32_t level,
+                                                int32_t over, bool record, int64_t *sm)
 {
     constexpr int kWarps = kThreads / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t items = p.batch * p.items_per_row;
+    // an item's tiles, and (high word) whether it has any
     auto tiles_of = [&](int32_t u, bool say) {
-        return u < items ? static_cast<int64_t>(latent_item<kRows, kKeys>(p, u, say).tiles) : 0;
+        const int32_t n = u < items ? latent_item<kRows, kKeys>(p, u, say).tiles : 0;
+        return static_cast<int64_t>(n) | (n > 0 ? 1ll << 32 : 0ll);
     };
-    // tiles in all; with one pass of items, they are looked up once
+    auto scan = [&](int64_t x) {  // inclusive, over the warp
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        return x;
+    };
+    // tiles in all; with one pass of items, they are looked up and scanned once
     const bool one = items <= kThreads;
     int64_t mine = 0;
     for (int32_t u = threadIdx.x; u < items; u += kThreads) mine += tiles_of(u, c == 0 && record);
-    int64_t sum = mine;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) sm[warp] = sum;
+    const int64_t inc0 = scan(mine);
+    if (lane == 31) sm[warp] = inc0;
     __syncthreads();
-    int64_t T = 0;
+    int64_t all = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) T += sm[w];
-    const int64_t n = min(static_cast<int64_t>(p.workers), max(static_cast<int64_t>(1), T / least));
-    LatentRun run{0, 0, 0, 0, 0};
-    if (c < n) {
-        run.pos = T * c / n;
-        run.end = T * (c + 1) / n;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm[w];
+        all += sm[w];
     }
-    // items that hold the run's first and last tile
-    int64_t *found = sm + kWarps;  // first: item, lo; last: item, its end
-    __syncthreads();
-    if (threadIdx.x == 0) found[0] = found[2] = -1;
-    int64_t before = 0;
+    const int32_t tiles = static_cast<int32_t>(all), used = static_cast<int32_t>(all >> 32);
+    LatentRun run{0, 0, 0, 0, tiles / level >= p.workers ? over : 0, 0};
+    const int32_t T = tiles + run.over * used;
+    const int32_t n = min(p.workers, max(1, T / least)), q = T / n, r = T - q * n;
+    auto start = [&](int32_t w) { return q * w + r * w / n; };  // T w / n
+    if (c < n) {
+        run.pos = start(c);
+        run.end = start(c + 1);
+    }
+    auto units = [&](int64_t x) { return static_cast<int32_t>(x) + run.over * static_cast<int32_t>(x >> 32); };
+    // items that hold the run's first and last unit: item, first unit; item, first unit, end
+    int32_t *found = reinterpret_cast<int32_t *>(sm + kWarps);
+    int64_t lo64 = before + inc0 - mine, x64 = mine, base64 = 0;
     for (int32_t base = 0; base < items && run.pos < run.end; base += kThreads) {
-        const int64_t x = one ? mine : tiles_of(base + threadIdx.x, false);
-        int64_t inc = x;
+        if (!one) {
+            x64 = tiles_of(base + threadIdx.x, false);
+            const int64_t inc = scan(x64);
+            __syncthreads();
+            if (lane == 31) sm[warp] = inc;
+            __syncthreads();
+            lo64 = base64 + inc - x64;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += y;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) lo64 += sm[w];
+                base64 += sm[w];
+            }
         }
-        __syncthreads();
-        if (lane == 31) sm[warp] = inc;
-        __syncthreads();
-        int64_t lo = before + inc - x;
-        int64_t all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) lo += sm[w];
-            all += sm[w];
-        }
-        if (lo <= run.pos && run.pos < lo + x) {
+        const int32_t lo = units(lo64), hi = units(lo64 + x64);
+        if (lo <= run.pos && run.pos < hi) {
             found[0] = base + threadIdx.x;
             found[1] = lo;
         }
-        if (lo <= run.end - 1 && run.end - 1 < lo + x) {
+        if (lo < run.end && run.end <= hi) {
             found[2] = base + threadIdx.x;
-            found[3] = lo + x;
+            found[3] = lo;
+            found[4] = hi;
         }
-        before += all;
-        if (before >= run.end) break;
+        if (!one && units(base64) >= run.end) break;
     }
     __syncthreads();
     if (run.pos < run.end) {
-        run.u = static_cast<int32_t>(found[0]);
+        run.u = found[0];
         run.lo = found[1];
     }
-    if (record && threadIdx.x == 0) {
-        // the item at the run's end goes on in later workers, and began here
-        int32_t u = -1, last = -1;
-        if (run.pos < run.end && found[3] > run.end) {
-            const int64_t E = found[3];
-            const bool began = found[2] != found[0] || run.pos == run.lo;
-            if (began) {
-                u = static_cast<int32_t>(found[2]);
-                last = static_cast<int32_t>((E * n + T - 1) / T - 1);  // the first worker that ends at or past E
+    if (record && threadIdx.x == 96) {  // (of a warp that does not lead)
+        // the item at the run's end goes on in later workers, and its first tile is here
+        int32_t u = -1, last = -1, slot = 0;
+        if (run.pos < run.end) {
+            const int32_t first = found[3] + run.over, E = found[4];
+            if (E > run.end && first >= run.pos && first < run.end) {
+                u = found[2];
+                last = static_cast<int32_t>((static_cast<int64_t>(E) * n + T - 1) / T - 1);  // the first that ends at or past E
+                slot = found[2] != found[0] ? 1 : 0;
             }
         }
         p.rec[2 * c] = u;
         p.rec[2 * c + 1] = last;
-        p.rec[2 * p.workers + c] = u >= 0 && found[2] != found[0] ? 1 : 0;  // its piece's slot
+        p.rec[2 * p.workers + c] = slot;
     }
     return run;
 }
@@ -179,21 +193,28 @@ __device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c
 template <int kRows, int kKeys>
 __device__ __forceinline__ bool latent_next(const LatentParams &p, LatentRun &run, LatentPiece &pc)
 {
-    if (run.pos >= run.end) return false;
-    pc.it = latent_item<kRows, kKeys>(p, run.u);
-    while (run.lo + pc.it.tiles <= run.pos) {  // (items without a query have no tile)
-        run.lo += pc.it.tiles;
-        pc.it = latent_item<kRows, kKeys>(p, ++run.u);
+    while (run.pos < run.end) {
+        pc.it = latent_item<kRows, kKeys>(p, run.u);
+        const int32_t first = run.lo + run.over, hi = pc.it.tiles > 0 ? first + pc.it.tiles : run.lo;
+        const int32_t from = max(run.pos, first), stop = min(hi, run.end);
+        pc.u = run.u;
+        if (hi <= run.end) {
+            ++run.u;
+            run.lo = hi;
+        }
+        run.pos = max(run.pos, stop);
+        if (from >= stop) {  // an item without a query, or one whose first tile is the next run's
+            if (hi > run.end) run.pos = run.end;
+            continue;
+        }
+        pc.t0 = from - first;
+        pc.n = stop - from;
+        pc.whole = pc.n == pc.it.tiles;
+        pc.slot = run.k == 0 ? 0 : 1;
+        ++run.k;
+        return true;
     }
-    const int64_t hi = run.lo + pc.it.tiles, stop = min(hi, run.end);
-    pc.u = run.u;
-    pc.t0 = static_cast<int32_t>(run.pos - run.lo);
-    pc.n = static_cast<int32_t>(stop - run.pos);
-    pc.whole = pc.n == pc.it.tiles;
-    pc.slot = run.k == 0 ? 0 : 1;
-    ++run.k;
-    run.pos = stop;
-    return true;
+    return false;
 }
 
 // Partials: value quad d4 of pair i of a piece, and its (maximum, sum).

@@ -47,6 +47,8 @@ constexpr int kRegion = kKeys * 128;      // 64 dims of a tile: 8 KiB, 128-byte 
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled only when the max grows past 2^8
 constexpr uint32_t kTmemCols = 512;
 constexpr int32_t kLeastTiles = 2;        // of a worker's run
+// A piece's cost beside its tiles, in tiles, where the runs are long enough to be levelled by it
+constexpr int32_t kItemCost = 4, kLevelTiles = 8;
 template <int H>  // latent dims of a CTA
 struct Layout {
     static constexpr int kRegions = H / 64 + 1;           // its latent dims, then the rotary ones (both halves)
@@ -55,8 +57,8 @@ struct Layout {
     static constexpr int kQOff = kStages * kStageBytes;   // Q's rotary dims: 128 rows of 128 bytes
     static constexpr int kXOff = kQOff + kRows * 128;     // the peer's half sums: [16 key quads][128 pairs] float4
     static constexpr int kBarOff = kXOff + kKeys * kRows * 4;
-    // kv_full, kv_empty [stages], s_full[2], p_full[2], s_sent[2][4], x_full[4], x_free[4], pv_done, o_done, q_full, drain
-    static constexpr int kNumBars = 2 * kStages + 4 + 8 + 8 + 4;
+    // kv_full, kv_empty [stages], s_full[2], p_full[2], x_full[4], x_free[4], pv_done, o_done, q_full, drain
+    static constexpr int kNumBars = 2 * kStages + 4 + 8 + 4;
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kScanOff = (kMaskOff + kStages * 4 + 15) & ~15;
     static constexpr int kTmemOff = kScanOff + (kThreads / 32 + 4) * 8;
@@ -164,8 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     uint64_t *kv_full = bars, *kv_empty = kv_full + kStages;
     uint64_t *s_full = kv_empty + kStages;  // [buffer]: S's own half computed
     uint64_t *p_full = s_full + 2;          // [buffer]: P stored
-    uint64_t *s_sent = p_full + 2;          // [buffer][warp]: own half read for the peer
-    uint64_t *x_full = s_sent + 8;          // [warp]: the peer's half has landed
+    uint64_t *x_full = p_full + 2;          // [warp]: the peer's half has landed, own half read by the sender
     uint64_t *x_free = x_full + 4;          // [warp]: the peer has read what was sent
     uint64_t *pv_done = x_free + 4, *o_done = pv_done + 1, *q_full = o_done + 1, *drain = q_full + 1;
     uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);  // [stage]: pages loaded
@@ -177,13 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     const int bs = p.block_size, nb = kKeys / bs;  // pages of a tile
     const uint32_t all_pages = (1u << nb) - 1u;
 
-    if (threadIdx.x == 0) tma_prefetch_desc(&map);
-    pdl_wait();
-    pdl_trigger();
-    const LatentRun run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, rank == 0, scan);
-    if (run0.pos >= run0.end) return;  // both CTAs of the pair
-
     if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 2);  // the two producers
             mbar_init(&kv_empty[i], 1);
@@ -192,9 +188,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&s_sent[i], 1);
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&x_full[i], 1);
+            mbar_init(&x_full[i], 2);  // armed by the softmax warp; the sender
             mbar_init(&x_free[i], 1);
         }
         mbar_init(pv_done, 1);
@@ -210,6 +205,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t tS = tmem + L::kS, tQ = tmem + L::kQ;
+    pdl_wait();
+    pdl_trigger();
+    // (a run without tiles: every role finds no piece)
+    const LatentRun run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, kLevelTiles, kItemCost, rank == 0, scan);
 
     if (warp == 0 || warp == 2) {
         // ------------------------------------------------------------ producers
@@ -281,68 +280,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         const uint64_t dv = tc::smem_desc(smem_u32(smem), kRegion, 1024);
         const uint64_t dq = tc::smem_desc(smem_u32(smem + L::kQOff), 16, 1024);
         constexpr uint64_t kStageStep = L::kStageBytes >> 4;
-        auto landed = [&](int32_t T) { return lat_wait(&kv_full[T % kStages], (T / kStages) & 1, p); };
-        auto s_issue = [&](int32_t T) {
-            const uint64_t kd = dk + static_cast<uint64_t>(T % kStages) * kStageStep;
-            const uint32_t d = tS + 64u * static_cast<uint32_t>(T & 1);
+        // One elected lane runs the whole role.  A product is issued about as it
+        // starts (the queue holds a few), so the waits for the next tile are looked
+        // at before a tile's last products: done between two tiles they left the
+        // tensor cores idle for 400 cycles each.
+        if (elect_one()) {
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (mbar_wait(bar, parity, p.wait_ns)) return true;
+                report(p.status, PKV_DEV_TIMEOUT);
+                return false;
+            };
+            auto kv_bar = [&](int32_t T) { return &kv_full[T % kStages]; };
+            auto kv_par = [&](int32_t T) { return static_cast<uint32_t>(T / kStages) & 1u; };
+            // products first .. last - 1 of S(T)'s H / 16 + 2
+            auto s_part = [&](int32_t T, int first, int last) {
+                const uint64_t kd = dk + static_cast<uint64_t>(T % kStages) * kStageStep;
+                const uint32_t d = tS + 64u * static_cast<uint32_t>(T & 1);
+                const uint64_t ro = static_cast<uint64_t>(rank * 64) >> 4;  // this CTA's half of the rotary dims
 #pragma unroll
-            for (int kk = 0; kk < H / 16; ++kk)
-                tc::mma_ts(d, tQ + 8 * kk, kd + (((kk >> 2) * kRegion + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
-            // this CTA's half of the rotary dims
-            const uint64_t ro = static_cast<uint64_t>(rank * 64) >> 4;
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk)
-                tc::mma_ss(d, dq + ro + 2 * kk, kd + (((H / 64) * kRegion) >> 4) + ro + 2 * kk, idS, 1u);
-            tc::commit(&s_full[T & 1]);
-        };
-        auto pv_issue = [&](int32_t T, bool start) {
-            const uint64_t vd = dv + static_cast<uint64_t>(T % kStages) * kStageStep;
-            const uint32_t a = tS + 64u * static_cast<uint32_t>(T & 1);
-#pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    tc::mma_ts(tmem, a + 16 * kk + 8 * part, vd + static_cast<uint64_t>(kk) * (2048 >> 4), idO,
-                               (part > 0 || kk > 0 || !start) ? 1u : 0u);
-            tc::commit(pv_done);
-            tc::commit(&kv_empty[T % kStages]);
-        };
-        LatentRun run = run0;
-        LatentPiece pc;
-        int32_t T0 = 0;
-        bool ok = true;
-        for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
-            const int32_t n = pc.n;
-            ok = lat_wait(q_full, k & 1, p);
-            ok = ok && landed(T0) && (n < 2 || landed(T0 + 1));
-            if (ok) {
-                tc::fence_after();
-                if (elect_one()) {
-                    s_issue(T0);
-                    if (n >= 2) s_issue(T0 + 1);
+                for (int kk = 0; kk < H / 16 + 2; ++kk) {
+                    if (kk < first || kk >= last) continue;
+                    if (kk < 2)  // queries in shared memory
+                        tc::mma_ss(d, dq + ro + 2 * kk, kd + (((H / 64) * kRegion) >> 4) + ro + 2 * kk, idS, kk > 0 ? 1u : 0u);
+                    else
+                        tc::mma_ts(d, tQ + 8 * (kk - 2), kd + ((((kk - 2) >> 2) * kRegion + ((kk - 2) & 3) * 32) >> 4), idS, 1u);
                 }
-                __syncwarp();
-            }
-            for (int32_t j = 0; j < n && ok; ++j) {
-                const int32_t T = T0 + j;
-                const bool more = j + 2 < n;
-                if (more) ok = landed(T + 2);
-                ok = ok && lat_wait(&p_full[T & 1], (T >> 1) & 1, p);
+            };
+            auto pv = [&](int32_t T, bool start) {
+                const uint64_t vd = dv + static_cast<uint64_t>(T % kStages) * kStageStep;
+                const uint32_t a = tS + 64u * static_cast<uint32_t>(T & 1);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        tc::mma_ts(tmem, a + 16 * kk + 8 * part, vd + static_cast<uint64_t>(kk) * (2048 >> 4), idO,
+                                   (part > 0 || kk > 0 || !start) ? 1u : 0u);
+                tc::commit(pv_done);
+                tc::commit(&kv_empty[T % kStages]);
+            };
+            constexpr int kAll = H / 16 + 2, kLate = 6;
+            LatentRun run = run0;
+            LatentPiece pc;
+            int32_t T0 = 0;
+            bool ok = true;
+            for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
+                const int32_t n = pc.n;
+                ok = wait(q_full, k & 1) && wait(kv_bar(T0), kv_par(T0));
                 if (!ok) break;
                 tc::fence_after();
-                if (elect_one()) {
-                    pv_issue(T, j == 0);
-                    if (j == n - 1) tc::commit(o_done);
-                    if (more) s_issue(T + 2);
+                s_part(T0, 0, kAll);
+                tc::commit(&s_full[T0 & 1]);
+                if (n >= 2) {
+                    if (!(ok = wait(kv_bar(T0 + 1), kv_par(T0 + 1)))) break;
+                    s_part(T0 + 1, 0, kAll);
+                    tc::commit(&s_full[(T0 + 1) & 1]);
                 }
-                __syncwarp();
+                bool have_kv = false, have_p = false;  // K/V(T + 2) landed, P(T) stored
+                for (int32_t j = 0; j < n; ++j) {
+                    const int32_t T = T0 + j;
+                    const bool more = j + 2 < n;
+                    ok = (!more || have_kv || wait(kv_bar(T + 2), kv_par(T + 2))) && (have_p || wait(&p_full[T & 1], (T >> 1) & 1));
+                    if (!ok) break;
+                    tc::fence_after();
+                    pv(T, j == 0);
+                    if (j == n - 1) tc::commit(o_done);
+                    if (more) s_part(T + 2, 0, kAll - kLate);
+                    have_kv = j + 3 < n && mbar_try_wait(kv_bar(T + 3), kv_par(T + 3));
+                    have_p = j + 1 < n && mbar_try_wait(&p_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
+                    if (more) {
+                        s_part(T + 2, kAll - kLate, kAll);
+                        tc::commit(&s_full[T & 1]);
+                    }
+                }
+                T0 += n;
             }
-            T0 += n;
+            // every product has completed before tensor memory is freed
+            tc::commit(drain);
+            mbar_wait(drain, 0);
         }
-        // every product has completed before tensor memory is freed
-        if (elect_one()) tc::commit(drain);
-        __syncwarp();
-        mbar_wait(drain, 0);
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------ senders (4-7), softmax (8-11)
@@ -361,8 +376,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         LatentRun run = run0;
         LatentPiece pc;
         int32_t T0 = 0;
-        uint32_t xn = 0;              // tiles exchanged by this warp
-        uint32_t sent = 0;            // softmax: bit b: parity of the exchanged tiles of S buffer b
+        uint32_t xn = 0;  // tiles sent by this warp
+        int32_t Tx = 0;   // the tile whose halves the softmax warp waits for next
         bool ok = true;
         for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
             const LatentItem &it = pc.it;
@@ -374,31 +389,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(p.q) +
                     (static_cast<int64_t>(it.q0) * p.heads + it.p0 + (live ? row : 0)) * W);
-                const int h0 = soft ? H / 2 : 0;  // first of the H / 2 dims
+                // H / 2 dims and two chunks of the rotary dims that this CTA
+                // multiplies (chunks 4 rank .. 4 rank + 3), all loads in flight at once
+                const int h0 = soft ? H / 2 : 0, ch = 4 * static_cast<int>(rank) + (soft ? 2 : 0);
+                uint4 v[H / 16 + 2];
 #pragma unroll
-                for (int c = 0; c < H / 2; c += 64) {
+                for (int i = 0; i < H / 16 + 2; ++i)
+                    v[i] = live ? __ldg(src + (i < H / 16 ? (rank * H + h0) / 8 + i : 2 * H / 8 + ch + i - H / 16))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < H / 16 + 2; ++i) {
+                    v[i].x ^= flip;
+                    v[i].y ^= flip;
+                    v[i].z ^= flip;
+                    v[i].w ^= flip;
+                }
+#pragma unroll
+                for (int c = 0; c < H / 16; c += 8) {
                     uint32_t r[32];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 v = live ? __ldg(src + (rank * H + h0 + c) / 8 + i) : make_uint4(0, 0, 0, 0);
-                        r[4 * i] = v.x ^ flip;
-                        r[4 * i + 1] = v.y ^ flip;
-                        r[4 * i + 2] = v.z ^ flip;
-                        r[4 * i + 3] = v.w ^ flip;
+                        r[4 * i] = v[c + i].x;
+                        r[4 * i + 1] = v[c + i].y;
+                        r[4 * i + 2] = v[c + i].z;
+                        r[4 * i + 3] = v[c + i].w;
                     }
-                    tc::st32(tQ + lane_base + (h0 + c) / 2, r);
+                    tc::st32(tQ + lane_base + h0 / 2 + 4 * c, r);
                 }
-                // the rotary chunks that this CTA multiplies: 4 rank .. 4 rank + 3
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int ch = 4 * static_cast<int>(rank) + (soft ? 2 : 0) + i;
-                    uint4 v = live ? __ldg(src + 2 * H / 8 + ch) : make_uint4(0, 0, 0, 0);
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
-                    *reinterpret_cast<uint4 *>(smem + L::kQOff + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
-                }
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4 *>(smem + L::kQOff + row * 128 + (((ch + i) ^ (row & 7)) << 4)) = v[H / 16 + i];
                 fence_proxy_async_smem();
                 tc::wait_st();
                 tc::fence_before();
@@ -408,44 +428,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             const bool warp_live = 32 * w < it.n;
             if (!soft) {
                 for (int32_t j = 0; j < pc.n; ++j) {
-                    const int32_t T = T0 + j, buf = T & 1;
+                    const int32_t T = T0 + j, buf = T & 1, st = T % kStages, tbase = (pc.t0 + j) * kKeys;
+                    // the peer has read the last tile's halves
+                    if (warp_live && xn > 0 && !(ok = lat_wait_cluster(&x_free[w], (xn - 1) & 1, p))) break;
                     if (!(ok = lat_wait(&s_full[buf], (T >> 1) & 1, p))) break;
-                    if (!warp_live) continue;  // (nobody waits for it)
                     tc::fence_after();
-                    uint32_t r0[32], r1[32];
-                    tc::ld32(tS + 64 * buf + lane_base, r0);
-                    tc::ld32(tS + 64 * buf + 32 + lane_base, r1);
-                    tc::wait_ld();
+                    if (warp_live) {
+                        uint32_t r0[32], r1[32];
+                        tc::ld32(tS + 64 * buf + lane_base, r0);
+                        tc::ld32(tS + 64 * buf + 32 + lane_base, r1);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            st_async(x_peer + q * (kRows * 16), x_full_peer, r0[4 * q], r0[4 * q + 1], r0[4 * q + 2], r0[4 * q + 3]);
+                            st_async(x_peer + (8 + q) * (kRows * 16), x_full_peer, r1[4 * q], r1[4 * q + 1], r1[4 * q + 2], r1[4 * q + 3]);
+                        }
+                        ++xn;
+                    }
+                    // value rows of keys past the item's or of pages not loaded
+                    // hold stale slots (possibly NaN): thread r zeroes half the
+                    // dims of key row r % 64 before the tile's products read them
+                    if (!(ok = lat_wait(&kv_full[st], (T / kStages) & 1, p))) break;
+                    const uint32_t mask = kmask[st];
+                    if (mask != all_pages || tbase + kKeys > it.hi) {
+                        const int kr = row & (kKeys - 1);
+                        if (tbase + kr >= it.hi || !((mask >> (kr / bs)) & 1u)) {
+                            uint8_t *v = smem + st * L::kStageBytes + (row >> 6) * (H / 128) * kRegion + kr * 128;
+#pragma unroll
+                            for (int i = 0; i < H / 128; ++i)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(v + i * kRegion + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
                     tc::fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_sent[4 * buf + w]);
-                    if (xn > 0 && !(ok = lat_wait_cluster(&x_free[w], (xn - 1) & 1, p))) break;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        st_async(x_peer + q * (kRows * 16), x_full_peer, r0[4 * q], r0[4 * q + 1], r0[4 * q + 2], r0[4 * q + 3]);
-                        st_async(x_peer + (8 + q) * (kRows * 16), x_full_peer, r1[4 * q], r1[4 * q + 1], r1[4 * q + 2], r1[4 * q + 3]);
-                    }
-                    ++xn;
+                    if (lane == 0) mbar_arrive(&x_full[w]);
                 }
                 T0 += pc.n;
                 continue;
             }
             const LatentRange rg = latent_range(p, it, row);
-            const int32_t sure = p.tree != nullptr ? min(rg.hi, it.first) : rg.hi;  // attended whatever the mask
+            // keys attended whatever the mask (a pair that is none takes every key: its
+            // output is not stored, and its warp keeps to the plain path)
+            const int32_t sure = row >= it.n ? INT32_MAX : p.tree != nullptr ? min(rg.hi, it.first) : rg.hi;
             float m_ref = -INFINITY, l = 0.f;
             for (int32_t j = 0; j < pc.n; ++j) {
                 const int32_t T = T0 + j, buf = T & 1, st = T % kStages;
                 const int32_t tbase = (pc.t0 + j) * kKeys;
                 const uint32_t sx = tS + 64 * buf + lane_base;
-                ok = lat_wait(&s_full[buf], (T >> 1) & 1, p);
-                ok = ok && lat_wait(&kv_full[st], (T / kStages) & 1, p);  // for kmask and the value rows
-                if (!ok) break;
+                // S's own half computed and read by the sender, the peer's half here,
+                // stale value rows zeroed: one barrier says it all
+                if (lane == 0) {
+                    if (warp_live)
+                        mbar_arrive_expect_tx(&x_full[w], 32 * kKeys * 4);
+                    else
+                        mbar_arrive(&x_full[w]);
+                }
+                if (!(ok = lat_wait_cluster(&x_full[w], T & 1, p))) break;
+                Tx = T + 1;
+                tc::fence_after();
                 const uint32_t mask = kmask[st];
                 if (warp_live) {
-                    if (lane == 0) mbar_arrive_expect_tx(&x_full[w], 32 * kKeys * 4);
-                    ok = lat_wait(&s_sent[4 * buf + w], (sent >> buf) & 1, p);
-                    sent ^= 1u << buf;
-                    tc::fence_after();
                     float s[64];
                     {
                         uint32_t r0[32], r1[32];
@@ -458,9 +503,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                             s[32 + e] = __uint_as_float(r1[e]);
                         }
                     }
-                    ok = ok && lat_wait_cluster(&x_full[w], xn & 1, p);
-                    if (!ok) break;
-                    ++xn;
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
                         const uint4 v = lds128(x_own + q * (kRows * 16));
@@ -551,21 +593,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                     f2_unpack(ls2[1], l2, l3);
                     l = l * (resc ? alpha : 1.f) + ((l0 + l1) + (l2 + l3));
                 }
-                // value rows of keys past the item's or of pages not loaded hold
-                // stale slots (possibly NaN): thread r zeroes half the dims of
-                // key row r % 64 before the tile's products read them
-                if (mask != all_pages || tbase + kKeys > it.hi) {
-                    const int kr = row & (kKeys - 1);
-                    if (tbase + kr >= it.hi || !((mask >> (kr / bs)) & 1u)) {
-                        uint8_t *v = smem + st * L::kStageBytes + (row >> 6) * (H / 128) * kRegion + kr * 128;
-#pragma unroll
-                        for (int i = 0; i < H / 128; ++i)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4 *>(v + i * kRegion + c * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                }
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
@@ -619,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         }
         // wind-down after a wait ran out: what the peer may still be sending
         // lands (or the limit passes) before this CTA's shared memory goes
-        if (soft && !ok) wait_cluster(&x_full[w], xn & 1, kWaitLimitNs);
+        if (soft && !ok) wait_cluster(&x_full[w], Tx & 1, kWaitLimitNs);
         __syncwarp();
     }
     // both CTAs: nothing is on its way into the other's shared memory any more
