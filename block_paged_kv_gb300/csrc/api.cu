@@ -1274,15 +1274,16 @@ bool latent_shape_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t b
     return dtype != PKV_FP8_E4M3 && latent % 16 == 0 && latent <= 512 && rope % 16 == 0 && rope <= 128 && bs <= 64;
 }
 
-// 3-D map over a latent pool [num_blocks][bs][row], box 64 dims x bs slots, 128-byte swizzle.
-bool encode_latent_map(CUtensorMap *map, const pkv_latent_pool &pool)
+// Maps over a latent pool [num_blocks][bs][row]: a 4-D view (64 dims, slot, 64-dim
+// region, block), box of 8 slots of the row's first `regions` regions, 128-byte
+// swizzle, so that a box lands region by region, 1 KiB each.
+bool encode_latent_map(CUtensorMap *map, const pkv_latent_pool &pool, int32_t regions)
 {
     const cuuint64_t W = static_cast<cuuint64_t>(pool.latent_dim) + pool.rope_dim, bs = pool.block_size;
-    cuuint64_t dims[3] = {W, bs, static_cast<cuuint64_t>(pool.num_blocks)};
-    cuuint64_t strides[2] = {W * 2, bs * W * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bs), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool.data, dims, strides, box, estr,
+    const cuuint64_t dims[4] = {64, bs, static_cast<cuuint64_t>(regions), static_cast<cuuint64_t>(pool.num_blocks)};
+    const cuuint64_t strides[3] = {W * 2, 128, bs * W * 2};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(regions), 1}, one[4] = {1, 1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool.data, dims, strides, box, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1550,9 +1551,10 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     if (!latent_tc_built(pool->dtype, p.latent, p.rope, p.block_size))
         return launch_latent_simple(p, pool->dtype, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
     if (!encode_fn_ready()) return PKV_ERR_CUDA;
-    CUtensorMap map;
-    if (!encode_latent_map(&map, *pool)) return PKV_ERR_UNSUPPORTED;
-    return launch_latent_tc(p, map, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    CUtensorMap map0, map1;  // whole rows, their latent parts
+    if (!encode_latent_map(&map0, *pool, (p.latent + p.rope) / 64) || !encode_latent_map(&map1, *pool, p.latent / 64))
+        return PKV_ERR_UNSUPPORTED;
+    return launch_latent_tc(p, map0, map1, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

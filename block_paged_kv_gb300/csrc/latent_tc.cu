@@ -7,30 +7,36 @@
 // row is read once for all of them.
 //
 // Layout.  128 pairs x 512 value dims in fp32 are the whole tensor memory of an
-// SM, so a pair of CTAs (a cluster) holds an item: CTA c has the c-th half of the
-// latent dims, and of the rotary dims, of queries and rows.  Each computes its
-// half of the reduction of S for all keys of a tile and all pairs, the halves are
-// exchanged through distributed shared memory and added (a + b on one side, b + a
-// on the other: the same bits), and each CTA then has the same weights and
-// multiplies them with its own half of the values.  No product is computed twice
-// and each CTA stages half a row, so that four 64-key tiles fit its shared memory.
-//   warps 0, 2   producers: 64-key tiles, one TMA box per (page, 64 dims);
-//   warp 1       issues tcgen05.mma from one elected lane: S = Q K^T (Q's latent
-//                half in tensor memory, its rotary part in shared memory), then
-//                O += P V with P read from tensor memory;
-//   warps 4-7    send S: each reads its 32 pairs' half sums and stores them into
-//                the peer's shared memory (st.async, counted by an mbarrier there);
-//   warps 8-11   softmax, one pair per thread: own half + peer's half, masks, the
-//                running maximum kept within 2^8 (O is rescaled in tensor memory
-//                only when it moves further), P written over S as two bf16 terms
-//                (hi + lo, 2^-17 relative, as in the paged prefill: a single term's
-//                2^-9 would be as large as the output's own rounding), epilogue.
-// Tensor memory: O 0 .. H-1 (H = latent_dim / 2), S buffers at H and H + 64, Q's
-// latent half (bf16 pairs) at H + 128.
+// SM, so a pair of CTAs (a cluster) holds an item, and the two products are split
+// between them: CTA 0 computes the scores and the softmax, CTA 1 the weighted
+// values.  What passes between them is the weights alone, one way, 16 KB a 64-key
+// tile through distributed shared memory (which carries about 21 bytes a cycle
+// between two SMs here: 800 cycles), so that neither waits for the other within a
+// tile.  Each CTA loads what it multiplies, CTA 0 whole rows, CTA 1 their latent
+// part a tile or two later, out of L2.
+//   both:  warps 0, 2, 3 producers (one issuing thread brings 21 to 25 bytes a cycle
+//     whatever its boxes' size, three of them 60), a box of 8 keys each;
+//   CTA 0: warp 1 issues S = Q K^T from one lane (Q in tensor memory, three S
+//     buffers); warps 4-7 and 8-11 softmax, a thread a pair, the even and the odd
+//     tiles: masks, the running maximum kept within 2^8 (handed from tile to tile),
+//     weights to CTA 1 (st.async, counted by an mbarrier there);
+//   CTA 1: warp 1 issues O += P V (P in shared memory as it came, 8 x 16-byte core
+//     matrices); warps 4-11: O rescaled in tensor memory when the maximum moved
+//     further, stale value rows zeroed, epilogue, half the dims each.
+// (With the dims of both products split instead, each CTA held half of the scores'
+// reduction, and exchanging those, 32 KB of fp32 a tile each way, took 1700 cycles
+// of a 3100-cycle tile.)
 //
-// Bound: a 64-key tile takes 18 N=64 products (32 cycles each) and 8 N=H products
-// (128 cycles at H = 256): about 1600 cycles, as many as the tile's bytes take at
-// the HBM rate (both CTAs' 72 KB at 1/76 of the copy rate: 0.82 us).
+// P enters P.V as one bf16 term, and the sums are those of the rounded weights, so
+// that a rounding moves a weight against the others but not their sum: the result
+// is off by 2^-9 of its size beside its own rounding of as much (2-norm against 64
+// bits 0.0023; 0.0017 with a second term, which would double CTA 1's products to
+// 2048 cycles a tile).
+//
+// Bound: a 64-key tile of 128 pairs takes 36 N=64 products (32 cycles each) on one
+// SM beside 8 N=256 ones (128 cycles) on the other, 1152 cycles, and its 72 KB at
+// 1/76 of the HBM copy rate 0.82 us, 1600 cycles: HBM, or the tensor cores where the
+// rows come from L2 (chunks).
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -43,30 +49,43 @@ constexpr int kRows = kLatentTcRows;
 constexpr int kKeys = 64;
 constexpr int kRope = 64;
 constexpr int kThreads = 384;
-constexpr int kRegion = kKeys * 128;      // 64 dims of a tile: 8 KiB, 128-byte swizzled rows
+constexpr int kSoftWarps = 8;             // of either CTA: warps 4 .. 11
+constexpr int kFins = 3;                  // pieces whose sums may be on their way
+constexpr int kSBufs = 3, kPBufs = 2;
+// What a tile's softmax waits for, in one barrier: its scores; what the producer wrote
+// of it, passed on by the issuing lane; the last tile's reference maximum (four
+// warps); the products of the tile kPBufs before, whose place its weights take.
+constexpr int kSArrivals = 1 + 1 + kSoftWarps / 2 + 1;
+constexpr int kMasks = 16;                // tiles between a producer and the softmax, at most stages + S buffers
+constexpr int kPBytes = kRows * kKeys * 2;
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled only when the max grows past 2^8
 constexpr uint32_t kTmemCols = 512;
 constexpr int32_t kLeastTiles = 2;        // of a worker's run
 // A piece's cost beside its tiles, in tiles, where the runs are long enough to be levelled by it
 constexpr int32_t kItemCost = 4, kLevelTiles = 8;
-template <int H>  // latent dims of a CTA
+template <int NR>  // 64-dim regions of the latent
 struct Layout {
-    static constexpr int kRegions = H / 64 + 1;           // its latent dims, then the rotary ones (both halves)
-    static constexpr int kStageBytes = kRegions * kRegion;
-    static constexpr int kStages = H == 256 ? 4 : 6;
-    static constexpr int kQOff = kStages * kStageBytes;   // Q's rotary dims: 128 rows of 128 bytes
-    static constexpr int kXOff = kQOff + kRows * 128;     // the peer's half sums: [16 key quads][128 pairs] float4
-    static constexpr int kBarOff = kXOff + kKeys * kRows * 4;
-    // kv_full, kv_empty [stages], s_full[2], p_full[2], x_full[4], x_free[4], pv_done, o_done, q_full, drain
-    static constexpr int kNumBars = 2 * kStages + 4 + 8 + 4;
+    // a tile: [8-key group][region][8 keys][128 bytes], 128-byte swizzled; CTA 0 has
+    // the rotary region too
+    static constexpr int kGroup0 = (NR + 1) * 1024, kGroup1 = NR * 1024;
+    static constexpr int kStages = NR == 8 ? 3 : 5;
+    // CTA 0, behind its stages: reference maxima [tile % 2][128], one half's (maximum, sum) [128]
+    static constexpr int kMaxOff = kStages * 8 * kGroup0;
+    // CTA 1: weights [buffer][8-key chunk][128 pairs][16 bytes]
+    static constexpr int kPOff = kStages * 8 * kGroup1;
+    static constexpr int kAfter0 = kMaxOff + 4 * kRows * 4, kAfter1 = kPOff + kPBufs * kPBytes;
+    static constexpr int kAlphaOff = kAfter0 > kAfter1 ? kAfter0 : kAfter1;  // [buffer][128]: factors of O
+    static constexpr int kFinOff = kAlphaOff + kPBufs * kRows * 4;           // [piece % kFins][128]: weight sums
+    static constexpr int kBarOff = kFinOff + kFins * kRows * 4;
+    // kv_full, kv_empty [stages], s_full, s_free [3], p_full, p_ready [2], fin_full [3], pv_done, o_done, q_full, l_full, drain
+    static constexpr int kNumBars = 2 * kStages + 2 * kSBufs + 2 * kPBufs + kFins + 5;
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
-    static constexpr int kScanOff = (kMaskOff + kStages * 4 + 15) & ~15;
+    static constexpr int kScanOff = (kMaskOff + kMasks * 4 + 15) & ~15;  // (of its own: the peer may be sending already)
     static constexpr int kTmemOff = kScanOff + (kThreads / 32 + 4) * 8;
     static constexpr int kBytes = kTmemOff + 16;
-    static constexpr int kLaunchBytes = kBytes + 1024;
-    static_assert(kLaunchBytes <= 227 * 1024, "shared memory of one CTA");
-    static constexpr uint32_t kS = H, kQ = H + 128;       // tensor-memory columns
-    static_assert(kQ + H / 2 <= kTmemCols, "tensor memory of one CTA");
+    static_assert(kBytes <= 227 * 1024 && kStages + kSBufs <= kMasks, "shared memory of one CTA");
+    static constexpr uint32_t kQCols = NR * 32 + 32;  // CTA 0's tensor memory: Q, then the S buffers
+    static_assert(kQCols + kSBufs * 64 <= kTmemCols && NR * 64 <= kTmemCols, "tensor memory of one CTA");
 };
 }  // namespace lt
 
@@ -97,12 +116,11 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t bar, uint32_t a
                  "r"(a), "r"(b), "r"(c), "r"(d), "r"(bar)
                  : "memory");
 }
-// Arrive on another CTA's mbarrier without ordering this thread's earlier accesses
-// (a release at cluster scope took 1.2 us here): for a buffer whose reads have
-// already returned their values.
-__device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar)
+// 4 bytes likewise
+__device__ __forceinline__ void st_async1(uint32_t addr, uint32_t bar, uint32_t a)
 {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(a), "r"(bar)
+                 : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 {
@@ -142,59 +160,76 @@ __device__ __forceinline__ bool lat_wait_cluster(uint64_t *bar, uint32_t parity,
     return ok;
 }
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int32_t c0, int32_t c1,
-                                            int32_t c2, uint64_t policy)
+// arrive on the mbarrier of every CTA in `mask` once the products issued so far have completed
+__device__ __forceinline__ void commit_to(uint64_t *bar, uint16_t mask)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(mask)
         : "memory");
 }
 
-template <int H>
+// Shared-memory matrix descriptor without swizzle, K-major: core matrices of 8 rows
+// x 16 bytes; lbo between core matrices along K, sbo between those along M.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
+}
+
+// An item's queries (one run of memory) into L2; threads 0 .. 255.
+__device__ __forceinline__ void prefetch_q(const LatentParams &p, const LatentItem &it, int tid, int row_elems)
+{
+    const char *q = static_cast<const char *>(p.q) + (static_cast<int64_t>(it.q0) * p.heads + it.p0) * row_elems * 2;
+    const int32_t bytes = it.n * row_elems * 2;
+    for (int32_t b = tid * 128; b < bytes; b += 256 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + b));
+}
+
+template <int NR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
-    latent_tc_kernel(const __grid_constant__ CUtensorMap map, const LatentParams p)
+    latent_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+                     const LatentParams p)
 {
     using namespace lt;
-    using L = Layout<H>;
-    constexpr int kStages = L::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
+    using L = Layout<NR>;
+    constexpr int kStages = L::kStages, R = NR * 64;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *kv_full = bars, *kv_empty = kv_full + kStages;
-    uint64_t *s_full = kv_empty + kStages;  // [buffer]: S's own half computed
-    uint64_t *p_full = s_full + 2;          // [buffer]: P stored
-    uint64_t *x_full = p_full + 2;          // [warp]: the peer's half has landed, own half read by the sender
-    uint64_t *x_free = x_full + 4;          // [warp]: the peer has read what was sent
-    uint64_t *pv_done = x_free + 4, *o_done = pv_done + 1, *q_full = o_done + 1, *drain = q_full + 1;
-    uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);  // [stage]: pages loaded
-    int64_t *scan = reinterpret_cast<int64_t *>(smem + L::kScanOff);
+    uint64_t *s_full = kv_empty + kStages, *s_free = s_full + kSBufs;   // CTA 0
+    uint64_t *p_full = s_free + kSBufs;     // CTA 1: weights landed
+    uint64_t *p_ready = p_full + kPBufs;    // CTA 1: O and the value rows ready for them
+    uint64_t *fin_full = p_ready + kPBufs;  // CTA 1: a piece's sums landed
+    uint64_t *pv_done = fin_full + kFins, *o_done = pv_done + 1;
+    uint64_t *q_full = o_done + 1, *l_full = q_full + 1, *drain = l_full + 1;
+    uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);  // [tile % kMasks]: pages loaded
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+    const uint32_t rank = cluster_rank();
     const int32_t worker = blockIdx.x >> 1;
     const int bs = p.block_size, nb = kKeys / bs;  // pages of a tile
     const uint32_t all_pages = (1u << nb) - 1u;
 
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&map);
+        tma_prefetch_desc(rank == 0 ? &map0 : &map1);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 2);  // the two producers
+            mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+        for (int i = 0; i < kSBufs; ++i) {
+            mbar_init(&s_full[i], kSArrivals);
+            mbar_init(&s_free[i], kSoftWarps / 2);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&x_full[i], 2);  // armed by the softmax warp; the sender
-            mbar_init(&x_free[i], 1);
+        for (int i = 0; i < kPBufs; ++i) {
+            mbar_init(&p_full[i], 1);
+            mbar_init(&p_ready[i], kSoftWarps);
         }
+        for (int i = 0; i < kFins; ++i) mbar_init(&fin_full[i], 1);
         mbar_init(pv_done, 1);
         mbar_init(o_done, 1);
-        mbar_init(q_full, 8);
+        mbar_init(q_full, kSoftWarps);
+        mbar_init(l_full, kSoftWarps / 2);
         mbar_init(drain, 1);
         fence_mbar_init();
     }
@@ -204,25 +239,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     cluster_sync();  // the peer's barriers exist before anything is sent
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tS = tmem + L::kS, tQ = tmem + L::kQ;
+    const uint32_t tS = tmem + L::kQCols;
     pdl_wait();
     pdl_trigger();
     // (a run without tiles: every role finds no piece)
-    const LatentRun run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, kLevelTiles, kItemCost, rank == 0, scan);
+    const LatentRun run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, kLevelTiles, kItemCost, rank == 0,
+                                                              reinterpret_cast<int64_t *>(smem + L::kScanOff));
+    LatentRun run = run0;
+    LatentPiece pc;
+    bool ok = true;
 
-    if (warp == 0 || warp == 2) {
+    if (warp == 0 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ producers
-        // Tile T (a running count) goes to stage T % kStages; warp 0 brings the
-        // first half of its latent regions and the rotary one, warp 2 the rest.
-        constexpr int kMine = H / 128;  // latent regions of a producer
-        const int first = warp == 0 ? 0 : kMine;
-        const uint32_t tile_bytes = static_cast<uint32_t>(kMine + (warp == 0 ? 1 : 0)) * bs * 128;  // of a page
-        const uint64_t policy = l2_evict_first_policy();
+        // Tile T (a running count) goes to stage T % kStages; producer w brings its
+        // 8-key groups w, w + 3, w + 6.
+        const int w = warp == 0 ? 0 : warp - 1;
+        const CUtensorMap *map = rank == 0 ? &map0 : &map1;
+        const int group = rank == 0 ? L::kGroup0 : L::kGroup1;
+        // CTA 1 is the rows' last reader
+        const uint64_t policy = rank == 0 ? l2_evict_normal_policy() : l2_evict_first_policy();
         auto withheld = [&](int32_t T) { return (p.drill & kDrillWithholdFirst) != 0 && T == 0; };
-        LatentRun run = run0;
-        LatentPiece pc;
         int32_t T = 0;
-        bool ok = true;
         while (ok && latent_next<kRows, kKeys>(p, run, pc)) {
             const int32_t *table = p.tables + static_cast<int64_t>(pc.it.r) * p.width;
             auto page_of = [&](int32_t t, bool &in) {  // lane < nb: page `lane` of tile t
@@ -239,380 +276,361 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 id = page_of(pc.t0 + j + 1, in);
                 if (T >= kStages && !(ok = lat_wait(&kv_empty[st], ((T / kStages) + 1) & 1, p))) break;
                 const bool good = cur_in && static_cast<uint32_t>(cur) < static_cast<uint32_t>(p.num_blocks);
-                if (warp == 0 && rank == 0 && cur_in && !good) report(p.status, PKV_DEV_BAD_BLOCK);
+                if (w == 0 && rank == 0 && cur_in && !good) report(p.status, PKV_DEV_BAD_BLOCK);
                 const uint32_t mask = __ballot_sync(0xffffffffu, good) & all_pages;
-                if (warp == 0 && lane == 0) kmask[st] = mask;
+                if (w == 0 && lane == 0) kmask[T % kMasks] = mask;
                 if (withheld(T)) continue;
-                if (lane == 0) {
+                if (w == 0 && lane == 0) {
                     if (mask == 0)
                         mbar_arrive(&kv_full[st]);
                     else
-                        mbar_arrive_expect_tx(&kv_full[st], __popc(mask) * tile_bytes);
+                        mbar_arrive_expect_tx(&kv_full[st], __popc(mask) * (bs / 8) * group);
                 }
                 __syncwarp();
-                uint8_t *dst = smem + st * L::kStageBytes;
-                for (int b = 0; b < nb; ++b) {
-                    const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
-                    if (((mask >> b) & 1u) && elect_one()) {
+                uint8_t *dst = smem + st * 8 * group;
 #pragma unroll
-                        for (int i = 0; i < kMine; ++i)
-                            tma_load_3d(dst + (first + i) * kRegion + b * bs * 128, &map, &kv_full[st],
-                                        static_cast<int32_t>(rank) * H + 64 * (first + i), 0, blk, policy);
-                        if (warp == 0)
-                            tma_load_3d(dst + (H / 64) * kRegion + b * bs * 128, &map, &kv_full[st], 2 * H, 0, blk, policy);
-                    }
+                for (int i = 0; i < 3; ++i) {
+                    const int g = w + 3 * i, b = (g & 7) * 8 / bs;
+                    const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
+                    if (g < 8 && ((mask >> b) & 1u) && elect_one())
+                        tma_load_4d(dst + g * group, map, &kv_full[st], 0, g * 8 - b * bs, 0, blk, policy);
                     __syncwarp();
                 }
             }
         }
-        // the last ring's worth of loads has landed before the warp leaves (a
-        // barrier counts both producers: waiting for its phase covers this
-        // warp's part whenever the other one issued its own)
+        // what is on its way into this CTA has landed before the warp leaves
         if (lane == 0)
             for (int32_t t = max(0, T - kStages); t < T; ++t)
                 if (!withheld(t)) mbar_wait(&kv_full[t % kStages], (t / kStages) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issue
-        constexpr uint32_t idS = tc::idesc_bf16(kRows, kKeys, 0, 0);
-        constexpr uint32_t idO = tc::idesc_bf16(kRows, H, 0, 1);  // values: MN-major (rows of dims)
-        const uint64_t dk = tc::smem_desc(smem_u32(smem), 16, 1024);
-        const uint64_t dv = tc::smem_desc(smem_u32(smem), kRegion, 1024);
-        const uint64_t dq = tc::smem_desc(smem_u32(smem + L::kQOff), 16, 1024);
-        constexpr uint64_t kStageStep = L::kStageBytes >> 4;
-        // One elected lane runs the whole role.  A product is issued about as it
-        // starts (the queue holds a few), so the waits for the next tile are looked
-        // at before a tile's last products: done between two tiles they left the
-        // tensor cores idle for 400 cycles each.
+        // ------------------------------------------------------------ products
+        // One elected lane runs the whole role: a product is issued about as it
+        // starts (the queue holds a few).
         if (elect_one()) {
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (mbar_wait(bar, parity, p.wait_ns)) return true;
                 report(p.status, PKV_DEV_TIMEOUT);
                 return false;
             };
-            auto kv_bar = [&](int32_t T) { return &kv_full[T % kStages]; };
-            auto kv_par = [&](int32_t T) { return static_cast<uint32_t>(T / kStages) & 1u; };
-            // products first .. last - 1 of S(T)'s H / 16 + 2
-            auto s_part = [&](int32_t T, int first, int last) {
-                const uint64_t kd = dk + static_cast<uint64_t>(T % kStages) * kStageStep;
-                const uint32_t d = tS + 64u * static_cast<uint32_t>(T & 1);
-                const uint64_t ro = static_cast<uint64_t>(rank * 64) >> 4;  // this CTA's half of the rotary dims
+            int32_t T = 0;
+            if (rank == 0) {
+                constexpr uint32_t idS = tc::idesc_bf16(kRows, kKeys, 0, 0);
+                const uint64_t dk = tc::smem_desc(smem_u32(smem), 16, L::kGroup0);
+                for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
+                    ok = wait(q_full, k & 1);
+                    for (int32_t j = 0; ok && j < pc.n; ++j, ++T) {
+                        const int st = T % kStages, buf = T % kSBufs;
+                        ok = wait(&kv_full[st], (T / kStages) & 1) &&
+                             (T < kSBufs || wait(&s_free[buf], ((T / kSBufs) + 1) & 1));
+                        if (!ok) break;
+                        // (and what the first tiles have no predecessor for)
+                        for (int i = 1 + (T == 0 ? kSoftWarps / 2 : 0) + (T < kPBufs ? 1 : 0); i > 0; --i)
+                            mbar_arrive(&s_full[buf]);
+                        tc::fence_after();
+                        const uint64_t kd = dk + static_cast<uint64_t>(st) * (8 * L::kGroup0 >> 4);
+                        const uint32_t d = tS + 64u * static_cast<uint32_t>(buf);
 #pragma unroll
-                for (int kk = 0; kk < H / 16 + 2; ++kk) {
-                    if (kk < first || kk >= last) continue;
-                    if (kk < 2)  // queries in shared memory
-                        tc::mma_ss(d, dq + ro + 2 * kk, kd + (((H / 64) * kRegion) >> 4) + ro + 2 * kk, idS, kk > 0 ? 1u : 0u);
-                    else
-                        tc::mma_ts(d, tQ + 8 * (kk - 2), kd + ((((kk - 2) >> 2) * kRegion + ((kk - 2) & 3) * 32) >> 4), idS, 1u);
-                }
-            };
-            auto pv = [&](int32_t T, bool start) {
-                const uint64_t vd = dv + static_cast<uint64_t>(T % kStages) * kStageStep;
-                const uint32_t a = tS + 64u * static_cast<uint32_t>(T & 1);
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc::mma_ts(tmem, a + 16 * kk + 8 * part, vd + static_cast<uint64_t>(kk) * (2048 >> 4), idO,
-                                   (part > 0 || kk > 0 || !start) ? 1u : 0u);
-                tc::commit(pv_done);
-                tc::commit(&kv_empty[T % kStages]);
-            };
-            constexpr int kAll = H / 16 + 2, kLate = 6;
-            LatentRun run = run0;
-            LatentPiece pc;
-            int32_t T0 = 0;
-            bool ok = true;
-            for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
-                const int32_t n = pc.n;
-                ok = wait(q_full, k & 1) && wait(kv_bar(T0), kv_par(T0));
-                if (!ok) break;
-                tc::fence_after();
-                s_part(T0, 0, kAll);
-                tc::commit(&s_full[T0 & 1]);
-                if (n >= 2) {
-                    if (!(ok = wait(kv_bar(T0 + 1), kv_par(T0 + 1)))) break;
-                    s_part(T0 + 1, 0, kAll);
-                    tc::commit(&s_full[(T0 + 1) & 1]);
-                }
-                bool have_kv = false, have_p = false;  // K/V(T + 2) landed, P(T) stored
-                for (int32_t j = 0; j < n; ++j) {
-                    const int32_t T = T0 + j;
-                    const bool more = j + 2 < n;
-                    ok = (!more || have_kv || wait(kv_bar(T + 2), kv_par(T + 2))) && (have_p || wait(&p_full[T & 1], (T >> 1) & 1));
-                    if (!ok) break;
-                    tc::fence_after();
-                    pv(T, j == 0);
-                    if (j == n - 1) tc::commit(o_done);
-                    if (more) s_part(T + 2, 0, kAll - kLate);
-                    have_kv = j + 3 < n && mbar_try_wait(kv_bar(T + 3), kv_par(T + 3));
-                    have_p = j + 1 < n && mbar_try_wait(&p_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
-                    if (more) {
-                        s_part(T + 2, kAll - kLate, kAll);
-                        tc::commit(&s_full[T & 1]);
+                        for (int kk = 0; kk < (NR + 1) * 4; ++kk)
+                            tc::mma_ts(d, tmem + 8 * kk, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                        tc::commit(&s_full[buf]);
+                        tc::commit(&kv_empty[st]);
                     }
                 }
-                T0 += n;
+                // CTA 1's last arrivals, for two tiles that do not follow, have come
+                for (int32_t t = T; ok && T > 0 && t < T + kPBufs; ++t) {
+                    if (t >= kSBufs && !(ok = wait(&s_free[t % kSBufs], ((t / kSBufs) + 1) & 1))) break;
+                    for (int i = kSArrivals - (t == T ? kSoftWarps / 2 : 0) - (t >= kPBufs ? 1 : 0); i > 0; --i)
+                        mbar_arrive(&s_full[t % kSBufs]);
+                    ok = wait(&s_full[t % kSBufs], (t / kSBufs) & 1);
+                }
+            } else {
+                constexpr int N = R < 256 ? R : 256;
+                constexpr uint32_t idO = tc::idesc_bf16(kRows, N, 0, 1);  // values: MN-major (rows of dims)
+                const uint64_t dv = tc::smem_desc(smem_u32(smem), 1024, L::kGroup1);
+                const uint64_t dp = smem_desc_plain(smem_u32(smem + L::kPOff), kRows * 16, 128);
+                while (ok && latent_next<kRows, kKeys>(p, run, pc)) {
+                    for (int32_t j = 0; j < pc.n; ++j, ++T) {
+                        const int st = T % kStages, buf = T % kPBufs;
+                        ok = wait(&p_ready[buf], (T / kPBufs) & 1) && wait(&kv_full[st], (T / kStages) & 1);
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint64_t vd = dv + static_cast<uint64_t>(st) * (8 * L::kGroup1 >> 4);
+                        const uint64_t pd = dp + static_cast<uint64_t>(buf) * (kPBytes >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+#pragma unroll
+                            for (int n = 0; n < R / N; ++n)
+                                tc::mma_ss(tmem + n * N, pd + kk * ((2 * kRows * 16) >> 4),
+                                           vd + ((kk * 2 * L::kGroup1 + n * (N / 64) * 1024) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
+                        tc::commit(pv_done);
+                        tc::commit(&kv_empty[st]);
+                        commit_to(&s_full[(T + kPBufs) % kSBufs], 1);  // CTA 0's
+                        if (j == pc.n - 1) tc::commit(o_done);
+                    }
+                }
             }
             // every product has completed before tensor memory is freed
             tc::commit(drain);
             mbar_wait(drain, 0);
         }
         __syncwarp();
-    } else if (warp >= 4) {
-        // ------------------------------------------------ senders (4-7), softmax (8-11)
-        const bool soft = warp >= 8;
-        const int w = warp & 3, row = 32 * w + lane;
+    } else if (warp >= 4 && rank == 0) {
+        // ------------------------------------------------------------ softmax
+        // group g = 0 (warps 4-7) takes the even tiles, g = 1 (warps 8-11) the odd ones
+        const int g = (warp >> 2) - 1, w = warp & 3, row = 32 * w + lane;
         const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
         // a negative scale: -q is staged (exact), so that scores take a positive factor
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         // kept away from 0 so that a masked score (-inf) never meets a zero factor
         const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
-        const int W = 2 * H + kRope;
-        uint8_t *x_mem = smem + L::kXOff;
-        const uint32_t x_own = smem_u32(x_mem) + row * 16;
-        const uint32_t x_peer = map_shared(x_own, peer), x_full_peer = map_shared(smem_u32(&x_full[w]), peer);
-        const uint32_t x_free_peer = map_shared(smem_u32(&x_free[w]), peer);
-        LatentRun run = run0;
-        LatentPiece pc;
+        float *refs = reinterpret_cast<float *>(smem + L::kMaxOff);                       // [T % 2][128]
+        float2 *sums = reinterpret_cast<float2 *>(smem + L::kMaxOff + 2 * kRows * 4);     // [128]
+        const uint32_t p_peer = map_shared(smem_u32(smem + L::kPOff), 1) + row * 16;
+        const uint32_t alpha_peer = map_shared(smem_u32(smem + L::kAlphaOff), 1) + row * 4;
+        const uint32_t fin_peer = map_shared(smem_u32(smem + L::kFinOff), 1) + row * 4;
+        const uint32_t p_full_peer = map_shared(smem_u32(p_full), 1), fin_full_peer = map_shared(smem_u32(fin_full), 1);
         int32_t T0 = 0;
-        uint32_t xn = 0;  // tiles sent by this warp
-        int32_t Tx = 0;   // the tile whose halves the softmax warp waits for next
-        bool ok = true;
         for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
             const LatentItem &it = pc.it;
-            // Q: this warp's 32 pairs, half of the CTA's dims (the senders the
-            // first half); the last piece's products have read the old one
+            // Q: this warp's 32 pairs, half of their dims (the last piece's products
+            // have read the old one: this warp saw its last tile's scores)
             tc::fence_after();
             {
                 const bool live = row < it.n;
                 const uint4 *src = reinterpret_cast<const uint4 *>(
                     static_cast<const uint16_t *>(p.q) +
-                    (static_cast<int64_t>(it.q0) * p.heads + it.p0 + (live ? row : 0)) * W);
-                // H / 2 dims and two chunks of the rotary dims that this CTA
-                // multiplies (chunks 4 rank .. 4 rank + 3), all loads in flight at once
-                const int h0 = soft ? H / 2 : 0, ch = 4 * static_cast<int>(rank) + (soft ? 2 : 0);
-                uint4 v[H / 16 + 2];
+                    (static_cast<int64_t>(it.q0) * p.heads + it.p0 + (live ? row : 0)) * (R + kRope));
+                constexpr int kVecs = (R + kRope) / 16, kFly = 20;  // 16-byte vectors of a half, in flight
+                static_assert(kVecs % 4 == 0, "stored four at a time");
 #pragma unroll
-                for (int i = 0; i < H / 16 + 2; ++i)
-                    v[i] = live ? __ldg(src + (i < H / 16 ? (rank * H + h0) / 8 + i : 2 * H / 8 + ch + i - H / 16))
-                                : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < kVecs; c += kFly) {
+                    uint4 v[kFly];
 #pragma unroll
-                for (int i = 0; i < H / 16 + 2; ++i) {
-                    v[i].x ^= flip;
-                    v[i].y ^= flip;
-                    v[i].z ^= flip;
-                    v[i].w ^= flip;
-                }
+                    for (int i = 0; i < kFly; ++i)
+                        v[i] = live && c + i < kVecs ? __ldg(src + g * kVecs + c + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int c = 0; c < H / 16; c += 8) {
-                    uint32_t r[32];
+                    for (int i = 0; i < kFly; i += 4) {
+                        if (c + i >= kVecs) continue;
+                        uint32_t r[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        r[4 * i] = v[c + i].x;
-                        r[4 * i + 1] = v[c + i].y;
-                        r[4 * i + 2] = v[c + i].z;
-                        r[4 * i + 3] = v[c + i].w;
+                        for (int e = 0; e < 4; ++e) {
+                            r[4 * e] = v[i + e].x ^ flip;
+                            r[4 * e + 1] = v[i + e].y ^ flip;
+                            r[4 * e + 2] = v[i + e].z ^ flip;
+                            r[4 * e + 3] = v[i + e].w ^ flip;
+                        }
+                        tc::st16(tmem + lane_base + (g * kVecs + c + i) * 4, r);
                     }
-                    tc::st32(tQ + lane_base + h0 / 2 + 4 * c, r);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<uint4 *>(smem + L::kQOff + row * 128 + (((ch + i) ^ (row & 7)) << 4)) = v[H / 16 + i];
-                fence_proxy_async_smem();
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
             const bool warp_live = 32 * w < it.n;
-            if (!soft) {
-                for (int32_t j = 0; j < pc.n; ++j) {
-                    const int32_t T = T0 + j, buf = T & 1, st = T % kStages, tbase = (pc.t0 + j) * kKeys;
-                    // the peer has read the last tile's halves
-                    if (warp_live && xn > 0 && !(ok = lat_wait_cluster(&x_free[w], (xn - 1) & 1, p))) break;
-                    if (!(ok = lat_wait(&s_full[buf], (T >> 1) & 1, p))) break;
-                    tc::fence_after();
-                    if (warp_live) {
-                        uint32_t r0[32], r1[32];
-                        tc::ld32(tS + 64 * buf + lane_base, r0);
-                        tc::ld32(tS + 64 * buf + 32 + lane_base, r1);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            st_async(x_peer + q * (kRows * 16), x_full_peer, r0[4 * q], r0[4 * q + 1], r0[4 * q + 2], r0[4 * q + 3]);
-                            st_async(x_peer + (8 + q) * (kRows * 16), x_full_peer, r1[4 * q], r1[4 * q + 1], r1[4 * q + 2], r1[4 * q + 3]);
-                        }
-                        ++xn;
-                    }
-                    // value rows of keys past the item's or of pages not loaded
-                    // hold stale slots (possibly NaN): thread r zeroes half the
-                    // dims of key row r % 64 before the tile's products read them
-                    if (!(ok = lat_wait(&kv_full[st], (T / kStages) & 1, p))) break;
-                    const uint32_t mask = kmask[st];
-                    if (mask != all_pages || tbase + kKeys > it.hi) {
-                        const int kr = row & (kKeys - 1);
-                        if (tbase + kr >= it.hi || !((mask >> (kr / bs)) & 1u)) {
-                            uint8_t *v = smem + st * L::kStageBytes + (row >> 6) * (H / 128) * kRegion + kr * 128;
-#pragma unroll
-                            for (int i = 0; i < H / 128; ++i)
-#pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    *reinterpret_cast<uint4 *>(v + i * kRegion + c * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&x_full[w]);
-                }
-                T0 += pc.n;
-                continue;
-            }
             const LatentRange rg = latent_range(p, it, row);
             // keys attended whatever the mask (a pair that is none takes every key: its
             // output is not stored, and its warp keeps to the plain path)
             const int32_t sure = row >= it.n ? INT32_MAX : p.tree != nullptr ? min(rg.hi, it.first) : rg.hi;
-            float m_ref = -INFINITY, l = 0.f;
-            for (int32_t j = 0; j < pc.n; ++j) {
-                const int32_t T = T0 + j, buf = T & 1, st = T % kStages;
-                const int32_t tbase = (pc.t0 + j) * kKeys;
-                const uint32_t sx = tS + 64 * buf + lane_base;
-                // S's own half computed and read by the sender, the peer's half here,
-                // stale value rows zeroed: one barrier says it all
-                if (lane == 0) {
-                    if (warp_live)
-                        mbar_arrive_expect_tx(&x_full[w], 32 * kKeys * 4);
-                    else
-                        mbar_arrive(&x_full[w]);
+            const int32_t end = T0 + pc.n;
+            float m_ref = -INFINITY, l = 0.f;  // of this group's tiles: l in units of 2^m_ref
+            for (int32_t T = T0 + ((T0 ^ g) & 1); T < end; T += 2) {
+                const int buf = T % kSBufs, pb = T & 1;
+                const int32_t tbase = (pc.t0 + T - T0) * kKeys;
+                if (!(ok = lat_wait_cluster(&s_full[buf], (T / kSBufs) & 1, p))) break;
+                const uint32_t mask = kmask[T % kMasks];
+                if (!warp_live) {
+                    if (lane == 0) {
+                        mbar_arrive(&s_free[buf]);
+                        mbar_arrive(&s_full[(T + 1) % kSBufs]);
+                    }
+                    continue;
                 }
-                if (!(ok = lat_wait_cluster(&x_full[w], T & 1, p))) break;
-                Tx = T + 1;
                 tc::fence_after();
-                const uint32_t mask = kmask[st];
-                if (warp_live) {
-                    float s[64];
-                    {
-                        uint32_t r0[32], r1[32];
-                        tc::ld32(sx, r0);
-                        tc::ld32(sx + 32, r1);
-                        tc::wait_ld();
+                float s[64];
+                {
+                    uint32_t r0[32], r1[32];
+                    tc::ld32(tS + 64 * buf + lane_base, r0);
+                    tc::ld32(tS + 64 * buf + 32 + lane_base, r1);
+                    tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            s[e] = __uint_as_float(r0[e]);
-                            s[32 + e] = __uint_as_float(r1[e]);
-                        }
+                    for (int e = 0; e < 32; ++e) {
+                        s[e] = __uint_as_float(r0[e]);
+                        s[32 + e] = __uint_as_float(r1[e]);
                     }
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        const uint4 v = lds128(x_own + q * (kRows * 16));
-                        s[4 * q] += __uint_as_float(v.x);
-                        s[4 * q + 1] += __uint_as_float(v.y);
-                        s[4 * q + 2] += __uint_as_float(v.z);
-                        s[4 * q + 3] += __uint_as_float(v.w);
-                    }
-                    if (!(mask == all_pages && tbase + kKeys <= sure)) {
-                        // attended keys as bits
-                        const auto below = [](int32_t n) {  // bits 0 .. n-1
-                            return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
-                        };
-                        uint64_t bits = below(rg.hi - tbase);
-                        if (p.tree != nullptr) bits &= tree_bits(rg.mask, tbase, it.first);
-                        uint64_t pages = 0;
-                        for (int b = 0; b < nb; ++b) pages |= ((mask >> b) & 1u) ? below(bs) << (b * bs) : 0ull;
-                        bits &= pages;
-                        const uint32_t b0 = static_cast<uint32_t>(bits), b1 = static_cast<uint32_t>(bits >> 32);
-#pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            s[e] = (((e < 32 ? b0 : b1) >> (e & 31)) & 1u) ? s[e] : -INFINITY;
-                    }
-                    float mt;
-                    {
-                        float m8[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            m8[e] = fmax3(s[e], s[8 + e], s[16 + e]);
-                            m8[e] = fmax3(m8[e], s[24 + e], s[32 + e]);
-                            m8[e] = fmax3(m8[e], s[40 + e], s[48 + e]);
-                            m8[e] = fmaxf(m8[e], s[56 + e]);
-                        }
-                        mt = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7]))) * sl;
-                    }
-                    // the reference max stays within 2^8 of the running max
-                    const float new_ref = (mt > m_ref + kRescaleLog2) ? mt : m_ref;
-                    const float alpha = fast_exp2(m_ref - new_ref);  // 0 from -inf, 1 if unchanged
-                    const bool resc = new_ref != m_ref && m_ref != -INFINITY;
-                    const bool any = __any_sync(0xffffffffu, resc);
-                    // every lane's vote came of values that it has read: the peer
-                    // may overwrite them
-                    if (lane == 0) arrive_remote_relaxed(x_free_peer);
-                    if (any) {
-                        // O holds P.V up to tile j-1 once that product completes
-                        if (j > 0) {
-                            if (!(ok = lat_wait(pv_done, (T - 1) & 1, p))) break;
-                            tc::fence_after();
-                        }
-                        const float f = resc ? alpha : 1.f;
-#pragma unroll 1
-                        for (int c = 0; c < H; c += 32) {
-                            uint32_t r[32];
-                            tc::ld32(tmem + lane_base + c, r);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                            tc::st32(tmem + lane_base + c, r);
-                        }
-                        tc::wait_st();
-                    }
-                    m_ref = new_ref;
-                    const float nmu = new_ref == -INFINITY ? 0.f : -new_ref;
-                    const uint64_t sl2 = f2_pack(sl, sl), nmu2 = f2_pack(nmu, nmu);
-                    uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                    // group g (16 keys) -> 8 columns of P hi then 8 of P lo
-#pragma unroll
-                    for (int g = 0; g < kKeys / 16; ++g) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float a, b;
-                            f2_unpack(f2_fma(f2_pack(s[16 * g + 2 * e], s[16 * g + 2 * e + 1]), sl2, nmu2), a, b);
-                            a = fast_exp2(a);
-                            b = fast_exp2(b);
-                            const uint64_t ab = f2_pack(a, b);
-                            ls2[e & 1] = f2_add(ls2[e & 1], ab);
-                            const uint32_t hi = pack_bf16x2(a, b);
-                            pk[e] = hi;
-                            float ra, rb;
-                            f2_unpack(f2_sub(ab, f2_pack(bf16lo_to_f32(hi), bf16hi_to_f32(hi))), ra, rb);
-                            pk[8 + e] = pack_bf16x2(ra, rb);
-                        }
-                        tc::st16(sx + 16 * g, pk);
-                    }
-                    float l0, l1, l2, l3;
-                    f2_unpack(ls2[0], l0, l1);
-                    f2_unpack(ls2[1], l2, l3);
-                    l = l * (resc ? alpha : 1.f) + ((l0 + l1) + (l2 + l3));
                 }
-                tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[buf]);
+                if (lane == 0) mbar_arrive(&s_free[buf]);
+                if (!(mask == all_pages && tbase + kKeys <= sure)) {
+                    // attended keys as bits
+                    const auto below = [](int32_t n) {  // bits 0 .. n-1
+                        return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+                    };
+                    uint64_t bits = below(rg.hi - tbase);
+                    if (p.tree != nullptr) bits &= tree_bits(rg.mask, tbase, it.first);
+                    uint64_t pages = 0;
+                    for (int b = 0; b < nb; ++b) pages |= ((mask >> b) & 1u) ? below(bs) << (b * bs) : 0ull;
+                    bits &= pages;
+                    const uint32_t b0 = static_cast<uint32_t>(bits), b1 = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) s[e] = (((e < 32 ? b0 : b1) >> (e & 31)) & 1u) ? s[e] : -INFINITY;
+                }
+                float mt;
+                {
+                    float m8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        m8[e] = fmax3(s[e], s[8 + e], s[16 + e]);
+                        m8[e] = fmax3(m8[e], s[24 + e], s[32 + e]);
+                        m8[e] = fmax3(m8[e], s[40 + e], s[48 + e]);
+                        m8[e] = fmaxf(m8[e], s[56 + e]);
+                    }
+                    mt = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], fmax3(m8[5], m8[6], m8[7]))) * sl;
+                }
+                // the reference max stays within 2^8 of the running max
+                const float last_ref = T > T0 ? refs[(1 - pb) * kRows + row] : -INFINITY;
+                const float new_ref = (mt > last_ref + kRescaleLog2) ? mt : last_ref;
+                refs[pb * kRows + row] = new_ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_full[(T + 1) % kSBufs]);  // the next tile's group may take it
+                const float alpha = new_ref != last_ref && last_ref != -INFINITY ? fast_exp2(last_ref - new_ref) : 1.f;
+                if (new_ref != m_ref) l *= fast_exp2(m_ref - new_ref);  // (0 from -inf)
+                m_ref = new_ref;
+                const float nmu = new_ref == -INFINITY ? 0.f : -new_ref;
+                const uint64_t sl2 = f2_pack(sl, sl), nmu2 = f2_pack(nmu, nmu);
+                uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                const uint32_t bar = p_full_peer + 8 * pb, dst = p_peer + pb * kPBytes;
+                // eight keys a time: weights to bf16, their sums, and off to CTA 1
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(s[8 * i + 2 * e], s[8 * i + 2 * e + 1]), sl2, nmu2), a, b);
+                        pk[e] = pack_bf16x2(fast_exp2(a), fast_exp2(b));
+                        ls2[e & 1] = f2_add(ls2[e & 1], f2_pack(bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e])));
+                    }
+                    st_async(dst + i * (kRows * 16), bar, pk[0], pk[1], pk[2], pk[3]);
+                }
+                st_async1(alpha_peer + pb * (kRows * 4), bar, __float_as_uint(alpha));
+                float l0, l1, l2, l3;
+                f2_unpack(ls2[0], l0, l1);
+                f2_unpack(ls2[1], l2, l3);
+                l += (l0 + l1) + (l2 + l3);
             }
             if (!ok) break;
-            T0 += pc.n;
+            const int32_t Tl = end - 1;
+            if ((Tl & 1) != g) {
+                // the other group has the piece's last tile: this group's sums go to it
+                sums[row] = make_float2(m_ref, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_full);
+                if (!(ok = lat_wait_cluster(&s_full[Tl % kSBufs], (Tl / kSBufs) & 1, p))) break;  // Q has been read
+            } else {
+                if (!(ok = lat_wait(l_full, k & 1, p))) break;
+                const float2 o = sums[row];
+                l += o.x == m_ref ? o.y : o.y * fast_exp2(o.x - m_ref);  // (0 from -inf)
+                if (!pc.whole) {
+                    if (row < it.n) latent_part_ml<kRows>(p, worker, pc.slot)[row] = make_float2(m_ref, l);
+                } else if (warp_live) {
+                    // (CTA 1 has read the sums of kFins pieces ago: this tile's barrier
+                    // came after the products of the tile two before, hence after the
+                    // epilogue before that tile's piece)
+                    st_async1(fin_peer + (k % kFins) * (kRows * 4), fin_full_peer + 8 * (k % kFins), __float_as_uint(l));
+                }
+            }
+            T0 = end;
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ values (CTA 1)
+        const int half = (warp >> 2) - 1, w = warp & 3, row = 32 * w + lane;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * w) << 16;
+        const uint32_t ox = tmem + lane_base + half * (R / 2);
+        const float *alphas = reinterpret_cast<const float *>(smem + L::kAlphaOff);
+        const float *fins = reinterpret_cast<const float *>(smem + L::kFinOff);
+        const int tid = threadIdx.x - 128;
+        const bool arms = warp == 4 && lane == 0;
+        int32_t T = 0, Tp = 0;   // Tp: the tile whose weights are waited for next
+        uint32_t fin_phase = 0;  // bit b: parity of fin_full[b]'s next phase
+        for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
+            const LatentItem &it = pc.it;
+            const uint32_t live_warps = static_cast<uint32_t>((it.n + 31) / 32);
+            const bool warp_live = 32 * w < it.n, live = row < it.n;
+            // CTA 0's queries into L2: the first piece's, and the next one's (a load
+            // that goes to HBM waits behind the rows on their way, 4 us)
+            {
+                LatentRun ahead = run;
+                LatentPiece nx;
+                if (k == 0) prefetch_q(p, it, tid, R + kRope);
+                if (latent_next<kRows, kKeys>(p, ahead, nx)) prefetch_q(p, nx.it, tid, R + kRope);
+            }
+            for (int32_t j = 0; j < pc.n; ++j, ++T) {
+                const int st = T % kStages, pb = T % kPBufs;
+                const int32_t tbase = (pc.t0 + j) * kKeys;
+                if (arms) mbar_arrive_expect_tx(&p_full[pb], live_warps * (32 * kKeys * 2 + 32 * 4));
+                ok = lat_wait(&kv_full[st], (T / kStages) & 1, p);
+                // value rows of keys past the item's or of pages not loaded hold stale
+                // slots (possibly NaN): zeroed before the tile's products read them
+                if (ok) {
+                    const uint32_t mask = kmask[T % kMasks];
+                    if (mask != all_pages || tbase + kKeys > it.hi) {
+                        const int kr = tid & (kKeys - 1), quarter = tid >> 6;
+                        if (tbase + kr >= it.hi || !((mask >> (kr / bs)) & 1u)) {
+                            uint8_t *v = smem + st * 8 * L::kGroup1 + (kr >> 3) * L::kGroup1 + quarter * (NR / 4) * 1024 + (kr & 7) * 128;
+#pragma unroll
+                            for (int i = 0; i < NR / 4; ++i)
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    *reinterpret_cast<uint4 *>(v + i * 1024 + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
+                ok = ok && lat_wait_cluster(&p_full[pb], (T / kPBufs) & 1, p);
+                if (!ok) break;
+                Tp = T + 1;
+                const float alpha = warp_live ? alphas[pb * kRows + row] : 1.f;
+                if (j > 0 && __any_sync(0xffffffffu, live && alpha != 1.f)) {
+                    // O holds P.V up to the last tile once that product completes
+                    if (!(ok = lat_wait(pv_done, (T - 1) & 1, p))) break;
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < R / 2; c += 32) {
+                        uint32_t r[32];
+                        tc::ld32(ox + c, r);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+                        tc::st32(ox + c, r);
+                    }
+                    tc::wait_st();
+                }
+                fence_proxy_async_smem();  // the weights and zeroed rows, before the tensor cores read them
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[pb]);
+            }
+            if (!ok) break;
             // epilogue, once the piece's last product is in (a parity names one
             // phase only: o_done completes once a piece, its next needs this warp)
-            if (!(ok = lat_wait(o_done, k & 1, p))) break;
+            const int fb = k % kFins;
+            if (pc.whole && arms) mbar_arrive_expect_tx(&fin_full[fb], live_warps * 128);
+            ok = lat_wait(o_done, k & 1, p);
+            if (ok && pc.whole) ok = lat_wait_cluster(&fin_full[fb], (fin_phase >> fb) & 1, p);
+            if (!ok) break;
+            if (pc.whole) fin_phase ^= 1u << fb;
             tc::fence_after();
-            const bool live = row < it.n;
             if (pc.whole) {
+                const float l = live ? fins[fb * kRows + row] : 0.f;
                 const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                                       latent_out_row(p, it, live ? row : 0) + rank * H);
+                                                       latent_out_row(p, it, live ? row : 0) + half * (R / 2));
 #pragma unroll 1
-                for (int c = 0; warp_live && c < H; c += 32) {
+                for (int c = 0; warp_live && c < R / 2; c += 32) {
                     uint32_t r[32];
-                    tc::ld32(tmem + lane_base + c, r);
+                    tc::ld32(ox + c, r);
                     tc::wait_ld();
                     if (!live) continue;
 #pragma unroll
@@ -627,11 +645,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 }
             } else {
                 // a partial: value quads of 32 pairs side by side
-                float4 *dst = latent_part_o<kRows>(p, worker, pc.slot) + (rank * H / 4) * kRows + row;
+                float4 *dst = latent_part_o<kRows>(p, worker, pc.slot) + (half * (R / 8)) * kRows + row;
 #pragma unroll 1
-                for (int c = 0; warp_live && c < H; c += 32) {
+                for (int c = 0; warp_live && c < R / 2; c += 32) {
                     uint32_t r[32];
-                    tc::ld32(tmem + lane_base + c, r);
+                    tc::ld32(ox + c, r);
                     tc::wait_ld();
                     if (!live) continue;
 #pragma unroll
@@ -640,13 +658,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                             make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
                                         __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
                 }
-                if (rank == 0 && live) latent_part_ml<kRows>(p, worker, pc.slot)[row] = make_float2(m_ref, l);
             }
             tc::fence_before();
         }
-        // wind-down after a wait ran out: what the peer may still be sending
-        // lands (or the limit passes) before this CTA's shared memory goes
-        if (soft && !ok) wait_cluster(&x_full[w], Tx & 1, kWaitLimitNs);
+        // wind-down after a wait ran out: what CTA 0 may still be sending lands (or the
+        // limit passes) before this CTA's shared memory goes
+        if (!ok)
+            for (int32_t t = Tp; t < Tp + kPBufs; ++t) wait_cluster(&p_full[t % kPBufs], (t / kPBufs) & 1, kWaitLimitNs);
         __syncwarp();
     }
     // both CTAs: nothing is on its way into the other's shared memory any more
@@ -661,14 +679,15 @@ bool latent_tc_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs)
     return dtype == PKV_BF16 && (latent == 256 || latent == 512) && rope == lt::kRope && (bs == 16 || bs == 32 || bs == 64);
 }
 
-template <int H>
-static cudaError_t launch(const LatentParams &p, const CUtensorMap &map, cudaStream_t stream)
+template <int NR>
+static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, cudaStream_t stream)
 {
-    constexpr int smem = lt::Layout<H>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(latent_tc_kernel<H>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = lt::Layout<NR>::kBytes;
+    cudaError_t err = cudaFuncSetAttribute(latent_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_LATENT, stream);
-    err = launch_pdl(latent_tc_kernel<H>, dim3(static_cast<unsigned>(2 * p.workers)), dim3(lt::kThreads), smem, stream, map, p);
+    err = launch_pdl(latent_tc_kernel<NR>, dim3(static_cast<unsigned>(2 * p.workers)), dim3(lt::kThreads), smem, stream, map0,
+                     map1, p);
     if (err == cudaSuccess)
         err = launch_pdl(latent_merge_kernel<__nv_bfloat16, lt::kRows, lt::kKeys>,
                          dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>((p.latent + 63) / 64)),
@@ -677,9 +696,9 @@ static cudaError_t launch(const LatentParams &p, const CUtensorMap &map, cudaStr
     return err;
 }
 
-cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map, cudaStream_t stream)
+cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, cudaStream_t stream)
 {
-    return p.latent == 512 ? launch<256>(p, map, stream) : launch<128>(p, map, stream);
+    return p.latent == 512 ? launch<8>(p, map0, map1, stream) : launch<4>(p, map0, map1, stream);
 }
 
 }  // namespace pkv

@@ -152,6 +152,13 @@ __device__ __forceinline__ uint64_t l2_evict_last_policy()
     return p;
 }
 
+__device__ __forceinline__ uint64_t l2_evict_normal_policy()
+{
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");

@@ -59,7 +59,7 @@ class Case:
             ok = seen(int(L), int(b - a), None if self.masks is None else self.masks[a:b])
             for h in heads or range(self.H):
                 ref, mag, A = attend(q[a:b, h], rows, rows[:, :self.R], ok, self.scale if scale is None else scale)
-                check(out[a:b, h], ref, mag, A, self.R + self.Dr, self.kind, self.act, f"row {r} head {h}")
+                check(out[a:b, h], ref, mag, A, self.R + self.Dr, "bf16 weights" if self.kind == "bf16" else self.kind, self.act, f"row {r} head {h}")
 
 
 DECODE = [
@@ -166,7 +166,7 @@ def test_device_reports(pkv):
         keep[48:64] = False               # the missing page counts as masked
         rows = f64(c.rows[0])
         ref, mag, A = attend(f64(c.q)[0:1, 1], rows, rows[:, :R], keep[None], c.scale)
-        check(out[0:1, 1], ref, mag, A, R + Dr, kind, c.act)
+        check(out[0:1, 1], ref, mag, A, R + Dr, "bf16 weights" if kind == "bf16" else kind, c.act)
         c = Case(pkv, kind, H, R, Dr, [100])
         c.d_lens[0] = 5000
         c.run(pkv)

@@ -13,7 +13,7 @@ import torch
 
 BS = 16
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
-WEIGHT = {"f32": 2.0 ** -16, "bf16": 2.0 ** -16, "fp8": 2.0 ** -10}
+WEIGHT = {"f32": 2.0 ** -16, "bf16": 2.0 ** -16, "fp8": 2.0 ** -10, "bf16 weights": 2.0 ** -7 + 2.0 ** -14}
 
 
 def random_tree(rng, n, chain=0.4):
