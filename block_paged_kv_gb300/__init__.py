@@ -197,7 +197,7 @@ _lib.paged_latent_append.argtypes = [_LP, _vp, _i32, _vp, _i64, _vp, _i64, _vp, 
 _lib.paged_latent_append.restype = ctypes.c_int
 _lib.paged_latent_workspace_size.argtypes = [_i32] * 7
 _lib.paged_latent_workspace_size.restype = _sz
-_lib.paged_latent_attention.argtypes = [_vp, _vp, _vp, _i32, _LP, _vp, _i32, _vp, _i32, _i32, _i32,
+_lib.paged_latent_attention.argtypes = [_vp, _i32, _vp, _vp, _i32, _LP, _vp, _i32, _vp, _i32, _i32, _i32,
                                         ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
 _lib.paged_latent_attention.restype = ctypes.c_int
 
@@ -1115,7 +1115,7 @@ def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int,
                 latent_workspace_size(B, H, latent_dim, c.rope_dim, c.block_size, max_q_len, max_seq_len),
                 q.device)
         code = _lib.paged_latent_attention(
-            q.data_ptr(), None if cu_q_lens is None else cu_q_lens.data_ptr(),
+            q.data_ptr(), qshape[0], None if cu_q_lens is None else cu_q_lens.data_ptr(),
             None if tree_masks is None else tree_masks.data_ptr(), H, ctypes.byref(c), block_tables.data_ptr(),
             width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, scale, out.data_ptr(), workspace.data_ptr(),
             workspace.nbytes, None if status is None else status.data_ptr(), _raw_stream(gpu))

@@ -1493,17 +1493,17 @@ size_t paged_latent_workspace_size(int32_t batch, int32_t num_q_heads, int32_t l
                     latent_ws_bytes(latent_plan(PKV_BF16, latent_dim, rope_dim, block_size, sms), latent_dim));
 }
 
-pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
-                                  int32_t num_q_heads, const pkv_latent_pool *pool, const int32_t *block_tables,
+pkv_status paged_latent_attention(const void *q, int32_t num_queries, const int32_t *cu_q_lens,
+                                  const uint64_t *tree_masks, int32_t num_q_heads, const pkv_latent_pool *pool, const int32_t *block_tables,
                                   int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t batch,
                                   int32_t max_q_len, int32_t max_seq_len, float scale, void *out, void *workspace,
                                   size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
 {
-    if (!valid_latent_pool(pool) || num_q_heads <= 0 || batch < 0 || max_q_len < 0 || max_seq_len < 0 ||
-        !std::isfinite(scale) || (cu_q_lens == nullptr && max_q_len != 1) ||
+    if (!valid_latent_pool(pool) || num_q_heads <= 0 || num_queries < 0 || batch < 0 || max_q_len < 0 || max_seq_len < 0 ||
+        !std::isfinite(scale) || (cu_q_lens == nullptr && (max_q_len != 1 || num_queries != batch)) ||
         (tree_masks != nullptr && (cu_q_lens == nullptr || max_q_len > PKV_MAX_TREE)))
         return PKV_ERR_INVALID_ARG;
-    if (batch == 0 || max_q_len == 0) return PKV_OK;
+    if (batch == 0 || max_q_len == 0 || num_queries == 0) return PKV_OK;
     if (q == nullptr || out == nullptr || block_tables == nullptr || seq_lens == nullptr || max_blocks_per_seq <= 0 ||
         !aligned16(q) || !aligned16(out))
         return PKV_ERR_INVALID_ARG;
@@ -1513,7 +1513,8 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     const int64_t max_len = std::min<int64_t>(max_seq_len, static_cast<int64_t>(max_blocks_per_seq) * pool->block_size);
     // the runs' sums are 32 bits: key tiles of all items, and some beside them
     const int64_t item_tiles = max_len / (pl.rows == kLatentTcRows ? 64 : 16) + 8;
-    if (static_cast<int64_t>(max_q_len) * num_q_heads > INT32_MAX / 2 || per_row > INT32_MAX / item_tiles / batch)
+    if (static_cast<int64_t>(max_q_len) * num_q_heads > INT32_MAX / 2 || per_row > INT32_MAX / item_tiles / batch ||
+        static_cast<int64_t>(num_queries) * num_q_heads > INT32_MAX / 2)
         return PKV_ERR_UNSUPPORTED;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
         ws_bytes < latent_ws_bytes(pl, pool->latent_dim))
@@ -1536,6 +1537,7 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     p.num_blocks = pool->num_blocks;
     p.max_len = static_cast<int32_t>(max_len);
     p.max_q = max_q_len;
+    p.num_queries = num_queries;
     p.items_per_row = static_cast<int32_t>(per_row);
     p.workers = pl.workers;
     const size_t pieces = static_cast<size_t>(pl.workers) * 2 * pl.rows;
@@ -1551,10 +1553,12 @@ pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const
     if (!latent_tc_built(pool->dtype, p.latent, p.rope, p.block_size))
         return launch_latent_simple(p, pool->dtype, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
     if (!encode_fn_ready()) return PKV_ERR_CUDA;
-    CUtensorMap map0, map1;  // whole rows, their latent parts
-    if (!encode_latent_map(&map0, *pool, (p.latent + p.rope) / 64) || !encode_latent_map(&map1, *pool, p.latent / 64))
+    CUtensorMap map0, map1, q_map;  // whole rows, their latent parts, the queries as pages of one
+    const pkv_latent_pool queries = {const_cast<void *>(q), 1, num_queries * num_q_heads, p.latent, p.rope, PKV_BF16};
+    if (!encode_latent_map(&map0, *pool, (p.latent + p.rope) / 64) || !encode_latent_map(&map1, *pool, p.latent / 64) ||
+        !encode_latent_map(&q_map, queries, (p.latent + p.rope) / 64))
         return PKV_ERR_UNSUPPORTED;
-    return launch_latent_tc(p, map0, map1, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch_latent_tc(p, map0, map1, q_map, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

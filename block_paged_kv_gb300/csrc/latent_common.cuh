@@ -42,9 +42,10 @@ __device__ __forceinline__ LatentItem latent_item(const LatentParams &p, int32_t
     if (p.cu_q_lens != nullptr) {
         const int32_t c0 = __ldg(p.cu_q_lens + it.r), c1 = __ldg(p.cu_q_lens + it.r + 1);
         C = c1 - c0;
-        if (c0 < 0 || C < 0 || C > p.max_q || C > L) {
+        const bool outside = c0 < 0 || C < 0 || c1 > p.num_queries;
+        if (outside || C > p.max_q || C > L) {
             if (say) report(p.status, PKV_DEV_BAD_LEN);
-            C = c0 < 0 || C < 0 ? 0 : min(min(C, p.max_q), L);
+            C = outside ? 0 : min(min(C, p.max_q), L);
         }
         it.q0 = c0;
     }

@@ -12,7 +12,8 @@
 // values.  What passes between them is the weights alone, one way, 16 KB a 64-key
 // tile through distributed shared memory (which carries about 21 bytes a cycle
 // between two SMs here: 800 cycles), so that neither waits for the other within a
-// tile.  Each CTA loads what it multiplies, CTA 0 whole rows, CTA 1 their latent
+// tile.  An item's queries come through CTA 0's ring like two tiles more (read by
+// their pairs' threads, 32 rows an instruction, they took 9 us).  Each CTA loads what it multiplies, CTA 0 whole rows, CTA 1 their latent
 // part a tile or two later, out of L2.
 //   both:  warps 0, 2, 3 producers (one issuing thread brings 21 to 25 bytes a cycle
 //     whatever its boxes' size, three of them 60), a box of 8 keys each;
@@ -178,18 +179,10 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo,
            (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
-// An item's queries (one run of memory) into L2; threads 0 .. 255.
-__device__ __forceinline__ void prefetch_q(const LatentParams &p, const LatentItem &it, int tid, int row_elems)
-{
-    const char *q = static_cast<const char *>(p.q) + (static_cast<int64_t>(it.q0) * p.heads + it.p0) * row_elems * 2;
-    const int32_t bytes = it.n * row_elems * 2;
-    for (int32_t b = tid * 128; b < bytes; b += 256 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + b));
-}
-
 template <int NR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     latent_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
-                     const LatentParams p)
+                     const __grid_constant__ CUtensorMap q_map, const LatentParams p)
 {
     using namespace lt;
     using L = Layout<NR>;
@@ -213,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(rank == 0 ? &map0 : &map1);
+        if (rank == 0) tma_prefetch_desc(&q_map);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -251,15 +245,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
 
     if (warp == 0 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ producers
-        // Tile T (a running count) goes to stage T % kStages; producer w brings its
-        // 8-key groups w, w + 3, w + 6.
+        // Ring entry U goes to stage U % kStages: in CTA 1 tile T is entry T, in CTA 0
+        // the queries of every piece are two entries before its tiles (64 pairs
+        // each, laid out as 64 keys are).  Producer w brings an entry's 8-row
+        // groups w, w + 3, w + 6.
         const int w = warp == 0 ? 0 : warp - 1;
         const CUtensorMap *map = rank == 0 ? &map0 : &map1;
         const int group = rank == 0 ? L::kGroup0 : L::kGroup1;
         // CTA 1 is the rows' last reader
         const uint64_t policy = rank == 0 ? l2_evict_normal_policy() : l2_evict_first_policy();
-        auto withheld = [&](int32_t T) { return (p.drill & kDrillWithholdFirst) != 0 && T == 0; };
-        int32_t T = 0;
+        auto withheld = [&](int32_t U) { return (p.drill & kDrillWithholdFirst) != 0 && U == 0; };
+        int32_t T = 0, U = 0;
+        auto free_stage = [&]() {
+            return U < kStages || lat_wait(&kv_empty[U % kStages], ((U / kStages) + 1) & 1, p);
+        };
+        auto arm = [&](int32_t groups) {  // (the first producer: an entry's bytes)
+            if (w != 0 || lane != 0) return;
+            if (groups == 0)
+                mbar_arrive(&kv_full[U % kStages]);
+            else
+                mbar_arrive_expect_tx(&kv_full[U % kStages], groups * group);
+        };
         while (ok && latent_next<kRows, kKeys>(p, run, pc)) {
             const int32_t *table = p.tables + static_cast<int64_t>(pc.it.r) * p.width;
             auto page_of = [&](int32_t t, bool &in) {  // lane < nb: page `lane` of tile t
@@ -269,38 +275,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             };
             bool in;
             int32_t id = page_of(pc.t0, in);
-            for (int32_t j = 0; j < pc.n; ++j, ++T) {
-                const int st = T % kStages;
+            for (int h = 0; h < 2 && rank == 0; ++h, ++U) {
+                if (!(ok = free_stage())) break;
+                const int32_t row = pc.it.q0 * p.heads + pc.it.p0 + 64 * h;
+                const int32_t groups = min(max((pc.it.n - 64 * h + 7) / 8, 0), 8);
+                if (withheld(U)) continue;
+                arm(groups);
+                __syncwarp();
+                uint8_t *dst = smem + (U % kStages) * 8 * group;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int g = w + 3 * i;
+                    if (g < groups && elect_one())
+                        tma_load_4d(dst + g * group, &q_map, &kv_full[U % kStages], 0, row + 8 * g, 0, 0, policy);
+                    __syncwarp();
+                }
+            }
+            for (int32_t j = 0; ok && j < pc.n; ++j, ++T, ++U) {
                 const int32_t cur = id;
                 const bool cur_in = in;
                 id = page_of(pc.t0 + j + 1, in);
-                if (T >= kStages && !(ok = lat_wait(&kv_empty[st], ((T / kStages) + 1) & 1, p))) break;
+                if (!(ok = free_stage())) break;
                 const bool good = cur_in && static_cast<uint32_t>(cur) < static_cast<uint32_t>(p.num_blocks);
                 if (w == 0 && rank == 0 && cur_in && !good) report(p.status, PKV_DEV_BAD_BLOCK);
                 const uint32_t mask = __ballot_sync(0xffffffffu, good) & all_pages;
                 if (w == 0 && lane == 0) kmask[T % kMasks] = mask;
-                if (withheld(T)) continue;
-                if (w == 0 && lane == 0) {
-                    if (mask == 0)
-                        mbar_arrive(&kv_full[st]);
-                    else
-                        mbar_arrive_expect_tx(&kv_full[st], __popc(mask) * (bs / 8) * group);
-                }
+                if (withheld(U)) continue;
+                arm(__popc(mask) * (bs / 8));
                 __syncwarp();
-                uint8_t *dst = smem + st * 8 * group;
+                uint8_t *dst = smem + (U % kStages) * 8 * group;
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const int g = w + 3 * i, b = (g & 7) * 8 / bs;
                     const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
                     if (g < 8 && ((mask >> b) & 1u) && elect_one())
-                        tma_load_4d(dst + g * group, map, &kv_full[st], 0, g * 8 - b * bs, 0, blk, policy);
+                        tma_load_4d(dst + g * group, map, &kv_full[U % kStages], 0, g * 8 - b * bs, 0, blk, policy);
                     __syncwarp();
                 }
             }
         }
         // what is on its way into this CTA has landed before the warp leaves
         if (lane == 0)
-            for (int32_t t = max(0, T - kStages); t < T; ++t)
+            for (int32_t t = max(0, U - kStages); t < U; ++t)
                 if (!withheld(t)) mbar_wait(&kv_full[t % kStages], (t / kStages) & 1);
         __syncwarp();
     } else if (warp == 1) {
@@ -313,15 +329,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 report(p.status, PKV_DEV_TIMEOUT);
                 return false;
             };
-            int32_t T = 0;
+            int32_t T = 0, U = 0;
             if (rank == 0) {
                 constexpr uint32_t idS = tc::idesc_bf16(kRows, kKeys, 0, 0);
                 const uint64_t dk = tc::smem_desc(smem_u32(smem), 16, L::kGroup0);
                 for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
                     ok = wait(q_full, k & 1);
-                    for (int32_t j = 0; ok && j < pc.n; ++j, ++T) {
-                        const int st = T % kStages, buf = T % kSBufs;
-                        ok = wait(&kv_full[st], (T / kStages) & 1) &&
+                    if (!ok) break;
+                    for (int h = 0; h < 2; ++h, ++U) mbar_arrive(&kv_empty[U % kStages]);  // in tensor memory now
+                    for (int32_t j = 0; j < pc.n; ++j, ++T, ++U) {
+                        const int st = U % kStages, buf = T % kSBufs;
+                        ok = wait(&kv_full[st], (U / kStages) & 1) &&
                              (T < kSBufs || wait(&s_free[buf], ((T / kSBufs) + 1) & 1));
                         if (!ok) break;
                         // (and what the first tiles have no predecessor for)
@@ -393,36 +411,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         int32_t T0 = 0;
         for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
             const LatentItem &it = pc.it;
-            // Q: this warp's 32 pairs, half of their dims (the last piece's products
-            // have read the old one: this warp saw its last tile's scores)
-            tc::fence_after();
+            // Q into tensor memory: this warp's 32 pairs, half of their dims (the last
+            // piece's products have read the old one: this warp saw its last scores)
             {
+                const int32_t U = T0 + 2 * k + (w >> 1);  // its ring entry
+                if (!(ok = lat_wait(&kv_full[U % kStages], (U / kStages) & 1, p))) break;
+                tc::fence_after();
                 const bool live = row < it.n;
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    static_cast<const uint16_t *>(p.q) +
-                    (static_cast<int64_t>(it.q0) * p.heads + it.p0 + (live ? row : 0)) * (R + kRope));
-                constexpr int kVecs = (R + kRope) / 16, kFly = 20;  // 16-byte vectors of a half, in flight
+                const uint32_t src = smem_u32(smem + (U % kStages) * 8 * L::kGroup0) + ((row & 63) >> 3) * L::kGroup0 + (row & 7) * 128;
+                constexpr int kVecs = (R + kRope) / 16;  // 16-byte vectors of a half
                 static_assert(kVecs % 4 == 0, "stored four at a time");
 #pragma unroll
-                for (int c = 0; c < kVecs; c += kFly) {
-                    uint4 v[kFly];
+                for (int c = 0; c < kVecs; c += 4) {
+                    uint32_t r[16];
 #pragma unroll
-                    for (int i = 0; i < kFly; ++i)
-                        v[i] = live && c + i < kVecs ? __ldg(src + g * kVecs + c + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < kFly; i += 4) {
-                        if (c + i >= kVecs) continue;
-                        uint32_t r[16];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            r[4 * e] = v[i + e].x ^ flip;
-                            r[4 * e + 1] = v[i + e].y ^ flip;
-                            r[4 * e + 2] = v[i + e].z ^ flip;
-                            r[4 * e + 3] = v[i + e].w ^ flip;
-                        }
-                        tc::st16(tmem + lane_base + (g * kVecs + c + i) * 4, r);
+                    for (int e = 0; e < 4; ++e) {
+                        const int v = g * kVecs + c + e;
+                        uint4 x = lds128(src + (v >> 3) * 1024 + (((v & 7) ^ (row & 7)) << 4));
+                        if (!live) x = make_uint4(0, 0, 0, 0);
+                        r[4 * e] = x.x ^ flip;
+                        r[4 * e + 1] = x.y ^ flip;
+                        r[4 * e + 2] = x.z ^ flip;
+                        r[4 * e + 3] = x.w ^ flip;
                     }
+                    tc::st16(tmem + lane_base + (g * kVecs + c) * 4, r);
                 }
+                fence_proxy_async_smem();  // read before the stage is loaded again
                 tc::wait_st();
                 tc::fence_before();
                 __syncwarp();
@@ -559,14 +573,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             const LatentItem &it = pc.it;
             const uint32_t live_warps = static_cast<uint32_t>((it.n + 31) / 32);
             const bool warp_live = 32 * w < it.n, live = row < it.n;
-            // CTA 0's queries into L2: the first piece's, and the next one's (a load
-            // that goes to HBM waits behind the rows on their way, 4 us)
-            {
-                LatentRun ahead = run;
-                LatentPiece nx;
-                if (k == 0) prefetch_q(p, it, tid, R + kRope);
-                if (latent_next<kRows, kKeys>(p, ahead, nx)) prefetch_q(p, nx.it, tid, R + kRope);
-            }
             for (int32_t j = 0; j < pc.n; ++j, ++T) {
                 const int st = T % kStages, pb = T % kPBufs;
                 const int32_t tbase = (pc.t0 + j) * kKeys;
@@ -680,14 +686,15 @@ bool latent_tc_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs)
 }
 
 template <int NR>
-static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, cudaStream_t stream)
+static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, const CUtensorMap &q_map,
+                          cudaStream_t stream)
 {
     constexpr int smem = lt::Layout<NR>::kBytes;
     cudaError_t err = cudaFuncSetAttribute(latent_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_LATENT, stream);
     err = launch_pdl(latent_tc_kernel<NR>, dim3(static_cast<unsigned>(2 * p.workers)), dim3(lt::kThreads), smem, stream, map0,
-                     map1, p);
+                     map1, q_map, p);
     if (err == cudaSuccess)
         err = launch_pdl(latent_merge_kernel<__nv_bfloat16, lt::kRows, lt::kKeys>,
                          dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>((p.latent + 63) / 64)),
@@ -696,9 +703,10 @@ static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const 
     return err;
 }
 
-cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, cudaStream_t stream)
+cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, const CUtensorMap &q_map,
+                          cudaStream_t stream)
 {
-    return p.latent == 512 ? launch<8>(p, map0, map1, stream) : launch<4>(p, map0, map1, stream);
+    return p.latent == 512 ? launch<8>(p, map0, map1, q_map, stream) : launch<4>(p, map0, map1, q_map, stream);
 }
 
 }  // namespace pkv

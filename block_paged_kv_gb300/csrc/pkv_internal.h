@@ -123,7 +123,7 @@ struct LatentParams {
     const uint64_t *tree;      // nullptr: chains
     int32_t *status;
     int32_t batch, heads, latent, rope, block_size, width, num_blocks;
-    int32_t max_len, max_q;
+    int32_t max_len, max_q, num_queries;
     int32_t items_per_row;     // item bound of a row: ceil(max_q * heads / pairs of an item)
     int32_t workers;
     float *ws_o;    // [workers][2][latent / 4][pairs of an item][4] unnormalised weighted values
@@ -287,7 +287,8 @@ cudaError_t launch_copy_blocks(const CopyParams &p, cudaStream_t stream);
 cudaError_t launch_commit(const CommitParams &p, bool fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_latent_append(const LatentAppendParams &p, pkv_dtype dtype, int num_sms, cudaStream_t stream);
 bool latent_tc_built(pkv_dtype dtype, int32_t latent, int32_t rope, int32_t bs);
-cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, cudaStream_t stream);
+cudaError_t launch_latent_tc(const LatentParams &p, const CUtensorMap &map0, const CUtensorMap &map1, const CUtensorMap &q_map,
+                             cudaStream_t stream);
 cudaError_t launch_latent_simple(const LatentParams &p, pkv_dtype dtype, cudaStream_t stream);
 bool prefill_shape_built(pkv_dtype dtype, int32_t D, int32_t bs, int32_t G);
 int32_t prefill_queries_per_cta(pkv_dtype dtype, int32_t G);

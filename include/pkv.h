@@ -554,8 +554,10 @@ pkv_status paged_latent_append(const pkv_latent_pool *pool, const int32_t *slot_
  * at seq_lens[r] - 1), chunks (cu_q_lens: query i of C at seq_lens[r] - C + i,
  * causally) or drafted trees (tree_masks, max_q_len <= PKV_MAX_TREE; without a
  * window).  A query without a key gives zeros.
- *   q:   device [queries][num_q_heads][latent_dim + rope_dim], contiguous
- *   out: device [queries][num_q_heads][latent_dim], contiguous
+ *   q:   device [num_queries][num_q_heads][latent_dim + rope_dim], contiguous
+ *   out: device [num_queries][num_q_heads][latent_dim], contiguous
+ *   num_queries: host, the queries that q and out hold (decode: batch); a row whose
+ *        queries lie past them is left out (PKV_DEV_BAD_LEN)
  *   workspace: device, >= paged_latent_workspace_size(...) bytes, 256-byte aligned
  * Types are the pool's.  Rows that no query of a row attends may hold anything; the
  * rows of a chunk or tree are finite.  Built: latent_dim a multiple of 16 up to 512,
@@ -565,8 +567,8 @@ size_t paged_latent_workspace_size(int32_t batch, int32_t num_q_heads, int32_t l
                                    int32_t rope_dim, int32_t block_size, int32_t max_q_len,
                                    int32_t max_seq_len);
 
-pkv_status paged_latent_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,
-                                  int32_t num_q_heads, const pkv_latent_pool *pool,
+pkv_status paged_latent_attention(const void *q, int32_t num_queries, const int32_t *cu_q_lens,
+                                  const uint64_t *tree_masks, int32_t num_q_heads, const pkv_latent_pool *pool,
                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
                                   const int32_t *seq_lens, int32_t batch, int32_t max_q_len,
                                   int32_t max_seq_len, float scale, void *out, void *workspace,

@@ -63,9 +63,9 @@ def test_refused_before_launch(pkv):
     assert commit(pool=odd) == pkv.PKV_ERR_UNSUPPORTED
     lp = pkv._LatentPool(16, 4, 16, 512, 64, pkv.PKV_BF16)
     att = lambda **k: lib.paged_latent_attention(  # noqa: E731
-        16, k.get("cu", 16), k.get("m"), k.get("h", 4), P(k.get("pool", lp)), 16, 8, 16, 1, k.get("mq", 4), 64,
+        16, k.get("nq", 4), k.get("cu", 16), k.get("m"), k.get("h", 4), P(k.get("pool", lp)), 16, 8, 16, 1, k.get("mq", 4), 64,
         k.get("s", 0.1), 16, 256, 0, None, None)
-    assert att(cu=None) == bad and att(h=0) == bad and att(s=float("nan")) == bad and att(m=16, mq=65) == bad
+    assert att(cu=None) == bad and att(cu=None, mq=1) == bad and att(nq=-1) == bad and att(h=0) == bad and att(s=float("nan")) == bad and att(m=16, mq=65) == bad
     for shape in ((528, 64, pkv.PKV_BF16), (512, 72, pkv.PKV_BF16), (500, 64, pkv.PKV_BF16), (512, 64, pkv.PKV_FP8_E4M3)):
         assert att(pool=pkv._LatentPool(16, 4, 16, *shape)) == pkv.PKV_ERR_UNSUPPORTED
     assert att() == pkv.PKV_ERR_WORKSPACE
