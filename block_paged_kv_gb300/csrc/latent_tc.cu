@@ -54,9 +54,8 @@ constexpr int kSoftWarps = 8;             // of either CTA: warps 4 .. 11
 constexpr int kFins = 3;                  // pieces whose sums may be on their way
 constexpr int kSBufs = 3, kPBufs = 2;
 // What a tile's softmax waits for, in one barrier: its scores; what the producer wrote
-// of it, passed on by the issuing lane; the last tile's reference maximum (four
-// warps); the products of the tile kPBufs before, whose place its weights take.
-constexpr int kSArrivals = 1 + 1 + kSoftWarps / 2 + 1;
+// of it, passed on by the issuing lane; the last tile's reference maximum (four warps).
+constexpr int kSArrivals = 1 + 1 + kSoftWarps / 2;
 constexpr int kMasks = 16;                // tiles between a producer and the softmax, at most stages + S buffers
 constexpr int kPBytes = kRows * kKeys * 2;
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled only when the max grows past 2^8
@@ -78,8 +77,8 @@ struct Layout {
     static constexpr int kAlphaOff = kAfter0 > kAfter1 ? kAfter0 : kAfter1;  // [buffer][128]: factors of O
     static constexpr int kFinOff = kAlphaOff + kPBufs * kRows * 4;           // [piece % kFins][128]: weight sums
     static constexpr int kBarOff = kFinOff + kFins * kRows * 4;
-    // kv_full, kv_empty [stages], s_full, s_free [3], p_full, p_ready [2], fin_full [3], pv_done, o_done, q_full, l_full, drain
-    static constexpr int kNumBars = 2 * kStages + 2 * kSBufs + 2 * kPBufs + kFins + 5;
+    // kv_full, kv_empty [stages], s_full, s_free [3], p_full, p_free, p_ready [2], fin_full [3], pv_done, o_done, q_full, l_full, drain
+    static constexpr int kNumBars = 2 * kStages + 2 * kSBufs + 3 * kPBufs + kFins + 5;
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kScanOff = (kMaskOff + kMasks * 4 + 15) & ~15;  // (of its own: the peer may be sending already)
     static constexpr int kTmemOff = kScanOff + (kThreads / 32 + 4) * 8;
@@ -179,6 +178,93 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo,
            (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
+// A producer warp (w of three) of CTA kRank.  Ring entry U goes to stage
+// U % kStages: in CTA 1 tile T is entry T, in CTA 0 the queries of every piece are two
+// entries before its tiles (64 pairs each, laid out as 64 keys are).  Producer w
+// brings an entry's 8-row groups w, w + 3, w + 6.
+template <int NR, int kRank>
+__device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUtensorMap &q_map, const LatentParams &p,
+                                               LatentRun run, uint8_t *smem, uint64_t *kv_full, uint64_t *kv_empty,
+                                               uint32_t *kmask, int w, int lane)
+{
+    using namespace lt;
+    using L = Layout<NR>;
+    constexpr int n = L::kStages, group = kRank == 0 ? L::kGroup0 : L::kGroup1, stage = 8 * group;
+    const int bs_log = 31 - __clz(p.block_size), nb = kKeys >> bs_log;  // pages of a tile
+    const uint32_t all_pages = (1u << nb) - 1u;
+    // CTA 1 is the rows' last reader
+    const uint64_t policy = kRank == 0 ? l2_evict_normal_policy() : l2_evict_first_policy();
+    auto withheld = [&](int32_t U) { return (p.drill & kDrillWithholdFirst) != 0 && U == 0; };
+    LatentPiece pc;
+    bool ok = true;
+    int32_t T = 0, U = 0;
+    auto free_stage = [&]() { return U < n || lat_wait(&kv_empty[U % n], ((U / n) + 1) & 1, p); };
+    auto arm = [&](int32_t groups) {  // (the first producer: an entry's bytes)
+        if (w != 0 || lane != 0) return;
+        if (groups == 0)
+            mbar_arrive(&kv_full[U % n]);
+        else
+            mbar_arrive_expect_tx(&kv_full[U % n], groups * group);
+    };
+    while (ok && latent_next<kRows, kKeys>(p, run, pc)) {
+        const int32_t *table = p.tables + static_cast<int64_t>(pc.it.r) * p.width;
+        auto page_of = [&](int32_t t, bool &in) {  // lane < nb: page `lane` of tile t
+            const int32_t b = t * nb + lane;
+            in = lane < nb && t < pc.t0 + pc.n && b < p.width && (static_cast<int64_t>(b) << bs_log) < pc.it.hi;
+            return in ? __ldg(table + b) : -1;
+        };
+        bool in;
+        int32_t id = page_of(pc.t0, in);
+        if constexpr (kRank == 0) {
+            for (int h = 0; h < 2; ++h, ++U) {
+                if (!(ok = free_stage())) break;
+                const int32_t row = pc.it.q0 * p.heads + pc.it.p0 + 64 * h;
+                const int32_t groups = min(max((pc.it.n - 64 * h + 7) / 8, 0), 8);
+                if (withheld(U)) continue;
+                arm(groups);
+                __syncwarp();
+                uint8_t *dst = smem + (U % n) * stage;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int g = w + 3 * i;
+                    if (g < groups && elect_one())
+                        tma_load_4d(dst + g * group, &q_map, &kv_full[U % n], 0, row + 8 * g, 0, 0, policy);
+                    __syncwarp();
+                }
+            }
+        }
+        for (int32_t j = 0; ok && j < pc.n; ++j, ++T) {
+            const int32_t cur = id;
+            const bool cur_in = in;
+            id = page_of(pc.t0 + j + 1, in);
+            const bool good = cur_in && static_cast<uint32_t>(cur) < static_cast<uint32_t>(p.num_blocks);
+            if (w == 0 && kRank == 0 && cur_in && !good) report(p.status, PKV_DEV_BAD_BLOCK);
+            const uint32_t mask = __ballot_sync(0xffffffffu, good) & all_pages;
+            if (!(ok = free_stage())) break;
+            if (w == 0 && lane == 0) kmask[T % kMasks] = mask;
+            if (!withheld(U)) {
+                arm(__popc(mask) << (bs_log - 3));
+                __syncwarp();
+                uint8_t *dst = smem + (U % n) * stage;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int g = w + 3 * i, b = ((g & 7) * 8) >> bs_log;
+                    const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
+                    if (g < 8 && ((mask >> b) & 1u) && elect_one())
+                        tma_load_4d(dst + g * group, &map, &kv_full[U % n], 0, g * 8 - (b << bs_log), 0, blk, policy);
+                    __syncwarp();
+                }
+            }
+            ++U;
+        }
+    }
+    // what is on its way into this CTA has landed before the warp leaves
+    if (lane == 0)
+        for (int32_t t = max(0, U - n); t < U; ++t)
+            if (!withheld(t)) mbar_wait(&kv_full[t % n], (t / n) & 1);
+    __syncwarp();
+}
+
 template <int NR>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     latent_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
@@ -192,7 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     uint64_t *kv_full = bars, *kv_empty = kv_full + kStages;
     uint64_t *s_full = kv_empty + kStages, *s_free = s_full + kSBufs;   // CTA 0
     uint64_t *p_full = s_free + kSBufs;     // CTA 1: weights landed
-    uint64_t *p_ready = p_full + kPBufs;    // CTA 1: O and the value rows ready for them
+    uint64_t *p_free = p_full + kPBufs;     // CTA 0: weights multiplied
+    uint64_t *p_ready = p_free + kPBufs;    // CTA 1: O and the value rows ready for them
     uint64_t *fin_full = p_ready + kPBufs;  // CTA 1: a piece's sums landed
     uint64_t *pv_done = fin_full + kFins, *o_done = pv_done + 1;
     uint64_t *q_full = o_done + 1, *l_full = q_full + 1, *drain = l_full + 1;
@@ -217,6 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         }
         for (int i = 0; i < kPBufs; ++i) {
             mbar_init(&p_full[i], 1);
+            mbar_init(&p_free[i], 1);
             mbar_init(&p_ready[i], kSoftWarps);
         }
         for (int i = 0; i < kFins; ++i) mbar_init(&fin_full[i], 1);
@@ -245,80 +333,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
 
     if (warp == 0 || warp == 2 || warp == 3) {
         // ------------------------------------------------------------ producers
-        // Ring entry U goes to stage U % kStages: in CTA 1 tile T is entry T, in CTA 0
-        // the queries of every piece are two entries before its tiles (64 pairs
-        // each, laid out as 64 keys are).  Producer w brings an entry's 8-row
-        // groups w, w + 3, w + 6.
         const int w = warp == 0 ? 0 : warp - 1;
-        const CUtensorMap *map = rank == 0 ? &map0 : &map1;
-        const int group = rank == 0 ? L::kGroup0 : L::kGroup1;
-        // CTA 1 is the rows' last reader
-        const uint64_t policy = rank == 0 ? l2_evict_normal_policy() : l2_evict_first_policy();
-        auto withheld = [&](int32_t U) { return (p.drill & kDrillWithholdFirst) != 0 && U == 0; };
-        int32_t T = 0, U = 0;
-        auto free_stage = [&]() {
-            return U < kStages || lat_wait(&kv_empty[U % kStages], ((U / kStages) + 1) & 1, p);
-        };
-        auto arm = [&](int32_t groups) {  // (the first producer: an entry's bytes)
-            if (w != 0 || lane != 0) return;
-            if (groups == 0)
-                mbar_arrive(&kv_full[U % kStages]);
-            else
-                mbar_arrive_expect_tx(&kv_full[U % kStages], groups * group);
-        };
-        while (ok && latent_next<kRows, kKeys>(p, run, pc)) {
-            const int32_t *table = p.tables + static_cast<int64_t>(pc.it.r) * p.width;
-            auto page_of = [&](int32_t t, bool &in) {  // lane < nb: page `lane` of tile t
-                const int32_t b = t * nb + lane;
-                in = lane < nb && t < pc.t0 + pc.n && b < p.width && static_cast<int64_t>(b) * bs < pc.it.hi;
-                return in ? __ldg(table + b) : -1;
-            };
-            bool in;
-            int32_t id = page_of(pc.t0, in);
-            for (int h = 0; h < 2 && rank == 0; ++h, ++U) {
-                if (!(ok = free_stage())) break;
-                const int32_t row = pc.it.q0 * p.heads + pc.it.p0 + 64 * h;
-                const int32_t groups = min(max((pc.it.n - 64 * h + 7) / 8, 0), 8);
-                if (withheld(U)) continue;
-                arm(groups);
-                __syncwarp();
-                uint8_t *dst = smem + (U % kStages) * 8 * group;
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int g = w + 3 * i;
-                    if (g < groups && elect_one())
-                        tma_load_4d(dst + g * group, &q_map, &kv_full[U % kStages], 0, row + 8 * g, 0, 0, policy);
-                    __syncwarp();
-                }
-            }
-            for (int32_t j = 0; ok && j < pc.n; ++j, ++T, ++U) {
-                const int32_t cur = id;
-                const bool cur_in = in;
-                id = page_of(pc.t0 + j + 1, in);
-                if (!(ok = free_stage())) break;
-                const bool good = cur_in && static_cast<uint32_t>(cur) < static_cast<uint32_t>(p.num_blocks);
-                if (w == 0 && rank == 0 && cur_in && !good) report(p.status, PKV_DEV_BAD_BLOCK);
-                const uint32_t mask = __ballot_sync(0xffffffffu, good) & all_pages;
-                if (w == 0 && lane == 0) kmask[T % kMasks] = mask;
-                if (withheld(U)) continue;
-                arm(__popc(mask) * (bs / 8));
-                __syncwarp();
-                uint8_t *dst = smem + (U % kStages) * 8 * group;
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const int g = w + 3 * i, b = (g & 7) * 8 / bs;
-                    const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
-                    if (g < 8 && ((mask >> b) & 1u) && elect_one())
-                        tma_load_4d(dst + g * group, map, &kv_full[U % kStages], 0, g * 8 - b * bs, 0, blk, policy);
-                    __syncwarp();
-                }
-            }
-        }
-        // what is on its way into this CTA has landed before the warp leaves
-        if (lane == 0)
-            for (int32_t t = max(0, U - kStages); t < U; ++t)
-                if (!withheld(t)) mbar_wait(&kv_full[t % kStages], (t / kStages) & 1);
-        __syncwarp();
+        if (rank == 0)
+            latent_produce<NR, 0>(map0, q_map, p, run0, smem, kv_full, kv_empty, kmask, w, lane);
+        else
+            latent_produce<NR, 1>(map1, q_map, p, run0, smem, kv_full, kv_empty, kmask, w, lane);
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         // One elected lane runs the whole role: a product is issued about as it
@@ -342,9 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                         ok = wait(&kv_full[st], (U / kStages) & 1) &&
                              (T < kSBufs || wait(&s_free[buf], ((T / kSBufs) + 1) & 1));
                         if (!ok) break;
-                        // (and what the first tiles have no predecessor for)
-                        for (int i = 1 + (T == 0 ? kSoftWarps / 2 : 0) + (T < kPBufs ? 1 : 0); i > 0; --i)
-                            mbar_arrive(&s_full[buf]);
+                        // (and what the first tile has no predecessor for)
+                        for (int i = 1 + (T == 0 ? kSoftWarps / 2 : 0); i > 0; --i) mbar_arrive(&s_full[buf]);
                         tc::fence_after();
                         const uint64_t kd = dk + static_cast<uint64_t>(st) * (8 * L::kGroup0 >> 4);
                         const uint32_t d = tS + 64u * static_cast<uint32_t>(buf);
@@ -354,13 +372,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                         tc::commit(&s_full[buf]);
                         tc::commit(&kv_empty[st]);
                     }
-                }
-                // CTA 1's last arrivals, for two tiles that do not follow, have come
-                for (int32_t t = T; ok && T > 0 && t < T + kPBufs; ++t) {
-                    if (t >= kSBufs && !(ok = wait(&s_free[t % kSBufs], ((t / kSBufs) + 1) & 1))) break;
-                    for (int i = kSArrivals - (t == T ? kSoftWarps / 2 : 0) - (t >= kPBufs ? 1 : 0); i > 0; --i)
-                        mbar_arrive(&s_full[t % kSBufs]);
-                    ok = wait(&s_full[t % kSBufs], (t / kSBufs) & 1);
                 }
             } else {
                 constexpr int N = R < 256 ? R : 256;
@@ -383,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                                            vd + ((kk * 2 * L::kGroup1 + n * (N / 64) * 1024) >> 4), idO, (j > 0 || kk > 0) ? 1u : 0u);
                         tc::commit(pv_done);
                         tc::commit(&kv_empty[st]);
-                        commit_to(&s_full[(T + kPBufs) % kSBufs], 1);  // CTA 0's
+                        commit_to(&p_free[buf], 1);  // CTA 0's
                         if (j == pc.n - 1) tc::commit(o_done);
                     }
                 }
@@ -408,7 +419,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         const uint32_t alpha_peer = map_shared(smem_u32(smem + L::kAlphaOff), 1) + row * 4;
         const uint32_t fin_peer = map_shared(smem_u32(smem + L::kFinOff), 1) + row * 4;
         const uint32_t p_full_peer = map_shared(smem_u32(p_full), 1), fin_full_peer = map_shared(smem_u32(fin_full), 1);
-        int32_t T0 = 0;
+        int32_t T0 = 0, sent = 0;  // one past the last tile whose weights this warp sent
         for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
             const LatentItem &it = pc.it;
             // Q into tensor memory: this warp's 32 pairs, half of their dims (the last
@@ -515,21 +526,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 const float nmu = new_ref == -INFINITY ? 0.f : -new_ref;
                 const uint64_t sl2 = f2_pack(sl, sl), nmu2 = f2_pack(nmu, nmu);
                 uint64_t ls2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                const uint32_t bar = p_full_peer + 8 * pb, dst = p_peer + pb * kPBytes;
-                // eight keys a time: weights to bf16, their sums, and off to CTA 1
+                uint32_t pk[32];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float a, b;
-                        f2_unpack(f2_fma(f2_pack(s[8 * i + 2 * e], s[8 * i + 2 * e + 1]), sl2, nmu2), a, b);
-                        pk[e] = pack_bf16x2(fast_exp2(a), fast_exp2(b));
-                        ls2[e & 1] = f2_add(ls2[e & 1], f2_pack(bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e])));
-                    }
-                    st_async(dst + i * (kRows * 16), bar, pk[0], pk[1], pk[2], pk[3]);
+                for (int e = 0; e < 32; ++e) {
+                    float a, b;
+                    f2_unpack(f2_fma(f2_pack(s[2 * e], s[2 * e + 1]), sl2, nmu2), a, b);
+                    pk[e] = pack_bf16x2(fast_exp2(a), fast_exp2(b));
+                    ls2[e & 1] = f2_add(ls2[e & 1], f2_pack(bf16lo_to_f32(pk[e]), bf16hi_to_f32(pk[e])));
                 }
+                // off to CTA 1 once the buffer's last weights are multiplied (waited for
+                // here and not before the scores are read: the way from those products
+                // through a softmax to these took two tiles' time)
+                if (T >= kPBufs && !(ok = lat_wait_cluster(&p_free[pb], ((T / kPBufs) + 1) & 1, p))) break;
+                const uint32_t bar = p_full_peer + 8 * pb, dst = p_peer + pb * kPBytes;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_async(dst + i * (kRows * 16), bar, pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
                 st_async1(alpha_peer + pb * (kRows * 4), bar, __float_as_uint(alpha));
+                sent = T + 1;
                 float l0, l1, l2, l3;
                 f2_unpack(ls2[0], l0, l1);
                 f2_unpack(ls2[1], l2, l3);
@@ -550,14 +564,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 if (!pc.whole) {
                     if (row < it.n) latent_part_ml<kRows>(p, worker, pc.slot)[row] = make_float2(m_ref, l);
                 } else if (warp_live) {
-                    // (CTA 1 has read the sums of kFins pieces ago: this tile's barrier
-                    // came after the products of the tile two before, hence after the
+                    // (CTA 1 has read the sums of kFins pieces ago: the last weights went
+                    // after the products of the tile two before, hence after the
                     // epilogue before that tile's piece)
                     st_async1(fin_peer + (k % kFins) * (kRows * 4), fin_full_peer + 8 * (k % kFins), __float_as_uint(l));
                 }
             }
             T0 = end;
         }
+        // CTA 1's last arrivals have come (a group's first warp has pairs in every piece)
+        if (ok && w == 0 && sent > 0) lat_wait_cluster(&p_free[(sent - 1) % kPBufs], ((sent - 1) / kPBufs) & 1, p);
     } else if (warp >= 4) {
         // ------------------------------------------------------------ values (CTA 1)
         const int half = (warp >> 2) - 1, w = warp & 3, row = 32 * w + lane;
