@@ -1304,7 +1304,7 @@ size_t latent_ws_bytes(const LatentPlan &pl, int32_t latent)
     const size_t pieces = static_cast<size_t>(pl.workers) * 2 * pl.rows;
     const auto up = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
     return up(pieces * latent * sizeof(float)) + up(pieces * 2 * sizeof(float)) +
-           static_cast<size_t>(pl.workers) * 3 * sizeof(int32_t);
+           static_cast<size_t>(pl.workers) * kLatentRecordBytes;
 }
 
 }  // namespace
@@ -1546,7 +1546,7 @@ pkv_status paged_latent_attention(const void *q, int32_t num_queries, const int3
     ws += (pieces * p.latent * sizeof(float) + 255) & ~static_cast<size_t>(255);
     p.ws_ml = reinterpret_cast<float *>(ws);
     ws += (pieces * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255);
-    p.rec = reinterpret_cast<int32_t *>(ws);
+    p.rec = ws;
     p.scale_log2 = scale * 1.4426950408889634f;
     drill_settings(&p.wait_ns, &p.drill);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

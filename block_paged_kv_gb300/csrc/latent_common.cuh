@@ -11,6 +11,8 @@
 // merge kernel joins.
 #pragma once
 
+#include <algorithm>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -72,6 +74,16 @@ __device__ __forceinline__ LatentRange latent_range(const LatentParams &p, const
     if (p.tree != nullptr) rg.mask = tree_mask(p.tree, it.q0 + i, i);
     return rg;
 }
+
+// What the merge needs of an item that a worker's run begins and does not end.
+struct alignas(8) LatentRecord {
+    int64_t row;     // its first pair's row of out
+    int32_t pieces;  // workers that hold a piece of it, this one first (0: there is no such item)
+    int32_t slot;    // this worker's piece's partial slot (the others': 0)
+    int32_t pairs;
+    int32_t pad;
+};
+static_assert(sizeof(LatentRecord) == kLatentRecordBytes, "the workspace holds one per worker");
 
 // A worker's run, in units: an item counts its tiles and `over` units before them
 // (what a piece costs beside its tiles: queries staged, first products, epilogue).
@@ -174,18 +186,18 @@ __device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c
     }
     if (record && threadIdx.x == 96) {  // (of a warp that does not lead)
         // the item at the run's end goes on in later workers, and its first tile is here
-        int32_t u = -1, last = -1, slot = 0;
+        LatentRecord rec{};
         if (run.pos < run.end) {
             const int32_t first = found[3] + run.over, E = found[4];
             if (E > run.end && first >= run.pos && first < run.end) {
-                u = found[2];
-                last = static_cast<int32_t>((static_cast<int64_t>(E) * n + T - 1) / T - 1);  // the first that ends at or past E
-                slot = found[2] != found[0] ? 1 : 0;
+                const LatentItem it = latent_item<kRows, kKeys>(p, found[2]);
+                rec.pieces = static_cast<int32_t>((static_cast<int64_t>(E) * n + T - 1) / T) - c;  // to the first worker that ends at or past E
+                rec.slot = found[2] != found[0] ? 1 : 0;
+                rec.pairs = it.n;
+                rec.row = static_cast<int64_t>(it.q0) * p.heads + it.p0;
             }
         }
-        p.rec[2 * c] = u;
-        p.rec[2 * c + 1] = last;
-        p.rec[2 * p.workers + c] = slot;
+        static_cast<LatentRecord *>(p.rec)[c] = rec;
     }
     return run;
 }
@@ -235,102 +247,92 @@ __device__ __forceinline__ int64_t latent_out_row(const LatentParams &p, const L
     return (static_cast<int64_t>(it.q0) * p.heads + it.p0 + pair) * p.latent;
 }
 
-// Joins the pieces of an item cut between workers: CTA (x, y) the item that
-// worker x's run begins, dims 64y .. 64y + 63.
-// The pieces' weights are worked out once a CTA (a thread per pair and piece), and
-// four pieces' values are in flight at a time: one piece after another, each read
-// waiting for the last, joined 20 pieces in 20 us.
+// Joins the pieces of an item cut between workers: worker x's (CTAs (x, ..)).  A
+// thread has 16 dims of a pair; nothing but the record comes before the partials, of
+// which it has four in flight (one piece after another, each read waiting for the
+// last, joined 20 pieces in 20 us).
 constexpr int kLatMergeThreads = 256;
-constexpr int kLatMergePieces = 32;  // of a pass
 
-template <typename T, int kRows, int kKeys>
-__global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const LatentParams p)
+template <typename T, int kRows>
+__global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const LatentParams p, const int32_t pairs)
 {
-    __shared__ float wgt[kLatMergePieces][kRows];
+    constexpr int kFly = 4;
     pdl_wait();  // the records and partials come from the kernel just before
-    const int32_t c = blockIdx.x, u = p.rec[2 * c], last = p.rec[2 * c + 1];
-    // the piece that the item begins with: slot 0 if it was its worker's first
-    const int32_t s0 = p.rec[2 * p.workers + c];
-    if (u < 0) return;
-    const LatentItem it = latent_item<kRows, kKeys>(p, u);
-    // this thread's pair, and 4 of the CTA's 64 dims (16 dims of 128 pairs)
-    constexpr int kGroups = kLatMergeThreads / kRows;        // threads of a pair
-    constexpr int kD4 = kGroups >= 16 ? 1 : 16 / kGroups;    // value quads of a thread
-    const int pair = threadIdx.x % kRows, grp = threadIdx.x / kRows;
-    const int d4 = blockIdx.y * 16 + grp * kD4;
-    const bool live = pair < it.n && d4 * 4 < p.latent;
+    pdl_trigger();
+    const int32_t c = blockIdx.x, idx = blockIdx.y * kLatMergeThreads + threadIdx.x;
+    const LatentRecord rec = static_cast<const LatentRecord *>(p.rec)[c];
+    const int32_t pair = idx % pairs, d4 = idx / pairs * 4;  // pairs: of an item, at most
+    if (pair >= rec.pairs || d4 * 4 >= p.latent) return;     // (no item: no pairs)
     float M = -INFINITY, l = 0.f;
-    float4 acc[kD4] = {};
-    const int32_t np = last - c + 1;
-    const auto slot = [&](int32_t i) { return i == 0 ? s0 : 0; };
-    for (int32_t i0 = 0; i0 < np; i0 += kLatMergePieces) {
-        const int32_t n = min(np - i0, kLatMergePieces);
-        __syncthreads();  // the last pass's weights are read
-        for (int32_t i = grp; i < n; i += kGroups)
-            wgt[i][pair] = pair < it.n ? latent_part_ml<kRows>(p, c + i0 + i, slot(i0 + i))[pair].x : -INFINITY;
-        __syncthreads();
+    float4 acc[4] = {};
+    for (int32_t i = 0; i < rec.pieces; i += kFly) {
+        float4 v[kFly][4];
+        float2 ml[kFly];
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) {
+            ml[j] = make_float2(-INFINITY, 0.f);
+            if (i + j >= rec.pieces) continue;
+            const int32_t w = c + i + j, slot = i + j == 0 ? rec.slot : 0;
+            ml[j] = latent_part_ml<kRows>(p, w, slot)[pair];
+            const float4 *o = latent_part_o<kRows>(p, w, slot) + d4 * kRows + pair;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j][e] = o[e * kRows];
+        }
         float mn = M;
-        for (int32_t i = 0; i < n; ++i) mn = fmaxf(mn, wgt[i][pair]);
-        if (!live || mn == -INFINITY) continue;
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) mn = fmaxf(mn, ml[j].x);
+        if (mn == -INFINITY) continue;  // nothing attended so far
         const float f0 = fast_exp2(M - mn);
         M = mn;
         l *= f0;
 #pragma unroll
-        for (int e = 0; e < kD4; ++e) {
+        for (int e = 0; e < 4; ++e) {
             acc[e].x *= f0;
             acc[e].y *= f0;
             acc[e].z *= f0;
             acc[e].w *= f0;
         }
-        constexpr int kFly = kD4 >= 8 ? 2 : kD4 >= 4 ? 4 : 8;  // pieces in flight
-        for (int32_t i = 0; i < n; i += kFly) {
-            float4 v[kFly][kD4];
-            float sum[kFly];
 #pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                if (i + j >= n) continue;
-                const int32_t w = c + i0 + i + j, s = slot(i0 + i + j);
-                sum[j] = latent_part_ml<kRows>(p, w, s)[pair].y;
-                const float4 *o = latent_part_o<kRows>(p, w, s) + d4 * kRows + pair;
+        for (int j = 0; j < kFly; ++j) {
+            if (i + j >= rec.pieces) continue;
+            const float f = fast_exp2(ml[j].x - M);
+            l = fmaf(f, ml[j].y, l);
 #pragma unroll
-                for (int e = 0; e < kD4; ++e) v[j][e] = o[e * kRows];
-            }
-#pragma unroll
-            for (int j = 0; j < kFly; ++j) {
-                if (i + j >= n) continue;
-                const float f = fast_exp2(wgt[i + j][pair] - M);
-                l = fmaf(f, sum[j], l);
-#pragma unroll
-                for (int e = 0; e < kD4; ++e) {
-                    acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
-                    acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
-                    acc[e].z = fmaf(f, v[j][e].z, acc[e].z);
-                    acc[e].w = fmaf(f, v[j][e].w, acc[e].w);
-                }
+            for (int e = 0; e < 4; ++e) {
+                acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
+                acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
+                acc[e].z = fmaf(f, v[j][e].z, acc[e].z);
+                acc[e].w = fmaf(f, v[j][e].w, acc[e].w);
             }
         }
     }
-    if (!live) return;
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
-    T *out = static_cast<T *>(p.out) + latent_out_row(p, it, pair) + d4 * 4;
+    T *out = static_cast<T *>(p.out) + (rec.row + pair) * p.latent + d4 * 4;
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int e = 0; e < kD4; ++e)
+        for (int e = 0; e < 4; ++e)
             reinterpret_cast<float4 *>(out)[e] =
                 make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
     } else {
-        uint2 v[kD4];
+        uint32_t v[8];
 #pragma unroll
-        for (int e = 0; e < kD4; ++e)
-            v[e] = make_uint2(pack_bf16x2(acc[e].x * inv, acc[e].y * inv), pack_bf16x2(acc[e].z * inv, acc[e].w * inv));
-        if constexpr (kD4 >= 2) {
-#pragma unroll
-            for (int e = 0; e < kD4; e += 2)
-                reinterpret_cast<uint4 *>(out)[e / 2] = make_uint4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
-        } else {
-            *reinterpret_cast<uint2 *>(out) = v[0];
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
+            v[2 * e + 1] = pack_bf16x2(acc[e].z * inv, acc[e].w * inv);
         }
+        reinterpret_cast<uint4 *>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
     }
+}
+
+template <typename T, int kRows>
+static cudaError_t launch_latent_merge(const LatentParams &p, cudaStream_t stream)
+{
+    const int32_t pairs = static_cast<int32_t>(std::min<int64_t>(kRows, static_cast<int64_t>(p.max_q) * p.heads));
+    const int32_t threads = pairs * (p.latent / 16);
+    return launch_pdl(latent_merge_kernel<T, kRows>,
+                      dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>((threads + kLatMergeThreads - 1) / kLatMergeThreads)),
+                      dim3(kLatMergeThreads), 0, stream, p, pairs);
 }
 
 }  // namespace pkv

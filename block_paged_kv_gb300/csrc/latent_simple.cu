@@ -162,9 +162,7 @@ static cudaError_t launch(const LatentParams &p, cudaStream_t stream)
     prof_begin(PKV_KERNEL_LATENT, stream);
     err = launch_pdl(latent_simple_kernel<T>, dim3(static_cast<unsigned>(p.workers)), dim3(ls::kThreads), smem, stream, p);
     if (err == cudaSuccess)
-        err = launch_pdl(latent_merge_kernel<T, ls::kRows, ls::kKeys>,
-                         dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>((p.latent + 63) / 64)),
-                         dim3(kLatMergeThreads), 0, stream, p);
+        err = launch_latent_merge<T, ls::kRows>(p, stream);
     prof_end(PKV_KERNEL_LATENT, stream);
     return err;
 }

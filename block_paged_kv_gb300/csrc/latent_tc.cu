@@ -77,12 +77,13 @@ struct Layout {
     static constexpr int kAlphaOff = kAfter0 > kAfter1 ? kAfter0 : kAfter1;  // [buffer][128]: factors of O
     static constexpr int kFinOff = kAlphaOff + kPBufs * kRows * 4;           // [piece % kFins][128]: weight sums
     static constexpr int kBarOff = kFinOff + kFins * kRows * 4;
-    // kv_full, kv_empty [stages], s_full, s_free [3], p_full, p_free, p_ready [2], fin_full [3], pv_done, o_done, q_full, l_full, drain
-    static constexpr int kNumBars = 2 * kStages + 2 * kSBufs + 3 * kPBufs + kFins + 5;
+    // kv_full, kv_empty [stages], s_full, s_free [3], p_full, p_free, p_ready [2], fin_full [3], pv_done, o_done, q_full, l_full, drain, go
+    static constexpr int kNumBars = 2 * kStages + 2 * kSBufs + 3 * kPBufs + kFins + 6;
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kScanOff = (kMaskOff + kMasks * 4 + 15) & ~15;  // (of its own: the peer may be sending already)
     static constexpr int kTmemOff = kScanOff + (kThreads / 32 + 4) * 8;
     static constexpr int kBytes = kTmemOff + 16;
+    static_assert(kPBufs == 2, "a softmax group keeps to one of the weights' buffers");
     static_assert(kBytes <= 227 * 1024 && kStages + kSBufs <= kMasks, "shared memory of one CTA");
     static constexpr uint32_t kQCols = NR * 32 + 32;  // CTA 0's tensor memory: Q, then the S buffers
     static_assert(kQCols + kSBufs * 64 <= kTmemCols && NR * 64 <= kTmemCols, "tensor memory of one CTA");
@@ -121,6 +122,12 @@ __device__ __forceinline__ void st_async1(uint32_t addr, uint32_t bar, uint32_t 
 {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(a), "r"(bar)
                  : "memory");
+}
+// Arrive on another CTA's mbarrier without ordering this thread's earlier accesses (a
+// release at cluster scope takes 1.2 us).
+__device__ __forceinline__ void arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 {
@@ -282,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     uint64_t *p_ready = p_free + kPBufs;    // CTA 1: O and the value rows ready for them
     uint64_t *fin_full = p_ready + kPBufs;  // CTA 1: a piece's sums landed
     uint64_t *pv_done = fin_full + kFins, *o_done = pv_done + 1;
-    uint64_t *q_full = o_done + 1, *l_full = q_full + 1, *drain = l_full + 1;
+    uint64_t *q_full = o_done + 1, *l_full = q_full + 1, *drain = l_full + 1, *go = drain + 1;
     uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);  // [tile % kMasks]: pages loaded
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemOff);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -313,6 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         mbar_init(q_full, kSoftWarps);
         mbar_init(l_full, kSoftWarps / 2);
         mbar_init(drain, 1);
+        mbar_init(go, 1);
         fence_mbar_init();
     }
     if (warp == 1) tc::alloc(tmem_slot, kTmemCols);
@@ -336,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         const int w = warp == 0 ? 0 : warp - 1;
         if (rank == 0)
             latent_produce<NR, 0>(map0, q_map, p, run0, smem, kv_full, kv_empty, kmask, w, lane);
-        else
+        else if (run0.pos >= run0.end || lat_wait(go, 0, p))  // the queries come first
             latent_produce<NR, 1>(map1, q_map, p, run0, smem, kv_full, kv_empty, kmask, w, lane);
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
@@ -355,6 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
                     ok = wait(q_full, k & 1);
                     if (!ok) break;
+                    if (k == 0) arrive_remote(map_shared(smem_u32(go), 1));
                     for (int h = 0; h < 2; ++h, ++U) mbar_arrive(&kv_empty[U % kStages]);  // in tensor memory now
                     for (int32_t j = 0; j < pc.n; ++j, ++T, ++U) {
                         const int st = U % kStages, buf = T % kSBufs;
@@ -712,9 +721,7 @@ static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const 
     err = launch_pdl(latent_tc_kernel<NR>, dim3(static_cast<unsigned>(2 * p.workers)), dim3(lt::kThreads), smem, stream, map0,
                      map1, q_map, p);
     if (err == cudaSuccess)
-        err = launch_pdl(latent_merge_kernel<__nv_bfloat16, lt::kRows, lt::kKeys>,
-                         dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>((p.latent + 63) / 64)),
-                         dim3(kLatMergeThreads), 0, stream, p);
+        err = launch_latent_merge<__nv_bfloat16, lt::kRows>(p, stream);
     prof_end(PKV_KERNEL_LATENT, stream);
     return err;
 }

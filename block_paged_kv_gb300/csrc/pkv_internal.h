@@ -128,12 +128,12 @@ struct LatentParams {
     int32_t workers;
     float *ws_o;    // [workers][2][latent / 4][pairs of an item][4] unnormalised weighted values
     float *ws_ml;   // [workers][2][pairs of an item][2]: reference max (log2 units), weight sum
-    int32_t *rec;   // [workers][2]: the item that a worker's run begins and does not end (-1: none),
-                    // the last worker that holds a piece of it; then [workers]: its partial's slot
+    void *rec;      // [workers] records of kLatentRecordBytes: the item that a run begins and does not end
     float scale_log2;
     uint64_t wait_ns;
     uint32_t drill;
 };
+constexpr int kLatentRecordBytes = 24;
 constexpr int kLatentSimpleRows = 16;  // pairs of an item: CUDA-core kernel
 constexpr int kLatentTcRows = 128;     // tensor-core kernel
 
