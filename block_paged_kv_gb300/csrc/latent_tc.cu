@@ -360,26 +360,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             if (rank == 0) {
                 constexpr uint32_t idS = tc::idesc_bf16(kRows, kKeys, 0, 0);
                 const uint64_t dk = tc::smem_desc(smem_u32(smem), 16, L::kGroup0);
+                // The next tile's waits are looked at before a tile's last products:
+                // done between two tiles they left the tensor cores idle.
+                constexpr int kAll = (NR + 1) * 4, kLate = 8;
+                auto products = [&](int32_t tile, int32_t entry, int first, int last) {
+                    const uint64_t kd = dk + static_cast<uint64_t>(entry % kStages) * (8 * L::kGroup0 >> 4);
+                    const uint32_t d = tS + 64u * static_cast<uint32_t>(tile % kSBufs);
+#pragma unroll
+                    for (int kk = 0; kk < kAll; ++kk)
+                        if (kk >= first && kk < last)
+                            tc::mma_ts(d, tmem + 8 * kk, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                };
                 for (int32_t k = 0; ok && latent_next<kRows, kKeys>(p, run, pc); ++k) {
                     ok = wait(q_full, k & 1);
                     if (!ok) break;
                     if (k == 0) arrive_remote(map_shared(smem_u32(go), 1));
                     for (int h = 0; h < 2; ++h, ++U) mbar_arrive(&kv_empty[U % kStages]);  // in tensor memory now
+                    bool have_kv = false, have_s = false;  // this tile's rows landed, its S buffer free
                     for (int32_t j = 0; j < pc.n; ++j, ++T, ++U) {
-                        const int st = U % kStages, buf = T % kSBufs;
-                        ok = wait(&kv_full[st], (U / kStages) & 1) &&
-                             (T < kSBufs || wait(&s_free[buf], ((T / kSBufs) + 1) & 1));
+                        const int buf = T % kSBufs;
+                        ok = (have_kv || wait(&kv_full[U % kStages], (U / kStages) & 1)) &&
+                             (have_s || T < kSBufs || wait(&s_free[buf], ((T / kSBufs) + 1) & 1));
                         if (!ok) break;
+                        // what the producer wrote of the tile, passed on
                         // (and what the first tile has no predecessor for)
                         for (int i = 1 + (T == 0 ? kSoftWarps / 2 : 0); i > 0; --i) mbar_arrive(&s_full[buf]);
                         tc::fence_after();
-                        const uint64_t kd = dk + static_cast<uint64_t>(st) * (8 * L::kGroup0 >> 4);
-                        const uint32_t d = tS + 64u * static_cast<uint32_t>(buf);
-#pragma unroll
-                        for (int kk = 0; kk < (NR + 1) * 4; ++kk)
-                            tc::mma_ts(d, tmem + 8 * kk, kd + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idS, kk > 0 ? 1u : 0u);
+                        products(T, U, 0, kAll - kLate);
+                        have_kv = j + 1 < pc.n && mbar_test(&kv_full[(U + 1) % kStages], ((U + 1) / kStages) & 1);
+                        have_s = j + 1 < pc.n && T + 1 >= kSBufs && mbar_test(&s_free[(T + 1) % kSBufs], (((T + 1) / kSBufs) + 1) & 1);
+                        products(T, U, kAll - kLate, kAll);
                         tc::commit(&s_full[buf]);
-                        tc::commit(&kv_empty[st]);
+                        tc::commit(&kv_empty[U % kStages]);
                     }
                 }
             } else {
