@@ -964,7 +964,7 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     p.q_tiles = static_cast<int32_t>(ceil_div64(max_q_len, qpt));
     p.kv_splits = 1;
     p.split_tiles = 0;
-    if (pool->dtype != PKV_F32) {
+    if (pool->dtype != PKV_F32 && tree == nullptr) {
         const PrefillSplit sp = prefill_split_plan(batch, num_q_heads, pool->num_kv_heads,
                                                    pool->head_dim, pool->block_size, max_q_len,
                                                    p.max_len, window, sinks, num_sms_current());
@@ -991,12 +991,25 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     drill_settings(&p.wait_ns, &p.drill);
     p.sk_ctas = 0;
     p.sk_items = 0;
-    if (pool->dtype != PKV_F32 && p.kv_splits == 1) {
+    if (pool->dtype != PKV_F32 && tree != nullptr) {
+        const int32_t items = prefill_items(batch, num_q_heads, pool->num_kv_heads, max_q_len);
+        const int32_t ctas = prefill_tree_ctas(items, num_sms_current());
+        if (ctas > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len, verify_window(window, max_q_len), 0)) {
+            const PrefillTreeWs w = prefill_tree_ws(ctas);
+            if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || ws_bytes < w.bytes)
+                return PKV_ERR_WORKSPACE;
+            char *ws = static_cast<char *>(workspace);
+            p.sk_ctas = ctas;
+            p.sk_items = items;
+            p.sk_rec = ws;
+            p.sk_o = reinterpret_cast<float *>(ws + w.o);
+            p.sk_ml = reinterpret_cast<float *>(ws + w.ml);
+        }
+    } else if (pool->dtype != PKV_F32 && p.kv_splits == 1) {
         const int32_t sk = prefill_sk_ctas(pool->dtype, batch, num_q_heads, pool->num_kv_heads,
                                            pool->head_dim, pool->block_size, max_q_len, num_sms_current());
         const int32_t items = sk > 0 ? prefill_items(batch, num_q_heads, pool->num_kv_heads, max_q_len) : 0;
-        if (sk > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len,
-                                        tree != nullptr ? verify_window(window, max_q_len) : window, sinks)) {
+        if (sk > 0 && prefill_sk_counts(items, max_q_len, G, p.max_len, window, sinks)) {
             if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
                 ws_bytes < prefill_sk_ws_bytes(items, sk))
                 return PKV_ERR_WORKSPACE;
@@ -1320,7 +1333,9 @@ size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
     if (tree_on_decode(num_q_heads / num_kv_heads, head_dim, block_size, max_q_len))
         return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
                               verify_window(window, max_q_len), nullptr, 0, max_q_len);
-    return prefill_ws(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_q_len, max_seq_len, window, 0);
+    if (!prefill_shape_built(PKV_BF16, head_dim, block_size, num_q_heads / num_kv_heads)) return 0;
+    const int32_t ctas = prefill_tree_ctas(prefill_items(batch, num_q_heads, num_kv_heads, max_q_len), num_sms_current());
+    return ctas > 0 ? prefill_tree_ws(ctas).bytes : 0;
 }
 
 pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,

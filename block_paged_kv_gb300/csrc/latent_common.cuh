@@ -1,20 +1,16 @@
-// Work items, runs and partials of the attention over latent rows, shared by its
-// kernels and the merge.
+// Work items and partials of the attention over latent rows, shared by its kernels
+// and the merge.
 //
 // Item u = (row u / items_per_row, pairs kRows (u % items_per_row) .. of the row's
 // (query, head) pairs, query-major).  Its keys are the positions up to its last
-// query's, in tiles of kKeys.  The items' tiles in item order form one sequence;
-// worker c of n takes units T c / n .. T (c + 1) / n of the T there are, so that
-// every worker has the same work whatever the rows' lengths.  Only the first and
-// the last piece of a run can cut an item; a cut piece leaves a partial (maximum,
-// sum, weighted values) in slot 0 (first piece) or 1 of its worker, which the
-// merge kernel joins.
+// query's, in tiles of kKeys.  The items' tiles are levelled over the workers.
 #pragma once
 
 #include <algorithm>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "runs.cuh"
 
 namespace pkv {
 
@@ -85,117 +81,29 @@ struct alignas(8) LatentRecord {
 };
 static_assert(sizeof(LatentRecord) == kLatentRecordBytes, "the workspace holds one per worker");
 
-// A worker's run, in units: an item counts its tiles and `over` units before them
-// (what a piece costs beside its tiles: queries staged, first products, epilogue).
-struct LatentRun {
-    int32_t pos, end;  // units still ahead, in the sequence
-    int32_t lo;        // item u's first unit
-    int32_t u;         // the item that holds pos
-    int32_t over;
-    int32_t k;         // pieces so far
-};
-struct LatentPiece {
+struct LatentPiece : RunPiece {
     LatentItem it;
-    int32_t u;
-    int32_t t0, n;     // tiles t0 .. t0 + n - 1 of the item
-    bool whole;        // all of them
-    int32_t slot;      // a cut piece's partial slot
 };
 
-// Every thread of the CTA (kThreads of them, at least 128): worker `c`'s run, and the
-// record of the item that it begins and does not end; `sm`: kThreads / 32 + 4 words
-// of shared memory (64 bits).  An empty run has pos == end.  The runs have `least`
-// units at least; where they have `level` tiles or more, items count `over` units
-// beside their tiles (`level` > `over`, so that every run holds a tile).
+// Every thread of the CTA: worker `c`'s run, and the record of the item that it
+// begins and does not end.
 template <int kRows, int kKeys, int kThreads>
-__device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c, int32_t least, int32_t level,
-                                                int32_t over, bool record, int64_t *sm)
+__device__ __forceinline__ Run latent_run(const LatentParams &p, int32_t c, int32_t least, int32_t level,
+                                          int32_t over, bool record, int64_t *sm)
 {
-    constexpr int kWarps = kThreads / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t items = p.batch * p.items_per_row;
-    // an item's tiles, and (high word) whether it has any
-    auto tiles_of = [&](int32_t u, bool say) {
-        const int32_t n = u < items ? latent_item<kRows, kKeys>(p, u, say).tiles : 0;
-        return static_cast<int64_t>(n) | (n > 0 ? 1ll << 32 : 0ll);
-    };
-    auto scan = [&](int64_t x) {  // inclusive, over the warp
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        return x;
-    };
-    // tiles in all; with one pass of items, they are looked up and scanned once
-    const bool one = items <= kThreads;
-    int64_t mine = 0;
-    for (int32_t u = threadIdx.x; u < items; u += kThreads) mine += tiles_of(u, c == 0 && record);
-    const int64_t inc0 = scan(mine);
-    if (lane == 31) sm[warp] = inc0;
-    __syncthreads();
-    int64_t all = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sm[w];
-        all += sm[w];
-    }
-    const int32_t tiles = static_cast<int32_t>(all), used = static_cast<int32_t>(all >> 32);
-    LatentRun run{0, 0, 0, 0, tiles / level >= p.workers ? over : 0, 0};
-    const int32_t T = tiles + run.over * used;
-    const int32_t n = min(p.workers, max(1, T / least)), q = T / n, r = T - q * n;
-    auto start = [&](int32_t w) { return q * w + r * w / n; };  // T w / n
-    if (c < n) {
-        run.pos = start(c);
-        run.end = start(c + 1);
-    }
-    auto units = [&](int64_t x) { return static_cast<int32_t>(x) + run.over * static_cast<int32_t>(x >> 32); };
-    // items that hold the run's first and last unit: item, first unit; item, first unit, end
-    int32_t *found = reinterpret_cast<int32_t *>(sm + kWarps);
-    int64_t lo64 = before + inc0 - mine, x64 = mine, base64 = 0;
-    for (int32_t base = 0; base < items && run.pos < run.end; base += kThreads) {
-        if (!one) {
-            x64 = tiles_of(base + threadIdx.x, false);
-            const int64_t inc = scan(x64);
-            __syncthreads();
-            if (lane == 31) sm[warp] = inc;
-            __syncthreads();
-            lo64 = base64 + inc - x64;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) lo64 += sm[w];
-                base64 += sm[w];
-            }
-        }
-        const int32_t lo = units(lo64), hi = units(lo64 + x64);
-        if (lo <= run.pos && run.pos < hi) {
-            found[0] = base + threadIdx.x;
-            found[1] = lo;
-        }
-        if (lo < run.end && run.end <= hi) {
-            found[2] = base + threadIdx.x;
-            found[3] = lo;
-            found[4] = hi;
-        }
-        if (!one && units(base64) >= run.end) break;
-    }
-    __syncthreads();
-    if (run.pos < run.end) {
-        run.u = found[0];
-        run.lo = found[1];
-    }
+    RunEnd e;
+    const Run run = level_run<kThreads>(
+        p.batch * p.items_per_row,
+        [&](int32_t u, bool say) { return latent_item<kRows, kKeys>(p, u, say && record).tiles; },
+        p.workers, c, least, level, over, sm, e);
     if (record && threadIdx.x == 96) {  // (of a warp that does not lead)
-        // the item at the run's end goes on in later workers, and its first tile is here
         LatentRecord rec{};
-        if (run.pos < run.end) {
-            const int32_t first = found[3] + run.over, E = found[4];
-            if (E > run.end && first >= run.pos && first < run.end) {
-                const LatentItem it = latent_item<kRows, kKeys>(p, found[2]);
-                rec.pieces = static_cast<int32_t>((static_cast<int64_t>(E) * n + T - 1) / T) - c;  // to the first worker that ends at or past E
-                rec.slot = found[2] != found[0] ? 1 : 0;
-                rec.pairs = it.n;
-                rec.row = static_cast<int64_t>(it.q0) * p.heads + it.p0;
-            }
+        if (e.pieces > 0) {
+            const LatentItem it = latent_item<kRows, kKeys>(p, e.u);
+            rec.pieces = e.pieces;
+            rec.slot = e.slot;
+            rec.pairs = it.n;
+            rec.row = static_cast<int64_t>(it.q0) * p.heads + it.p0;
         }
         static_cast<LatentRecord *>(p.rec)[c] = rec;
     }
@@ -204,28 +112,11 @@ __device__ __forceinline__ LatentRun latent_run(const LatentParams &p, int32_t c
 
 // Next piece of the run (false at its end).
 template <int kRows, int kKeys>
-__device__ __forceinline__ bool latent_next(const LatentParams &p, LatentRun &run, LatentPiece &pc)
+__device__ __forceinline__ bool latent_next(const LatentParams &p, Run &run, LatentPiece &pc)
 {
     while (run.pos < run.end) {
         pc.it = latent_item<kRows, kKeys>(p, run.u);
-        const int32_t first = run.lo + run.over, hi = pc.it.tiles > 0 ? first + pc.it.tiles : run.lo;
-        const int32_t from = max(run.pos, first), stop = min(hi, run.end);
-        pc.u = run.u;
-        if (hi <= run.end) {
-            ++run.u;
-            run.lo = hi;
-        }
-        run.pos = max(run.pos, stop);
-        if (from >= stop) {  // an item without a query, or one whose first tile is the next run's
-            if (hi > run.end) run.pos = run.end;
-            continue;
-        }
-        pc.t0 = from - first;
-        pc.n = stop - from;
-        pc.whole = pc.n == pc.it.tiles;
-        pc.slot = run.k == 0 ? 0 : 1;
-        ++run.k;
-        return true;
+        if (run_step(run, pc.it.tiles, pc)) return true;
     }
     return false;
 }
@@ -248,64 +139,24 @@ __device__ __forceinline__ int64_t latent_out_row(const LatentParams &p, const L
 }
 
 // Joins the pieces of an item cut between workers: worker x's (CTAs (x, ..)).  A
-// thread has 16 dims of a pair; nothing but the record comes before the partials, of
-// which it has four in flight (one piece after another, each read waiting for the
-// last, joined 20 pieces in 20 us).
+// thread has 16 dims of a pair; nothing but the record comes before the partials.
 constexpr int kLatMergeThreads = 256;
 
 template <typename T, int kRows>
 __global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const LatentParams p, const int32_t pairs)
 {
-    constexpr int kFly = 4;
     pdl_wait();  // the records and partials come from the kernel just before
     pdl_trigger();
     const int32_t c = blockIdx.x, idx = blockIdx.y * kLatMergeThreads + threadIdx.x;
     const LatentRecord rec = static_cast<const LatentRecord *>(p.rec)[c];
     const int32_t pair = idx % pairs, d4 = idx / pairs * 4;  // pairs: of an item, at most
     if (pair >= rec.pairs || d4 * 4 >= p.latent) return;     // (no item: no pairs)
-    float M = -INFINITY, l = 0.f;
-    float4 acc[4] = {};
-    for (int32_t i = 0; i < rec.pieces; i += kFly) {
-        float4 v[kFly][4];
-        float2 ml[kFly];
-#pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-            ml[j] = make_float2(-INFINITY, 0.f);
-            if (i + j >= rec.pieces) continue;
-            const int32_t w = c + i + j, slot = i + j == 0 ? rec.slot : 0;
-            ml[j] = latent_part_ml<kRows>(p, w, slot)[pair];
-            const float4 *o = latent_part_o<kRows>(p, w, slot) + d4 * kRows + pair;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[j][e] = o[e * kRows];
-        }
-        float mn = M;
-#pragma unroll
-        for (int j = 0; j < kFly; ++j) mn = fmaxf(mn, ml[j].x);
-        if (mn == -INFINITY) continue;  // nothing attended so far
-        const float f0 = fast_exp2(M - mn);
-        M = mn;
-        l *= f0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            acc[e].x *= f0;
-            acc[e].y *= f0;
-            acc[e].z *= f0;
-            acc[e].w *= f0;
-        }
-#pragma unroll
-        for (int j = 0; j < kFly; ++j) {
-            if (i + j >= rec.pieces) continue;
-            const float f = fast_exp2(ml[j].x - M);
-            l = fmaf(f, ml[j].y, l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                acc[e].x = fmaf(f, v[j][e].x, acc[e].x);
-                acc[e].y = fmaf(f, v[j][e].y, acc[e].y);
-                acc[e].z = fmaf(f, v[j][e].z, acc[e].z);
-                acc[e].w = fmaf(f, v[j][e].w, acc[e].w);
-            }
-        }
-    }
+    const auto slot = [&](int32_t i) { return i == 0 ? rec.slot : 0; };
+    float4 acc[4];
+    const float l = join_pieces(
+        rec.pieces, kRows,
+        [&](int32_t i) -> const float4 * { return latent_part_o<kRows>(p, c + i, slot(i)) + d4 * kRows + pair; },
+        [&](int32_t i) { return latent_part_ml<kRows>(p, c + i, slot(i))[pair]; }, acc);
     const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
     T *out = static_cast<T *>(p.out) + (rec.row + pair) * p.latent + d4 * 4;
     if constexpr (sizeof(T) == 4) {
@@ -314,14 +165,7 @@ __global__ void __launch_bounds__(kLatMergeThreads) latent_merge_kernel(const La
             reinterpret_cast<float4 *>(out)[e] =
                 make_float4(acc[e].x * inv, acc[e].y * inv, acc[e].z * inv, acc[e].w * inv);
     } else {
-        uint32_t v[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
-            v[2 * e + 1] = pack_bf16x2(acc[e].z * inv, acc[e].w * inv);
-        }
-        reinterpret_cast<uint4 *>(out)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<uint4 *>(out)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        store_bf16x16(out, acc, inv);
     }
 }
 

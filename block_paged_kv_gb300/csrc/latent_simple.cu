@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(ls::kThreads) latent_simple_kernel(const Laten
     const int tid = threadIdx.x, pair = tid >> 4, sub = tid & 15;
     pdl_wait();
     pdl_trigger();
-    LatentRun run = latent_run<kRows, kKeys, kThreads>(p, blockIdx.x, 4, 8, 0, true, scan);
+    Run run = latent_run<kRows, kKeys, kThreads>(p, blockIdx.x, 4, 8, 0, true, scan);
     LatentPiece pc;
     while (latent_next<kRows, kKeys>(p, run, pc)) {
         const LatentItem &it = pc.it;

@@ -62,7 +62,7 @@ constexpr float kRescaleLog2 = 8.f;       // O is rescaled only when the max gro
 constexpr uint32_t kTmemCols = 512;
 constexpr int32_t kLeastTiles = 2;        // of a worker's run
 // A piece's cost beside its tiles, in tiles, where the runs are long enough to be levelled by it
-constexpr int32_t kItemCost = 4, kLevelTiles = 8;
+constexpr int32_t kItemCost = 6, kLevelTiles = 8;
 template <int NR>  // 64-dim regions of the latent
 struct Layout {
     // a tile: [8-key group][region][8 keys][128 bytes], 128-byte swizzled; CTA 0 has
@@ -191,7 +191,7 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo,
 // brings an entry's 8-row groups w, w + 3, w + 6.
 template <int NR, int kRank>
 __device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUtensorMap &q_map, const LatentParams &p,
-                                               LatentRun run, uint8_t *smem, uint64_t *kv_full, uint64_t *kv_empty,
+                                               Run run, uint8_t *smem, uint64_t *kv_full, uint64_t *kv_empty,
                                                uint32_t *kmask, int w, int lane)
 {
     using namespace lt;
@@ -333,9 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
     pdl_wait();
     pdl_trigger();
     // (a run without tiles: every role finds no piece)
-    const LatentRun run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, kLevelTiles, kItemCost, rank == 0,
+    const Run run0 = latent_run<kRows, kKeys, kThreads>(p, worker, kLeastTiles, kLevelTiles, kItemCost, rank == 0,
                                                               reinterpret_cast<int64_t *>(smem + L::kScanOff));
-    LatentRun run = run0;
+    Run run = run0;
     LatentPiece pc;
     bool ok = true;
 

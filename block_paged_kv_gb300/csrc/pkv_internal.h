@@ -134,6 +134,7 @@ struct LatentParams {
     uint32_t drill;
 };
 constexpr int kLatentRecordBytes = 24;
+constexpr int kTreeRecordBytes = 24;
 constexpr int kLatentSimpleRows = 16;  // pairs of an item: CUDA-core kernel
 constexpr int kLatentTcRows = 128;     // tensor-core kernel
 
@@ -259,7 +260,8 @@ struct PrefillParams {
     int32_t sk_ctas, sk_items;
     int32_t *sk_plan;    // written by the plan kernel: starts of the CTAs' runs [sk_ctas + 1], the items
                          // there [sk_ctas], the CTAs' whole items [sk_ctas]
-    void *sk_rec;        // [sk_items] records of kSkItemBytes (written by the plan kernel)
+    void *sk_rec;        // [sk_items] records of kSkItemBytes (written by the plan kernel); drafted
+                         // trees: [sk_ctas] of kTreeRecordBytes (no plan, no counters)
     int32_t *sk_count;   // [sk_ctas][2 query tiles][4 warps]: pieces done of the item cut
                          // after the CTA's first tile (zeroed by the plan kernel)
     float *sk_o;         // [sk_ctas][2][2 query tiles][4 warps][32 dim groups][32 rows][4] unnormalised weighted values
@@ -306,6 +308,13 @@ size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, cons
 // (0 = off: the grid then holds one CTA per item) and its workspace.
 int32_t prefill_sk_ctas(pkv_dtype dtype, int32_t batch, int32_t hq, int32_t hkv, int32_t D,
                         int32_t bs, int32_t max_q_len, int num_sms);
+// Drafted trees: CTAs of the levelled runs over the items (0: one CTA an item), and
+// their workspace (offsets of the pieces' values and of their maxima and sums).
+int32_t prefill_tree_ctas(int32_t items, int num_sms);
+struct PrefillTreeWs {
+    size_t o, ml, bytes;
+};
+PrefillTreeWs prefill_tree_ws(int32_t ctas);
 size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas);
 // Whether the plan's 32-bit sums hold items of up to max_len keys (else the call
 // takes one CTA per item; past 65536 items of two million keys, say).

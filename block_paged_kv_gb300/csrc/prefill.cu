@@ -40,6 +40,7 @@
 #include <algorithm>
 
 #include "decode_common.cuh"
+#include "runs.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -70,8 +71,9 @@ struct Layout {
     static constexpr int kBarOff = kStagingOff + kStagingBytes;
     // barriers: k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[tile][buf],
     // p_full[tile][buf], pv_done[tile], mma_drain[tile], q_full[tile],
-    // o_done[tile], FP8: staged[K/V][2], stg_free[K/V][2]
-    static constexpr int kNumBars = 4 * kStages + 4 + 4 + 2 + 2 + 2 + 2 + (kF8 ? 8 : 0);
+    // o_done[tile], sums (of two, for the alignment), FP8: staged[K/V][2],
+    // stg_free[K/V][2]
+    static constexpr int kNumBars = 4 * kStages + 4 + 4 + 2 + 2 + 2 + 2 + 2 + (kF8 ? 8 : 0);
     // kmask[kStages], FP8: smask[K/V][2] (blocks loaded of each staging buffer)
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
     static constexpr int kTmemOff = kMaskOff + (kStages + 4) * 4;
@@ -180,6 +182,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //     first and the last segment of a run can cut an item; a cut segment
 //     writes a partial to slot 0 (first) or 1 (last) of the CTA, and the warp
 //     that completes an item's pieces merges them.
+//   drafted trees (kTree, sk_ctas > 0): every CTA a levelled run of the items'
+//     tiles, none of them dealt whole, the pieces joined by prefill_tree_merge_kernel:
+//     its items are few and long, a row's keys read by one of them (bf16, 32/8 heads,
+//     4 rows of 8000 keys x 16 drafts: 56.6 us under the schedule above, 39.5 here).
 // ---------------------------------------------------------------------------
 struct Seg {
     PrefillRowInfo w;
@@ -191,11 +197,9 @@ struct Seg {
                          // the first and the last CTA whose runs hold its tiles
 };
 
-struct SegWalk {
-    int32_t pos, end;  // persistent schedule: tiles of the CTA's run still ahead
-    int32_t u;         // the item holding tile pos
-    int32_t k;         // segments returned so far
-};
+// persistent schedule: pos .. end are the tiles of the CTA's run still ahead, u the
+// item holding tile pos, k the segments returned so far
+using SegWalk = Run;
 
 // the plan's arrays: start of CTA c's run (c = n: the end of the sequence), the
 // item that holds it, the item CTA c runs whole (-1: none)
@@ -247,6 +251,69 @@ __device__ __forceinline__ bool sk_next(const PrefillParams &p, int qpc, SegWalk
     return true;
 }
 
+// What the merge needs of an item that a tree's run begins and does not end.
+struct alignas(8) TreeRecord {
+    int32_t q0, g;   // its first query, kv head
+    int32_t rows;    // (query, head) pairs
+    int32_t pieces;  // CTAs that hold a piece of it, this one first (0: there is no such item)
+    int32_t slot;    // this CTA's piece's partial slot (the others': 0)
+    int32_t pad;
+};
+static_assert(sizeof(TreeRecord) == kTreeRecordBytes, "the workspace holds one per CTA");
+
+__device__ __forceinline__ int32_t tree_tiles(const PrefillParams &p, int32_t u, int qpc, PrefillRowInfo &w)
+{
+    return prefill_item(p, u, qpc, w) ? item_tiles(w) : 0;
+}
+
+// Next segment of a tree's run.
+__device__ __forceinline__ bool tree_next(const PrefillParams &p, int qpc, SegWalk &sw, Seg &sg)
+{
+    RunPiece pc;
+    while (sw.pos < sw.end) {
+        const int32_t tiles = tree_tiles(p, sw.u, qpc, sg.w);
+        if (!run_step(sw, tiles, pc)) continue;
+        sg.jt0 = item_first_tile<false>(sg.w) + pc.t0;
+        sg.ntile = pc.n;
+        sg.whole = pc.whole;
+        sg.slot = pc.slot;
+        sg.lo = sg.cf = sg.cl = 0;
+        return true;
+    }
+    return false;
+}
+
+// A tree's run, its first segment, the run's tiles (every thread of the CTA), and
+// the record of the item that it begins and does not end.
+constexpr int32_t kTreeLeast = 8, kTreeLevel = 16, kTreeOver = 6;
+__device__ __forceinline__ bool tree_first(const PrefillParams &p, int qpc, int64_t *sm, SegWalk &sw, Seg &sg,
+                                           int32_t &tiles)
+{
+    RunEnd e;
+    sw = level_run<pf::kThreads>(
+        p.sk_items,
+        [&](int32_t u, bool) {
+            PrefillRowInfo w;
+            return tree_tiles(p, u, qpc, w);
+        },
+        p.sk_ctas, blockIdx.x, kTreeLeast, kTreeLevel, kTreeOver, sm, e);
+    tiles = e.tiles;
+    if (threadIdx.x == 96) {  // (of a warp that does not lead)
+        TreeRecord rec{};
+        if (e.pieces > 0) {
+            PrefillRowInfo w;
+            prefill_item(p, e.u, qpc, w);
+            rec.q0 = w.q0;
+            rec.g = w.g;
+            rec.rows = w.nq * p.group;
+            rec.pieces = e.pieces;
+            rec.slot = e.slot;
+        }
+        static_cast<TreeRecord *>(p.sk_rec)[blockIdx.x] = rec;
+    }
+    return tree_next(p, qpc, sw, sg);
+}
+
 // First segment of CTA `cta` (false: nothing to do).  One CTA per item: the
 // item (or its key-range run; an empty run sets ntile <= 0).
 template <bool kSink>
@@ -287,14 +354,15 @@ __device__ __forceinline__ bool seg_first(const PrefillParams &p, int qpc, int32
     return true;
 }
 
-template <bool kSink>
+template <bool kSink, bool kTree = false>
 __device__ __forceinline__ bool seg_next(const PrefillParams &p, int qpc, SegWalk &sw, Seg &sg)
 {
+    if (kTree) return p.sk_ctas > 0 && tree_next(p, qpc, sw, sg);
     return p.sk_ctas > 0 && sk_next<kSink>(p, qpc, sw, sg);
 }
 
 // The key tiles of a CTA in order, over its segments (producers).
-template <bool kSink>
+template <bool kSink, bool kTree>
 struct TileCursor {
     SegWalk sw;
     Seg sg;
@@ -314,7 +382,7 @@ struct TileCursor {
         if (!valid) return;
         if (++j < sg.ntile) return;
         j = 0;
-        valid = seg_next<kSink>(p, qpc, sw, sg);
+        valid = seg_next<kSink, kTree>(p, qpc, sw, sg);
     }
     __device__ __forceinline__ int32_t kt() const { return key_tile<kSink>(sg.w, sg.jt0 + j); }  // absolute key tile
 };
@@ -387,7 +455,10 @@ __device__ __forceinline__ void come_late(uint32_t ns)
 // ---------------------------------------------------------------------------
 // kSink: a window with sink tokens (their tiles first, then the window's)
 // kTree: the queries are a drafted tree's, masked by their ancestors
-template <bool kF8, bool kSink, bool kTree>
+// kAlt: every chunk fills one query tile at most; tile B's warps then take the
+// same rows (their own copy of the queries, S and O) and the two alternate over
+// the key tiles, joined in the epilogue
+template <bool kF8, bool kSink, bool kTree, bool kAlt>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PrefillParams p)
@@ -409,8 +480,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     uint64_t *mma_drain = bars + 4 * kStages + 10;  // [tile]: the issuer's last products
     uint64_t *q_full = bars + 4 * kStages + 12;     // [tile]: a segment's query tile staged
     uint64_t *o_done = bars + 4 * kStages + 14;  // [tile]: a segment's last P.V product
-    uint64_t *staged = bars + 4 * kStages + 16;  // FP8: [K/V * 2 + buffer]
-    uint64_t *stg_free = bars + 4 * kStages + 20;  // FP8: [K/V * 2 + buffer] widened by the softmax warps
+    uint64_t *sums = bars + 4 * kStages + 16;    // kAlt: tile B's maxima and sums of a segment stored
+    uint64_t *staged = bars + 4 * kStages + 18;  // FP8: [K/V * 2 + buffer]
+    uint64_t *stg_free = bars + 4 * kStages + 22;  // FP8: [K/V * 2 + buffer] widened by the softmax warps
     uint32_t *kmask = reinterpret_cast<uint32_t *>(smem + L::kMaskOff);
     uint32_t *smask = kmask + kStages;  // FP8: [K/V * 2 + buffer] blocks loaded of a staging buffer
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemOff);
@@ -428,7 +500,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     const int qpc = kQTiles * qpt;  // queries per item
     SegWalk sw0;
     Seg seg0;
-    if (!seg_first<kSink>(p, qpc, blockIdx.x, sw0, seg0)) return;
+    int32_t run_tiles = 0;  // kTree: of the CTA's run
+    if (kTree && p.sk_ctas > 0) {
+        // (the words are the segment walks' once every thread is past the barrier below)
+        if (!tree_first(p, qpc, reinterpret_cast<int64_t *>(smem + L::kSegOff), sw0, seg0, run_tiles)) return;
+    } else if (!seg_first<kSink>(p, qpc, blockIdx.x, sw0, seg0)) {
+        return;
+    }
     const bool split = p.kv_splits > 1;  // one CTA per key-range run of a short chunk
     if (split && seg0.ntile <= 0) {
         // an empty run: an empty partial (no weight) for every live row
@@ -447,17 +525,21 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     // query tiles with queries in them: a short chunk (a verify step of a few
     // queries) fills tile A only, and tile B's warps then stay idle; the
     // persistent schedule runs both (its segments' items differ)
-    const int nqt = (p.sk_ctas > 0 || seg0.w.nq > qpt) ? 2 : 1;
+    const int nqt = (kAlt || p.sk_ctas > 0 || seg0.w.nq > qpt) ? 2 : 1;
+    const int users = kAlt ? 1 : nqt;  // query tiles that read a K/V tile
+    // kAlt: tile T is warpgroup T & 1's, as its tile T >> 1
+    constexpr int kStep = kAlt ? 2 : 1;
+    const auto own = [](int32_t T) { return kAlt ? T >> 1 : T; };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             // the S products of the live tiles + their warpgroups' kmask reads
-            mbar_init(&k_empty[i], nqt + nqt * (kSoftmaxWarps / kQTiles));
+            mbar_init(&k_empty[i], users + users * (kSoftmaxWarps / kQTiles));
             // FP8: one softmax warpgroup widens K into the stages, the other
             // V (tile A's both when it runs alone); bf16: one TMA arrival
             mbar_init(&k_full[i], kF8 ? kSoftmaxWarps / kQTiles : 1);
             mbar_init(&v_full[i], kF8 ? kSoftmaxWarps / kQTiles : 1);
-            mbar_init(&v_empty[i], nqt);  // the live tiles' P.V products
+            mbar_init(&v_empty[i], users);  // the live tiles' P.V products
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
@@ -470,7 +552,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         mbar_init(&o_done[0], 1);
         mbar_init(&o_done[1], 1);
         mbar_init(&q_full[0], kSoftmaxWarps / kQTiles);
-        mbar_init(&q_full[1], kSoftmaxWarps / kQTiles);
+        // kAlt: tile A's warps too, once they have read the last segment's O of tile B
+        mbar_init(&q_full[1], kAlt ? kSoftmaxWarps : kSoftmaxWarps / kQTiles);
+        mbar_init(&sums[0], kSoftmaxWarps / kQTiles);
         if (kF8) {
             for (int i = 0; i < 4; ++i) mbar_init(&staged[i], 1);
             for (int i = 0; i < 4; ++i) mbar_init(&stg_free[i], kSoftmaxWarps / kQTiles);
@@ -486,7 +570,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
     const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
     const int glog = __ffs(G) - 1;  // G divides the tile's 128 rows
     auto load_q_rows = [&](const PrefillRowInfo &w) {
-        stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.hq, glog, qpt, w.q0, w.nq, w.g, flip, p.status, q_s, warp - 4, lane);
+        stage_q_rows<kF8>(static_cast<const uint4 *>(p.q), p.hq, glog, kAlt ? 0 : qpt, w.q0, w.nq, w.g, flip, p.status, q_s, warp - 4, lane);
     };
     tc::fence_before();
     __syncthreads();
@@ -507,12 +591,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         uint64_t *empty = is_k ? k_empty : v_empty;
         // lane < kBlocks: logical block kt * kBlocks + lane of the cursor's
         // tile, inside the table and the item's key range
-        auto in_range_of = [&](const TileCursor<kSink> &c) {
+        auto in_range_of = [&](const TileCursor<kSink, kTree> &c) {
             const int32_t kb = c.kt() * kBlocks + lane;
             return c.valid && lane < kBlocks && kb < p.width && kb * 16 < c.sg.w.kv_hi &&
                    ((kb + 1) * 16 > c.sg.w.kv_lo || (kSink && kb * 16 < p.sinks));
         };
-        auto load_id = [&](const TileCursor<kSink> &c) {
+        auto load_id = [&](const TileCursor<kSink, kTree> &c) {
             return in_range_of(c) ? __ldg(p.tables + static_cast<int64_t>(c.sg.w.r) * p.width +
                                           c.kt() * kBlocks + lane)
                                   : -1;
@@ -533,7 +617,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             int32_t nf = 0;  // tiles 0 .. nf-1 fetched into the staging buffers
             // fetch tile nf at cursor c (block ids read one tile before);
             // whole warp; returns the mask of loaded blocks
-            auto fetch = [&](const TileCursor<kSink> &c, int32_t id) {
+            auto fetch = [&](const TileCursor<kSink, kTree> &c, int32_t id) {
                 const bool in_range = in_range_of(c);
                 const bool good = in_range && static_cast<uint32_t>(id) < static_cast<uint32_t>(p.num_blocks);
                 if (is_k && in_range && !good) report(p.status, PKV_DEV_BAD_BLOCK);
@@ -562,7 +646,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             };
             // bulk copies only, two tiles ahead; the softmax warps widen each
             // tile into the ring and release the staging buffer
-            TileCursor<kSink> cf, ci;
+            TileCursor<kSink, kTree> cf, ci;
             cf.start(p, qpc, sw0, seg0);
             ci = cf;
             int32_t id_next = load_id(ci);
@@ -585,7 +669,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         } else {
             const CUtensorMap *map = is_k ? &kmap : &vmap;
             const uint64_t policy = l2_evict_last_policy();  // re-read by the row's other CTAs
-            TileCursor<kSink> cur;
+            TileCursor<kSink, kTree> cur;
             cur.start(p, qpc, sw0, seg0);
             int32_t T = 0;
             for (; cur.valid; ++T, cur.advance(p, qpc)) {
@@ -654,21 +738,21 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         };
         auto s_issue = [&](int32_t T) {  // S(T) = Q K(T)^T
             const uint64_t kd = dk + static_cast<uint64_t>(T % kStages) * kStageStep;
-            const uint32_t d = tS(x, T & 1);
+            const uint32_t d = tS(x, own(T) & 1);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const uint64_t qo = static_cast<uint64_t>(((kk >> 2) * (kRows * 128) + (kk & 3) * 32) >> 4);
                 const uint64_t ko = static_cast<uint64_t>(((kk >> 2) * kKVRegion + (kk & 3) * 32) >> 4);
                 tc::mma_ss(d, dq + qo, kd + ko, idS, kk > 0 ? 1u : 0u);
             }
-            tc::commit(&s_full[x * 2 + (T & 1)]);
+            tc::commit(&s_full[x * 2 + (own(T) & 1)]);
             tc::commit(&k_empty[T % kStages]);
         };
         // O += P(T) V(T); V(T) has landed (the warpgroup checked it before
         // handing P over); a segment's first tile starts O afresh
         auto pv_issue = [&](int32_t T, bool seg_start) {
             const uint64_t vd = dv + static_cast<uint64_t>(T % kStages) * kStageStep;
-            const uint32_t a = tS(x, T & 1);
+            const uint32_t a = tS(x, own(T) & 1);
             const uint32_t first = seg_start ? 0u : 1u;
             // bf16: keys 16g..16g+15 hold P hi in S columns 16g..16g+7 and P
             // lo in 16g+8..16g+15 (bf16 pairs); FP8 pools: one f16 term, keys
@@ -690,35 +774,38 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             // the segment's query tile is staged (the previous segment's
             // products, which read the old one, completed before its epilogue)
             bool ok = warp_wait(&q_full[x], k & 1, lane, p.status, p.wait_ns);
-            ok = ok && k_landed(T0) && (n < 2 || k_landed(T0 + 1));
+            const int32_t j0 = kAlt ? (T0 ^ x) & 1 : 0;  // its first tile of the segment
+            const bool one = j0 < n, two = j0 + kStep < n;
+            ok = ok && (!one || k_landed(T0 + j0)) && (!two || k_landed(T0 + j0 + kStep));
             if (ok) {
                 tc::fence_after();
                 if (elect_one()) {
-                    s_issue(T0);
-                    if (n >= 2) s_issue(T0 + 1);
+                    if (one) s_issue(T0 + j0);
+                    if (two) s_issue(T0 + j0 + kStep);
+                    if (kAlt && !one) tc::commit(&o_done[x]);  // nothing of this segment
                 }
                 __syncwarp();
             }
-            // per tile: K(T+2) is waited for first (it landed, or was widened,
+            // per tile (kAlt: every other): K(T+2) is waited for first (it landed, or was widened,
             // long before P(T) is ready), so that P(T).V(T) and S(T+2) leave
             // in one block as soon as P(T) is
-            for (int32_t j = 0; j < n && ok; ++j) {
-                const int32_t T = T0 + j;
-                const bool more = j + 2 < n;
-                if (more) ok = k_landed(T + 2);
-                ok = ok && warp_wait(&p_full[x * 2 + (T & 1)], (T >> 1) & 1, lane, p.status, p.wait_ns);
+            for (int32_t j = j0; j < n && ok; j += kStep) {
+                const int32_t T = T0 + j, u = own(T);
+                const bool more = j + 2 * kStep < n;
+                if (more) ok = k_landed(T + 2 * kStep);
+                ok = ok && warp_wait(&p_full[x * 2 + (u & 1)], (u >> 1) & 1, lane, p.status, p.wait_ns);
                 if (!ok) break;
                 tc::fence_after();
                 if (elect_one()) {
-                    pv_issue(T, j == 0);
-                    if (j == n - 1) tc::commit(&o_done[x]);
-                    if (more) s_issue(T + 2);
+                    pv_issue(T, j == j0);
+                    if (j + kStep >= n) tc::commit(&o_done[x]);
+                    if (more) s_issue(T + 2 * kStep);
                 }
                 __syncwarp();
             }
             if (!ok) break;
             T0 += n;
-            if (!seg_next<kSink>(p, qpc, sw, sg)) break;
+            if (!seg_next<kSink, kTree>(p, qpc, sw, sg)) break;
         }
         // every product this warp issued has completed before the CTA frees
         // tensor memory (after a wait ran out, some may still be running)
@@ -733,7 +820,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int x = (warp >> 2) - 1;
         const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const int row = 32 * (warp & 3) + lane;
-        const int t = x * qpt + row / G;
+        const int t = (kAlt ? 0 : x * qpt) + row / G;
         const uint32_t ox = tO(x) + lane_base;
         // |scale| * log2(e) (q was staged negated for a negative scale), kept
         // away from 0 so that a masked score (-inf) never meets a zero factor
@@ -742,13 +829,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         // FP8: tile A's warpgroup widens K, tile B's V (tile A's both when it
         // runs alone), each 128 threads over a tile's 512 staged chunks: a
         // warp then waits for one staging and one ring barrier per tile, and
-        // the two warpgroups need not run in step.
+        // the two warpgroups need not run in step.  kAlt: each both of its own tiles.
         // K(Tk)'s staged E4M3 chunks, this thread's share, widened to f16
         // into ring stage Tk % kStages (key rows, 64-dim 128-byte-swizzled
         // regions, as the bf16 path lays them out); keys of blocks not loaded
         // are left as they are (their scores are masked).  The stage is free
         // once tile Tk - kStages's S products and mask reads are done.
-        const bool do_k = nqt == 1 || x == 0, do_v = nqt == 1 || x == 1;
+        const bool do_k = kAlt || nqt == 1 || x == 0, do_v = kAlt || nqt == 1 || x == 1;
         const int wq0 = (threadIdx.x - 128) & (kRows - 1);  // this thread's first chunk
         auto widen_k = [&](int32_t Tk) {
             const int sb = Tk & 1, st = Tk % kStages;
@@ -756,7 +843,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             if (Tk >= kStages) okw = okw && mbar_wait(&k_empty[st], ((Tk / kStages) + 1) & 1, p.wait_ns);
             if (__any_sync(0xffffffffu, !okw)) return false;
             const uint32_t km = smask[sb];
-            if (threadIdx.x == 128) kmask[st] = km;  // for the score masks of tile Tk
+            if ((kAlt ? row : static_cast<int>(threadIdx.x) - 128) == 0) kmask[st] = km;  // for the score masks of tile Tk
             const uint32_t src = smem_u32(smem + L::kStagingOff + sb * kF8StageTile);
             const uint32_t dst = smem_u32(k_s + st * kTileBytes);
             // A warp takes 32 chunks of one (block, 64-dim group, token half):
@@ -797,12 +884,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         };
         // the CTA's tiles over all its segments
         const int32_t T_total =
-            p.sk_ctas > 0 ? (seg0.whole && sk_whole_item(p, blockIdx.x) >= 0 ? seg0.ntile : 0) +
+            kTree && p.sk_ctas > 0 ? run_tiles
+            : p.sk_ctas > 0 ? (seg0.whole && sk_whole_item(p, blockIdx.x) >= 0 ? seg0.ntile : 0) +
                                 sk_run_start(p, blockIdx.x + 1) - sk_run_start(p, blockIdx.x)
                           : seg0.ntile;
         load_q_rows(seg0.w);  // while the producers' first copies are under way
         if constexpr (kF8) {
-            for (int32_t Tk = 0; do_k && Tk < min(2, T_total) && !abort; ++Tk)
+            for (int32_t Tk = kAlt ? x : 0; do_k && Tk < min(2 * kStep, T_total) && !abort; Tk += kStep)
                 if (!widen_k(Tk)) {
                     if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                     abort = true;
@@ -832,6 +920,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         if (k > 0) load_q_rows(cs.w);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[x]);
+        if (kAlt && x == 0 && lane == 0) mbar_arrive(&q_full[1]);
         const bool valid_row = row < qpt * G && t < cs.w.nq;
         const int32_t qpos = cs.w.kv_hi - cs.w.nq + t;
         // kTree: positions below `first` hold the cached tokens, the drafts follow
@@ -842,12 +931,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int32_t qlo = p.window > 0 ? max(0, at - p.window + 1) : 0;
         float m_ref = -INFINITY, l = 0.f;
         const bool warp_live = __any_sync(0xffffffffu, valid_row);
-        for (int32_t jj = 0; jj < ntile; ++jj) {
-            const int32_t T = T0 + jj;
-            const int ks = T % kStages, buf = T & 1;
+        const int32_t j0 = kAlt ? (T0 ^ x) & 1 : 0;  // this warpgroup's first tile
+        for (int32_t jj = j0; jj < ntile; jj += kStep) {
+            const int32_t T = T0 + jj, u = own(T);
+            const int ks = T % kStages, buf = u & 1;
             const int32_t tbase = (jt0 + jj + (kSink && jt0 + jj >= nst ? gap : 0)) * kKeys;
             const uint32_t sx = tS(x, buf) + lane_base;
-            if constexpr (kF8) {
+            if constexpr (kF8 && !kAlt) {
                 if (do_k && T + 2 < T_total && !widen_k(T + 2)) {
                     if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                     abort = true;
@@ -920,7 +1010,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     mbar_arrive(&stg_free[2 + sb]);
                 }
             }
-            bool got = mbar_wait(&s_full[x * 2 + buf], (T >> 1) & 1, p.wait_ns);
+            bool got = mbar_wait(&s_full[x * 2 + buf], (u >> 1) & 1, p.wait_ns);
             got = got && mbar_wait(&k_full[ks], (T / kStages) & 1, p.wait_ns);  // for kmask
             if (__any_sync(0xffffffffu, !got)) {
                 if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
@@ -930,6 +1020,13 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             const uint32_t mask = kmask[ks];
             __syncwarp();
             if (lane == 0) mbar_arrive(&k_empty[ks]);
+            if constexpr (kF8 && kAlt) {  // into the stage that S(T) and the warps' masks have just left
+                if (T + 2 * kStep < T_total && !widen_k(T + 2 * kStep)) {
+                    if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
+                    abort = true;
+                    break;
+                }
+            }
             tc::fence_after();
             // a warp whose 32 rows hold no query (a short chunk fills only the
             // first rows of the tile) leaves its S rows alone: the P.V product
@@ -989,8 +1086,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 const bool resc = new_ref != m_ref && m_ref != -INFINITY;
                 if (__any_sync(0xffffffffu, resc)) {
                     // O_x holds P.V up to tile jj-1 once that product completes
-                    if (jj > 0) {
-                        const bool done = mbar_wait(&pv_done[x], (T - 1) & 1, p.wait_ns);
+                    if (jj > j0) {
+                        const bool done = mbar_wait(&pv_done[x], (u - 1) & 1, p.wait_ns);
                         if (__any_sync(0xffffffffu, !done)) {
                             if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                             abort = true;
@@ -1101,7 +1198,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         if (lane == 0) {
             SegWalk sw = ss->sw;
             Seg sg;
-            more = seg_next<kSink>(p, qpc, sw, sg);
+            more = seg_next<kSink, kTree>(p, qpc, sw, sg);
             if (more) {
                 ss->sw = sw;
                 ss->sg[(k + 1) & 1] = sg;
@@ -1114,12 +1211,60 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         // pv_done alone cannot tell: a warp that comes late finds the last two
         // products done, where a wait for the first of them never ends
         {
-            const int32_t Tl = T0 + ntile - 1;
+            const int32_t Tl = kAlt ? T0 + j0 + ((ntile - 1 - j0) & ~1) : T0 + ntile - 1;  // its last tile
             bool done = mbar_wait(&o_done[x], k & 1, p.wait_ns);
-            done = done && mbar_wait(&pv_done[x], Tl & 1, p.wait_ns);
+            if (!kAlt || j0 < ntile) done = done && mbar_wait(&pv_done[x], own(Tl) & 1, p.wait_ns);
+            // kAlt: tile B's maximum and sum of every row go to tile A's warps
+            // through its S columns (free until the next segment's queries are
+            // announced, which tile A's warps take part in), which join the two
+            // tiles' O as they read them
+            float wa = 1.f, wb = 0.f;
+            if constexpr (kAlt) {
+                const uint32_t hand = tS(1, 0) + lane_base;
+                if (x == 1 && !__any_sync(0xffffffffu, !done)) {
+                    tc::fence_after();
+                    uint32_t ml[16] = {__float_as_uint(m_ref), __float_as_uint(l)};
+                    tc::st16(hand, ml);
+                    tc::wait_st();
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sums[0]);
+                } else if (x == 0) {
+                    done = done && mbar_wait(&sums[0], k & 1, p.wait_ns) && mbar_wait(&o_done[1], k & 1, p.wait_ns);
+                    if (!__any_sync(0xffffffffu, !done)) {
+                        tc::fence_after();
+                        uint32_t ml[32];
+                        tc::ld32(hand, ml);
+                        tc::wait_ld();
+                        const float mb = __uint_as_float(ml[0]), m = fmaxf(m_ref, mb);
+                        wa = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
+                        wb = mb == -INFINITY ? 0.f : fast_exp2(mb - m);
+                        l = wa * l + wb * __uint_as_float(ml[1]);
+                        m_ref = m;
+                    }
+                }
+            }
+            // 32 dims of the row's O, not yet divided (a tile without weight may hold anything)
+            const auto load_o = [&](int c, uint32_t (&r32)[32]) {
+                tc::ld32(ox + c * 32, r32);
+                if constexpr (kAlt) {
+                    uint32_t b32[32];
+                    tc::ld32(ox + 128 + c * 32, b32);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float a = wa > 0.f ? wa * __uint_as_float(r32[e]) : 0.f;
+                        r32[e] = __float_as_uint(wb > 0.f ? fmaf(wb, __uint_as_float(b32[e]), a) : a);
+                    }
+                } else {
+                    tc::wait_ld();
+                }
+            };
             if (__any_sync(0xffffffffu, !done)) {
                 if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                 break;
+            } else if (kAlt && x == 1) {
+                // tile A's warps write the rows
             } else if (p.sk_ctas > 0 && !cs.whole) {
                 // a piece of an item cut by this CTA's run: a partial in the
                 // CTA's slot (first or last segment), merged afterwards.  Each
@@ -1136,8 +1281,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r32[32];
-                    tc::ld32(ox + c * 32, r32);
-                    tc::wait_ld();
+                    load_o(c, r32);
                     const float vs = kF8 ? p.v_scale : 1.f;
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
@@ -1145,6 +1289,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                                                             __uint_as_float(r32[4 * v + 2]) * vs, __uint_as_float(r32[4 * v + 3]) * vs);
                 }
                 reinterpret_cast<float2 *>(p.sk_ml)[own * 32 + lane] = make_float2(m_ref, l);
+                if constexpr (!kTree) {
                 // the item's pieces: CTAs cf .. cl; per (query tile, warp) the
                 // warp whose piece completes last merges their 32 rows (no
                 // waiting: the others published theirs before counting)
@@ -1227,6 +1372,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                         }
                     }
                 }
+                }
             } else if (split) {
                 // a partial: O unnormalised with its reference max and sum
                 tc::fence_after();
@@ -1236,8 +1382,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r32[32];
-                    tc::ld32(ox + c * 32, r32);
-                    tc::wait_ld();
+                    load_o(c, r32);
                     if (valid_row) {
                         const float vs = kF8 ? p.v_scale : 1.f;
 #pragma unroll
@@ -1257,8 +1402,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t r32[32];
-                    tc::ld32(ox + c * 32, r32);
-                    tc::wait_ld();
+                    load_o(c, r32);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint4 o;
@@ -1470,6 +1614,34 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const P
     for (int e = 0; e < D / 32; ++e) out[32 * e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
+// Drafted trees: joins the pieces of the item that CTA x's run begins and does not
+// end (CTAs (x, ..)); a thread has 16 dims of a (query, head) pair.
+constexpr int kTreeMergeThreads = 256;
+__global__ void __launch_bounds__(kTreeMergeThreads) prefill_tree_merge_kernel(const PrefillParams p, int32_t rows)
+{
+    pdl_wait();  // the records and partials come from the kernel just before
+    pdl_trigger();
+    constexpr int kD = pf::kD;
+    const int32_t c = blockIdx.x, idx = blockIdx.y * kTreeMergeThreads + threadIdx.x;
+    const TreeRecord rec = static_cast<const TreeRecord *>(p.sk_rec)[c];
+    const int32_t row = idx % rows, d4 = idx / rows * 4;  // rows: of an item, at most
+    if (row >= rec.rows || d4 * 4 >= kD) return;          // (no item: no rows)
+    // a piece's warp of 32 rows
+    const auto at = [&](int32_t i) {
+        return (static_cast<size_t>(c + i) * 2 + (i == 0 ? rec.slot : 0)) * (pf::kQTiles * 4) + (row >> 5);
+    };
+    float4 acc[4];
+    const float l = join_pieces(
+        rec.pieces, 32,
+        [&](int32_t i) -> const float4 * {
+            return reinterpret_cast<const float4 *>(p.sk_o) + at(i) * (32 * kD / 4) + d4 * 32 + (row & 31);
+        },
+        [&](int32_t i) { return reinterpret_cast<const float2 *>(p.sk_ml)[at(i) * 32 + (row & 31)]; }, acc);
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
+                         ((static_cast<int64_t>(rec.q0) + row / p.group) * p.hq + rec.g * p.group + row % p.group) * kD + d4 * 4;
+    store_bf16x16(out, acc, l > 0.f ? 1.f / l : 0.f);
+}
+
 // ---------------------------------------------------------------------------
 // persistent balanced schedule: the plan (the items' records, the CTAs' whole
 // items and runs, the cut items' arrival counters zeroed), one CTA
@@ -1484,6 +1656,7 @@ constexpr int kSkMaxCtas = 512;
 // one of 4096 470 -> 465; 4 to 8 and 2 to 4 lie within 5 % of each other.
 constexpr int32_t kSkItemCost = 6;
 constexpr int32_t kSkLeastPiece = 4;
+static_assert(kTreeOver <= kSkItemCost, "prefill_sk_counts holds for the runs of trees");
 
 __global__ void __launch_bounds__(kSkPlanThreads) prefill_sk_plan_kernel(const PrefillParams p)
 {
@@ -1765,6 +1938,19 @@ bool prefill_sk_counts(int32_t items, int32_t max_q_len, int32_t group, int32_t 
     return items * (tiles + kSkItemCost) <= INT32_MAX - (1 << 20);  // the margin: sums round up per CTA
 }
 
+int32_t prefill_tree_ctas(int32_t items, int num_sms) { return items > 0 && items <= 65536 ? num_sms : 0; }
+
+// the records, the pieces' values, their maxima and sums
+PrefillTreeWs prefill_tree_ws(int32_t ctas)
+{
+    const size_t rows = static_cast<size_t>(ctas) * 2 * pf::kQTiles * pf::kRows;
+    PrefillTreeWs w{};
+    w.o = (static_cast<size_t>(ctas) * kTreeRecordBytes + 255) & ~static_cast<size_t>(255);
+    w.ml = w.o + rows * pf::kD * sizeof(float);
+    w.bytes = w.ml + rows * 2 * sizeof(float);
+    return w;
+}
+
 size_t prefill_sk_ws_bytes(int32_t items, int32_t ctas)
 {
     if (ctas <= 0) return 0;
@@ -1784,7 +1970,7 @@ size_t prefill_split_ws_bytes(int32_t batch, int32_t hq, int32_t max_q_len, cons
     return o + n * 2 * sizeof(float);
 }
 
-template <bool kF8, bool kSink, bool kTree = false>
+template <bool kF8, bool kSink, bool kTree = false, bool kAlt = false>
 static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &kmap,
                                     const CUtensorMap &vmap, cudaStream_t stream)
 {
@@ -1792,20 +1978,27 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
                                        : static_cast<int64_t>(p.batch) * p.hkv * p.q_tiles * p.kv_splits;
     if (ctas == 0) return cudaSuccess;
     constexpr int smem = pf::Layout<kF8>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink, kTree>,
+    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink, kTree, kAlt>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_PREFILL, stream);
-    if (p.sk_ctas > 0)
+    if (p.sk_ctas > 0 && !kTree)
         err = launch_pdl(prefill_sk_plan_kernel, dim3(1), dim3(kSkPlanThreads), 0, stream, p);
     if (err == cudaSuccess)
-        err = launch_pdl(prefill_kernel<kF8, kSink, kTree>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
+        err = launch_pdl(prefill_kernel<kF8, kSink, kTree, kAlt>, dim3(static_cast<unsigned>(ctas)), dim3(pf::kThreads), smem,
                          stream, kmap, vmap, p);
     if (err == cudaSuccess && p.kv_splits > 1) {
         const int64_t items = static_cast<int64_t>(p.batch) * p.max_q_len * p.hq;
         err = launch_pdl(prefill_merge_kernel,
                          dim3(static_cast<unsigned>((items + kMergeWarps - 1) / kMergeWarps)),
                          dim3(kMergeWarps * 32), 0, stream, p);
+    }
+    if (kTree && err == cudaSuccess && p.sk_ctas > 0) {
+        const int32_t rows = std::min(pf::kQTiles * pf::kRows, p.max_q_len * p.group);
+        err = launch_pdl(prefill_tree_merge_kernel,
+                         dim3(static_cast<unsigned>(p.sk_ctas),
+                              static_cast<unsigned>((rows * (pf::kD / 16) + kTreeMergeThreads - 1) / kTreeMergeThreads)),
+                         dim3(kTreeMergeThreads), 0, stream, p, rows);
     }
     prof_end(PKV_KERNEL_PREFILL, stream);
     return err;
@@ -1814,7 +2007,9 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
 cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
                                 const CUtensorMap &vmap, cudaStream_t stream)
 {
-    if (p.tree != nullptr) return launch_prefill_tc<false, false, true>(p, kmap, vmap, stream);
+    if (p.tree != nullptr)
+        return p.max_q_len <= pf::kRows / p.group ? launch_prefill_tc<false, false, true, true>(p, kmap, vmap, stream)
+                                                  : launch_prefill_tc<false, false, true>(p, kmap, vmap, stream);
     return p.sinks > 0 ? launch_prefill_tc<false, true>(p, kmap, vmap, stream)
                        : launch_prefill_tc<false, false>(p, kmap, vmap, stream);
 }
@@ -1822,7 +2017,9 @@ cudaError_t launch_prefill_bf16(const PrefillParams &p, const CUtensorMap &kmap,
 cudaError_t launch_prefill_fp8(const PrefillParams &p, cudaStream_t stream)
 {
     const CUtensorMap none{};  // the FP8 producers read the pools by bulk copy
-    if (p.tree != nullptr) return launch_prefill_tc<true, false, true>(p, none, none, stream);
+    if (p.tree != nullptr)
+        return p.max_q_len <= pf::kRows / p.group ? launch_prefill_tc<true, false, true, true>(p, none, none, stream)
+                                                  : launch_prefill_tc<true, false, true>(p, none, none, stream);
     return p.sinks > 0 ? launch_prefill_tc<true, true>(p, none, none, stream)
                        : launch_prefill_tc<true, false>(p, none, none, stream);
 }

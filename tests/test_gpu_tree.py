@@ -110,7 +110,9 @@ def test_attention(pkv, kind, hq, hkv, D, ctx, nodes, window):
 
 @pytest.mark.parametrize("kind,hq,hkv,D", [("bf16", 16, 8, 128), ("bf16", 32, 8, 128), ("fp8", 32, 8, 128), ("f32", 4, 2, 64)])
 def test_chain_is_the_chunk(pkv, kind, hq, hkv, D):
-    """A tree without branches is the causal chunk, bit for bit where the kernel is the same."""
+    """A tree without branches is the causal chunk: bit for bit where the key range is cut alike (the decode
+    kernel's plan, the f32 kernel's whole range); the tensor-core kernel levels a tree's key range over the
+    GPU and cuts a chunk's evenly, and each is held to the exact result."""
     nodes = [7, 1, 5] if hq == 16 else [40, 1, 13]
     chain = np.concatenate([[(1 << (i + 1)) - 1 for i in range(c)] for c in nodes])
     c = Case(pkv, kind, hq, hkv, D, [130, 40, 900], nodes, masks=chain, seed=3)
@@ -118,7 +120,10 @@ def test_chain_is_the_chunk(pkv, kind, hq, hkv, D):
     c.check(out)
     ref = pkv.paged_prefill_chunk_attention(c.args[0], c.args[1], c.kp, c.vp, c.d_tables, c.d_lens, max(nodes), 0,
                                             c.scale, k_scale=KS, v_scale=VS)
-    assert torch.equal(out, ref)
+    if kind == "f32" or max(nodes) * hq // hkv <= 16:
+        assert torch.equal(out, ref)
+    else:
+        c.check(ref)
 
 
 @pytest.mark.parametrize("hq,D,nodes", [(8, 128, 2), (32, 128, 20), (8, 64, 20)])
