@@ -1253,6 +1253,8 @@ pkv_status commit_call(CommitParams &p, void *const *base, const int32_t *num_bl
         p.base[z] = base[z];
         p.num_blocks[z] = num_blocks[z];
     }
+    // a thread's index over the tensors' rows has 32 bits
+    if (static_cast<int64_t>(p.heads) * p.row_vecs > (1 << 30) / n_tensors) return PKV_ERR_UNSUPPORTED;
     return launch_commit(p, fp8, num_sms_current(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PKV_OK
                : PKV_ERR_CUDA;

@@ -87,7 +87,6 @@ struct CommitParams {
     int32_t batch, width, max_path, block_size, heads;
     int32_t row_vecs;   // 16-byte vectors of one head's row (FP8: of one head's codes)
     int32_t n_tensors;
-    int32_t tensors_per_cta;  // set by the launch
     void *base[kCommitTensors];
     int32_t num_blocks[kCommitTensors];
 };

@@ -285,7 +285,7 @@ __device__ __forceinline__ bool tree_next(const PrefillParams &p, int qpc, SegWa
 
 // A tree's run, its first segment, the run's tiles (every thread of the CTA), and
 // the record of the item that it begins and does not end.
-constexpr int32_t kTreeLeast = 8, kTreeLevel = 16, kTreeOver = 6;
+constexpr int32_t kTreeLeast = 4, kTreeLevel = 16, kTreeOver = 6;
 __device__ __forceinline__ bool tree_first(const PrefillParams &p, int qpc, int64_t *sm, SegWalk &sw, Seg &sg,
                                            int32_t &tiles)
 {
