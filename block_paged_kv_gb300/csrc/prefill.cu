@@ -54,18 +54,21 @@ constexpr int kBlocks = kKeys / 16;
 constexpr int kQBytes = kRows * 2 * 128;  // one query tile: two 64-dim swizzled regions
 constexpr int kKVRegion = kKeys * 128;    // 8 KiB: one 64-dim half of a K/V tile
 constexpr int kTileBytes = 2 * kKVRegion; // 16 KiB: a K or a V tile
-constexpr int kStages = 4;                // K ring and V ring depth
 constexpr int kQOff = 0;
-constexpr int kKOff = kQOff + kQTiles * kQBytes;
-constexpr int kVOff = kKOff + kStages * kTileBytes;
 // FP8 pools: the producers stage each tile's E4M3 bytes (4 blocks x 2 KiB)
 // by bulk copy, two tiles deep, and widen them into the ring
 constexpr int kF8BlockBytes = 16 * kD;                 // one (block, kv head) E4M3 tile
 constexpr int kF8StageTile = kBlocks * kF8BlockBytes;  // 8 KiB
 constexpr int kSoftmaxWarps = 8;  // 4-7 softmax of query tile A, 8-11 of tile B
 constexpr int kSegBytes = 160;    // a softmax warp's segment walk, current and next segment
-template <bool kF8>
+// kAlt (both warpgroups on one query tile, alternate key tiles): one query tile, and
+// for bf16 pools rings of 6, whose third tile ahead covers the loads' latency (32 rows
+// of 1024 to 8192 keys x 16 drafts, 32/8 heads: 122.8 us with 4, 118.6 with 6)
+template <bool kF8, bool kAlt = false>
 struct Layout {
+    static constexpr int kStages = kAlt && !kF8 ? 6 : 4;  // K ring and V ring depth
+    static constexpr int kKOff = kQOff + (kAlt ? 1 : kQTiles) * kQBytes;
+    static constexpr int kVOff = kKOff + kStages * kTileBytes;
     static constexpr int kStagingOff = kVOff + kStages * kTileBytes;
     static constexpr int kStagingBytes = kF8 ? 2 * 2 * kF8StageTile : 0;  // K and V, 2 deep
     static constexpr int kBarOff = kStagingOff + kStagingBytes;
@@ -76,7 +79,7 @@ struct Layout {
     static constexpr int kNumBars = 4 * kStages + 4 + 4 + 2 + 2 + 2 + 2 + 2 + (kF8 ? 8 : 0);
     // kmask[kStages], FP8: smask[K/V][2] (blocks loaded of each staging buffer)
     static constexpr int kMaskOff = kBarOff + kNumBars * 8;
-    static constexpr int kTmemOff = kMaskOff + (kStages + 4) * 4;
+    static constexpr int kTmemOff = kMaskOff + ((kStages + 4) * 4 + 15) / 16 * 16;
     static constexpr int kSegOff = kTmemOff + 16;  // per softmax warp: its segment walk
     static constexpr int kBytes = kSegOff + kSoftmaxWarps * kSegBytes;
     static constexpr int kLaunchBytes = kBytes + 1024;
@@ -456,7 +459,7 @@ __device__ __forceinline__ void come_late(uint32_t ns)
 // kSink: a window with sink tokens (their tiles first, then the window's)
 // kTree: the queries are a drafted tree's, masked by their ancestors
 // kAlt: every chunk fills one query tile at most; tile B's warps then take the
-// same rows (their own copy of the queries, S and O) and the two alternate over
+// same rows (their own S and O) and the two alternate over
 // the key tiles, joined in the epilogue
 template <bool kF8, bool kSink, bool kTree, bool kAlt>
 __global__ void __launch_bounds__(pf::kThreads, 1)
@@ -464,13 +467,14 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                    const PrefillParams p)
 {
     using namespace pf;
-    using L = Layout<kF8>;
+    using L = Layout<kF8, kAlt>;
+    constexpr int kStages = L::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *q_s = smem + kQOff;
-    uint8_t *k_s = smem + kKOff;
-    uint8_t *v_s = smem + kVOff;
+    uint8_t *k_s = smem + L::kKOff;
+    uint8_t *v_s = smem + L::kVOff;
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBarOff);
     uint64_t *k_full = bars, *k_empty = bars + kStages, *v_full = bars + 2 * kStages,
              *v_empty = bars + 3 * kStages;
@@ -552,8 +556,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         mbar_init(&o_done[0], 1);
         mbar_init(&o_done[1], 1);
         mbar_init(&q_full[0], kSoftmaxWarps / kQTiles);
-        // kAlt: tile A's warps too, once they have read the last segment's O of tile B
-        mbar_init(&q_full[1], kAlt ? kSoftmaxWarps : kSoftmaxWarps / kQTiles);
+        // (kAlt: both by tile A's warps, once they have read the last segment's O of
+        // both tiles and staged the queries)
+        mbar_init(&q_full[1], kSoftmaxWarps / kQTiles);
         mbar_init(&sums[0], kSoftmaxWarps / kQTiles);
         if (kF8) {
             for (int i = 0; i < 4; ++i) mbar_init(&staged[i], 1);
@@ -722,7 +727,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         // Descriptors are built once; moving along K (or to the next 16 keys
         // of V) adds the byte offset / 16 to the start-address field, which
         // cannot carry out of it inside shared memory.
-        const uint64_t dq = tc::smem_desc(smem_u32(q_s + x * kQBytes), 16, 1024);
+        const uint64_t dq = tc::smem_desc(smem_u32(q_s + (kAlt ? 0 : x) * kQBytes), 16, 1024);
         const uint64_t dk = tc::smem_desc(smem_u32(k_s), 16, 1024);
         const uint64_t dv = kF8 ? tc::smem_desc(smem_u32(v_s), 16, 1024)
                                 : tc::smem_desc(smem_u32(v_s), kKVRegion, 1024);
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             : p.sk_ctas > 0 ? (seg0.whole && sk_whole_item(p, blockIdx.x) >= 0 ? seg0.ntile : 0) +
                                 sk_run_start(p, blockIdx.x + 1) - sk_run_start(p, blockIdx.x)
                           : seg0.ntile;
-        load_q_rows(seg0.w);  // while the producers' first copies are under way
+        if (!kAlt || x == 0) load_q_rows(seg0.w);  // while the producers' first copies are under way
         if constexpr (kF8) {
             for (int32_t Tk = kAlt ? x : 0; do_k && Tk < min(2 * kStep, T_total) && !abort; Tk += kStep)
                 if (!widen_k(Tk)) {
@@ -917,10 +922,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int32_t nst = kSink ? cs.w.nst : 0, gap = kSink ? cs.w.gap : 0;
         // the segment's query tile: staged (the first above), then handed to
         // the MMA-issue warp
-        if (k > 0) load_q_rows(cs.w);
+        if (k > 0 && (!kAlt || x == 0)) load_q_rows(cs.w);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[x]);
-        if (kAlt && x == 0 && lane == 0) mbar_arrive(&q_full[1]);
+        if (lane == 0 && (!kAlt || x == 0)) {
+            mbar_arrive(&q_full[x]);
+            if (kAlt) mbar_arrive(&q_full[1]);
+        }
         const bool valid_row = row < qpt * G && t < cs.w.nq;
         const int32_t qpos = cs.w.kv_hi - cs.w.nq + t;
         // kTree: positions below `first` hold the cached tokens, the drafts follow
@@ -1283,12 +1290,14 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     uint32_t r32[32];
                     load_o(c, r32);
                     const float vs = kF8 ? p.v_scale : 1.f;
+                    if (kTree && !valid_row) continue;  // (a tree's merge reads its rows alone)
 #pragma unroll
                     for (int v = 0; v < 8; ++v)
                         dst[(c * 8 + v) * 32] = make_float4(__uint_as_float(r32[4 * v]) * vs, __uint_as_float(r32[4 * v + 1]) * vs,
                                                             __uint_as_float(r32[4 * v + 2]) * vs, __uint_as_float(r32[4 * v + 3]) * vs);
                 }
-                reinterpret_cast<float2 *>(p.sk_ml)[own * 32 + lane] = make_float2(m_ref, l);
+                if (!kTree || valid_row)
+                    reinterpret_cast<float2 *>(p.sk_ml)[own * 32 + lane] = make_float2(m_ref, l);
                 if constexpr (!kTree) {
                 // the item's pieces: CTAs cf .. cl; per (query tile, warp) the
                 // warp whose piece completes last merges their 32 rows (no
@@ -1977,7 +1986,7 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
     const int64_t ctas = p.sk_ctas > 0 ? p.sk_ctas
                                        : static_cast<int64_t>(p.batch) * p.hkv * p.q_tiles * p.kv_splits;
     if (ctas == 0) return cudaSuccess;
-    constexpr int smem = pf::Layout<kF8>::kLaunchBytes;
+    constexpr int smem = pf::Layout<kF8, kAlt>::kLaunchBytes;
     cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink, kTree, kAlt>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
