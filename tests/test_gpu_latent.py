@@ -177,6 +177,104 @@ def test_device_reports(pkv):
         assert int(c.status.item()) == pkv.DEV_BAD_LEN
 
 
+def test_queries_bound(pkv):
+    """Rows whose chunk passes the queries that the call has are reported and left out."""
+    for kind, H, R, Dr in (("bf16", 16, 512, 64), ("f32", 4, 64, 16)):
+        c = Case(pkv, kind, H, R, Dr, [100, 30], [3, 4])
+        c.d_cu[2] = 9
+        out = torch.full((7, H, R), 7.0, dtype=c.act, device="cuda")
+        c.run(pkv, max_q=6, out=out)
+        assert int(c.status.item()) == pkv.DEV_BAD_LEN and (out[3:] == 7).all()
+        c.status.zero_()
+        c.lens, c.cu = c.lens[:1], c.cu[:2]
+        c.check(out[:3])
+
+
+@pytest.mark.parametrize("R,C", [(512, None), (256, [40, 3])])
+def test_wait_runs_out(pkv, R, C):
+    """The first load withheld, the limit a millisecond: the call returns with a timeout, the next one is clean."""
+    c = Case(pkv, "bf16", 16, R, 64, [300, 70], C)
+    c.run(pkv)
+    torch.cuda.synchronize()
+    pkv.set_wait_drill(1_000_000, pkv.DRILL_WITHHOLD_FIRST_LOAD)
+    try:
+        c.run(pkv)
+        torch.cuda.synchronize()
+    finally:
+        pkv.set_wait_drill()
+    assert int(c.status.item()) == pkv.DEV_TIMEOUT
+    c.status.zero_()
+    c.check(c.run(pkv))
+
+
+def test_two_graphs_one_workspace_and_calls_at_once(pkv):
+    """Captured calls that share a workspace, replayed in turn; calls on two streams with one each."""
+    a = Case(pkv, "bf16", 16, 512, 64, [900, 40, 333], seed=1)
+    b = Case(pkv, "bf16", 16, 512, 64, [20, 500], [64, 9], True, seed=2)
+    size = max(pkv.latent_workspace_size(3, 16, 512, 64, 16, 64, 1024), 1)
+    ws = [pkv.alloc_workspace(size, "cuda") for _ in range(2)]
+    want = [a.run(pkv), b.run(pkv)]
+    outs = [torch.empty_like(w) for w in want]
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for x in s:
+        x.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(s[0]):
+        for c, o in ((a, outs[0]), (b, outs[1])):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s[0]):
+                c.run(pkv, workspace=ws[0], out=o)
+            graphs.append(g)
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            for g in graphs:
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(s[i]):
+                c.run(pkv, workspace=ws[i], out=outs[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_far_pages(pkv):
+    """Pages past 2^32 elements: append, decode, a tree and the commit."""
+    R, Dr, H, nb = 512, 64, 16, 470_000                # 4.33e9 elements, 8.7 GB
+    pool = torch.empty(nb, 16, R + Dr, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.RandomState(0)
+    L, C = 120, 20
+    table = np.concatenate([rng.choice(1000, 4, replace=False), nb - 1 - rng.choice(1000, 4, replace=False)])
+    pos = np.arange(L)
+    slots = torch.from_numpy((table[pos // 16] * 16 + pos % 16).astype(np.int32)).cuda()
+    rope = pkv.make_rope(10000.0 ** (-2.0 * np.arange(Dr // 2) / Dr))
+    c, k = [as_type(rng.randn(L, n), "bf16").cuda() for n in (R, Dr)]
+    pkv.paged_latent_append(pool, slots, c, k, torch.zeros(L, dtype=torch.int32, device="cuda"), rope)
+    rows = torch.cat([c, k], 1)                        # (position 0: not turned)
+    assert torch.equal(pool.view(-1, R + Dr)[slots.long()], rows)
+    to = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    t, lens, cu = to(table[None].astype(np.int32)), to(np.array([L], dtype=np.int32)), to(np.array([0, C], dtype=np.int32))
+    masks = pkv.tree_masks_host(random_tree(rng, C), [0, C])
+    q = as_type(rng.randn(C, H, R + Dr) * 0.2, "bf16")
+    out = pkv.paged_latent_attention(q.cuda(), pool, R, t, lens, 0.125, cu_q_lens=cu, max_q_len=C, tree_masks=to(masks))
+    one = pkv.paged_latent_attention(q[:1].cuda(), pool, R, t, lens, 0.125)
+    r64 = f64(rows)
+    for h in range(0, H, 5):
+        ref, mag, A = attend(f64(q)[:, h], r64, r64[:, :R], seen(L, C, masks), 0.125)
+        check(out[:, h], ref, mag, A, R + Dr, "bf16 weights", torch.bfloat16)
+        ref, mag, A = attend(f64(q)[:1, h], r64, r64[:, :R], seen(L, 1), 0.125)
+        check(one[:, h], ref, mag, A, R + Dr, "bf16 weights", torch.bfloat16)
+    path = np.array([[1, 4, 17]], dtype=np.int32)
+    new = pkv.paged_tree_commit(pkv.LatentPoolSet([pool]), t, lens, cu, to(path), to(np.array([3], dtype=np.int32)))
+    assert new.tolist() == [L - C + 3]
+    assert torch.equal(pool.view(-1, R + Dr)[slots.long()][L - C:L - C + 3], rows[[L - C + i for i in path[0]]])
+
+
 def test_refusals(pkv):
     c = Case(pkv, "bf16", 16, 512, 64, [40], [5], True)
     for kw, code in ((dict(max_q=65), pkv.PKV_ERR_INVALID_ARG),

@@ -180,6 +180,99 @@ def test_device_reports(pkv):
         assert int(c.status.item()) == pkv.DEV_BAD_LEN
 
 
+@pytest.mark.parametrize("kind,hq,nodes", [("bf16", 32, 20), ("bf16", 32, 50), ("fp8", 32, 20), ("fp8", 32, 50), ("bf16", 8, 2)])
+def test_many_rows(pkv, kind, hq, nodes):
+    """More rows than one pass of a run's plan looks at, empty ones among them; few long ones, cut many times."""
+    rng = np.random.RandomState(nodes)
+    B = 60
+    ctx, C = rng.randint(0, 90, B), rng.randint(0, nodes + 1, B)
+    ctx[3], C[5], C[6] = 1500, nodes, 0
+    c = Case(pkv, kind, hq, 8, 128, ctx, C, seed=4)
+    c.check(c.run(pkv))
+    c = Case(pkv, kind, hq, 8, 128, [7000], [nodes], seed=5)
+    c.check(c.run(pkv))
+
+
+@pytest.mark.parametrize("kind,nodes", [("bf16", 2), ("bf16", 20), ("bf16", 50), ("fp8", 20), ("fp8", 50)])
+def test_wait_runs_out(pkv, kind, nodes):
+    """The first load withheld, the limit a millisecond: the call returns with a timeout, the next one is clean."""
+    c = Case(pkv, kind, 32, 8, 128, [300, 70], [nodes, 1])
+    pkv.set_wait_drill(1_000_000, pkv.DRILL_WITHHOLD_FIRST_LOAD)
+    try:
+        c.run(pkv)
+        torch.cuda.synchronize()
+    finally:
+        pkv.set_wait_drill()
+    assert int(c.status.item()) == pkv.DEV_TIMEOUT
+    c.status.zero_()
+    c.check(c.run(pkv))
+
+
+@pytest.mark.parametrize("nodes", [20, 50])
+def test_late_warps(pkv, nodes):
+    """Softmax warps that come late to an output, over runs of several pieces."""
+    c = Case(pkv, "bf16", 32, 8, 128, [700, 70, 0, 300] * 6, [nodes, 1, 7, 13] * 6)
+    want = c.run(pkv)
+    pkv.set_wait_drill(100_000_000, pkv.DRILL_LATE_CONSUMERS)
+    try:
+        got = c.run(pkv)
+        torch.cuda.synchronize()
+    finally:
+        pkv.set_wait_drill()
+    assert torch.equal(got, want)
+    c.check(got)
+
+
+def test_two_graphs_one_workspace(pkv):
+    a, b = [Case(pkv, "bf16", 32, 8, 128, ctx, n, seed=i) for i, (ctx, n) in enumerate([([900, 40], [20, 3]), ([300], [60])])]
+    ws = pkv.alloc_workspace(pkv.tree_workspace_size(2, 32, 8, 128, 16, 64, 1024), "cuda")
+    want = [a.run(pkv), b.run(pkv)]
+    outs = [torch.empty_like(w) for w in want]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graphs = []
+        for c, o in ((a, outs[0]), (b, outs[1])):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                c.run(pkv, workspace=ws, out=o)
+            graphs.append(g)
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            for g in graphs:
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_far_pages(pkv):
+    """Pages past 2^32 elements of a pool: attention and the commit."""
+    nb, hkv, D, C, L = 270_000, 8, 128, 20, 100        # 4.42e9 elements, 8.8 GB a pool
+    rng = np.random.RandomState(0)
+    kp, vp = [torch.empty(nb, hkv, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    table = np.concatenate([rng.choice(1000, 3, replace=False), nb - 1 - rng.choice(1000, 4, replace=False)])
+    k, v = [as_type(rng.randn(L, hkv, D), "bf16") for _ in range(2)]
+    for pool, x in ((kp, k), (vp, v)):
+        for p in range(L):
+            pool[table[p // 16], :, p % 16] = x[p].cuda()
+    to = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    t, lens, cu = to(table[None].astype(np.int32)), to(np.array([L], dtype=np.int32)), to(np.array([0, C], dtype=np.int32))
+    masks = pkv.tree_masks_host(random_tree(rng, C), [0, C])
+    q = as_type(rng.randn(C, 32, D), "bf16")
+    out = pkv.paged_tree_attention(q.cuda(), cu, to(masks), kp, vp, t, lens, C, 0, 0.1)
+    for h in range(0, 32, 7):
+        ref, mag, A = attend(f64(q)[:, h], f64(k)[:, h // 4], f64(v)[:, h // 4], seen(L, C, masks), 0.1)
+        check(out[:, h], ref, mag, A, D, "bf16", torch.bfloat16)
+    path = np.array([[1, 4, 17]], dtype=np.int32)
+    new = pkv.paged_tree_commit(pkv.PoolSet([(kp, vp)]), t, lens, cu, to(path), to(np.array([3], dtype=np.int32)))
+    n = L - C
+    assert new.tolist() == [n + 3]
+    for pool, x in ((kp, k), (vp, v)):
+        for i, a in enumerate(path[0]):
+            assert torch.equal(pool[table[(n + i) // 16], :, (n + i) % 16].cpu(), x[n + a])
+
+
 def test_refusals(pkv):
     c = Case(pkv, "bf16", 16, 8, 128, [40], [5])
     q, cu, m = c.args

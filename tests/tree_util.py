@@ -5,7 +5,14 @@ errors of its weights.  A score of W products is off by at most
 W 2^-23 sum |q k| scale (fp32 sums, each step rounded or cut), a weight then
 relatively by twice that (its own and the normaliser's), plus the weight's own
 rounding and the exponential's (`weight`): 2^-16 where weights are carried in two
-bf16 terms or fp32, 2^-10 where they are one f16 term (2^-11, twice)."""
+bf16 terms or fp32, 2^-10 where they are one f16 term (2^-11, twice).
+
+Weights that are one bf16 term, with the sum taken over the rounded ones ("bf16
+weights"): with p the exact weights, L their sum, |d| <= e = 2^-8 each one's rounding
+and d' = sum p d / L, so |d'| <= e, the output differs by
+    |(sum p (1 + d) v) / (L (1 + d')) - sum p v / L| = |sum p d v - d' sum p v| / (L (1 + d'))
+                                                    <= 2 e / (1 - e) * sum p |v| / L,
+which is 2^-7 (1 + 2^-8 + ..) <= 2^-7 + 2^-14 - 2^-16, leaving 2^-16 for the exponential."""
 from __future__ import annotations
 
 import numpy as np
