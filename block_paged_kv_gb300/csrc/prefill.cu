@@ -62,8 +62,8 @@ constexpr int kF8StageTile = kBlocks * kF8BlockBytes;  // 8 KiB
 constexpr int kSoftmaxWarps = 8;  // 4-7 softmax of query tile A, 8-11 of tile B
 constexpr int kSegBytes = 160;    // a softmax warp's segment walk, current and next segment
 // kAlt (both warpgroups on one query tile, alternate key tiles): one query tile, and
-// for bf16 pools rings of 6, whose third tile ahead covers the loads' latency (32 rows
-// of 1024 to 8192 keys x 16 drafts, 32/8 heads: 122.8 us with 4, 118.6 with 6)
+// for bf16 pools rings of 6 in its place (32 rows of 1024 to 8192 keys x 16 drafts, 32/8
+// heads: 112.4 us with 4, 111.2 with 6)
 template <bool kF8, bool kAlt = false>
 struct Layout {
     static constexpr int kStages = kAlt && !kF8 ? 6 : 4;  // K ring and V ring depth
@@ -189,6 +189,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 //     tiles, none of them dealt whole, the pieces joined by prefill_tree_merge_kernel:
 //     its items are few and long, a row's keys read by one of them (bf16, 32/8 heads,
 //     4 rows of 8000 keys x 16 drafts: 56.6 us under the schedule above, 39.5 here).
+//     An item counts kTreeOver tiles more than it has where runs are long: with 0 in
+//     place of 6, 32 rows x 16 drafts 133.7 us against 122.8, with 10, 124.0; runs of
+//     fewer than kTreeLeast tiles cost more than they bring (1 row of 1000 keys: 14.2 us
+//     with 4, 17.3 with 8, 23.2 with 16).
 // ---------------------------------------------------------------------------
 struct Seg {
     PrefillRowInfo w;
@@ -453,6 +457,15 @@ __device__ __forceinline__ void come_late(uint32_t ns)
         : "memory");
 }
 
+// K/V is re-read by the row's other CTAs; a tree that one item covers reads it once
+// (32 rows x 16 drafts: 118.7 us with evict_last, 119.0 with evict_normal, 110.7 with
+// evict_first).
+template <bool kTree>
+__device__ __forceinline__ uint64_t kv_policy(const PrefillParams &p)
+{
+    return kTree && p.q_tiles == 1 ? l2_evict_first_policy() : l2_evict_last_policy();
+}
+
 // ---------------------------------------------------------------------------
 // bf16, tcgen05
 // ---------------------------------------------------------------------------
@@ -615,7 +628,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             // one 4-byte store.  Value columns of keys outside [kv_lo, kv_hi)
             // or of blocks not loaded are written as zeros (stale slots may
             // hold NaN codes).
-            const uint64_t policy = l2_evict_last_policy();  // re-read by the row's other CTAs
+            const uint64_t policy = kv_policy<kTree>(p);
             const uint8_t *pool = static_cast<const uint8_t *>(is_k ? p.k_pool : p.v_pool);
             uint8_t *stg = smem + L::kStagingOff + (is_k ? 0 : 2) * kF8StageTile;
             uint64_t *stg_bar = staged + (is_k ? 0 : 2);
@@ -673,7 +686,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             __syncwarp();
         } else {
             const CUtensorMap *map = is_k ? &kmap : &vmap;
-            const uint64_t policy = l2_evict_last_policy();  // re-read by the row's other CTAs
+            const uint64_t policy = kv_policy<kTree>(p);
             TileCursor<kSink, kTree> cur;
             cur.start(p, qpc, sw0, seg0);
             int32_t T = 0;
