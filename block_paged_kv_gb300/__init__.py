@@ -807,6 +807,10 @@ def tree_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_di
                                               max_q_len, max_seq_len, window))
 
 
+def _is_row(t, n: int) -> bool:
+    return t.ndim == 1 and t.numel() == n
+
+
 def _workspace_ok(workspace, gpu) -> bool:
     return workspace is None or (workspace.get_device() == gpu and workspace.is_contiguous())
 
@@ -834,10 +838,10 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
             q.dtype is (torch.float32 if pool.dtype == PKV_F32 else torch.bfloat16) and
             block_tables.dtype is i32 and block_tables.is_contiguous() and block_tables.get_device() == gpu and
             len(tshape) == 2 and seq_lens.dtype is i32 and seq_lens.is_contiguous() and
-            seq_lens.get_device() == gpu and seq_lens.shape == tshape[:1] and
+            seq_lens.get_device() == gpu and _is_row(seq_lens, tshape[0]) and
             cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
-            cu_q_lens.shape == (tshape[0] + 1,) and
-            tree_masks.dtype is torch.int64 and tree_masks.shape == qshape[:1] and tree_masks.is_contiguous() and
+            _is_row(cu_q_lens, tshape[0] + 1) and
+            tree_masks.dtype is torch.int64 and _is_row(tree_masks, qshape[0]) and tree_masks.is_contiguous() and
             tree_masks.get_device() == gpu and
             (out is None or (out.shape == qshape and out.dtype is q.dtype and out.is_contiguous() and
                              out.get_device() == gpu)) and
@@ -882,11 +886,10 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
     return out
 
 
-def _latent_pool(pool: torch.Tensor, latent_dim: int) -> _LatentPool:
-    shape, dt = pool.shape, pool.dtype
-    if not (len(shape) == 3 and pool.is_cuda and pool.is_contiguous() and 0 < latent_dim < shape[2]):
+def _latent_pool(pool: torch.Tensor, latent_dim: int, shape, dt, gpu: int) -> _LatentPool:
+    if not (len(shape) == 3 and gpu >= 0 and pool.is_contiguous() and 0 < latent_dim < shape[2]):
         _require(len(shape) == 3, "a latent pool is [num_blocks, block_size, latent_dim + rope_dim]")
-        _require(pool.is_cuda, "pools live on the GPU")
+        _require(gpu >= 0, "pools live on the GPU")
         _require(pool.is_contiguous(), "pools are contiguous")
         raise ValueError("latent_dim lies below the pool's row")
     return _LatentPool(pool.data_ptr(), shape[0], shape[1], latent_dim, shape[2] - latent_dim,
@@ -903,7 +906,7 @@ class LatentPoolSet:
         _require(len(self.pools) > 0, "at least one pool")
         self.device, self.n, self.gpu = self.pools[0].device, len(self.pools), self.pools[0].get_device()
         # rows move whole: where the latent ends plays no part
-        self._c = (_LatentPool * self.n)(*[_latent_pool(t, t.shape[-1] - 1) for t in self.pools])
+        self._c = (_LatentPool * self.n)(*[_latent_pool(t, t.shape[-1] - 1, t.shape, t.dtype, t.get_device()) for t in self.pools])
         f = self.pools[0]
         for t in self.pools:
             _require(t.device == self.device, "every pool on one GPU")
@@ -929,9 +932,9 @@ def paged_tree_commit(pools, block_tables: torch.Tensor, seq_lens: torch.Tensor,
             cu_q_lens.get_device() == gpu and path.get_device() == gpu and path_lens.get_device() == gpu and
             block_tables.is_contiguous() and seq_lens.is_contiguous() and cu_q_lens.is_contiguous() and
             path.is_contiguous() and path_lens.is_contiguous() and len(tshape) == 2 and len(pshape) == 2 and
-            pshape[0] == tshape[0] and seq_lens.shape == tshape[:1] and path_lens.shape == tshape[:1] and
-            cu_q_lens.shape == (tshape[0] + 1,) and
-            (new_seq_lens is None or (new_seq_lens.dtype is i32 and new_seq_lens.shape == tshape[:1] and
+            pshape[0] == tshape[0] and _is_row(seq_lens, tshape[0]) and _is_row(path_lens, tshape[0]) and
+            _is_row(cu_q_lens, tshape[0] + 1) and
+            (new_seq_lens is None or (new_seq_lens.dtype is i32 and _is_row(new_seq_lens, tshape[0]) and
                                       new_seq_lens.is_contiguous() and new_seq_lens.get_device() == gpu)) and
             _status_word(status, gpu)):
         dev = pools.device
@@ -996,19 +999,21 @@ def paged_latent_append(pool: torch.Tensor, slot_mapping: torch.Tensor, latent_n
     (``q_rope_out``, which may be ``q_rope`` or the tail of the absorbed queries).
     Token rows may be cut from wider tensors.  ``positions`` as for
     ``paged_kv_append_rope``; the descriptor's rotary_dim is Dr."""
-    shape, dt, gpu, i32 = latent_new.shape, pool.dtype, pool.get_device(), torch.int32
+    shape, dt, gpu, i32, rows = latent_new.shape, pool.dtype, pool.get_device(), torch.int32, pool.shape
     T, axes, kshape, pshape = slot_mapping.numel(), rope.num_axes, k_rope_new.shape, positions.shape
-    ok = (len(shape) == 2 and shape[0] == T and len(kshape) == 2 and kshape[0] == T and pool.dim() == 3 and
-          shape[1] + kshape[1] == pool.shape[2] and slot_mapping.dtype is i32 and slot_mapping.ndim == 1 and
+    cs, ks, ps = latent_new.stride(), k_rope_new.stride(), positions.stride()
+    ok = (len(shape) == 2 and shape[0] == T and len(kshape) == 2 and kshape[0] == T and len(rows) == 3 and
+          shape[1] + kshape[1] == rows[2] and slot_mapping.dtype is i32 and slot_mapping.ndim == 1 and
           slot_mapping.is_contiguous() and slot_mapping.get_device() == gpu and
           latent_new.dtype is dt and k_rope_new.dtype is dt and latent_new.get_device() == gpu and
           k_rope_new.get_device() == gpu and
-          (T == 0 or ((latent_new.stride(1) == 1 or shape[1] == 1) and (k_rope_new.stride(1) == 1 or kshape[1] == 1))) and
+          (T == 0 or ((cs[1] == 1 or shape[1] == 1) and (ks[1] == 1 or kshape[1] == 1))) and
           positions.dtype is i32 and positions.get_device() == gpu and
-          (pshape == (axes, T) or (axes == 1 and pshape == (T,))) and (positions.stride(-1) == 1 or T <= 1) and
-          (norm_weight is None or (norm_weight.dtype is dt and norm_weight.shape == shape[1:] and
-                                   norm_weight.get_device() == gpu and norm_weight.is_contiguous())) and
-          _status_word(status, gpu))
+          (pshape[0] == T if axes == 1 and len(ps) == 1 else pshape == (axes, T)) and (ps[-1] == 1 or T <= 1) and
+          (norm_weight is None or (norm_weight.dtype is dt and norm_weight.ndim == 1 and
+                                   norm_weight.numel() == shape[1] and norm_weight.get_device() == gpu and
+                                   norm_weight.is_contiguous())) and
+          (status is None or _status_word(status, gpu)))
     H, qp, op, qs, qh, os_, oh = 0, None, None, 0, 0, 0, 0
     if ok:
         if q_rope is None:
@@ -1033,11 +1038,11 @@ def paged_latent_append(pool: torch.Tensor, slot_mapping: torch.Tensor, latent_n
         _latent_append_refuse(pool.device, dt, slot_mapping, latent_new, k_rope_new, positions, rope, q_rope,
                               q_rope_out, norm_weight, status, pool.shape[-1])
         raise ValueError("paged_latent_append: invalid arguments")
-    c = _latent_pool(pool, shape[1])
+    c = _latent_pool(pool, shape[1], rows, dt, gpu)
     args = (ctypes.byref(c), slot_mapping.data_ptr(), T, latent_new.data_ptr(),
-            latent_new.stride(0) if T > 1 else shape[1], k_rope_new.data_ptr(),
-            k_rope_new.stride(0) if T > 1 else kshape[1], None if norm_weight is None else norm_weight.data_ptr(),
-            norm_eps, qp, qs, qh, H, positions.data_ptr(), positions.stride(0) if axes > 1 else T,
+            cs[0] if T > 1 else shape[1], k_rope_new.data_ptr(),
+            ks[0] if T > 1 else kshape[1], None if norm_weight is None else norm_weight.data_ptr(),
+            norm_eps, qp, qs, qh, H, positions.data_ptr(), ps[0] if axes > 1 else T,
             ctypes.byref(rope._c), op, os_, oh, None if status is None else status.data_ptr(), _raw_stream(gpu))
     if _current_device() == gpu:
         code = _lib.paged_latent_append(*args)
@@ -1068,17 +1073,17 @@ def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int,
     One query per row (decode) without ``cu_q_lens``; with it [B+1] the last C
     positions of each row hold a chunk's queries, causally, or, with ``tree_masks``,
     a drafted tree's (as for ``paged_tree_attention``)."""
-    c = _latent_pool(pool, latent_dim)
-    gpu, i32, dt, qshape, tshape = pool.get_device(), torch.int32, pool.dtype, q.shape, block_tables.shape
-    if not (len(qshape) == 3 and qshape[2] == pool.shape[2] and q.is_contiguous() and q.get_device() == gpu and
+    gpu, i32, dt, qshape, tshape, rows = pool.get_device(), torch.int32, pool.dtype, q.shape, block_tables.shape, pool.shape
+    c = _latent_pool(pool, latent_dim, rows, dt, gpu)
+    if not (len(qshape) == 3 and qshape[2] == rows[2] and q.is_contiguous() and q.get_device() == gpu and
             q.dtype is dt and block_tables.dtype is i32 and block_tables.is_contiguous() and
             block_tables.get_device() == gpu and len(tshape) == 2 and seq_lens.dtype is i32 and
-            seq_lens.is_contiguous() and seq_lens.get_device() == gpu and seq_lens.shape == tshape[:1] and
+            seq_lens.is_contiguous() and seq_lens.get_device() == gpu and _is_row(seq_lens, tshape[0]) and
             (qshape[0] == tshape[0] and max_q_len == 1 if cu_q_lens is None else
              (cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
-              cu_q_lens.shape == (tshape[0] + 1,))) and
+              _is_row(cu_q_lens, tshape[0] + 1))) and
             (tree_masks is None or (cu_q_lens is not None and tree_masks.dtype is torch.int64 and
-                                    tree_masks.shape == qshape[:1] and tree_masks.is_contiguous() and
+                                    _is_row(tree_masks, qshape[0]) and tree_masks.is_contiguous() and
                                     tree_masks.get_device() == gpu)) and
             (out is None or (out.shape == (qshape[0], qshape[1], latent_dim) and out.dtype is dt and
                              out.is_contiguous() and out.get_device() == gpu)) and
