@@ -5,9 +5,9 @@
 // sums and products in fp32, one rounding to the row's type.
 //
 // Bound: HBM (every row read once and written once), launch latency for a decode
-// step (32 tokens of 16 heads: 3.1 us).  A CTA takes a few tokens: their sines and cosines go to shared memory
-// once and serve all heads; a warp normalises a token's latent, which it holds
-// in registers between the sum and the product.
+// step (32 tokens of 16 heads: 3.1 us).  A CTA takes a few tokens: their sines and
+// cosines go to shared memory once and serve all heads; a warp normalises a token's
+// latent, which it holds in registers between the sum and the product.
 #include <algorithm>
 
 #include "pkv_device.cuh"

@@ -4,7 +4,8 @@
 //   s = scale q . [c | k],  out = softmax(s) c
 // with one pass over the rows (running maximum and sum; the weighted values in
 // registers, a thread 1/16 of a pair's dims).  Bound: shared-memory reads of the
-// products' operands.
+// products' operands: 8 rows of 2048 x 16 heads 73 us in f32 (512 + 64 dims, 0.5 TB/s),
+// 43 in bf16 (128 + 32 dims); 2 chunks of 64 in f32 762.
 #include "latent_common.cuh"
 
 namespace pkv {

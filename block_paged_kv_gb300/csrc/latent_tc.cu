@@ -13,8 +13,9 @@
 // tile through distributed shared memory (which carries about 21 bytes a cycle
 // between two SMs here: 800 cycles), so that neither waits for the other within a
 // tile.  An item's queries come through CTA 0's ring like two tiles more (read by
-// their pairs' threads, 32 rows an instruction, they took 9 us).  Each CTA loads what it multiplies, CTA 0 whole rows, CTA 1 their latent
-// part a tile or two later, out of L2.
+// their pairs' threads, 32 rows an instruction, they took 9 us).  Each CTA loads what
+// it multiplies, CTA 0 whole rows, CTA 1 their latent part a tile or two later, out of
+// L2.
 //   both:  warps 0, 2, 3 producers (one issuing thread brings 21 to 25 bytes a cycle
 //     whatever its boxes' size, three of them 60), a box of 8 keys each;
 //   CTA 0: warp 1 issues S = Q K^T from one lane (Q in tensor memory, three S
@@ -29,15 +30,17 @@
 // of a 3100-cycle tile.)
 //
 // P enters P.V as one bf16 term, and the sums are those of the rounded weights, so
-// that a rounding moves a weight against the others but not their sum: the result
-// is off by 2^-9 of its size beside its own rounding of as much (2-norm against 64
-// bits 0.0023; 0.0017 with a second term, which would double CTA 1's products to
-// 2048 cycles a tile).
+// that a rounding moves a weight against the others but not their sum (2-norm against
+// 64 bits 0.0019 to 0.0021; 0.0017, the output's own rounding, with a second term, which
+// would double CTA 1's products to 2048 cycles a tile).
 //
 // Bound: a 64-key tile of 128 pairs takes 36 N=64 products (32 cycles each) on one
 // SM beside 8 N=256 ones (128 cycles) on the other, 1152 cycles, and its 72 KB at
 // 1/76 of the HBM copy rate 0.82 us, 1600 cycles: HBM, or the tensor cores where the
-// rows come from L2 (chunks).
+// rows come from L2 (chunks).  Measured: 2 chunks of 512 x 16 heads 131.8 us (tensor
+// pipe 50 % busy, L2 hits 92 %), decode of 32 rows x 128 heads 57.5 us (186 MB from HBM,
+// 3.4 TB/s; tensor pipe 33 %), of 4 rows x 16 heads 16.9 us, launches and one chain of
+// dependent steps.
 #include <algorithm>
 
 #include "latent_common.cuh"
@@ -60,8 +63,12 @@ constexpr int kMasks = 16;                // tiles between a producer and the so
 constexpr int kPBytes = kRows * kKeys * 2;
 constexpr float kRescaleLog2 = 8.f;       // O is rescaled only when the max grows past 2^8
 constexpr uint32_t kTmemCols = 512;
-constexpr int32_t kLeastTiles = 2;        // of a worker's run
-// A piece's cost beside its tiles, in tiles, where the runs are long enough to be levelled by it
+// Tiles of a worker's run, at least: 4 rows x 16 heads 16.9 us with 2, 19.4 with 1, 17.7
+// with 4.
+constexpr int32_t kLeastTiles = 2;
+// A piece's cost beside its tiles, in tiles, where the runs are long enough to be
+// levelled by it: 16 trees of 1 to 64 drafts 95.5 us with 6, 97.7 with 4, 103.9 with 2,
+// 97.2 with 10 (chunks 131.8, 134.2, 132.9, 132.9).
 constexpr int32_t kItemCost = 6, kLevelTiles = 8;
 template <int NR>  // 64-dim regions of the latent
 struct Layout {

@@ -34,7 +34,8 @@
 // items' tiles that levels the CTAs, cut pieces merged in the kernel).  A short chunk
 // fills tile A only (tile B's warps stay idle, warps whose rows hold no query
 // skip the softmax work); on a grid too small for the GPU its key range is
-// cut into runs whose fp32 partials prefill_merge_kernel merges.
+// cut into runs whose fp32 partials prefill_merge_kernel merges.  Drafted trees: a
+// levelled run of the items' tiles a CTA, the pieces joined by prefill_tree_merge_kernel.
 // f32 kernel: CUDA cores, the same work split with 16 (query, head) pairs per
 // CTA, for the fp32 pools.
 #include <algorithm>
@@ -472,8 +473,9 @@ __device__ __forceinline__ uint64_t kv_policy(const PrefillParams &p)
 // kSink: a window with sink tokens (their tiles first, then the window's)
 // kTree: the queries are a drafted tree's, masked by their ancestors
 // kAlt: every chunk fills one query tile at most; tile B's warps then take the
-// same rows (their own S and O) and the two alternate over
-// the key tiles, joined in the epilogue
+// same rows (their own S and O) and the two alternate over the key tiles, joined in
+// the epilogue: a tile's chain (scores, softmax, products) has two tiles' time.  32 rows
+// x 16 drafts 111 us, 142 without (32 drafts 133 and 148; FP8 132 and 167, 153 and 191)
 template <bool kF8, bool kSink, bool kTree, bool kAlt>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,

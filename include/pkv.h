@@ -494,7 +494,8 @@ pkv_status pkv_tree_masks_host(const int32_t *parents, const int32_t *cu_q_lens,
  * A path that breaks these rules sets PKV_DEV_BAD_PATH: nothing of its row is
  * moved, and its new length is n.  A token whose page is missing is skipped
  * (PKV_DEV_BAD_BLOCK).  The drafts' pages belong to one row each.  Rows of a head
- * are a multiple of 16 bytes, else PKV_ERR_UNSUPPORTED.
+ * are a multiple of 16 bytes, and those of all heads and of the pools of one launch at
+ * most 16 GB, else PKV_ERR_UNSUPPORTED.
  */
 pkv_status paged_tree_commit(const pkv_pool *pools, int32_t n_pools, const int32_t *block_tables,
                              int32_t max_blocks_per_seq, const int32_t *seq_lens,
@@ -561,7 +562,12 @@ pkv_status paged_latent_append(const pkv_latent_pool *pool, const int32_t *slot_
  *   workspace: device, >= paged_latent_workspace_size(...) bytes, 256-byte aligned
  * Types are the pool's.  Rows that no query of a row attends may hold anything; the
  * rows of a chunk or tree are finite.  Built: latent_dim a multiple of 16 up to 512,
- * rope_dim a multiple of 16 up to 128, any number of heads, block_size up to 64.
+ * rope_dim a multiple of 16 up to 128, any number of heads, block_size up to 64; bf16
+ * pools of latent_dim 256 or 512, rope_dim 64 and block_size 16, 32 or 64 run on the
+ * tensor cores, the others on CUDA cores.  Scores, maxima and sums are fp32; the
+ * tensor-core kernel's weights enter their product with the latents as one bf16 term
+ * each (half a step: 2^-8 of the weight) and are summed as rounded, so that an output
+ * is within 2^-7 sum p |c| beside its own rounding; the CUDA-core kernel's are fp32.
  */
 size_t paged_latent_workspace_size(int32_t batch, int32_t num_q_heads, int32_t latent_dim,
                                    int32_t rope_dim, int32_t block_size, int32_t max_q_len,

@@ -61,6 +61,8 @@ def test_refused_before_launch(pkv):
     assert commit(n=0) == bad and commit(mp=0) == bad and commit(mp=65) == bad and commit(new=16) == bad and commit(new=None) == bad
     odd = pkv._Pool(16, 16, 4, 16, 2, 12, pkv.PKV_BF16, 0.0, 0.0)
     assert commit(pool=odd) == pkv.PKV_ERR_UNSUPPORTED
+    wide = pkv._Pool(16, 16, 4, 16, 1 << 26, 128, pkv.PKV_BF16, 0.0, 0.0)   # a token's rows past 16 GB
+    assert commit(pool=wide) == pkv.PKV_ERR_UNSUPPORTED
     lp = pkv._LatentPool(16, 4, 16, 512, 64, pkv.PKV_BF16)
     att = lambda **k: lib.paged_latent_attention(  # noqa: E731
         16, k.get("nq", 4), k.get("cu", 16), k.get("m"), k.get("h", 4), P(k.get("pool", lp)), 16, 8, 16, 1, k.get("mq", 4), 64,
