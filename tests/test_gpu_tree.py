@@ -92,6 +92,8 @@ CASES = [
     ("bf16", 8, 1, 256, [129, 40], [2, 7], 0),
     ("bf16", 8, 1, 256, [900], [64], 100),
     ("bf16", 6, 2, 64, [77], [20], 0),
+    ("bf16", 6, 2, 128, [77, 300], [20, 64], 0),
+    ("fp8", 12, 4, 128, [77, 300], [5, 31], 70),
     ("fp8", 16, 4, 128, [100, 1500, 0], [4, 2, 3], 0),
     ("fp8", 16, 4, 128, [100, 1500, 0], [64, 1, 30], 0),
     ("fp8", 16, 4, 128, [5000, 900], [30, 64], 1000),
@@ -385,6 +387,25 @@ def test_commit_reports(pkv):
     status.zero_()
     new = pkv.paged_tree_commit(pkv.PoolSet([(k, v)]), to(tables), to([40, 3, -1, 20, 20, 30]), to(cu), to(path), to([1] * 6), status=status)
     assert int(status.item()) & pkv.DEV_BAD_LEN
+
+
+def test_commit_of_very_many_rows(pkv):
+    """More rows than a grid's second dimension has."""
+    B = 66_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v = [torch.randn(B, 1, 16, 64, generator=g, device="cuda").bfloat16() for _ in range(2)]
+    want = [x.clone() for x in (k, v)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    rows = torch.arange(B, **i32)
+    move = torch.randint(0, 8, (B,), generator=g, device="cuda")       # draft of 8 accepted, behind 5 tokens
+    tables = rows.flip(0)[:, None].contiguous()
+    new = pkv.paged_tree_commit(pkv.PoolSet([(k, v)]), tables, torch.full((B,), 13, **i32), torch.arange(B + 1, **i32) * 8,
+                                move[:, None].int().contiguous(), torch.ones(B, **i32))
+    assert (new == 6).all()
+    for x, w in zip((k, v), want):
+        page = tables[:, 0].long()
+        w[page, :, 5] = w[page, :, 5 + move]
+        assert torch.equal(x, w)
 
 
 def test_commit_refusals(pkv):
