@@ -978,11 +978,8 @@ static cudaError_t launch_split(const DecodeParams &p, const CUtensorMap &kmap,
     if (ctas == 0) return cudaSuccess;
     auto kern = decode_split_kernel<D, kMQ, kF8, NQ, kSink, kTree>;
     const int smem = KvSmem<D, kF8, NQ>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
     // the largest shared-memory carveout, so that kCtasPerSm CTAs are resident per SM
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
+    cudaError_t err = kernel_smem<decode_split_kernel<D, kMQ, kF8, NQ, kSink, kTree>>(smem, true);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_DECODE_SPLIT, stream);
     err = launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(kDecodeWarps * 32), smem,

@@ -157,8 +157,7 @@ template <typename T>
 static cudaError_t launch(const LatentParams &p, cudaStream_t stream)
 {
     const size_t smem = static_cast<size_t>(2) * ls::kRows * (p.latent + p.rope + 4) * sizeof(float);
-    cudaError_t err = cudaFuncSetAttribute(latent_simple_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           100 * 1024);
+    cudaError_t err = kernel_smem<latent_simple_kernel<T>>(100 * 1024);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_LATENT, stream);
     err = launch_pdl(latent_simple_kernel<T>, dim3(static_cast<unsigned>(p.workers)), dim3(ls::kThreads), smem, stream, p);

@@ -734,7 +734,7 @@ static cudaError_t launch(const LatentParams &p, const CUtensorMap &map0, const 
                           cudaStream_t stream)
 {
     constexpr int smem = lt::Layout<NR>::kBytes;
-    cudaError_t err = cudaFuncSetAttribute(latent_tc_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t err = kernel_smem<latent_tc_kernel<NR>>(smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_LATENT, stream);
     err = launch_pdl(latent_tc_kernel<NR>, dim3(static_cast<unsigned>(2 * p.workers)), dim3(lt::kThreads), smem, stream, map0,

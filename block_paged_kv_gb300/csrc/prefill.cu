@@ -2002,8 +2002,7 @@ static cudaError_t launch_prefill_tc(const PrefillParams &p, const CUtensorMap &
                                        : static_cast<int64_t>(p.batch) * p.hkv * p.q_tiles * p.kv_splits;
     if (ctas == 0) return cudaSuccess;
     constexpr int smem = pf::Layout<kF8, kAlt>::kLaunchBytes;
-    cudaError_t err = cudaFuncSetAttribute(prefill_kernel<kF8, kSink, kTree, kAlt>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t err = kernel_smem<prefill_kernel<kF8, kSink, kTree, kAlt>>(smem);
     if (err != cudaSuccess) return err;
     prof_begin(PKV_KERNEL_PREFILL, stream);
     if (p.sk_ctas > 0 && !kTree)
