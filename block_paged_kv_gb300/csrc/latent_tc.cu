@@ -174,6 +174,25 @@ __device__ __forceinline__ bool lat_wait_cluster(uint64_t *bar, uint32_t parity,
     return ok;
 }
 
+// v[i] of lane b of a quad (four neighbouring lanes) becomes v[b] of its lane i.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4], int b)
+{
+    auto swap = [&](int i, int j, int d) {  // v[i] of the upper lane with v[j] of the lower one
+        const bool upper = (b & d) != 0;
+        uint4 x = upper ? v[i] : v[j];
+        x.x = __shfl_xor_sync(0xffffffffu, x.x, d);
+        x.y = __shfl_xor_sync(0xffffffffu, x.y, d);
+        x.z = __shfl_xor_sync(0xffffffffu, x.z, d);
+        x.w = __shfl_xor_sync(0xffffffffu, x.w, d);
+        if (upper) v[i] = x;
+        else v[j] = x;
+    };
+    swap(0, 1, 1);
+    swap(2, 3, 1);
+    swap(0, 2, 2);
+    swap(1, 3, 2);
+}
+
 // arrive on the mbarrier of every CTA in `mask` once the products issued so far have completed
 __device__ __forceinline__ void commit_to(uint64_t *bar, uint16_t mask)
 {
@@ -675,23 +694,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
             if (pc.whole) {
                 const float l = live ? fins[fb * kRows + row] : 0.f;
                 const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays NaN)
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) +
-                                                       latent_out_row(p, it, live ? row : 0) + half * (R / 2));
+                // a thread's 64 bytes change places with those of its three neighbours, so
+                // that a store covers 64 bytes of 8 pairs and not 16 of 32
+                const int first = 32 * w + (lane & ~3), b = lane & 3;
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + latent_out_row(p, it, first) +
+                                                       half * (R / 2)) + b;
 #pragma unroll 1
                 for (int c = 0; warp_live && c < R / 2; c += 32) {
                     uint32_t r[32];
                     tc::ld32(ox + c, r);
                     tc::wait_ld();
-                    if (!live) continue;
+                    uint4 v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        uint32_t v[4];
+                        uint32_t x[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            v[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv,
+                            x[e] = pack_bf16x2(__uint_as_float(r[8 * i + 2 * e]) * inv,
                                                __uint_as_float(r[8 * i + 2 * e + 1]) * inv);
-                        out[c / 8 + i] = make_uint4(v[0], v[1], v[2], v[3]);
+                        v[i] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
+                    quad_transpose(v, b);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (first + i < it.n) out[i * (R / 8) + c / 8] = v[i];
                 }
             } else {
                 // a partial: value quads of 32 pairs side by side
