@@ -168,6 +168,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
     return ok;
 }
 
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1, int lane,
+                                           int32_t *status, unsigned long long limit_ns)
+{
+    const bool ok = __all_sync(0xffffffffu, mbar_wait2(bar0, parity0, bar1, parity1, limit_ns));
+    if (!ok && lane == 0) report(status, PKV_DEV_TIMEOUT);
+    return ok;
+}
+
 // ---------------------------------------------------------------------------
 // Segments: the (item, key-tile range) pieces a CTA works through.  An item
 // is a (row, kv head, query-tile pair); its key tiles are the 64-key tiles of
@@ -768,7 +776,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             tc::commit(&s_full[x * 2 + (own(T) & 1)]);
             tc::commit(&k_empty[T % kStages]);
         };
-        // O += P(T) V(T); V(T) has landed (the warpgroup checked it before
+        // O += P(T) V(T); V(T) has landed (bf16: the warpgroup checked it before
         // handing P over); a segment's first tile starts O afresh
         auto pv_issue = [&](int32_t T, bool seg_start) {
             const uint64_t vd = dv + static_cast<uint64_t>(T % kStages) * kStageStep;
@@ -813,7 +821,11 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 const int32_t T = T0 + j, u = own(T);
                 const bool more = j + 2 * kStep < n;
                 if (more) ok = k_landed(T + 2 * kStep);
-                ok = ok && warp_wait(&p_full[x * 2 + (u & 1)], (u >> 1) & 1, lane, p.status, p.wait_ns);
+                // FP8: V(T) is waited for here (on bf16 pools the softmax warps, which may have
+                // rows of it to zero, do: 4 chunks of 512 480 us, 483 with the wait here)
+                ok = ok && (kF8 ? warp_wait2(&p_full[x * 2 + (u & 1)], (u >> 1) & 1, &v_full[T % kStages],
+                                             (T / kStages) & 1, lane, p.status, p.wait_ns)
+                                : warp_wait(&p_full[x * 2 + (u & 1)], (u >> 1) & 1, lane, p.status, p.wait_ns));
                 if (!ok) break;
                 tc::fence_after();
                 if (elect_one()) {
@@ -859,8 +871,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
         const int wq0 = (threadIdx.x - 128) & (kRows - 1);  // this thread's first chunk
         auto widen_k = [&](int32_t Tk) {
             const int sb = Tk & 1, st = Tk % kStages;
-            bool okw = mbar_wait(&staged[sb], (Tk >> 1) & 1, p.wait_ns);
-            if (Tk >= kStages) okw = okw && mbar_wait(&k_empty[st], ((Tk / kStages) + 1) & 1, p.wait_ns);
+            const bool okw = Tk < kStages ? mbar_wait(&staged[sb], (Tk >> 1) & 1, p.wait_ns)
+                                          : mbar_wait2(&staged[sb], (Tk >> 1) & 1, &k_empty[st],
+                                                       ((Tk / kStages) + 1) & 1, p.wait_ns);
             if (__any_sync(0xffffffffu, !okw)) return false;
             const uint32_t km = smask[sb];
             if ((kAlt ? row : static_cast<int>(threadIdx.x) - 128) == 0) kmask[st] = km;  // for the score masks of tile Tk
@@ -973,8 +986,9 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 // outside [kv_lo, kv_hi) or of blocks not loaded as zeros.  The
                 // stage is free once both tiles' P.V(T - kStages) completed.
                 const int sb = T & 1;
-                bool okw = mbar_wait(&staged[2 + sb], (T >> 1) & 1, p.wait_ns);
-                if (T >= kStages) okw = okw && mbar_wait(&v_empty[ks], ((T / kStages) + 1) & 1, p.wait_ns);
+                const bool okw = T < kStages ? mbar_wait(&staged[2 + sb], (T >> 1) & 1, p.wait_ns)
+                                             : mbar_wait2(&staged[2 + sb], (T >> 1) & 1, &v_empty[ks],
+                                                          ((T / kStages) + 1) & 1, p.wait_ns);
                 if (__any_sync(0xffffffffu, !okw)) {
                     if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                     abort = true;
@@ -1032,8 +1046,12 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                     mbar_arrive(&stg_free[2 + sb]);
                 }
             }
-            bool got = mbar_wait(&s_full[x * 2 + buf], (u >> 1) & 1, p.wait_ns);
-            got = got && mbar_wait(&k_full[ks], (T / kStages) & 1, p.wait_ns);  // for kmask
+            // (k_full for kmask; on bf16 pools one after the other: together 478 -> 484 us
+            // for 4 chunks of 512, on FP8 pools 585 -> 549 with the widening's pairs, and
+            // 525 with V's wait in the issuing warp)
+            const bool got = kF8 ? mbar_wait2(&s_full[x * 2 + buf], (u >> 1) & 1, &k_full[ks], (T / kStages) & 1, p.wait_ns)
+                                 : mbar_wait(&s_full[x * 2 + buf], (u >> 1) & 1, p.wait_ns) &&
+                                       mbar_wait(&k_full[ks], (T / kStages) & 1, p.wait_ns);
             if (__any_sync(0xffffffffu, !got)) {
                 if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
                 abort = true;
@@ -1179,18 +1197,20 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 f2_unpack(ls2[1], l2, l3);
                 l = l * (resc ? alpha : 1.f) + ((l0 + l1) + (l2 + l3));
             }
-            // V(jj) must have landed before this tile's P.V is issued.  Value
+            // bf16: V(jj) must have landed before this tile's P.V is issued.  Value
             // rows of keys outside [kv_lo, kv_hi) or of blocks not loaded hold
             // stale slots (possibly NaN): each warpgroup zeroes them before its
             // own P.V reads them (both write the same zeros, so whichever
             // product runs first reads zeros)
-            const bool landed = mbar_wait(&v_full[ks], (T / kStages) & 1, p.wait_ns);
-            if (__any_sync(0xffffffffu, !landed)) {
-                if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
-                abort = true;
-                break;
+            if constexpr (!kF8) {
+                const bool landed = mbar_wait(&v_full[ks], (T / kStages) & 1, p.wait_ns);
+                if (__any_sync(0xffffffffu, !landed)) {
+                    if (lane == 0) report(p.status, PKV_DEV_TIMEOUT);
+                    abort = true;
+                    break;
+                }
             }
-            // (FP8: the V producer wrote those columns as zeros)
+            // (FP8: the issuing warp waits for V, whose columns of those keys are zeros)
             const bool edge = !kF8 && (mask != (1u << kBlocks) - 1u ||
                                        (tbase < kv_lo && !(kSink && tbase + kKeys <= p.sinks)) ||
                                        tbase + kKeys > kv_hi);
