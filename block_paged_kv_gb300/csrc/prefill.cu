@@ -483,7 +483,8 @@ __device__ __forceinline__ uint64_t kv_policy(const PrefillParams &p)
 // kAlt: every chunk fills one query tile at most; tile B's warps then take the
 // same rows (their own S and O) and the two alternate over the key tiles, joined in
 // the epilogue: a tile's chain (scores, softmax, products) has two tiles' time.  32 rows
-// x 16 drafts 111 us, 142 without (32 drafts 133 and 148; FP8 132 and 167, 153 and 191)
+// x 16 drafts 111 us, 142 without (32 drafts 133 and 148; FP8 132 and 167, 153 and 191
+// before the waits in pairs)
 template <bool kF8, bool kSink, bool kTree, bool kAlt>
 __global__ void __launch_bounds__(pf::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
