@@ -807,14 +807,6 @@ def tree_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_di
                                               max_q_len, max_seq_len, window))
 
 
-def _is_row(t, n: int) -> bool:
-    return t.ndim == 1 and t.numel() == n
-
-
-def _workspace_ok(workspace, gpu) -> bool:
-    return workspace is None or (workspace.get_device() == gpu and workspace.is_contiguous())
-
-
 def _status_word(status, gpu) -> bool:
     return status is None or (status.get_device() == gpu and status.dtype is torch.int32 and status.numel() >= 1)
 
@@ -838,14 +830,15 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
             q.dtype is (torch.float32 if pool.dtype == PKV_F32 else torch.bfloat16) and
             block_tables.dtype is i32 and block_tables.is_contiguous() and block_tables.get_device() == gpu and
             len(tshape) == 2 and seq_lens.dtype is i32 and seq_lens.is_contiguous() and
-            seq_lens.get_device() == gpu and _is_row(seq_lens, tshape[0]) and
+            seq_lens.get_device() == gpu and seq_lens.ndim == 1 and seq_lens.numel() == tshape[0] and
             cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
-            _is_row(cu_q_lens, tshape[0] + 1) and
-            tree_masks.dtype is torch.int64 and _is_row(tree_masks, qshape[0]) and tree_masks.is_contiguous() and
-            tree_masks.get_device() == gpu and
+            cu_q_lens.ndim == 1 and cu_q_lens.numel() == tshape[0] + 1 and
+            tree_masks.dtype is torch.int64 and tree_masks.ndim == 1 and tree_masks.numel() == qshape[0] and
+            tree_masks.is_contiguous() and tree_masks.get_device() == gpu and
             (out is None or (out.shape == qshape and out.dtype is q.dtype and out.is_contiguous() and
                              out.get_device() == gpu)) and
-            _workspace_ok(workspace, gpu) and _status_word(status, gpu)):
+            (workspace is None or (workspace.get_device() == gpu and workspace.is_contiguous())) and
+            (status is None or _status_word(status, gpu))):
         dev = k_pool.device
         _require(q.dim() == 3 and q.shape[2] == pool.head_dim and q.dtype == _act_dtype(k_pool.dtype) and
                  q.is_contiguous() and q.device == dev, "q is [sum C, Hq, D], contiguous, pool dtype")
@@ -868,19 +861,22 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
     hq = qshape[1]
     if max_seq_len is None:
         max_seq_len = width * pool.block_size
-    # the plan reads the SM count of the current device
-    with _NULL if _current_device() == gpu else torch.cuda.device(gpu):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        with torch.cuda.device(gpu):  # the plan reads the SM count of the current device
             workspace = alloc_workspace(
                 tree_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, pool.block_size, max_q_len,
                                     max_seq_len, window), k_pool.device)
-        code = _lib.paged_tree_attention(
-            q.data_ptr(), cu_q_lens.data_ptr(), tree_masks.data_ptr(), hq, ctypes.byref(pool),
+    args = (q.data_ptr(), cu_q_lens.data_ptr(), tree_masks.data_ptr(), hq, ctypes.byref(pool),
             block_tables.data_ptr(), width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, scale,
             out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
             None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = _lib.paged_tree_attention(*args)
+    else:
+        with torch.cuda.device(gpu):
+            code = _lib.paged_tree_attention(*args)
     if code != PKV_OK:
         raise PkvError("paged_tree_attention", code)
     return out
@@ -906,7 +902,8 @@ class LatentPoolSet:
         _require(len(self.pools) > 0, "at least one pool")
         self.device, self.n, self.gpu = self.pools[0].device, len(self.pools), self.pools[0].get_device()
         # rows move whole: where the latent ends plays no part
-        self._c = (_LatentPool * self.n)(*[_latent_pool(t, t.shape[-1] - 1, t.shape, t.dtype, t.get_device()) for t in self.pools])
+        self._c = (_LatentPool * self.n)(*[_latent_pool(t, t.shape[-1] - 1, t.shape, t.dtype, t.get_device())
+                                           for t in self.pools])
         f = self.pools[0]
         for t in self.pools:
             _require(t.device == self.device, "every pool on one GPU")
@@ -932,11 +929,13 @@ def paged_tree_commit(pools, block_tables: torch.Tensor, seq_lens: torch.Tensor,
             cu_q_lens.get_device() == gpu and path.get_device() == gpu and path_lens.get_device() == gpu and
             block_tables.is_contiguous() and seq_lens.is_contiguous() and cu_q_lens.is_contiguous() and
             path.is_contiguous() and path_lens.is_contiguous() and len(tshape) == 2 and len(pshape) == 2 and
-            pshape[0] == tshape[0] and _is_row(seq_lens, tshape[0]) and _is_row(path_lens, tshape[0]) and
-            _is_row(cu_q_lens, tshape[0] + 1) and
-            (new_seq_lens is None or (new_seq_lens.dtype is i32 and _is_row(new_seq_lens, tshape[0]) and
+            pshape[0] == tshape[0] and seq_lens.ndim == 1 and seq_lens.numel() == tshape[0] and
+            path_lens.ndim == 1 and path_lens.numel() == tshape[0] and cu_q_lens.ndim == 1 and
+            cu_q_lens.numel() == tshape[0] + 1 and
+            (new_seq_lens is None or (new_seq_lens.dtype is i32 and new_seq_lens.ndim == 1 and
+                                      new_seq_lens.numel() == tshape[0] and
                                       new_seq_lens.is_contiguous() and new_seq_lens.get_device() == gpu)) and
-            _status_word(status, gpu)):
+            (status is None or _status_word(status, gpu))):
         dev = pools.device
         for t, name in ((block_tables, "block_tables"), (seq_lens, "seq_lens"), (cu_q_lens, "cu_q_lens"),
                         (path, "path"), (path_lens, "path_lens"), (new_seq_lens, "new_seq_lens")):
@@ -1073,21 +1072,25 @@ def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int,
     One query per row (decode) without ``cu_q_lens``; with it [B+1] the last C
     positions of each row hold a chunk's queries, causally, or, with ``tree_masks``,
     a drafted tree's (as for ``paged_tree_attention``)."""
-    gpu, i32, dt, qshape, tshape, rows = pool.get_device(), torch.int32, pool.dtype, q.shape, block_tables.shape, pool.shape
+    gpu, i32, dt, rows = pool.get_device(), torch.int32, pool.dtype, pool.shape
+    qshape, tshape = q.shape, block_tables.shape
     c = _latent_pool(pool, latent_dim, rows, dt, gpu)
     if not (len(qshape) == 3 and qshape[2] == rows[2] and q.is_contiguous() and q.get_device() == gpu and
             q.dtype is dt and block_tables.dtype is i32 and block_tables.is_contiguous() and
             block_tables.get_device() == gpu and len(tshape) == 2 and seq_lens.dtype is i32 and
-            seq_lens.is_contiguous() and seq_lens.get_device() == gpu and _is_row(seq_lens, tshape[0]) and
+            seq_lens.is_contiguous() and seq_lens.get_device() == gpu and seq_lens.ndim == 1 and
+            seq_lens.numel() == tshape[0] and
             (qshape[0] == tshape[0] and max_q_len == 1 if cu_q_lens is None else
              (cu_q_lens.dtype is i32 and cu_q_lens.is_contiguous() and cu_q_lens.get_device() == gpu and
-              _is_row(cu_q_lens, tshape[0] + 1))) and
+              cu_q_lens.ndim == 1 and cu_q_lens.numel() == tshape[0] + 1)) and
             (tree_masks is None or (cu_q_lens is not None and tree_masks.dtype is torch.int64 and
-                                    _is_row(tree_masks, qshape[0]) and tree_masks.is_contiguous() and
+                                    tree_masks.ndim == 1 and tree_masks.numel() == qshape[0] and
+                                    tree_masks.is_contiguous() and
                                     tree_masks.get_device() == gpu)) and
             (out is None or (out.shape == (qshape[0], qshape[1], latent_dim) and out.dtype is dt and
                              out.is_contiguous() and out.get_device() == gpu)) and
-            _workspace_ok(workspace, gpu) and _status_word(status, gpu)):
+            (workspace is None or (workspace.get_device() == gpu and workspace.is_contiguous())) and
+            (status is None or _status_word(status, gpu))):
         dev = pool.device
         _require(q.dim() == 3 and q.shape[2] == pool.shape[2] and q.dtype == dt and q.is_contiguous() and
                  q.device == dev, "q is [queries, H, latent_dim + rope_dim], contiguous, pool dtype")
@@ -1112,18 +1115,22 @@ def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int,
     H = qshape[1]
     if max_seq_len is None:
         max_seq_len = width * c.block_size
-    with _NULL if _current_device() == gpu else torch.cuda.device(gpu):
-        if out is None:
-            out = torch.empty((qshape[0], H, latent_dim), dtype=dt, device=q.device)
-        if workspace is None:
+    if out is None:
+        out = torch.empty((qshape[0], H, latent_dim), dtype=dt, device=q.device)
+    if workspace is None:
+        with torch.cuda.device(gpu):  # the plan reads the SM count of the current device
             workspace = alloc_workspace(
                 latent_workspace_size(B, H, latent_dim, c.rope_dim, c.block_size, max_q_len, max_seq_len),
                 q.device)
-        code = _lib.paged_latent_attention(
-            q.data_ptr(), qshape[0], None if cu_q_lens is None else cu_q_lens.data_ptr(),
+    args = (q.data_ptr(), qshape[0], None if cu_q_lens is None else cu_q_lens.data_ptr(),
             None if tree_masks is None else tree_masks.data_ptr(), H, ctypes.byref(c), block_tables.data_ptr(),
             width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, scale, out.data_ptr(), workspace.data_ptr(),
             workspace.nbytes, None if status is None else status.data_ptr(), _raw_stream(gpu))
+    if _current_device() == gpu:
+        code = _lib.paged_latent_attention(*args)
+    else:
+        with torch.cuda.device(gpu):
+            code = _lib.paged_latent_attention(*args)
     if code != PKV_OK:
         raise PkvError("paged_latent_attention", code)
     return out
