@@ -1189,6 +1189,7 @@ def profile_times(kind: int) -> list:
 
 DRILL_WITHHOLD_FIRST_LOAD = 1
 DRILL_LATE_CONSUMERS = 4
+DRILL_LATE_PRODUCERS = 8
 
 
 def set_wait_drill(wait_limit_ns: int = 0, flags: int = 0) -> None:
@@ -1196,7 +1197,9 @@ def set_wait_drill(wait_limit_ns: int = 0, flags: int = 0) -> None:
     each pipeline data wait (0 = the 2 s default) and, with
     DRILL_WITHHOLD_FIRST_LOAD, every pipeline's first load left unissued so
     that the wait for it runs out, or, with DRILL_LATE_CONSUMERS, the prefill's
-    softmax warps late at each item's output.  set_wait_drill() restores normal operation."""
+    softmax warps late at each item's output, or, with DRILL_LATE_PRODUCERS, two of the
+    latent attention's three loading warps late at everything they load.
+    set_wait_drill() restores normal operation."""
     _check("pkv_set_wait_drill", _lib.pkv_set_wait_drill(int(wait_limit_ns), int(flags)))
 
 

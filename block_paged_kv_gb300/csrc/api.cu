@@ -451,7 +451,8 @@ extern "C" {
 
 pkv_status pkv_set_wait_drill(uint64_t wait_limit_ns, uint32_t flags)
 {
-    if ((flags & ~static_cast<uint32_t>(PKV_DRILL_WITHHOLD_FIRST_LOAD | PKV_DRILL_LATE_CONSUMERS)) != 0)
+    if ((flags & ~static_cast<uint32_t>(PKV_DRILL_WITHHOLD_FIRST_LOAD | PKV_DRILL_LATE_CONSUMERS |
+                                        PKV_DRILL_LATE_PRODUCERS)) != 0)
         return PKV_ERR_INVALID_ARG;
     g_drill_wait_ns.store(wait_limit_ns == 0 ? kWaitLimitNs
                                              : std::min<uint64_t>(wait_limit_ns, kWaitLimitNs));

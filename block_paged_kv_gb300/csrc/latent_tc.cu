@@ -55,6 +55,7 @@ constexpr int kRows = kLatentTcRows;
 constexpr int kKeys = 64;
 constexpr int kRope = 64;
 constexpr int kThreads = 384;
+constexpr int kProducers = 3;             // warps of either CTA
 constexpr int kSoftWarps = 8;             // of either CTA: warps 4 .. 11
 constexpr int kFins = 3;                  // pieces whose sums may be on their way
 constexpr int kSBufs = 3, kPBufs = 2;
@@ -216,7 +217,10 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t addr, uint32_t lbo,
 // A producer warp (w of three) of CTA kRank.  Ring entry U goes to stage
 // U % kStages: in CTA 1 tile T is entry T, in CTA 0 the queries of every piece are two
 // entries before its tiles (64 pairs each, laid out as 64 keys are).  Producer w
-// brings an entry's 8-row groups w, w + 3, w + 6.
+// brings an entry's 8-row groups w, w + 3, w + 6, and arrives for it also where it has
+// none of them: an entry that completed without a producer could be used and freed, and
+// its stage's next one too, before that producer looks at the stage, and the parity that
+// it waits for would then be two phases old.
 template <int NR, int kRank>
 __device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUtensorMap &q_map, const LatentParams &p,
                                                Run run, uint8_t *smem, uint64_t *kv_full, uint64_t *kv_empty,
@@ -233,9 +237,12 @@ __device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUt
     LatentPiece pc;
     bool ok = true;
     int32_t T = 0, U = 0;
-    auto free_stage = [&]() { return U < n || lat_wait(&kv_empty[U % n], ((U / n) + 1) & 1, p); };
-    auto arm = [&](int32_t groups) {  // (the first producer: an entry's bytes)
-        if (w != 0 || lane != 0) return;
+    auto free_stage = [&]() {
+        if ((p.drill & kDrillLateProducers) != 0 && w != 0) come_late(5000 * w);
+        return U < n || lat_wait(&kv_empty[U % n], ((U / n) + 1) & 1, p);
+    };
+    auto arm = [&](int32_t groups) {  // this warp's part of an entry
+        if (lane != 0) return;
         if (groups == 0)
             mbar_arrive(&kv_full[U % n]);
         else
@@ -256,12 +263,12 @@ __device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUt
                 const int32_t row = pc.it.q0 * p.heads + pc.it.p0 + 64 * h;
                 const int32_t groups = min(max((pc.it.n - 64 * h + 7) / 8, 0), 8);
                 if (withheld(U)) continue;
-                arm(groups);
+                arm(max(0, groups - w + kProducers - 1) / kProducers);
                 __syncwarp();
                 uint8_t *dst = smem + (U % n) * stage;
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const int g = w + 3 * i;
+                    const int g = w + kProducers * i;
                     if (g < groups && elect_one())
                         tma_load_4d(dst + g * group, &q_map, &kv_full[U % n], 0, row + 8 * g, 0, 0, policy);
                     __syncwarp();
@@ -278,12 +285,18 @@ __device__ __forceinline__ void latent_produce(const CUtensorMap &map, const CUt
             if (!(ok = free_stage())) break;
             if (w == 0 && lane == 0) kmask[T % kMasks] = mask;
             if (!withheld(U)) {
-                arm(__popc(mask) << (bs_log - 3));
+                int32_t groups = 0;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int g = w + kProducers * i;
+                    groups += g < 8 && ((mask >> (g * 8 >> bs_log)) & 1u) ? 1 : 0;
+                }
+                arm(groups);
                 __syncwarp();
                 uint8_t *dst = smem + (U % n) * stage;
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const int g = w + 3 * i, b = ((g & 7) * 8) >> bs_log;
+                    const int g = w + kProducers * i, b = ((g & 7) * 8) >> bs_log;
                     const int32_t blk = __shfl_sync(0xffffffffu, cur, b);
                     if (g < 8 && ((mask >> b) & 1u) && elect_one())
                         tma_load_4d(dst + g * group, &map, &kv_full[U % n], 0, g * 8 - (b << bs_log), 0, blk, policy);
@@ -330,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
         tma_prefetch_desc(rank == 0 ? &map0 : &map1);
         if (rank == 0) tma_prefetch_desc(&q_map);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_full[i], kProducers);
             mbar_init(&kv_empty[i], 1);
         }
         for (int i = 0; i < kSBufs; ++i) {

@@ -167,6 +167,25 @@ __device__ __forceinline__ bool mbar_wait2(uint64_t *bar0, uint32_t parity0, uin
     return ok != 0 || (mbar_wait(bar0, parity0, limit_ns) && mbar_wait(bar1, parity1, limit_ns));
 }
 
+// Drill: `ns` pass (one sleep may end at once; 65536 of them are the limit).  One
+// opaque block, so that the loop takes no part in the kernel's scheduling.
+__device__ __forceinline__ void come_late(uint32_t ns)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t, n;\n\t"
+        "mov.u32 t0, %%globaltimer_lo;\n\t"
+        "mov.u32 n, 65536;\n\t"
+        "LATE:\n\t"
+        "nanosleep.u32 1000;\n\t"
+        "mov.u32 t, %%globaltimer_lo;\n\t"
+        "sub.u32 t, t, t0;\n\t"
+        "setp.lt.u32 p, t, %0;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.and.u32 q, n, 0, p;\n\t"
+        "@q bra LATE;\n\t}" ::"r"(ns)
+        : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // TMA (tensor) loads into shared memory, completing on an mbarrier
 // ---------------------------------------------------------------------------

@@ -30,6 +30,10 @@ constexpr uint32_t kDrillWithholdFirst = PKV_DRILL_WITHHOLD_FIRST_LOAD;
 // output, long after the tensor cores have finished it.
 constexpr uint32_t kDrillLate = PKV_DRILL_LATE_CONSUMERS;
 
+// Diagnostic drill flag: two of the three producer warps of the latent attention look
+// at every ring entry 5 and 10 us late.
+constexpr uint32_t kDrillLateProducers = PKV_DRILL_LATE_PRODUCERS;
+
 struct AppendParams {
     void *k_pool;
     void *v_pool;

@@ -447,25 +447,6 @@ __device__ __noinline__ void stage_q_rows(const uint4 *q, int32_t hq, int glog,
     fence_proxy_async_smem();  // read by the tensor cores (async proxy)
 }
 
-// Drill: `ns` pass (one sleep may end at once; 65536 of them are the limit).  One
-// opaque block, so that the loop takes no part in the kernel's scheduling.
-__device__ __forceinline__ void come_late(uint32_t ns)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 t0, t, n;\n\t"
-        "mov.u32 t0, %%globaltimer_lo;\n\t"
-        "mov.u32 n, 65536;\n\t"
-        "LATE:\n\t"
-        "nanosleep.u32 1000;\n\t"
-        "mov.u32 t, %%globaltimer_lo;\n\t"
-        "sub.u32 t, t, t0;\n\t"
-        "setp.lt.u32 p, t, %0;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.and.u32 q, n, 0, p;\n\t"
-        "@q bra LATE;\n\t}" ::"r"(ns)
-        : "memory");
-}
-
 // K/V is re-read by the row's other CTAs; a tree that one item covers reads it once
 // (32 rows x 16 drafts: 118.7 us with evict_last, 119.0 with evict_normal, 110.7 with
 // evict_first).

@@ -657,7 +657,7 @@ int32_t pkv_set_decode_split_blocks(int32_t blocks_per_split);
  * "paged-cache.md", fail-closed gates of the grouped coordinator;
  * "perf.md", paged knob table, MLX_PAGED_NATIVE_KV_WRITE row, where batched
  * decode hard-errors instead of falling back).  Process-wide, for the
- * launches that follow (bf16 and FP8 decode, tensor-core prefill):
+ * launches that follow (bf16 and FP8 decode, tensor-core prefill and latent attention):
  *   wait_limit_ns: limit of each pipeline data wait, 0 = the default
  *                  (2 s); values above the default are cut to it;
  *   flags:         0, or PKV_DRILL_WITHHOLD_FIRST_LOAD: every pipeline
@@ -665,7 +665,10 @@ int32_t pkv_set_decode_split_blocks(int32_t blocks_per_split);
  *                  runs out after wait_limit_ns;
  *                  PKV_DRILL_LATE_CONSUMERS: the tensor-core prefill's
  *                  softmax warps come to each item's output some 20 us late
- *                  (results are the same, calls are slower).
+ *                  (results are the same, calls are slower);
+ *                  PKV_DRILL_LATE_PRODUCERS: two of the three warps that load
+ *                  for the tensor-core latent attention start on each part of
+ *                  its ring 5 and 10 us late (results likewise).
  * A wait that runs out sets PKV_DEV_TIMEOUT in the status word; the CTA then
  * waits (with the 2 s default limit) for every copy it did issue to land
  * and for its tensor-core products to finish, and exits.  The call's output
@@ -674,6 +677,7 @@ int32_t pkv_set_decode_split_blocks(int32_t blocks_per_split);
  */
 #define PKV_DRILL_WITHHOLD_FIRST_LOAD 1u
 #define PKV_DRILL_LATE_CONSUMERS 4u
+#define PKV_DRILL_LATE_PRODUCERS 8u
 pkv_status pkv_set_wait_drill(uint64_t wait_limit_ns, uint32_t flags);
 
 /* Number of splits per row and blocks per split the automatic plan picks for
