@@ -1061,7 +1061,7 @@ def latent_workspace_size(batch: int, num_q_heads: int, latent_dim: int, rope_di
 
 def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int, block_tables: torch.Tensor,
                            seq_lens: torch.Tensor, scale: float, cu_q_lens: Optional[torch.Tensor] = None,
-                           max_q_len: int = 1, tree_masks: Optional[torch.Tensor] = None,
+                           max_q_len: Optional[int] = None, tree_masks: Optional[torch.Tensor] = None,
                            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                            max_seq_len: Optional[int] = None,
                            status: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -1071,10 +1071,14 @@ def paged_latent_attention(q: torch.Tensor, pool: torch.Tensor, latent_dim: int,
 
     One query per row (decode) without ``cu_q_lens``; with it [B+1] the last C
     positions of each row hold a chunk's queries, causally, or, with ``tree_masks``,
-    a drafted tree's (as for ``paged_tree_attention``)."""
+    a drafted tree's (as for ``paged_tree_attention``).  ``max_q_len`` bounds C; left
+    out it is the number of queries, which no row passes (a tight bound leaves fewer
+    empty items to look at; the result is the same)."""
     gpu, i32, dt, rows = pool.get_device(), torch.int32, pool.dtype, pool.shape
     qshape, tshape = q.shape, block_tables.shape
     c = _latent_pool(pool, latent_dim, rows, dt, gpu)
+    if max_q_len is None:
+        max_q_len = 1 if cu_q_lens is None else qshape[0] if tree_masks is None else min(qshape[0], MAX_TREE)
     if not (len(qshape) == 3 and qshape[2] == rows[2] and q.is_contiguous() and q.get_device() == gpu and
             q.dtype is dt and block_tables.dtype is i32 and block_tables.is_contiguous() and
             block_tables.get_device() == gpu and len(tshape) == 2 and seq_lens.dtype is i32 and
