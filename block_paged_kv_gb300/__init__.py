@@ -186,6 +186,8 @@ _lib.paged_tree_workspace_size.restype = _sz
 _lib.paged_tree_attention.argtypes = [_vp, _vp, _vp, _i32, _PP, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                       ctypes.c_float, _vp, _vp, _sz, _vp, _vp]
 _lib.paged_tree_attention.restype = ctypes.c_int
+_lib.paged_tree_attention_queries.argtypes = [_vp, _i32, *_lib.paged_tree_attention.argtypes[1:]]
+_lib.paged_tree_attention_queries.restype = ctypes.c_int
 _lib.pkv_tree_masks_host.argtypes = [_vp, _vp, _i32, _vp]
 _lib.pkv_tree_masks_host.restype = ctypes.c_int
 _lib.paged_tree_commit.argtypes = [_PP, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp]
@@ -220,7 +222,8 @@ EXPORTED = ["paged_kv_append", "paged_decode_workspace_size", "paged_decode_atte
             "paged_decode_groups_sinks_workspace_size", "paged_decode_attention_groups_sinks",
             "paged_prefill_sinks_workspace_size", "paged_prefill_chunk_attention_sinks",
             "pkv_allocator_expire_window", "pkv_allocator_fork", "pkv_allocator_truncate",
-            "pkv_allocator_compact", "paged_tree_workspace_size", "paged_tree_attention", "pkv_tree_masks_host",
+            "pkv_allocator_compact", "paged_tree_workspace_size", "paged_tree_attention",
+            "paged_tree_attention_queries", "pkv_tree_masks_host",
             "paged_tree_commit", "paged_latent_tree_commit", "paged_latent_append", "paged_latent_workspace_size",
             "paged_latent_attention"]
 
@@ -823,7 +826,8 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
     i's query attends the cached tokens and the drafts whose bits ``tree_masks``
     [sum C] (int64 bit patterns, ``tree_masks_host``) has set, j <= i.  With a
     ``window`` (at least ``max_q_len``) a node counts from its depth in the tree.
-    ``max_q_len`` is at most ``MAX_TREE``."""
+    ``max_q_len`` is at most ``MAX_TREE``.  A row whose drafts lie past ``q`` is left
+    out (``DEV_BAD_LEN``)."""
     pool = _pool(k_pool, v_pool, k_scale, v_scale)
     gpu, i32, qshape, tshape = k_pool.get_device(), torch.int32, q.shape, block_tables.shape
     if not (len(qshape) == 3 and qshape[2] == pool.head_dim and q.is_contiguous() and q.get_device() == gpu and
@@ -868,15 +872,15 @@ def paged_tree_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, tree_masks: t
             workspace = alloc_workspace(
                 tree_workspace_size(B, hq, pool.num_kv_heads, pool.head_dim, pool.block_size, max_q_len,
                                     max_seq_len, window), k_pool.device)
-    args = (q.data_ptr(), cu_q_lens.data_ptr(), tree_masks.data_ptr(), hq, ctypes.byref(pool),
+    args = (q.data_ptr(), qshape[0], cu_q_lens.data_ptr(), tree_masks.data_ptr(), hq, ctypes.byref(pool),
             block_tables.data_ptr(), width, seq_lens.data_ptr(), B, max_q_len, max_seq_len, window, scale,
             out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
             None if status is None else status.data_ptr(), _raw_stream(gpu))
     if _current_device() == gpu:
-        code = _lib.paged_tree_attention(*args)
+        code = _lib.paged_tree_attention_queries(*args)
     else:
         with torch.cuda.device(gpu):
-            code = _lib.paged_tree_attention(*args)
+            code = _lib.paged_tree_attention_queries(*args)
     if code != PKV_OK:
         raise PkvError("paged_tree_attention", code)
     return out

@@ -859,7 +859,8 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
                         const int32_t *block_tables, int32_t max_blocks_per_seq, const int32_t *seq_lens,
                         int32_t batch, int32_t max_q_len, int32_t max_seq_len, int32_t window,
                         int32_t sinks, float scale, void *out, void *workspace, size_t ws_bytes,
-                        int32_t *dev_status, pkv_stream_t stream, const uint64_t *tree = nullptr)
+                        int32_t *dev_status, pkv_stream_t stream, const uint64_t *tree = nullptr,
+                        int32_t num_queries = INT32_MAX)
 {
     if (!valid_pool(pool) || batch < 0 || num_q_heads <= 0 || max_q_len < 0 || max_seq_len < 0 ||
         window < 0 || sinks < 0 || !std::isfinite(scale))
@@ -919,6 +920,7 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
         d.tree = tree;
         d.q_chunk = q_chunk;
         d.q_chunks = q_chunks;
+        d.num_queries = num_queries;
         d.scale_log2 = scale * 1.4426950408889634f;
         d.v_scale = 1.f;
         drill_settings(&d.wait_ns, &d.drill);
@@ -964,6 +966,7 @@ pkv_status prefill_call(const void *q, const int32_t *cu_q_lens, int32_t num_q_h
     p.window = window;
     p.sinks = sinks;
     p.tree = tree;
+    p.num_queries = num_queries;
     const int32_t qpt = prefill_queries_per_cta(pool->dtype, G);
     p.q_tiles = static_cast<int32_t>(ceil_div64(max_q_len, qpt));
     p.kv_splits = 1;
@@ -1350,12 +1353,26 @@ pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const u
                                 int32_t max_q_len, int32_t max_seq_len, int32_t window, float scale, void *out,
                                 void *workspace, size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream)
 {
-    if (max_q_len > PKV_MAX_TREE || (batch > 0 && max_q_len > 0 && tree_masks == nullptr))
-        return PKV_ERR_INVALID_ARG;
+    return paged_tree_attention_queries(q, INT32_MAX, cu_q_lens, tree_masks, num_q_heads, pool, block_tables,
+                                        max_blocks_per_seq, seq_lens, batch, max_q_len, max_seq_len, window, scale, out,
+                                        workspace, ws_bytes, dev_status, stream);
+}
+
+pkv_status paged_tree_attention_queries(const void *q, int32_t num_queries, const int32_t *cu_q_lens,
+                                        const uint64_t *tree_masks, int32_t num_q_heads, const pkv_pool *pool,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *seq_lens, int32_t batch, int32_t max_q_len, int32_t max_seq_len,
+                                        int32_t window, float scale, void *out, void *workspace, size_t ws_bytes,
+                                        int32_t *dev_status, pkv_stream_t stream)
+{
+    if (num_queries < 0 || max_q_len > PKV_MAX_TREE) return PKV_ERR_INVALID_ARG;
+    if (num_queries == 0) max_q_len = std::min(max_q_len, 0);
+    if (batch > 0 && max_q_len > 0 && tree_masks == nullptr) return PKV_ERR_INVALID_ARG;
     if (window > 0 && window < max_q_len) return PKV_ERR_UNSUPPORTED;
     // (a call without rows or queries launches nothing)
     return prefill_call(q, cu_q_lens, num_q_heads, pool, block_tables, max_blocks_per_seq, seq_lens, batch, max_q_len,
-                        max_seq_len, window, 0, scale, out, workspace, ws_bytes, dev_status, stream, tree_masks);
+                        max_seq_len, window, 0, scale, out, workspace, ws_bytes, dev_status, stream, tree_masks,
+                        num_queries);
 }
 
 pkv_status paged_tree_commit(const pkv_pool *pools, int32_t n_pools, const int32_t *block_tables,

@@ -38,9 +38,10 @@ __device__ __forceinline__ RowRange row_range(const DecodeParams &p, int32_t r, 
     if (p.cu_q_lens != nullptr) {
         const int32_t c0 = __ldg(p.cu_q_lens + r), c1 = __ldg(p.cu_q_lens + r + 1);
         int32_t C = c1 - c0;
-        if (c0 < 0 || C < 0 || C > p.max_q || C > L) {
+        const bool outside = c0 < 0 || C < 0 || c1 > p.num_queries;
+        if (outside || C > p.max_q || C > L) {
             if (report_bad) report(p.status, PKV_DEV_BAD_LEN);
-            C = c0 < 0 || C < 0 ? 0 : min(min(C, p.max_q), L);
+            C = outside ? 0 : min(min(C, p.max_q), L);
         }
         rr.C = C;
         rr.q0 = c0 < 0 ? 0 : c0;

@@ -188,6 +188,7 @@ struct DecodeParams {
     // queries, q_chunks of them a row
     const uint64_t *tree;
     int32_t q_chunk, q_chunks;
+    int32_t num_queries;  // with cu_q_lens: rows whose queries lie past them are left out
     int32_t num_groups;
     float scale_log2;  // scale * log2(e) (* k_scale for FP8): scores are kept in base-2 units
     float v_scale;     // FP8: applied to each partial's weighted values
@@ -265,6 +266,7 @@ struct PrefillParams {
     int32_t batch, hq, hkv, group, head_dim, block_size, width, num_blocks;
     int32_t max_len;    // min(max_seq_len, width * block_size)
     int32_t max_q_len;
+    int32_t num_queries;  // rows whose queries lie past them are left out
     int32_t window;
     int32_t sinks;      // with a window: the first positions that stay visible (0 = none)
     const uint64_t *tree;  // drafted trees: bit j of tree[i] = the packed query i attends its row's draft j

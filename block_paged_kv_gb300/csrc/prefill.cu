@@ -139,9 +139,10 @@ __device__ __forceinline__ bool prefill_item(const PrefillParams &p, int32_t bid
         if (report_bad) report(p.status, PKV_DEV_BAD_LEN);
         L = L < 0 ? 0 : p.max_len;
     }
-    if (c0 < 0 || C < 0 || C > p.max_q_len || C > L) {
+    const bool outside = c0 < 0 || C < 0 || c1 > p.num_queries;
+    if (outside || C > p.max_q_len || C > L) {
         if (report_bad) report(p.status, PKV_DEV_BAD_LEN);
-        C = c0 < 0 || C < 0 ? 0 : min(min(C, p.max_q_len), L);
+        C = outside ? 0 : min(min(C, p.max_q_len), L);
     }
     w.i0 = qt * qpc;
     if (w.i0 >= C) return false;

@@ -457,6 +457,8 @@ pkv_status paged_prefill_chunk_attention_sinks(
  * also of one that no query attends.
  *   tree_masks: device uint64 [cu_q_lens[batch]]
  *   max_q_len:  host upper bound on C, at most PKV_MAX_TREE
+ * paged_tree_attention_queries is told on the host how many queries q, tree_masks and
+ * out hold: a row whose drafts lie past them is left out (PKV_DEV_BAD_LEN).
  */
 #define PKV_MAX_TREE 64
 
@@ -471,6 +473,14 @@ pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const u
                                 int32_t max_seq_len, int32_t window, float scale, void *out,
                                 void *workspace, size_t ws_bytes, int32_t *dev_status,
                                 pkv_stream_t stream);
+
+pkv_status paged_tree_attention_queries(const void *q, int32_t num_queries, const int32_t *cu_q_lens,
+                                        const uint64_t *tree_masks, int32_t num_q_heads,
+                                        const pkv_pool *pool, const int32_t *block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                        int32_t batch, int32_t max_q_len, int32_t max_seq_len,
+                                        int32_t window, float scale, void *out, void *workspace,
+                                        size_t ws_bytes, int32_t *dev_status, pkv_stream_t stream);
 
 /* Host helper: masks of drafted trees from their parents.  Node i of row r (at
  * cu_q_lens[r] + i in both arrays) has parent parents[..] in -1 .. i - 1 (-1: the
