@@ -905,7 +905,7 @@ __device__ __forceinline__ void decode_split_body(const CUtensorMap &kmap, const
             }
             if (g8 == 0)
                 *reinterpret_cast<float2 *>(mlbuf + (warp * R + row) * 2) =
-                    make_float2(mc[n][e], lc[n][e]);
+                    make_float2(kTree ? weight_max(mc[n][e], lc[n][e]) : mc[n][e], lc[n][e]);
         }
     __syncthreads();
     for (int idx = threadIdx.x; idx < R * D; idx += NW * 32) {

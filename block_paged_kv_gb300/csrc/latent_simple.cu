@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(ls::kThreads) latent_simple_kernel(const Laten
                     const int d = sub + i * 16;
                     part[((d >> 2) * kRows + pair) * 4 + (d & 3)] = o[i];
                 }
-            if (sub == 0) latent_part_ml<kRows>(p, blockIdx.x, pc.slot)[pair] = make_float2(m, l);
+            if (sub == 0) latent_part_ml<kRows>(p, blockIdx.x, pc.slot)[pair] = make_float2(weight_max(m, l), l);
         }
     }
 }

@@ -624,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lt::kThreads, 1)
                 const float2 o = sums[row];
                 l += o.x == m_ref ? o.y : o.y * fast_exp2(o.x - m_ref);  // (0 from -inf)
                 if (!pc.whole) {
-                    if (row < it.n) latent_part_ml<kRows>(p, worker, pc.slot)[row] = make_float2(m_ref, l);
+                    if (row < it.n) latent_part_ml<kRows>(p, worker, pc.slot)[row] = make_float2(weight_max(m_ref, l), l);
                 } else if (warp_live) {
                     // (CTA 1 has read the sums of kFins pieces ago: the last weights went
                     // after the products of the tile two before, hence after the

@@ -448,6 +448,11 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b)
     return r;
 }
 
+// The maximum that a partial keeps beside its sum l.  fmaxf passes over NaN, so that a
+// query whose scores are all NaN has the maximum of one that attends nothing, and its
+// sum tells them apart: it keeps a weight, so that every join carries the NaN on.
+__device__ __forceinline__ float weight_max(float m, float l) { return l != l && m == -INFINITY ? 0.f : m; }
+
 // max of three floats in one instruction (sm_100 and later); a NaN operand
 // is ignored as by fmaxf
 __device__ __forceinline__ float fmax3(float a, float b, float c)

@@ -1244,6 +1244,7 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
             // announced, which tile A's warps take part in), which join the two
             // tiles' O as they read them
             float wa = 1.f, wb = 0.f;
+            if constexpr (kTree) m_ref = weight_max(m_ref, l);
             if constexpr (kAlt) {
                 const uint32_t hand = tS(1, 0) + lane_base;
                 if (x == 1 && !__any_sync(0xffffffffu, !done)) {
@@ -1421,7 +1422,8 @@ __global__ void __launch_bounds__(pf::kThreads, 1)
                 if (valid_row) *reinterpret_cast<float2 *>(p.ws_ml + pi * 2) = make_float2(m_ref, l);
             } else {
                 tc::fence_after();
-                const float inv = (l > 0.f ? 1.f / l : 0.f) * (kF8 ? p.v_scale : 1.f);
+                // (kTree: NaN stays NaN)
+                const float inv = ((kTree ? l != 0.f : l > 0.f) ? 1.f / l : 0.f) * (kF8 ? p.v_scale : 1.f);
                 // the warp's rows go through its part of the query tile, which
                 // every product of the segment has read: 16-byte chunks
                 // swizzled by the row, then whole rows to global memory
@@ -1666,7 +1668,7 @@ __global__ void __launch_bounds__(kTreeMergeThreads) prefill_tree_merge_kernel(c
         [&](int32_t i) { return reinterpret_cast<const float2 *>(p.sk_ml)[at(i) * 32 + (row & 31)]; }, acc);
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) +
                          ((static_cast<int64_t>(rec.q0) + row / p.group) * p.hq + rec.g * p.group + row % p.group) * kD + d4 * 4;
-    store_bf16x16(out, acc, l > 0.f ? 1.f / l : 0.f);
+    store_bf16x16(out, acc, l != 0.f ? 1.f / l : 0.f);  // (NaN stays NaN)
 }
 
 // ---------------------------------------------------------------------------
