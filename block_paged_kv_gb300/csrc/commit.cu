@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const __grid_con
     __shared__ CommitMoves m;
     pdl_wait();
     pdl_trigger();
-    const int32_t per_token = p.heads * p.row_vecs, all = p.n_tensors * per_token;  // (of 2^20 at most)
+    const int32_t per_token = p.heads * p.row_vecs, all = p.n_tensors * per_token;  // (2^30 at most: commit_call checks)
     for (int32_t r = blockIdx.y; r < p.batch; r += gridDim.y) {
         commit_resolve(p, r, blockIdx.x == 0, m);
         const int32_t n = m.n;
