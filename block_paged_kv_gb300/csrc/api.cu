@@ -1339,12 +1339,20 @@ size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num
     if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || max_q_len <= 0 ||
         max_q_len > PKV_MAX_TREE || max_seq_len < 0 || window < 0 || head_dim <= 0 || block_size <= 0)
         return 0;
-    if (tree_on_decode(num_q_heads / num_kv_heads, head_dim, block_size, max_q_len))
-        return ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
-                              verify_window(window, max_q_len), nullptr, 0, max_q_len);
-    if (!prefill_shape_built(PKV_BF16, head_dim, block_size, num_q_heads / num_kv_heads)) return 0;
-    const int32_t ctas = prefill_tree_ctas(prefill_items(batch, num_q_heads, num_kv_heads, max_q_len), num_sms_current());
-    return ctas > 0 ? prefill_tree_ws(ctas).bytes : 0;
+    // enough for every smaller max_q_len too, some of which run on the other kernel
+    const int32_t G = num_q_heads / num_kv_heads;
+    size_t bytes = 0;
+    if (decode_shape_built(PKV_BF16, head_dim, block_size, G)) {
+        const int32_t n = tree_on_decode(G, head_dim, block_size, max_q_len) ? max_q_len : 16 / G;
+        bytes = ws_query_bytes(batch, num_q_heads, num_kv_heads, head_dim, block_size, max_seq_len,
+                               verify_window(window, n), nullptr, 0, n);
+    }
+    if (G * static_cast<int64_t>(max_q_len) > 16 && prefill_shape_built(PKV_BF16, head_dim, block_size, G)) {
+        const int32_t items = prefill_items(batch, num_q_heads, num_kv_heads, 1);
+        const int32_t ctas = prefill_tree_ctas(items, num_sms_current());
+        if (ctas > 0) bytes = std::max(bytes, prefill_tree_ws(ctas).bytes);
+    }
+    return bytes;
 }
 
 pkv_status paged_tree_attention(const void *q, const int32_t *cu_q_lens, const uint64_t *tree_masks,

@@ -462,6 +462,7 @@ pkv_status paged_prefill_chunk_attention_sinks(
  */
 #define PKV_MAX_TREE 64
 
+/* Holds for every smaller max_q_len and max_seq_len too. */
 size_t paged_tree_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, int32_t block_size, int32_t max_q_len,
                                  int32_t max_seq_len, int32_t window);
