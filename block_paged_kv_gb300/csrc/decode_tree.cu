@@ -3,8 +3,8 @@
 // FP8 pools.  A split item holds up to 16 (query, head) rows; the items of a
 // larger tree's further queries lie side by side and share their blocks through
 // L2.  Bound: HBM for up to 16 rows (32 trees of 4 drafts over 1024 to 8192 keys, 32/8
-// heads of 128: 110 us, 0.80 of the copy rate; FP8 91 us), the L2's re-reads above
-// (head_dim 64, 16 trees of 32: 68 us).
+// heads of 128: 107 to 110 us, 0.80 of the copy rate; FP8 91 us), the L2's re-reads above
+// (16 trees of 32 over such keys, 8/2 heads of 64: 67 us).
 #include "decode_kernel.cuh"
 
 namespace pkv {

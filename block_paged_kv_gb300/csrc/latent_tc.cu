@@ -39,9 +39,9 @@
 // 1/76 of the HBM copy rate 0.82 us, 1600 cycles: HBM, or the tensor cores where the
 // rows come from L2 (chunks); and shared memory, at 128 bytes a cycle: 147 KB of rows
 // written and read on CTA 0 (1152 cycles), 176 KB with the weights on CTA 1 (1375).
-// Measured: 2 chunks of 512 x 16 heads 129 us (tensor pipe 50 % busy, L2 hits 92 %, a
-// tile about 1750 cycles), decode of 32 rows x 128 heads 57.5 us (186 MB from HBM, 3.4
-// TB/s; tensor pipe 33 %), of 4 rows x 16 heads 17 us, launches and one chain of
+// Measured: 2 chunks of 512 x 16 heads 132 to 135 us (tensor pipe 49 % busy, L2 hits 92 %,
+// a tile about 1750 cycles), decode of 32 rows x 128 heads 58.4 us (186 MB from HBM, 3.4
+// TB/s; tensor pipe 32 %), of 4 rows x 16 heads 17 us, launches and one chain of
 // dependent steps.
 #include <algorithm>
 
